@@ -94,6 +94,12 @@ typedef enum kq_status {
  * entry points return KQ_ERR_TYPE for it). */
 typedef enum kq_wtype { KQ_Q4_K = 1, KQ_Q6_K = 2, KQ_TQ4_1S = 3, KQ_Q5_K = 4 } kq_wtype;
 
+/* Element types of the row operators' inputs and of the group scales. */
+typedef enum kq_dtype { KQ_F32 = 1, KQ_F16 = 2, KQ_BF16 = 3 } kq_dtype;
+
+/* Score function of kq_moe_route. */
+typedef enum kq_score { KQ_SCORE_SOFTMAX = 1, KQ_SCORE_SIGMOID = 2 } kq_score;
+
 typedef enum kq_op { KQ_OP_MATVEC = 1, KQ_OP_GEMM = 2, KQ_OP_MOE = 3 } kq_op;
 
 /* Device error codes reported by kq_get_device_error. */
@@ -267,6 +273,103 @@ KQ_API kq_status kq_moe_grouped_gemm(int wtype, const void* W_experts, int32_t n
  */
 KQ_API kq_status kq_moe_combine(const float* Y, const float* probs, float* out, int64_t M, int64_t T, int32_t top_k,
                                 kq_stream_t stream);
+
+/*
+ * The operators of a decode step around 4-bit experts with group scales. They
+ * hand Q8_1 rows to one another: kq_add_rmsnorm_q8_1 makes the layer's
+ * activations, kq_moe_route chooses the experts, kq_moe_matvec_g4 multiplies
+ * with the chosen experts' matrices (gate and up, then, after kq_swiglu_q8_1,
+ * down), kq_moe_combine sums the slots. They are additions of this library; the
+ * source pages have no counterpart to them. None needs a workspace.
+ *
+ * Rows of floating-point operands are `ld` elements apart and contiguous within
+ * a row; dtype is a kq_dtype (KQ_ERR_TYPE otherwise). For inputs ld is 0 (one
+ * row read for all) or at least the row's length, for outputs at least the
+ * row's length. Base pointers are 16-byte aligned; any ld is taken (rows that
+ * are not 16-byte aligned are read element by element).
+ *
+ * kq_add_rmsnorm_q8_1 — residual addition, RMSNorm and quantisation of N rows:
+ *   h = x + r (R NULL: h = x),  y[k] = h[k] * (1 / sqrt(Sum_k h[k]^2 / K + eps)) * gamma[k],
+ *   H = h, Y = y, each rounded once to dtype; Xq = Q8_1(y) from the unrounded y.
+ * All arithmetic is fp32 (the norm is that of the unrounded h, the sum of
+ * squares in a fixed order). Each operand is X, R, H, Y: dtype [N][K]; gamma:
+ * fp32 [K]; Xq: N * (K/32) * 36 bytes, written. R, H and Y may be NULL. H may be
+ * X or R itself (the same pointer and ld); outputs overlap nothing else.
+ * K % 32 == 0, eps >= 0.
+ * A block of y with an infinity or a NaN gets an infinite or NaN scale d_h (the
+ * block stands for non-finite values); so does one whose maximum is above
+ * 127 * 65504.
+ */
+KQ_API kq_status kq_add_rmsnorm_q8_1(int dtype, const void* X, int64_t ldx, const void* R, int64_t ldr,
+                                     const float* gamma, float eps, void* H, int64_t ldh, void* Y, int64_t ldy,
+                                     void* Xq, int64_t K, int64_t N, kq_stream_t stream);
+
+/*
+ * kq_swiglu_q8_1 — v[k] = silu(gate[k]) * up[k], silu(g) = g / (1 + exp(-g)), in
+ * fp32, quantised to Q8_1 as above. gate, up: dtype [N][K] (for instance the
+ * halves of one [N][2K] buffer, ld = 2K); Xq: N * (K/32) * 36 bytes, written.
+ * K % 32 == 0.
+ */
+KQ_API kq_status kq_swiglu_q8_1(int dtype, const void* gate, int64_t ldg, const void* up, int64_t ldu, void* Xq,
+                                int64_t K, int64_t N, kq_stream_t stream);
+
+/*
+ * kq_moe_route — routing of T tokens to top_k of n_experts experts.
+ *   s = softmax(l) over the token's experts, or 1 / (1 + exp(-l));
+ *   key = s + bias (bias NULL: s); the bias decides the selection only;
+ *   with topk_groups < n_groups: the experts form n_groups equal runs; a group's
+ *   score is the sum of its group_top (1 or 2) largest keys (fewer if it has
+ *   fewer available experts); only experts of the topk_groups best groups stay;
+ *   the top_k largest keys are chosen, in descending order; w_j = s_j; with
+ *   renormalise w_j /= Sum_j w_j (0 where the sum is 0); w_j *= scale.
+ * Ties go to the lowest index (of groups, of experts). The choice is that of
+ * the definition evaluated in 64 bits: keys that 32 bits cannot tell apart are
+ * computed again in fp64 (without a bias the experts are ordered by their
+ * logits, whose order is that of the scores). The weights are computed in fp32.
+ * An expert whose logit is -inf or NaN is not available: score 0, chosen by no
+ * token; so is one whose bias is -inf or NaN, but it keeps its share of the
+ * softmax sum. A logit of +inf counts as the largest finite fp32. A token with
+ * fewer available experts than slots gets the lowest-numbered experts not yet
+ * chosen for the others, with weight 0 (ids are always valid and distinct).
+ * logits: dtype [T][n_experts], rows ld apart; bias: fp32 [n_experts] or NULL;
+ * ids: int32 [T][top_k], probs: fp32 [T][top_k], written. 1 <= n_experts <= 512,
+ * n_experts % n_groups == 0, 1 <= topk_groups <= n_groups,
+ * 1 <= top_k <= topk_groups * n_experts / n_groups.
+ */
+KQ_API kq_status kq_moe_route(int dtype, const void* logits, int64_t ld, const float* bias, int score, int32_t n_groups,
+                              int32_t topk_groups, int32_t group_top, int32_t top_k, int renormalise, float scale,
+                              int32_t* ids, float* probs, int32_t n_experts, int64_t T, kq_stream_t stream);
+
+/*
+ * kq_matvec_g4 — Y[n][m] = Sum_k w[m][k] x_n[k] for Q8_1 rows x and 4-bit weights
+ * with group scales, w[m][k] = s[m][k / group] * (c[m][k] - z[m][k / group]).
+ * W: M rows of K/2 bytes, byte i of a row holding the code of k = 2i in its low
+ * half and of k = 2i + 1 in its high half; scales: scale_dtype (KQ_F16 or
+ * KQ_BF16) [M][ceil(K/group)]; zeros: uint8 [M][ceil(K/group)], any value, or
+ * NULL (8 everywhere). group: a power of two >= 32, not necessarily dividing K
+ * (a group >= K is one scale per row). Xq: N * (K/32) * 36 bytes as
+ * kq_quantize_q8_1, kq_add_rmsnorm_q8_1 and kq_swiglu_q8_1 write them (the
+ * stored block sums are not read). Y: fp32 [N][M], written. K % 32 == 0; W,
+ * scales, zeros, Xq and Y are 16-byte aligned.
+ * A decode operator: made for up to a few dozen rows of Xq; any N is taken.
+ * Block dot products are exact integers, scales and sums fp32: no rounding of
+ * the operands beside the Q8_1 codes themselves.
+ */
+KQ_API kq_status kq_matvec_g4(const void* W, const void* scales, int scale_dtype, const void* zeros, int64_t group,
+                              const void* Xq, float* Y, int64_t M, int64_t K, int64_t N, kq_stream_t stream);
+
+/*
+ * kq_moe_matvec_g4 — kq_matvec_g4 with the matrices that a router chose:
+ * Y[t][j][:] = W_e . x with e = expert_ids[t*top_k + j] and x row t of Xq, or row
+ * t*top_k + j where x_per_slot is non-zero. W, scales, zeros: the experts'
+ * matrices one after the other (n_experts * M rows); expert_ids: int32
+ * [T][top_k]; Y: fp32 [T][top_k][M], written. n_experts <= 512,
+ * top_k <= n_experts. An out-of-range expert id records KQ_DEVERR_EXPERT_ID and
+ * that slot's output row is written as zeros.
+ */
+KQ_API kq_status kq_moe_matvec_g4(const void* W, const void* scales, int scale_dtype, const void* zeros, int64_t group,
+                                  int32_t n_experts, const int32_t* expert_ids, int32_t top_k, int x_per_slot,
+                                  const void* Xq, float* Y, int64_t M, int64_t K, int64_t T, kq_stream_t stream);
 
 /*
  * kq_workspace_bytes — device workspace needed by an operation (0 for

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 
-from ._native import (KQ_DEVERR_EXPERT_ID, KQ_DEVERR_NONE, KQ_DEVERR_WAIT_TIMEOUT, KQ_GEMM_STATIC_WS_BYTES,
+from ._native import (KQ_BF16, KQ_F16, KQ_F32, KQ_SCORE_SIGMOID, KQ_SCORE_SOFTMAX, KQ_DEVERR_EXPERT_ID, KQ_DEVERR_NONE, KQ_DEVERR_WAIT_TIMEOUT, KQ_GEMM_STATIC_WS_BYTES,
                       KQ_OP_GEMM, KQ_OP_MATVEC, KQ_OP_MOE, KQ_Q4_K, KQ_Q5_K, KQ_Q6_K, KQ_TQ4_1S, KQError, check, lib)
 
 __all__ = [
@@ -18,6 +18,8 @@ __all__ = [
     "KQ_DEVERR_NONE", "KQ_DEVERR_WAIT_TIMEOUT", "KQ_DEVERR_EXPERT_ID",
     "KQ_GEMM_STATIC_WS_BYTES", "kq_quantize_q8_1", "kq_matvec", "kq_matvec_prefetch", "kq_matvec_swiglu", "kq_matvec_rmsnorm",
     "kq_gemm", "kq_gemm_noalloc", "kq_moe_grouped_gemm", "kq_moe_combine", "kq_workspace_bytes",
+    "kq_add_rmsnorm_q8_1", "kq_swiglu_q8_1", "kq_moe_route", "kq_matvec_g4", "kq_moe_matvec_g4",
+    "KQ_F32", "KQ_F16", "KQ_BF16", "KQ_SCORE_SOFTMAX", "KQ_SCORE_SIGMOID",
     "kq_get_device_error", "kq_test_hold_copies", "block_bytes", "row_bytes",
 ]
 
@@ -87,6 +89,59 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+_DTYPES = None  # torch dtype -> kq_dtype
+
+
+def _dtype(t, name: str) -> int:
+    """kq_dtype of a tensor of fp32, fp16 or bf16."""
+    global _DTYPES
+    if _DTYPES is None:
+        torch = _torch()
+        _DTYPES = {torch.float32: KQ_F32, torch.float16: KQ_F16, torch.bfloat16: KQ_BF16}
+    d = _DTYPES.get(getattr(t, "dtype", None))
+    if d is None:
+        raise TypeError(f"{name} must be a float32, float16 or bfloat16 CUDA tensor")
+    return d
+
+
+def _rows(t, name: str, shape, dtype):
+    """(device pointer, elements from row to row) of a 2-D CUDA tensor whose rows are contiguous."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor (libkq has no CPU path)")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    ld, step = t.stride()
+    if step != 1 and shape[1] != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
+
+
+def _sized(t, name: str, numel: int, dtype):
+    """Device pointer of a contiguous CUDA tensor with `numel` elements; None for None."""
+    if t is None:
+        return None
+    p = _dev(t, name, dtype)
+    if t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
+    return p
+
+
+def _out(shape, dtype, device, stream):
+    """A new output of a call on `stream`. Given a stream other than the current one, its
+    memory comes from that stream's pool: work that the current stream still has
+    queued on freed memory does not meet the call's writes."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def kq_quantize_q8_1(X, Xq=None, stream=None):
     """X: fp32 [N, K] -> Q8_1 bytes uint8 [N, K/32, 36]."""
     torch = _torch()
@@ -153,6 +208,135 @@ def kq_moe_combine(Y, probs, out=None, stream=None):
     check(lib().kq_moe_combine(_dev(Y, "Y", torch.float32), _dev(probs, "probs", torch.float32),
                                _dev(out, "out", torch.float32), M, T, top_k, _stream(stream)), "kq_moe_combine")
     return out
+
+
+def kq_add_rmsnorm_q8_1(X, R, gamma, eps: float, H=None, Y=False, Xq=None, stream=None):
+    """H = X + R, Y = H / sqrt(mean(H^2) + eps) * gamma, Xq = Q8_1(Y) for rows X, R [N, K] of one type.
+
+    Returns (H, Y, Xq), Xq uint8 [N, K/32, 36]. R None: H = X, and H is returned only where a
+    tensor is given for it. H may be X or R. Y: False for no normed rows, True for new ones.
+    """
+    torch = _torch()
+    dt = _dtype(X, "X")
+    if X.dim() != 2:
+        raise ValueError("X must have shape [N, K]")
+    shape = X.shape
+    N, K = shape
+    x, ldx = _rows(X, "X", shape, X.dtype)
+    r, ldr = _rows(R, "R", shape, X.dtype) if R is not None else (None, 0)
+    if H is None and R is not None:
+        H = _out((N, K), X.dtype, X.device, stream)
+    h, ldh = _rows(H, "H", shape, X.dtype) if H is not None else (None, 0)
+    if Y is True:
+        Y = _out((N, K), X.dtype, X.device, stream)
+    elif Y is False:
+        Y = None
+    y, ldy = _rows(Y, "Y", shape, X.dtype) if Y is not None else (None, 0)
+    if Xq is None:
+        Xq = _out((N, K // 32, 36), torch.uint8, X.device, stream)
+    check(lib().kq_add_rmsnorm_q8_1(dt, x, ldx, r, ldr, _sized(gamma, "gamma", K, torch.float32), float(eps), h, ldh,
+                                    y, ldy, _sized(Xq, "Xq", N * (K // 32) * 36, torch.uint8), K, N, _stream(stream)),
+          "kq_add_rmsnorm_q8_1")
+    return H, Y, Xq
+
+
+def kq_swiglu_q8_1(gate, up, Xq=None, stream=None):
+    """Xq = Q8_1(silu(gate) * up) for rows gate, up [N, K] of one type; uint8 [N, K/32, 36]."""
+    torch = _torch()
+    dt = _dtype(gate, "gate")
+    if gate.dim() != 2:
+        raise ValueError("gate must have shape [N, K]")
+    shape = gate.shape
+    N, K = shape
+    g, ldg = _rows(gate, "gate", shape, gate.dtype)
+    u, ldu = _rows(up, "up", shape, gate.dtype)
+    if Xq is None:
+        Xq = _out((N, K // 32, 36), torch.uint8, gate.device, stream)
+    check(lib().kq_swiglu_q8_1(dt, g, ldg, u, ldu, _sized(Xq, "Xq", N * (K // 32) * 36, torch.uint8), K, N,
+                               _stream(stream)), "kq_swiglu_q8_1")
+    return Xq
+
+
+_SCORES = {"softmax": KQ_SCORE_SOFTMAX, "sigmoid": KQ_SCORE_SIGMOID}
+
+
+def kq_moe_route(logits, top_k: int, score="softmax", bias=None, n_groups: int = 1, topk_groups: int = 1,
+                 group_top: int = 2, renormalise: bool = True, scale: float = 1.0, ids=None, probs=None, stream=None):
+    """The top_k experts of every token and their weights: (int32 [T, top_k], fp32 [T, top_k]).
+
+    logits: [T, E] (fp32, fp16 or bf16); score: "softmax" or "sigmoid"; bias: fp32 [E], added
+    to the scores for the selection only; with topk_groups < n_groups only the best groups'
+    experts are chosen from, a group's score being the sum of its group_top largest keys.
+    """
+    torch = _torch()
+    dt = _dtype(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must have shape [T, E]")
+    T, E = logits.shape
+    x, ld = _rows(logits, "logits", logits.shape, logits.dtype)
+    sc = _SCORES[score] if isinstance(score, str) else int(score)
+    top_k = int(top_k)
+    if ids is None:
+        ids = _out((T, top_k), torch.int32, logits.device, stream)
+    if probs is None:
+        probs = _out((T, top_k), torch.float32, logits.device, stream)
+    check(lib().kq_moe_route(dt, x, ld, _sized(bias, "bias", E, torch.float32), sc, n_groups, topk_groups, group_top,
+                             top_k, bool(renormalise), float(scale), _sized(ids, "ids", T * top_k, torch.int32),
+                             _sized(probs, "probs", T * top_k, torch.float32), E, T, _stream(stream)), "kq_moe_route")
+    return ids, probs
+
+
+def _g4(W, scales, zeros, rows: int, K: int, group: int):
+    torch = _torch()
+    if group <= 0:
+        raise ValueError("group must be a power of two >= 32")
+    sd = _dtype(scales, "scales")
+    groups = -(-K // group)
+    return (_sized(W, "W", rows * (K // 2), torch.uint8), _sized(scales, "scales", rows * groups, scales.dtype), sd,
+            _sized(zeros, "zeros", rows * groups, torch.uint8), group)
+
+
+def _q8_rows(Xq, K: int) -> int:
+    """Rows of Q8_1 blocks of K values in Xq."""
+    row = (K // 32) * 36
+    n = Xq.numel() // row if row > 0 else 0
+    if n == 0 or n * row != Xq.numel():
+        raise ValueError(f"Xq must hold rows of {row} bytes (K / 32 Q8_1 blocks)")
+    return n
+
+
+def kq_matvec_g4(W, scales, Xq, M: int, K: int, group: int, zeros=None, Y=None, stream=None):
+    """Y[N, M] = Xq . W^T for 4-bit codes W uint8 [M, K/2], scales fp16 or bf16 [M, ceil(K/group)],
+    zeros uint8 of the same shape (None: 8) and Q8_1 rows Xq uint8 [N, K/32, 36]."""
+    torch = _torch()
+    w = _g4(W, scales, zeros, M, K, group)
+    xq = _dev(Xq, "Xq", torch.uint8)
+    N = _q8_rows(Xq, K)
+    if Y is None:
+        Y = _out((N, M), torch.float32, Xq.device, stream)
+    check(lib().kq_matvec_g4(*w, xq, _sized(Y, "Y", N * M, torch.float32), M, K, N, _stream(stream)), "kq_matvec_g4")
+    return Y
+
+
+def kq_moe_matvec_g4(W, scales, n_experts: int, expert_ids, Xq, M: int, K: int, group: int, zeros=None, Y=None,
+                     stream=None):
+    """Y[T, top_k, M]: kq_matvec_g4 with the matrix of expert_ids[t, j] (int32 [T, top_k]).
+
+    W, scales, zeros: n_experts * M rows. Xq: Q8_1 rows, one per token or one per (token, slot).
+    """
+    torch = _torch()
+    w = _g4(W, scales, zeros, n_experts * M, K, group)
+    xq = _dev(Xq, "Xq", torch.uint8)
+    T, top_k = expert_ids.shape
+    n = _q8_rows(Xq, K)
+    if n != T and n != T * top_k:
+        raise ValueError(f"Xq must hold {T} or {T * top_k} rows, got {n}")
+    if Y is None:
+        Y = _out((T, top_k, M), torch.float32, Xq.device, stream)
+    check(lib().kq_moe_matvec_g4(*w, n_experts, _dev(expert_ids, "expert_ids", torch.int32), top_k, n != T, xq,
+                                 _sized(Y, "Y", T * top_k * M, torch.float32), M, K, T, _stream(stream)),
+          "kq_moe_matvec_g4")
+    return Y
 
 
 def kq_workspace_bytes(op: int, wtype, M: int, K: int, N_or_T: int, n_experts: int = 0, top_k: int = 0) -> int:

@@ -24,6 +24,11 @@ KQ_Q4_K = 1
 KQ_Q6_K = 2
 KQ_TQ4_1S = 3
 KQ_Q5_K = 4
+KQ_F32 = 1
+KQ_F16 = 2
+KQ_BF16 = 3
+KQ_SCORE_SOFTMAX = 1
+KQ_SCORE_SIGMOID = 2
 KQ_OP_MATVEC = 1
 KQ_OP_GEMM = 2
 KQ_OP_MOE = 3
@@ -50,6 +55,14 @@ SIGNATURES = {
     "kq_gemm_noalloc": (ctypes.c_int, [ctypes.c_int, _vp, _vp, _vp, _i64, _i64, _i64, _vp]),
     "kq_moe_grouped_gemm": (ctypes.c_int, [ctypes.c_int, _vp, _i32, _vp, _i32, _vp, _vp, _i64, _i64, _i64,
                                            _vp, _sz, _vp]),
+    "kq_add_rmsnorm_q8_1": (ctypes.c_int, [ctypes.c_int, _vp, _i64, _vp, _i64, _vp, ctypes.c_float, _vp, _i64, _vp, _i64,
+                                           _vp, _i64, _i64, _vp]),
+    "kq_swiglu_q8_1": (ctypes.c_int, [ctypes.c_int, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp]),
+    "kq_moe_route": (ctypes.c_int, [ctypes.c_int, _vp, _i64, _vp, ctypes.c_int, _i32, _i32, _i32, _i32, ctypes.c_int,
+                                    ctypes.c_float, _vp, _vp, _i32, _i64, _vp]),
+    "kq_matvec_g4": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _vp]),
+    "kq_moe_matvec_g4": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _vp, _i64, _i32, _vp, _i32, ctypes.c_int, _vp, _vp,
+                                        _i64, _i64, _i64, _vp]),
     "kq_workspace_bytes": (_sz, [ctypes.c_int, ctypes.c_int, _i64, _i64, _i64, _i32, _i32]),
     "kq_get_device_error": (ctypes.c_int, [ctypes.POINTER(_i32), _vp]),
     "kq_test_hold_copies": (ctypes.c_int, [ctypes.c_int]),

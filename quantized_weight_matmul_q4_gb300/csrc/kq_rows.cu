@@ -1,0 +1,180 @@
+// Row producers with a Q8_1 output: the residual addition with RMSNorm, and
+// SwiGLU. Each reads its rows once, computes in fp32 and quantises the produced
+// fp32 values, so that the activations of the next weight product go to memory
+// as 36 bytes per 32 values.
+//
+//   add + RMSNorm:  h = x + r,  y = (h * 1 / sqrt(Sum h^2 / K + eps)) * gamma
+//   SwiGLU:         v = gate / (1 + exp(-gate)) * up
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "kq_internal.h"
+#include "kq_quant.cuh"
+#include "kq_types.cuh"
+
+namespace kq {
+namespace {
+
+// The Q8_1 block of 32 values held by the four lanes of an aligned lane quad,
+// eight each (v), written to block `dst`. All 32 lanes of the warp call it;
+// lanes without `store` take part in the shuffles only.
+//
+// Same codes and scales as quantize_oct for finite values. Here a NaN or an
+// infinity reaches the scale (the maximum is taken over the bit patterns of
+// |v|, where NaN is above infinity), so that such a block stands for
+// non-finite values instead of hiding them.
+__device__ __forceinline__ void store_q8_block(const float (&v)[8], uint8_t* dst, bool store) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7fffffffu);
+  a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+  const float d = __fdiv_rn(__uint_as_float(a), 127.0f);
+  const float di = q8_inv_scale(d);
+  uint32_t q[2];
+  int s = 0;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    uint32_t u[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) u[k] = __float_as_uint(__fadd_rn(__fmul_rn(v[4 * w + k], di), 12582912.0f));
+    q[w] = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+    s = __dp4a(static_cast<int>(q[w]), 0x01010101, s);
+  }
+  s += __shfl_xor_sync(0xffffffffu, s, 1);
+  s += __shfl_xor_sync(0xffffffffu, s, 2);
+  if (!store) return;
+  const int j = threadIdx.x & 3;
+  // Blocks are 36 bytes apart: 4-byte stores.
+  uint32_t* p = reinterpret_cast<uint32_t*>(dst + 4 + 8 * j);
+  p[0] = q[0];
+  p[1] = q[1];
+  if (j == 0) {
+    const __half dh = __float2half_rn(d);
+    const __half sh = __float2half_rn(__fmul_rn(__half2float(dh), static_cast<float>(s)));
+    *reinterpret_cast<uint32_t*>(dst) =
+        static_cast<uint32_t>(__half_as_ushort(dh)) | (static_cast<uint32_t>(__half_as_ushort(sh)) << 16);
+  }
+}
+
+// One row per CTA; thread t takes the row's runs of eight values t, t + blockDim, ...
+// The row is read twice (the second time from L2): once for the sum of squares
+// and once for the outputs. H may be X or R themselves: an element is read and
+// written by the same thread, the read first.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(512) add_rmsnorm_kernel(const T* X, int64_t ldx, const T* R, int64_t ldr,
+                                                          const float* __restrict__ gamma, float eps, T* H, int64_t ldh,
+                                                          T* Y, int64_t ldy, uint8_t* __restrict__ Xq, int K) {
+  __shared__ float part[16];
+  pdl_enter();
+  const int64_t n = blockIdx.x;
+  const T* x = X + n * ldx;
+  const T* r = R ? R + n * ldr : nullptr;
+  const int runs = K >> 3;
+  float ss = 0.f;
+  for (int i = threadIdx.x; i < runs; i += blockDim.x) {
+    float v[8], w[8];
+    load8<T, VEC>(x + 8 * i, v);
+    if (r) {
+      load8<T, VEC>(r + 8 * i, w);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += w[k];
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ss = fmaf(v[k], v[k], ss);
+  }
+  ss = warp_sum_f(ss);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
+  __syncthreads();
+  ss = 0.f;
+  for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) ss += part[i];
+  const float rr = __fdiv_rn(1.0f, sqrtf(__fdiv_rn(ss, static_cast<float>(K)) + eps));
+  uint8_t* xq = Xq + n * (K >> 5) * Q8_1_BYTES;
+  for (int i0 = 0; i0 < runs; i0 += blockDim.x) {
+    const int i = i0 + threadIdx.x;
+    const bool in = i < runs;
+    float v[8] = {}, w[8];
+    if (in) {
+      load8<T, VEC>(x + 8 * i, v);
+      if (r) {
+        load8<T, VEC>(r + 8 * i, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += w[k];
+      }
+      if (H) store8<T, VEC>(H + n * ldh + 8 * i, v);
+      load8<float, true>(gamma + 8 * i, w);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = v[k] * rr * w[k];
+      if (Y) store8<T, VEC>(Y + n * ldy + 8 * i, v);
+    }
+    store_q8_block(v, xq + (i >> 2) * Q8_1_BYTES, in);
+  }
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) swiglu_kernel(const T* __restrict__ G, int64_t ldg, const T* __restrict__ U,
+                                                     int64_t ldu, uint8_t* __restrict__ Xq, int K, int64_t N) {
+  pdl_enter();
+  const int runs = K >> 3;
+  const int64_t total = N * runs;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * 256; t0 < total; t0 += stride) {
+    const int64_t t = t0 + threadIdx.x;
+    const bool in = t < total;
+    float g[8] = {}, u[8];
+    if (in) {
+      const int64_t n = t / runs;
+      const int64_t i = t - n * runs;
+      load8<T, VEC>(G + n * ldg + 8 * i, g);
+      load8<T, VEC>(U + n * ldu + 8 * i, u);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) g[k] = __fdiv_rn(g[k], 1.0f + expf(-g[k])) * u[k];
+    }
+    store_q8_block(g, Xq + (t >> 2) * Q8_1_BYTES, in);
+  }
+}
+
+// Sixteen-byte accesses are taken where every row starts on such a boundary.
+bool rows16(int64_t ld, int size) { return (ld * size) % 16 == 0; }
+
+template <typename T>
+cudaError_t launch_norm_t(const void* X, int64_t ldx, const void* R, int64_t ldr, const float* gamma, float eps, void* H,
+                          int64_t ldh, void* Y, int64_t ldy, void* Xq, int64_t K, int64_t N, cudaStream_t s) {
+  const int sz = sizeof(T);
+  const bool vec = rows16(ldx, sz) && (!R || rows16(ldr, sz)) && (!H || rows16(ldh, sz)) && (!Y || rows16(ldy, sz));
+  const int threads = static_cast<int>(std::min<int64_t>(512, ((K / 8) + 31) / 32 * 32));
+  auto k = vec ? add_rmsnorm_kernel<T, true> : add_rmsnorm_kernel<T, false>;
+  return launch_pdl(k, dim3(static_cast<unsigned>(N)), dim3(threads), 0, s, static_cast<const T*>(X), ldx,
+                    static_cast<const T*>(R), ldr, gamma, eps, static_cast<T*>(H), ldh, static_cast<T*>(Y), ldy,
+                    static_cast<uint8_t*>(Xq), static_cast<int>(K));
+}
+
+template <typename T>
+cudaError_t launch_swiglu_t(const void* G, int64_t ldg, const void* U, int64_t ldu, void* Xq, int64_t K, int64_t N,
+                            int num_sms, cudaStream_t s) {
+  const bool vec = rows16(ldg, sizeof(T)) && rows16(ldu, sizeof(T));
+  const int64_t blocks = std::min<int64_t>((N * (K / 8) + 255) / 256, static_cast<int64_t>(num_sms) * 8);
+  auto k = vec ? swiglu_kernel<T, true> : swiglu_kernel<T, false>;
+  return launch_pdl(k, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, static_cast<const T*>(G), ldg,
+                    static_cast<const T*>(U), ldu, static_cast<uint8_t*>(Xq), static_cast<int>(K), N);
+}
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm_q8_1(int dtype, const void* X, int64_t ldx, const void* R, int64_t ldr,
+                                    const float* gamma, float eps, void* H, int64_t ldh, void* Y, int64_t ldy,
+                                    void* Xq, int64_t K, int64_t N, cudaStream_t s) {
+  if (dtype == KQ_F32) return launch_norm_t<float>(X, ldx, R, ldr, gamma, eps, H, ldh, Y, ldy, Xq, K, N, s);
+  if (dtype == KQ_F16) return launch_norm_t<__half>(X, ldx, R, ldr, gamma, eps, H, ldh, Y, ldy, Xq, K, N, s);
+  return launch_norm_t<__nv_bfloat16>(X, ldx, R, ldr, gamma, eps, H, ldh, Y, ldy, Xq, K, N, s);
+}
+
+cudaError_t launch_swiglu_q8_1(int dtype, const void* G, int64_t ldg, const void* U, int64_t ldu, void* Xq, int64_t K,
+                               int64_t N, int num_sms, cudaStream_t s) {
+  if (dtype == KQ_F32) return launch_swiglu_t<float>(G, ldg, U, ldu, Xq, K, N, num_sms, s);
+  if (dtype == KQ_F16) return launch_swiglu_t<__half>(G, ldg, U, ldu, Xq, K, N, num_sms, s);
+  return launch_swiglu_t<__nv_bfloat16>(G, ldg, U, ldu, Xq, K, N, num_sms, s);
+}
+
+}  // namespace kq

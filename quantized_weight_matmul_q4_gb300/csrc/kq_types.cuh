@@ -1,0 +1,55 @@
+// Reads and writes of eight consecutive elements of a row in fp32, fp16 or bf16.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "kq_common.cuh"
+
+namespace kq {
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// VEC: p is 16-byte aligned (one or two 16-byte accesses); otherwise element
+// by element. Plain loads, not the read-only path: an output may be the input.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+  if constexpr (VEC) {
+    constexpr int W = sizeof(T) * 8 / 16;
+    alignas(16) uint4 raw[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) raw[i] = reinterpret_cast<const uint4*>(p)[i];
+    const T* e = reinterpret_cast<const T*>(raw);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f32(e[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f32(p[i]);
+  }
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
+  if constexpr (VEC) {
+    constexpr int W = sizeof(T) * 8 / 16;
+    alignas(16) T e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = from_f32<T>(v[i]);
+#pragma unroll
+    for (int i = 0; i < W; ++i) reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(e)[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = from_f32<T>(v[i]);
+  }
+}
+
+}  // namespace kq

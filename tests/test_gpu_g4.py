@@ -1,0 +1,185 @@
+"""kq_matvec_g4 and kq_moe_matvec_g4 on the GPU against the fp64 oracle."""
+import numpy as np
+import pytest
+
+from oracle import decode_oracle as deo
+import quantized_weight_matmul_q4_gb300 as kq
+from _decodeutil import assert_g4, g4_weights, q8_rows
+from _kqutil import to_dev
+
+pytestmark = pytest.mark.gpu
+
+
+def _dev_weights(W, s, z, scales):
+    import torch
+    t = torch.float16 if scales == "fp16" else torch.bfloat16
+    sd = torch.from_numpy(s).cuda().to(t)
+    return to_dev(W, torch), sd, sd.cpu().double().numpy(), None if z is None else to_dev(z, torch)
+
+
+CASES = [
+    # N, M, K, group, zeros, scales
+    (1, 1, 32, 32, False, "fp16"),
+    (1, 17, 64, 32, True, "bf16"),
+    (1, 4096, 4096, 128, False, "fp16"),
+    (1, 1000, 11008, 64, True, "fp16"),
+    (1, 130, 14336, 1 << 20, True, "bf16"),     # one scale per row
+    (1, 333, 1056, 128, True, "fp16"),          # the last group is short
+    (1, 70, 18944, 32, True, "bf16"),
+    (2, 257, 2048, 128, True, "bf16"),
+    (3, 100, 4128, 256, False, "fp16"),
+    (4, 515, 768, 64, False, "bf16"),
+    (5, 64, 3584, 512, True, "fp16"),
+    (7, 200, 4096, 32, True, "bf16"),
+    (8, 129, 11008, 128, False, "fp16"),
+    (9, 31, 992, 32, True, "fp16"),
+    (16, 300, 2080, 64, True, "bf16"),
+    (17, 48, 4096, 128, True, "fp16"),
+    (37, 150, 768, 128, False, "bf16"),
+    (130, 65, 512, 32, True, "fp16"),
+]
+
+
+@pytest.mark.parametrize("N,M,K,group,zeros,scales", CASES)
+def test_matvec_g4(N, M, K, group, zeros, scales):
+    import torch
+    rng = np.random.default_rng(N + M + K)
+    W, s, z = g4_weights(rng, M, K, group, zeros)
+    Xq = q8_rows(rng, N, K)
+    Wd, sd, sr, zd = _dev_weights(W, s, z, scales)
+    Y = torch.full((N * M + 64,), 7.5, device="cuda")
+    out = kq.kq_matvec_g4(Wd, sd, to_dev(Xq, torch), M, K, group, zeros=zd, Y=Y[:N * M].view(N, M))
+    assert bool((Y[N * M:] == 7.5).all())        # nothing past the output
+    ref, B = deo.g4_matmul(W, sr, z, group, Xq)
+    assert_g4(out.cpu().numpy(), ref, B, K, f"{N}x{M}x{K}")
+    again = kq.kq_matvec_g4(Wd, sd, to_dev(Xq, torch), M, K, group, zeros=zd)
+    assert torch.equal(out, again)
+    assert kq.kq_get_device_error() == 0
+
+
+def test_zero_points_beyond_four_bits():
+    import torch
+    rng = np.random.default_rng(1)
+    W, s, _ = g4_weights(rng, 90, 512, 64, False)
+    z = rng.integers(0, 256, s.shape, dtype=np.uint8)
+    for N in (1, 6, 12):
+        Xq = q8_rows(rng, N, 512)
+        Xq[0, 0, 4:] = 0x80                      # codes of -128
+        Wd, sd, sr, zd = _dev_weights(W, s, z, "fp16")
+        got = kq.kq_matvec_g4(Wd, sd, to_dev(Xq, torch), 90, 512, 64, zeros=zd)
+        ref, B = deo.g4_matmul(W, sr, z, 64, Xq)
+        assert_g4(got.cpu().numpy(), ref, B, 512, "wide zero points")
+
+
+def test_each_code_and_position():
+    """One-hot activations read back every weight exactly: s (c - z) of each k."""
+    import torch
+    K, M = 256, 16
+    rng = np.random.default_rng(2)
+    W, s, z = g4_weights(rng, M, K, 64, True)
+    Wd, sd, sr, zd = _dev_weights(W, s, z, "fp16")
+    Xq = np.zeros((K, K // 32, 36), np.uint8)
+    one = np.float16(1.0).view(np.uint16)
+    for k in range(K):
+        Xq[k, k // 32, 0:2] = np.array([one]).view(np.uint8)
+        Xq[k, k // 32, 4 + k % 32] = 1
+    want = (sr[:, np.arange(K) // 64] * (deo.g4_codes(W) - z.astype(int)[:, np.arange(K) // 64])).T
+    for n in (1, 5, 8, 16, K):
+        got = torch.cat([kq.kq_matvec_g4(Wd, sd, to_dev(Xq[i:i + n], torch), M, K, 64, zeros=zd) for i in range(0, K, n)])
+        assert np.array_equal(got.cpu().double().numpy(), want), n
+
+
+def test_non_finite_scales_reach_the_output():
+    import torch
+    rng = np.random.default_rng(6)
+    for N in (1, 9):
+        W, s, z = g4_weights(rng, 20, 256, 64, True)
+        s[3, 1] = np.inf
+        Xq = q8_rows(rng, N, 256)
+        Xq[0, 2, 0:2] = np.array([np.float16(np.nan)]).view(np.uint8)
+        Wd, sd, sr, zd = _dev_weights(W, s, z, "fp16")
+        got = kq.kq_matvec_g4(Wd, sd, to_dev(Xq, torch), 20, 256, 64, zeros=zd).cpu().numpy()
+        assert np.all(np.isnan(got[0]))
+        if N > 1:
+            assert not np.isfinite(got[1:, 3]).any()
+            assert np.isfinite(np.delete(got[1:], 3, 1)).all()
+
+
+MOE = [
+    # T, E, top_k, M, K, group, zeros, scales, per_slot
+    (1, 8, 2, 96, 256, 32, True, "fp16", False),
+    (1, 128, 8, 1536, 2048, 128, False, "fp16", False),
+    (1, 16, 8, 2048, 768, 64, True, "bf16", True),
+    (3, 4, 4, 50, 544, 128, True, "fp16", True),
+    (16, 32, 4, 130, 1024, 32, True, "bf16", False),
+    (40, 3, 2, 100, 768, 128, False, "bf16", True),     # many rows to every expert
+    (64, 96, 8, 64, 512, 64, True, "fp16", True),
+    (9, 1, 1, 33, 64, 32, True, "fp16", False),
+    (200, 6, 3, 40, 288, 32, True, "fp16", False),
+    (700, 512, 8, 17, 64, 64, False, "fp16", False),
+]
+
+
+@pytest.mark.parametrize("T,E,top_k,M,K,group,zeros,scales,per_slot", MOE)
+def test_moe_matvec_g4(T, E, top_k, M, K, group, zeros, scales, per_slot):
+    import torch
+    rng = np.random.default_rng(T + E + M)
+    W, s, z = g4_weights(rng, E * M, K, group, zeros)
+    Xq = q8_rows(rng, T * top_k if per_slot else T, K)
+    ids = np.argsort(rng.standard_normal((T, E)), 1)[:, :top_k].astype(np.int32)
+    Wd, sd, sr, zd = _dev_weights(W, s, z, scales)
+    Y = torch.full((T * top_k * M + 64,), 7.5, device="cuda")
+    got = kq.kq_moe_matvec_g4(Wd, sd, E, to_dev(ids, torch), to_dev(Xq, torch), M, K, group, zeros=zd,
+                              Y=Y[:T * top_k * M].view(T, top_k, M))
+    assert bool((Y[T * top_k * M:] == 7.5).all())
+    ref, B = deo.moe_g4(W, sr, z, group, E, ids, Xq, M)
+    assert_g4(got.cpu().numpy(), ref, B, K, f"T={T} E={E}")
+    again = kq.kq_moe_matvec_g4(Wd, sd, E, to_dev(ids, torch), to_dev(Xq, torch), M, K, group, zeros=zd)
+    assert torch.equal(got, again)
+    assert kq.kq_get_device_error() == 0
+
+
+@pytest.mark.parametrize("T", [1, 30])
+def test_repeated_and_invalid_expert_ids(T):
+    import torch
+    E, top_k, M, K = 5, 3, 70, 320
+    rng = np.random.default_rng(T)
+    W, s, z = g4_weights(rng, E * M, K, 64, True)
+    Xq = q8_rows(rng, T, K)
+    ids = rng.integers(0, E, (T, top_k)).astype(np.int32)    # repeats within a token
+    ids[0] = [4, 4, 4]
+    Wd, sd, sr, zd = _dev_weights(W, s, z, "fp16")
+    call = lambda i: kq.kq_moe_matvec_g4(Wd, sd, E, to_dev(i, torch), to_dev(Xq, torch), M, K, 64, zeros=zd).cpu().numpy()  # noqa: E731
+    ref, B = deo.moe_g4(W, sr, z, 64, E, ids, Xq, M)
+    kq.kq_get_device_error()
+    assert_g4(call(ids), ref, B, K, "repeats")
+    assert kq.kq_get_device_error() == kq.KQ_DEVERR_NONE
+    bad = ids.copy()
+    bad[0, 1], bad[T - 1, 2] = -1, E
+    got = call(bad)
+    assert kq.kq_get_device_error() == kq.KQ_DEVERR_EXPERT_ID
+    ok = bad == ids
+    assert np.all(got[~ok] == 0)
+    assert_g4(got[ok], ref[ok], B[ok], K, "valid slots")
+
+
+def test_on_another_stream_and_in_a_graph():
+    import torch
+    rng = np.random.default_rng(11)
+    M, K, N = 512, 1024, 3
+    W, s, z = g4_weights(rng, M, K, 128, True)
+    Wd, sd, _, zd = _dev_weights(W, s, z, "bf16")
+    xq = to_dev(q8_rows(rng, N, K), torch)
+    want = kq.kq_matvec_g4(Wd, sd, xq, M, K, 128, zeros=zd)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = kq.kq_matvec_g4(Wd, sd, xq, M, K, 128, zeros=zd, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    Y = torch.zeros(N, M, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kq.kq_matvec_g4(Wd, sd, xq, M, K, 128, zeros=zd, Y=Y)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(Y, want)
