@@ -114,8 +114,8 @@ int test_hold_copies();
 // device (later calls only read a flag, so launches stay cheap and capturable).
 cudaError_t allow_max_smem(const void* kernel, int slot);
 constexpr int kSmemRoute = 37;  // three slots: the routing kernel's input types
-constexpr int kSmemG4 = 40;     // 32 slots: the group-scaled products' tensor-core forms
-constexpr int kSmemSlots = 72;
+constexpr int kSmemG4 = 40;     // 36 slots: the group-scaled products
+constexpr int kSmemSlots = 76;
 
 // Launches `kernel` on `s` with programmatic stream serialization allowed (the
 // kernel calls pdl_enter() before its first global memory access).
