@@ -113,9 +113,8 @@ int test_hold_copies();
 // Raises a kernel's dynamic shared-memory limit to the 227 KB maximum, once per
 // device (later calls only read a flag, so launches stay cheap and capturable).
 cudaError_t allow_max_smem(const void* kernel, int slot);
-constexpr int kSmemRoute = 37;  // three slots: the routing kernel's input types
-constexpr int kSmemG4 = 40;     // 36 slots: the group-scaled products
-constexpr int kSmemSlots = 76;
+constexpr int kSmemG4 = 37;     // 36 slots: the group-scaled products
+constexpr int kSmemSlots = 73;
 
 // Launches `kernel` on `s` with programmatic stream serialization allowed (the
 // kernel calls pdl_enter() before its first global memory access).
