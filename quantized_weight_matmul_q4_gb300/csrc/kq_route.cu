@@ -30,30 +30,40 @@ namespace {
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int RT_WARPS = 4;
 
-// Order-preserving maps of keys to unsigned integers; -inf (not available, or
-// already taken) maps to 0, below every other key.
-__device__ __forceinline__ uint32_t ord(float v) {
-  const uint32_t b = __float_as_uint(v + 0.f);   // -0 and 0 are one key
-  if (b == 0xff800000u) return 0;
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+__device__ __forceinline__ float warp_max(float v) {   // no NaN
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
-__device__ __forceinline__ float from_ord(uint32_t o) {
-  return __uint_as_float(o == 0 ? 0xff800000u : (o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+__device__ __forceinline__ float warp_min(float v) { return -warp_max(-v); }
+// e^x as 2^(x log2 e): relative error at most 2^-22 (ex2.approx) and 1.5 |x| 2^-24 (the
+// product and its constant).
+__device__ __forceinline__ float fast_exp(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
 }
+__device__ __forceinline__ float fast_rcp(float x) {   // relative error at most 2^-23
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Order-preserving map of fp64 keys to integers; -inf (not available, or already
+// taken) maps to 0, below every other key.
 __device__ __forceinline__ uint64_t ord(double v) {
   const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.));
   if (b == 0xfff0000000000000ull) return 0;
   return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
 }
-__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(FULL, v); }
 __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
   const uint32_t hi = __reduce_max_sync(FULL, static_cast<uint32_t>(v >> 32));
   const uint32_t lo = __reduce_max_sync(FULL, static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
   return (static_cast<uint64_t>(hi) << 32) | lo;
 }
-__device__ __forceinline__ float warp_max_f(float v) { return from_ord(warp_max(ord(v))); }
 
 struct RouteArgs {
+  uint32_t per, recip;   // experts of a group; e / per = e * recip >> 20 for e < 512
   const void* logits;
   int64_t ld;
   const float* bias;
@@ -112,7 +122,7 @@ __device__ __noinline__ void select_exact(const RouteArgs& a, const T* row, floa
   }
   __syncwarp();
   if (a.topk_groups < a.n_groups) {
-    const int per = a.E / a.n_groups;
+    const int per = static_cast<int>(a.per);
     for (int g = lane; g < a.n_groups; g += 32) {
       double m1 = -INFINITY, m2 = -INFINITY;
       for (int i = 0; i < per; ++i) {
@@ -171,10 +181,8 @@ __device__ __forceinline__ int compact(F in, int* list, int lane) {
 template <typename T>
 __device__ __noinline__ double exact_sum(const T* row, int E, float mx, int lane) {
   double sum = 0.;
-  for (int e = lane; e < E; e += 32) {
-    const float l = logit(row, e);
-    if (l != -INFINITY) sum += exp(static_cast<double>(l) - static_cast<double>(mx));
-  }
+#pragma unroll 4
+  for (int e = lane; e < E; e += 32) sum += exp(static_cast<double>(logit(row, e)) - static_cast<double>(mx));   // exp(-inf) = 0
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
   return sum;
@@ -213,60 +221,61 @@ __global__ void __launch_bounds__(RT_WARPS * 32, 8) route_kernel(const __grid_co
     mx = key[0];
 #pragma unroll
     for (int i = 1; i < PER; ++i) mx = fmaxf(mx, key[i]);
-    mx = warp_max_f(mx);
-    if (by_score || !a.renorm) {
+    mx = warp_max(mx);
+    if (mx == -INFINITY) mx = 0.f;   // no expert is available
+    if (a.bias || !a.renorm) {   // without a bias the common factor 1 / Sum changes no order
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) sum += key[i] == -INFINITY ? 0.f : __expf(key[i] - mx);
+      for (int i = 0; i < PER; ++i) sum += fast_exp(key[i] - mx);
       sum = warp_sum_f(sum);
       inv = sum > 0.f ? __fdiv_rn(1.0f, sum) : 1.f;
     }
   }
-  float bmax = 0.f;
+  const float kinv = a.bias ? inv : 1.f;
   if (by_score) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const float b = a.bias && lane + 32 * i < a.E ? __ldg(a.bias + lane + 32 * i) : 0.f;
-      const float k = (softmax ? __expf(key[i] - mx) * inv : __fdividef(1.0f, 1.0f + __expf(-key[i]))) + b;
-      key[i] = (key[i] == -INFINITY || k != k) ? -INFINITY : k;
-      if (fabsf(b) < INFINITY) bmax = fmaxf(bmax, fabsf(b));
+      const float k = (softmax ? fast_exp(key[i] - mx) * kinv : fast_rcp(1.0f + fast_exp(-key[i]))) + b;
+      key[i] = key[i] == -INFINITY ? -INFINITY : fmaxf(k, -INFINITY);   // a NaN is -inf
     }
   }
-  // What two fp32 keys can be apart and still be in the wrong order. __expf(-x) is
-  // off by (2 + 1.173 x) ulp, so e^-x by 2.5 ulp of 1 at most. A softmax score is off
-  // by that, by the sum's own error (the scores' mean x is at most ln 512: 9.4 ulp, and
-  // E / 32 + 5 roundings) and by three roundings: under 2^-18 of the largest score,
-  // which is 1 / Sum. A sigmoid is off by a quarter of 2 + 1.173 ulp and a division of
-  // 2 ulp: under 2^-20 of 1. Adding the bias rounds once more, by 2^-24 of the key.
-  float tol = -1.f;
-  if (by_score) {
-    const float smax = softmax ? inv : 1.0f;
-    tol = 2.f * (smax * (softmax ? 3.8147e-6f : 9.5368e-7f) + 5.9605e-8f * (smax + warp_max_f(bmax)));
-  }
+  // What two fp32 keys can be apart and still be in the wrong order: tol + 2^-22 of the
+  // key. An e^-x <= 1 is off by 2^-22 + 0.37 * 1.5 * 2^-24. A softmax score is off by that,
+  // by the sum's own error (2^-22 and, as the scores' mean x is at most ln 512, 9.4 * 2^-24;
+  // E / 32 + 5 roundings of 2^-24) and by three roundings: under 2^-18 of the largest
+  // score, which is 1 / Sum (without a bias the scores are compared as e^-x: 2^-21). A sigmoid s is off by s (1 - s) times its exponential's error
+  // and by two roundings of 2^-23: under 2^-21 of 1. Adding the bias rounds by 2^-24 of the key.
+  const bool near = by_score && a.bias;   // else the experts go by the exact logits
+  const float tol = 2.f * (softmax && a.bias ? inv * 3.8147e-6f : 4.7684e-7f);
 
   bool clear = true;
   if (groups) {
+    // Keys by group, the groups an odd number of words apart: lanes that read the same
+    // place of different groups meet different banks.
     float* kf = reinterpret_cast<float*>(kd);
     float* gf = reinterpret_cast<float*>(gd);
-    const int per = a.E / a.n_groups;
+    float* in = gf + a.n_groups;
+    const int per = static_cast<int>(a.per), pitch = per | 1;
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (lane + 32 * i < a.E) kf[lane + 32 * i] = key[i];
+    for (int i = 0; i < PER; ++i) {
+      const int e = lane + 32 * i;
+      if (e < a.E) kf[e + static_cast<int>((e * a.recip) >> 20) * (pitch - per)] = key[i];
+    }
     __syncwarp();
-    // 2^sl lanes share a group, each with every 2^sl-th expert of it; a lane starts where
-    // its group's number says, so that groups of 32 do not meet in one bank.
+    // 2^sl lanes share a group, each with every 2^sl-th expert of it.
     int sl = 0;
     while (sl < 5 && (a.n_groups << (sl + 1)) <= 32) ++sl;
     const int step = 1 << sl, sub = lane & (step - 1);
+    float mag = 0.f;   // of the keys in the scores
     for (int g0 = 0; g0 < a.n_groups; g0 += 32 >> sl) {
       const int g = g0 + (lane >> sl);
       float m1 = -INFINITY, m2 = -INFINITY;
       if (g < a.n_groups) {
-        const int n = (per - sub + step - 1) >> sl;   // this lane's experts
-        int j = n > 0 ? g % n : 0;
-        for (int i = 0; i < n; ++i) {
-          const float v = kf[g * per + sub + (j << sl)];
-          j = j + 1 == n ? 0 : j + 1;
+        const float* k = kf + g * pitch;
+#pragma unroll 4
+        for (int j = sub; j < per; j += step) {
+          const float v = k[j];
           m2 = fmaxf(m2, fminf(m1, v));
           m1 = fmaxf(m1, v);
         }
@@ -276,11 +285,16 @@ __global__ void __launch_bounds__(RT_WARPS * 32, 8) route_kernel(const __grid_co
         m2 = fmaxf(fmaxf(m2, x2), fminf(m1, x1));
         m1 = fmaxf(m1, x1);
       }
-      if (g < a.n_groups && sub == 0) gf[g] = (a.group_top == 2 && m2 != -INFINITY) ? m1 + m2 : m1;
+      if (g < a.n_groups && sub == 0) {
+        const bool two = a.group_top == 2 && m2 != -INFINITY;
+        gf[g] = two ? m1 + m2 : m1;
+        const float x = fabsf(m1) + (two ? fabsf(m2) : 0.f);
+        if (x < INFINITY) mag = fmaxf(mag, x);
+      }
     }
     __syncwarp();
     // A group stays if fewer than topk_groups others are before it.
-    uint32_t worst_in = 0xffffffffu, best_out = 0;
+    float cut_in = INFINITY, cut_out = -INFINITY;
     for (int g = lane; g < a.n_groups; g += 32) {
       const float v = gf[g];
       int before = 0;
@@ -288,20 +302,18 @@ __global__ void __launch_bounds__(RT_WARPS * 32, 8) route_kernel(const __grid_co
         const float w = gf[h];
         before += (w > v || (w == v && h < g)) ? 1 : 0;
       }
-      const bool in = before < a.topk_groups;
-      const uint32_t o = ord(v);
-      if (o != 0) {
-        if (in) worst_in = min(worst_in, o); else best_out = max(best_out, o);
-      }
-      kf[g] = in ? 1.f : 0.f;   // the keys are in registers: their place is free
+      const bool stays = before < a.topk_groups;
+      if (stays && v != -INFINITY) cut_in = fminf(cut_in, v);
+      if (!stays) cut_out = fmaxf(cut_out, v);
+      in[g] = stays ? 1.f : 0.f;
     }
     __syncwarp();
-    best_out = warp_max(best_out);
-    const uint32_t recip = ((1u << 20) + per - 1) / per;   // e / per = e * recip >> 20, as e * per < 2^20
-    if (best_out != 0 && by_score) {
+    cut_out = warp_max(cut_out);
+    if (cut_out != -INFINITY && by_score) {
       // A group's score is the sum of two keys: twice a key's error, and a rounding.
-      const float cut_in = from_ord(__reduce_min_sync(FULL, worst_in)), cut_out = from_ord(best_out);
-      if (cut_in - cut_out <= 4 * tol) {
+      const float gtol = 2.f * tol + 4.7684e-7f * warp_max(mag);
+      cut_in = warp_min(cut_in);
+      if (cut_in - cut_out <= gtol) {
         // The groups that could be on either side, and of their experts those that could
         // be among the best group_top.
         float least[PER];
@@ -309,27 +321,27 @@ __global__ void __launch_bounds__(RT_WARPS * 32, 8) route_kernel(const __grid_co
         for (int i = 0; i < PER; ++i) least[i] = INFINITY;
         for (int g = 0; g < a.n_groups; ++g) {
           const float v = gf[g];
-          if (v == -INFINITY || (kf[g] != 0.f ? v > cut_out + 4 * tol : v < cut_in - 4 * tol)) continue;
-          uint32_t m = 0;
+          if (v == -INFINITY || (in[g] != 0.f ? v > cut_out + gtol : v < cut_in - gtol)) continue;
+          float m = -INFINITY;
 #pragma unroll
           for (int i = 0; i < PER; ++i) {
             const int e = lane + 32 * i;
-            if (e < a.E && static_cast<int>((e * recip) >> 20) == g) m = max(m, ord(key[i]));
+            if (e < a.E && static_cast<int>((e * a.recip) >> 20) == g) m = fmaxf(m, key[i]);
           }
           // With group_top 2 the least key that counts is the score less the largest key.
-          const float top = from_ord(warp_max(m));
-          const float low = (a.group_top == 2 ? fminf(v - top, top) : top) - 2 * tol;
+          const float top = warp_max(m);
+          const float low = (a.group_top == 2 ? fminf(v - top, top) : top) - gtol;
 #pragma unroll
           for (int i = 0; i < PER; ++i) {
             const int e = lane + 32 * i;
-            if (e < a.E && static_cast<int>((e * recip) >> 20) == g) least[i] = low;
+            if (e < a.E && static_cast<int>((e * a.recip) >> 20) == g) least[i] = low;
           }
         }
         const int n = compact<PER>([&](int i) { return key[i] != -INFINITY && key[i] >= least[i]; }, list, lane);
         if (n <= 32) {
-          const double sum = softmax ? exact_sum(row, a.E, mx, lane) : 1.;
+          const double sum = softmax && a.bias ? exact_sum(row, a.E, mx, lane) : 1.;
           const int e = lane < n ? list[lane] : -1;
-          const int g = e >= 0 ? e / per : -1;
+          const int g = e >= 0 ? static_cast<int>((e * a.recip) >> 20) : -1;
           const double k = e >= 0 ? exact_key(a, row, e, mx, sum) : 0.;
           double m1 = -INFINITY, m2 = -INFINITY;   // of this lane's group
           for (int c = 0; c < n; ++c) {
@@ -340,18 +352,19 @@ __global__ void __launch_bounds__(RT_WARPS * 32, 8) route_kernel(const __grid_co
             }
           }
           const double score = (a.group_top == 2 && m2 != -INFINITY) ? m1 + m2 : m1;
-          const bool head = e >= 0 && (lane == 0 || list[lane - 1] / per != g);   // the list is in order: one lane per group
+          const int g_left = __shfl_up_sync(FULL, g, 1);
+          const bool head = e >= 0 && (lane == 0 || g_left != g);   // the list is in order: one lane per group
           const unsigned heads = __ballot_sync(FULL, head);
           // Places for them: all but those of the groups that are surely in.
-          int sure = 0;
-          for (int h = lane; h < a.n_groups; h += 32) sure += kf[h] != 0.f && gf[h] > cut_out + 4 * tol ? 1 : 0;
-          sure = static_cast<int>(__reduce_add_sync(FULL, static_cast<unsigned>(sure)));
+          unsigned sure = 0;
+          for (int h = lane; h < a.n_groups; h += 32) sure += in[h] != 0.f && gf[h] > cut_out + gtol ? 1 : 0;
+          sure = __reduce_add_sync(FULL, sure);
           int before = 0;
           for (int c = 0; c < n; ++c) {
             const double v = __shfl_sync(FULL, score, c);
             if ((heads >> c & 1) && (v > score || (v == score && c < lane))) ++before;
           }
-          if (head) kf[g] = sure + before < a.topk_groups ? 1.f : 0.f;
+          if (head) in[g] = static_cast<int>(sure) + before < a.topk_groups ? 1.f : 0.f;
           __syncwarp();
         } else {
           clear = false;
@@ -361,81 +374,81 @@ __global__ void __launch_bounds__(RT_WARPS * 32, 8) route_kernel(const __grid_co
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int e = lane + 32 * i;
-      if (e < a.E && kf[(e * recip) >> 20] == 0.f) key[i] = -INFINITY;
+      if (e < a.E && in[(e * a.recip) >> 20] == 0.f) key[i] = -INFINITY;
     }
-    if (!a.bias) {
-      // Chosen by the logits: nothing is close.
+    if (by_score && !a.bias) {
 #pragma unroll
       for (int i = 0; i < PER; ++i)
         if (key[i] != -INFINITY) key[i] = logit(row, lane + 32 * i);
-      tol = -1.f;
     }
   }
 
   // Top k: each lane keeps its two best keys of those not taken.
-  uint32_t taken = 0, b1, b2;
-  int i1, i2;
-  auto scan = [&] {
-    b1 = b2 = 0;
-    i1 = i2 = 0;
+  uint32_t taken = 0;
+  float b1, b2;
+  int e1, e2;
+  b1 = b2 = -INFINITY;
+  e1 = e2 = 0x7fffffff;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const uint32_t o = (taken >> i) & 1 ? 0 : ord(key[i]);
-      if (o > b1) {
-        b2 = b1;
-        i2 = i1;
-        b1 = o;
-        i1 = i;
-      } else if (o > b2) {
-        b2 = o;
-        i2 = i;
-      }
-    }
-  };
-  scan();
+  for (int i = 0; i < PER; ++i) {
+    const float k = key[i];
+    const bool p = k > b1, q = k > b2;
+    b2 = p ? b1 : q ? k : b2;
+    e2 = p ? e1 : q ? lane + 32 * i : e2;
+    b1 = p ? k : b1;
+    e1 = p ? lane + 32 * i : e1;
+  }
   int held = 2;   // of this lane's best two, not taken yet
   float prev = 0.f;
   int prev_e = -1, found = 0;
   bool close = false;
-  const int rounds = tol >= 0.f ? a.top_k + 1 : a.top_k;   // the last one only to see how close it is
+  const int rounds = near ? a.top_k + 1 : a.top_k;   // the last one only to see how close it is
   for (int j = 0; j < rounds; ++j) {
-    const uint32_t m = warp_max(b1);
-    if (m == 0) {   // no expert is left
+    const float best = warp_max(b1);
+    if (best == -INFINITY) {   // no expert is left
       for (int i = j + lane; i < a.top_k; i += 32) ids[i] = -1;
       break;
     }
-    const unsigned mine = b1 == m ? static_cast<unsigned>(lane + 32 * i1) : 0x7fffffffu;
+    const unsigned mine = b1 == best ? static_cast<unsigned>(e1) : 0x7fffffffu;
     const unsigned e = __reduce_min_sync(FULL, mine);
-    const float best = from_ord(m);
-    if (prev_e >= 0 && prev - best <= tol) {
+    if (near) {
       // Two experts with the same logit and the same bias have the same key in
       // any precision: the lower index is first, as it should be.
-      if (!(logit(row, e) == logit(row, prev_e) && a.bias[e] == a.bias[prev_e])) close = true;
+      if (prev_e >= 0 && prev - best <= fmaf(2.3842e-7f, fabsf(best), tol) &&
+          !(logit(row, e) == logit(row, prev_e) && a.bias[e] == a.bias[prev_e]))
+        close = true;
+      prev_e = static_cast<int>(e);
     }
     if (j == a.top_k) break;
     prev = best;
-    prev_e = static_cast<int>(e);
     ++found;
     if (mine == e) {
       ids[j] = static_cast<int>(e);
-      taken |= 1u << i1;
+      taken |= 1u << (e1 >> 5);
       b1 = b2;
-      i1 = i2;
-      b2 = 0;
+      e1 = e2;
+      b2 = -INFINITY;
       --held;
     }
-    if (PER > 1 && __any_sync(FULL, held == 0)) {
-      if (held == 0) scan();
-      held = held == 0 ? 2 : held;
+    if (PER > 2 && j + 1 < rounds && __any_sync(FULL, held == 0)) {
+      if (held == 0) {   // the best of what is left
+        held = 1;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const bool p = key[i] > b1 && !(taken >> i & 1);
+          b1 = p ? key[i] : b1;
+          e1 = p ? lane + 32 * i : e1;
+        }
+      }
     }
   }
   __syncwarp();
   if (close && clear) {   // warp-uniform
     // The experts that could be among the top k, in the order of their fp64 keys.
-    const float low = found == a.top_k ? prev - tol : -INFINITY;
+    const float low = found == a.top_k ? prev - fmaf(2.3842e-7f, fabsf(prev), tol) : -INFINITY;
     const int n = compact<PER>([&](int i) { return key[i] != -INFINITY && key[i] >= low; }, list, lane);
     if (n <= 32) {
-      const double sum = softmax ? exact_sum(row, a.E, mx, lane) : 1.;
+      const double sum = softmax && a.bias ? exact_sum(row, a.E, mx, lane) : 1.;
       const int e = lane < n ? list[lane] : 0;
       const double k = lane < n ? exact_key(a, row, e, mx, sum) : 0.;
       int before = 0;
@@ -503,7 +516,8 @@ void (*route_for(int E))(RouteArgs, int) {
 cudaError_t launch_moe_route(int dtype, const void* logits, int64_t ld, const float* bias, int score, int n_groups,
                              int topk_groups, int group_top, int top_k, bool renorm, float scale, int* ids, float* probs,
                              int E, int64_t T, cudaStream_t s) {
-  RouteArgs a{logits, ld, bias, score, n_groups, topk_groups, group_top, top_k, renorm, scale, ids, probs, E, T};
+  const uint32_t per = static_cast<uint32_t>(E / n_groups);
+  RouteArgs a{per, ((1u << 20) + per - 1) / per, logits, ld, bias, score, n_groups, topk_groups, group_top, top_k, renorm, scale, ids, probs, E, T};
   const int warp_bytes = (8 * E + 8 * n_groups + 4 * top_k + 128 + 15) / 16 * 16;
   const size_t smem = static_cast<size_t>(RT_WARPS) * warp_bytes;   // at most 40 KB
   auto k = dtype == KQ_F32 ? route_for<float>(E) : dtype == KQ_F16 ? route_for<__half>(E) : route_for<__nv_bfloat16>(E);
