@@ -201,7 +201,7 @@ kq_status kq_add_rmsnorm_q8_1(int dtype, const void* X, int64_t ldx, const void*
   int* err;
   cudaError_t e = device_state(&dev, &sms, &err);
   if (e != cudaSuccess) return KQ_ERR_CUDA;
-  return finish(launch_add_rmsnorm_q8_1(dtype, X, ldx, R, ldr, gamma, eps, H, ldh, Y, ldy, Xq, K, N,
+  return finish(launch_add_rmsnorm_q8_1(dtype, X, ldx, R, ldr, gamma, eps, H, ldh, Y, ldy, Xq, K, N, sms,
                                         reinterpret_cast<cudaStream_t>(stream)),
                 KQ_OK);
 }

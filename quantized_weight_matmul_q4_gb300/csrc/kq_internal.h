@@ -77,7 +77,7 @@ cudaError_t launch_moe_combine(const float* Y, const float* probs, float* out, i
 // from row to row.
 cudaError_t launch_add_rmsnorm_q8_1(int dtype, const void* X, int64_t ldx, const void* R, int64_t ldr,
                                     const float* gamma, float eps, void* H, int64_t ldh, void* Y, int64_t ldy,
-                                    void* Xq, int64_t K, int64_t N, cudaStream_t s);
+                                    void* Xq, int64_t K, int64_t N, int num_sms, cudaStream_t s);
 cudaError_t launch_swiglu_q8_1(int dtype, const void* G, int64_t ldg, const void* U, int64_t ldu, void* Xq, int64_t K,
                                int64_t N, int num_sms, cudaStream_t s);
 

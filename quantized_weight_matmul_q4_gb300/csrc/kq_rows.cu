@@ -16,21 +16,26 @@
 namespace kq {
 namespace {
 
+__device__ __forceinline__ float max_nan(float a, float b) {   // a NaN stays
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // The Q8_1 block of 32 values held by the four lanes of an aligned lane quad,
 // eight each (v), written to block `dst`. All 32 lanes of the warp call it;
 // lanes without `store` take part in the shuffles only.
 //
 // Same codes and scales as quantize_oct for finite values. Here a NaN or an
-// infinity reaches the scale (the maximum is taken over the bit patterns of
-// |v|, where NaN is above infinity), so that such a block stands for
-// non-finite values instead of hiding them.
+// infinity reaches the scale, so that such a block stands for non-finite values
+// instead of hiding them.
 __device__ __forceinline__ void store_q8_block(const float (&v)[8], uint8_t* dst, bool store) {
-  uint32_t a = 0;
+  float a = fabsf(v[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7fffffffu);
-  a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-  a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-  const float d = __fdiv_rn(__uint_as_float(a), 127.0f);
+  for (int i = 1; i < 8; ++i) a = max_nan(a, fabsf(v[i]));
+  a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, 2));
+  const float d = __fdiv_rn(a, 127.0f);
   const float di = q8_inv_scale(d);
   uint32_t q[2];
   int s = 0;
@@ -58,8 +63,78 @@ __device__ __forceinline__ void store_q8_block(const float (&v)[8], uint8_t* dst
   }
 }
 
-// One row per CTA; thread t takes the row's runs of eight values t, t + blockDim, ...
-// The row is read twice (the second time from L2): once for the sum of squares
+// Sum of v over the CTA, in a fixed order (part: one float per warp).
+__device__ __forceinline__ float block_sum(float v, float* part) {
+  v = warp_sum_f(v);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.f;
+  for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) v += part[i];
+  return v;
+}
+
+// One row per CTA, held in registers: thread t has the row's runs of eight values
+// t, t + blockDim, ... (CH of them). Read once, all loads of a row in flight
+// together; H may be X or R themselves (an element is read and written by the
+// same thread, the read first).
+template <typename T, bool VEC, int CH>
+__global__ void __launch_bounds__(CH == 1 ? 1024 : 512) add_rmsnorm_reg_kernel(const T* X, int64_t ldx, const T* R, int64_t ldr,
+                                                              const float* __restrict__ gamma, float eps, T* H,
+                                                              int64_t ldh, T* Y, int64_t ldy, uint8_t* __restrict__ Xq,
+                                                              int K) {
+  __shared__ float part[32];
+  pdl_enter();
+  const int64_t n = blockIdx.x;
+  const T* x = X + n * ldx;
+  const int runs = K >> 3;
+  float v[CH][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i = threadIdx.x + c * blockDim.x;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[c][k] = 0.f;
+    if (i < runs) load8<T, VEC>(x + 8 * i, v[c]);
+  }
+  if (R) {
+    const T* r = R + n * ldr;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = threadIdx.x + c * blockDim.x;
+      float w[8];
+      if (i < runs) {
+        load8<T, VEC>(r + 8 * i, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[c][k] += w[k];
+      }
+    }
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i = threadIdx.x + c * blockDim.x;
+    if (H && i < runs) store8<T, VEC>(H + n * ldh + 8 * i, v[c]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ss = fmaf(v[c][k], v[c][k], ss);
+  }
+  ss = block_sum(ss, part);
+  const float rr = __fdiv_rn(1.0f, sqrtf(__fdiv_rn(ss, static_cast<float>(K)) + eps));
+  uint8_t* xq = Xq + n * (K >> 5) * Q8_1_BYTES;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i = threadIdx.x + c * blockDim.x;
+    if (i - (threadIdx.x & 31) >= runs) break;   // warp-uniform
+    if (i < runs) {
+      float w[8];
+      load8<float, true>(gamma + 8 * i, w);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[c][k] = v[c][k] * rr * w[k];
+      if (Y) store8<T, VEC>(Y + n * ldy + 8 * i, v[c]);
+    }
+    store_q8_block(v[c], xq + (i >> 2) * Q8_1_BYTES, i < runs);
+  }
+}
+
+// The same for rows too long for registers. The row is read twice (the second time from L2): once for the sum of squares
 // and once for the outputs. H may be X or R themselves: an element is read and
 // written by the same thread, the read first.
 template <typename T, bool VEC>
@@ -84,11 +159,7 @@ __global__ void __launch_bounds__(512) add_rmsnorm_kernel(const T* X, int64_t ld
 #pragma unroll
     for (int k = 0; k < 8; ++k) ss = fmaf(v[k], v[k], ss);
   }
-  ss = warp_sum_f(ss);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
-  __syncthreads();
-  ss = 0.f;
-  for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) ss += part[i];
+  ss = block_sum(ss, part);
   const float rr = __fdiv_rn(1.0f, sqrtf(__fdiv_rn(ss, static_cast<float>(K)) + eps));
   uint8_t* xq = Xq + n * (K >> 5) * Q8_1_BYTES;
   for (int i0 = 0; i0 < runs; i0 += blockDim.x) {
@@ -112,26 +183,53 @@ __global__ void __launch_bounds__(512) add_rmsnorm_kernel(const T* X, int64_t ld
   }
 }
 
+// silu(g) * u. The division is a product with the reciprocal (rcp.approx, at most
+// 2^-23 off): with expf's 2 ulp, the sum and the two products at most 9 * 2^-24.
+__device__ __forceinline__ float swiglu(float g, float u) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + expf(-g)));
+  return g * r * u;
+}
+
+// A thread takes runs of eight values, a grid's threads apart; the next run's
+// loads are in flight while one is computed. Row and place in the row are
+// carried along (no division per run): a step is `rows` rows and `places` places.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) swiglu_kernel(const T* __restrict__ G, int64_t ldg, const T* __restrict__ U,
-                                                     int64_t ldu, uint8_t* __restrict__ Xq, int K, int64_t N) {
+                                                     int64_t ldu, uint8_t* __restrict__ Xq, int runs, int64_t total,
+                                                     int64_t rows, int places) {
   pdl_enter();
-  const int runs = K >> 3;
-  const int64_t total = N * runs;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  int64_t n = t / runs;
+  int i = static_cast<int>(t - n * runs);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * 256; t0 < total; t0 += stride) {
-    const int64_t t = t0 + threadIdx.x;
-    const bool in = t < total;
-    float g[8] = {}, u[8];
-    if (in) {
-      const int64_t n = t / runs;
-      const int64_t i = t - n * runs;
-      load8<T, VEC>(G + n * ldg + 8 * i, g);
-      load8<T, VEC>(U + n * ldu + 8 * i, u);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) g[k] = __fdiv_rn(g[k], 1.0f + expf(-g[k])) * u[k];
+  float g[8] = {}, u[8] = {};
+  if (t < total) {
+    load8<T, VEC>(G + n * ldg + 8 * i, g);
+    load8<T, VEC>(U + n * ldu + 8 * i, u);
+  }
+  while (t - static_cast<int>(threadIdx.x & 31) < total) {   // warp-uniform
+    float v[8];
+    float gn[8] = {}, un[8] = {};
+    n += rows;
+    i += places;
+    if (i >= runs) {
+      i -= runs;
+      ++n;
     }
-    store_q8_block(g, Xq + (t >> 2) * Q8_1_BYTES, in);
+    if (t + stride < total) {
+      load8<T, VEC>(G + n * ldg + 8 * i, gn);
+      load8<T, VEC>(U + n * ldu + 8 * i, un);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = swiglu(g[k], u[k]);
+    store_q8_block(v, Xq + (t >> 2) * Q8_1_BYTES, t < total);
+    t += stride;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      g[k] = gn[k];
+      u[k] = un[k];
+    }
   }
 }
 
@@ -140,34 +238,45 @@ bool rows16(int64_t ld, int size) { return (ld * size) % 16 == 0; }
 
 template <typename T>
 cudaError_t launch_norm_t(const void* X, int64_t ldx, const void* R, int64_t ldr, const float* gamma, float eps, void* H,
-                          int64_t ldh, void* Y, int64_t ldy, void* Xq, int64_t K, int64_t N, cudaStream_t s) {
+                          int64_t ldh, void* Y, int64_t ldy, void* Xq, int64_t K, int64_t N, int num_sms, cudaStream_t s) {
   const int sz = sizeof(T);
   const bool vec = rows16(ldx, sz) && (!R || rows16(ldr, sz)) && (!H || rows16(ldh, sz)) && (!Y || rows16(ldy, sz));
-  const int threads = static_cast<int>(std::min<int64_t>(512, ((K / 8) + 31) / 32 * 32));
-  auto k = vec ? add_rmsnorm_kernel<T, true> : add_rmsnorm_kernel<T, false>;
-  return launch_pdl(k, dim3(static_cast<unsigned>(N)), dim3(threads), 0, s, static_cast<const T*>(X), ldx,
-                    static_cast<const T*>(R), ldr, gamma, eps, static_cast<T*>(H), ldh, static_cast<T*>(Y), ldy,
-                    static_cast<uint8_t*>(Xq), static_cast<int>(K));
+  auto go = [&](auto k, int64_t threads) {
+    return launch_pdl(k, dim3(static_cast<unsigned>(N)), dim3(static_cast<unsigned>((threads + 31) / 32 * 32)), 0, s,
+                      static_cast<const T*>(X), ldx, static_cast<const T*>(R), ldr, gamma, eps, static_cast<T*>(H), ldh,
+                      static_cast<T*>(Y), ldy, static_cast<uint8_t*>(Xq), static_cast<int>(K));
+  };
+  // Few rows: as many threads as a row has runs, for the latency. Many: four runs a
+  // thread, so that more of a row is in flight per thread and more rows share an SM.
+  const int64_t runs = K / 8;
+  if (N <= 2 * num_sms && runs <= 1024)
+    return go(vec ? add_rmsnorm_reg_kernel<T, true, 1> : add_rmsnorm_reg_kernel<T, false, 1>, runs);
+  if (runs <= 4 * 512)
+    return go(vec ? add_rmsnorm_reg_kernel<T, true, 4> : add_rmsnorm_reg_kernel<T, false, 4>, (runs + 3) / 4);
+  return go(vec ? add_rmsnorm_kernel<T, true> : add_rmsnorm_kernel<T, false>, 512);
 }
 
 template <typename T>
 cudaError_t launch_swiglu_t(const void* G, int64_t ldg, const void* U, int64_t ldu, void* Xq, int64_t K, int64_t N,
                             int num_sms, cudaStream_t s) {
   const bool vec = rows16(ldg, sizeof(T)) && rows16(ldu, sizeof(T));
-  const int64_t blocks = std::min<int64_t>((N * (K / 8) + 255) / 256, static_cast<int64_t>(num_sms) * 8);
+  const int64_t runs = K / 8, total = N * runs;
+  const int64_t blocks = std::min<int64_t>((total + 255) / 256, static_cast<int64_t>(num_sms) * 6);
+  const int64_t stride = blocks * 256;
   auto k = vec ? swiglu_kernel<T, true> : swiglu_kernel<T, false>;
   return launch_pdl(k, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, static_cast<const T*>(G), ldg,
-                    static_cast<const T*>(U), ldu, static_cast<uint8_t*>(Xq), static_cast<int>(K), N);
+                    static_cast<const T*>(U), ldu, static_cast<uint8_t*>(Xq), static_cast<int>(runs), total, stride / runs,
+                    static_cast<int>(stride % runs));
 }
 
 }  // namespace
 
 cudaError_t launch_add_rmsnorm_q8_1(int dtype, const void* X, int64_t ldx, const void* R, int64_t ldr,
                                     const float* gamma, float eps, void* H, int64_t ldh, void* Y, int64_t ldy,
-                                    void* Xq, int64_t K, int64_t N, cudaStream_t s) {
-  if (dtype == KQ_F32) return launch_norm_t<float>(X, ldx, R, ldr, gamma, eps, H, ldh, Y, ldy, Xq, K, N, s);
-  if (dtype == KQ_F16) return launch_norm_t<__half>(X, ldx, R, ldr, gamma, eps, H, ldh, Y, ldy, Xq, K, N, s);
-  return launch_norm_t<__nv_bfloat16>(X, ldx, R, ldr, gamma, eps, H, ldh, Y, ldy, Xq, K, N, s);
+                                    void* Xq, int64_t K, int64_t N, int num_sms, cudaStream_t s) {
+  if (dtype == KQ_F32) return launch_norm_t<float>(X, ldx, R, ldr, gamma, eps, H, ldh, Y, ldy, Xq, K, N, num_sms, s);
+  if (dtype == KQ_F16) return launch_norm_t<__half>(X, ldx, R, ldr, gamma, eps, H, ldh, Y, ldy, Xq, K, N, num_sms, s);
+  return launch_norm_t<__nv_bfloat16>(X, ldx, R, ldr, gamma, eps, H, ldh, Y, ldy, Xq, K, N, num_sms, s);
 }
 
 cudaError_t launch_swiglu_q8_1(int dtype, const void* G, int64_t ldg, const void* U, int64_t ldu, void* Xq, int64_t K,
