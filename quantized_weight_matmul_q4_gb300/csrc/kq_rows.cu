@@ -63,6 +63,57 @@ __device__ __forceinline__ void store_q8_block(const float (&v)[8], uint8_t* dst
   }
 }
 
+// Four blocks of a lane quad at once (v[c]: this lane's eight values of block c). The
+// maxima and sums are reduced so that lane j of the quad ends up with block j's: it
+// alone makes that block's scale, its reciprocal and its header. Bit for bit what
+// store_q8_block does, with a quarter of the divisions.
+__device__ __forceinline__ void store_q8_blocks4(const float (&v)[4][8], uint8_t* const (&dst)[4], const bool (&store)[4]) {
+  const int j = threadIdx.x & 3, quad = threadIdx.x & 28;
+  const bool hi = j & 2, lo = j & 1;
+  float m[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    m[c] = fabsf(v[c][0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m[c] = max_nan(m[c], fabsf(v[c][i]));
+  }
+  const float a0 = max_nan(hi ? m[2] : m[0], __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[2], 2));
+  const float a1 = max_nan(hi ? m[3] : m[1], __shfl_xor_sync(0xffffffffu, hi ? m[1] : m[3], 2));
+  const float a = max_nan(lo ? a1 : a0, __shfl_xor_sync(0xffffffffu, lo ? a0 : a1, 1));   // of block j
+  const float d = __fdiv_rn(a, 127.0f);
+  const float di = q8_inv_scale(d);
+  int s[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const float f = __shfl_sync(0xffffffffu, di, quad + c);
+    uint32_t q[2];
+    s[c] = 0;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      uint32_t u[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) u[k] = __float_as_uint(__fadd_rn(__fmul_rn(v[c][4 * w + k], f), 12582912.0f));
+      q[w] = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+      s[c] = __dp4a(static_cast<int>(q[w]), 0x01010101, s[c]);
+    }
+    if (store[c]) {   // blocks are 36 bytes apart: 4-byte stores
+      uint32_t* p = reinterpret_cast<uint32_t*>(dst[c] + 4 + 8 * j);
+      p[0] = q[0];
+      p[1] = q[1];
+    }
+  }
+  const int s0 = (hi ? s[2] : s[0]) + __shfl_xor_sync(0xffffffffu, hi ? s[0] : s[2], 2);
+  const int s1 = (hi ? s[3] : s[1]) + __shfl_xor_sync(0xffffffffu, hi ? s[1] : s[3], 2);
+  const int sum = (lo ? s1 : s0) + __shfl_xor_sync(0xffffffffu, lo ? s0 : s1, 1);
+  uint8_t* mine = hi ? (lo ? dst[3] : dst[2]) : (lo ? dst[1] : dst[0]);
+  if (hi ? (lo ? store[3] : store[2]) : (lo ? store[1] : store[0])) {
+    const __half dh = __float2half_rn(d);
+    const __half sh = __float2half_rn(__fmul_rn(__half2float(dh), static_cast<float>(sum)));
+    *reinterpret_cast<uint32_t*>(mine) =
+        static_cast<uint32_t>(__half_as_ushort(dh)) | (static_cast<uint32_t>(__half_as_ushort(sh)) << 16);
+  }
+}
+
 // Sum of v over the CTA, in a fixed order (part: one float per warp).
 __device__ __forceinline__ float block_sum(float v, float* part) {
   v = warp_sum_f(v);
@@ -119,19 +170,23 @@ __global__ void __launch_bounds__(CH == 1 ? 1024 : 512) add_rmsnorm_reg_kernel(c
   ss = block_sum(ss, part);
   const float rr = __fdiv_rn(1.0f, sqrtf(__fdiv_rn(ss, static_cast<float>(K)) + eps));
   uint8_t* xq = Xq + n * (K >> 5) * Q8_1_BYTES;
+  uint8_t* dst[CH];
+  bool in[CH];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int i = threadIdx.x + c * blockDim.x;
-    if (i - (threadIdx.x & 31) >= runs) break;   // warp-uniform
-    if (i < runs) {
+    in[c] = i < runs;
+    dst[c] = xq + (i >> 2) * Q8_1_BYTES;
+    if (in[c]) {
       float w[8];
       load8<float, true>(gamma + 8 * i, w);
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[c][k] = v[c][k] * rr * w[k];
       if (Y) store8<T, VEC>(Y + n * ldy + 8 * i, v[c]);
     }
-    store_q8_block(v[c], xq + (i >> 2) * Q8_1_BYTES, i < runs);
   }
+  if constexpr (CH == 4) store_q8_blocks4(v, dst, in);
+  else store_q8_block(v[0], dst[0], in[0]);
 }
 
 // The same for rows too long for registers. The row is read twice (the second time from L2): once for the sum of squares
@@ -193,9 +248,13 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 
 // A thread takes runs of eight values, a grid's threads apart; the next run's
 // loads are in flight while one is computed. Row and place in the row are
-// carried along (no division per run): a step is `rows` rows and `places` places.
+// carried along (no division per run): a step is `rows` rows and `places` places. (Four
+// runs a thread with the divisions shared as above: 35.6 us instead of 32.5 for
+// 2048 x 14336 in bf16, and 2.4 instead of 1.5 for eight rows of 768.)
+template <typename T>
+constexpr int swiglu_ctas() { return sizeof(T) == 4 ? 5 : 6; }   // per SM: what the registers allow
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) swiglu_kernel(const T* __restrict__ G, int64_t ldg, const T* __restrict__ U,
+__global__ void __launch_bounds__(256, swiglu_ctas<T>()) swiglu_kernel(const T* __restrict__ G, int64_t ldg, const T* __restrict__ U,
                                                      int64_t ldu, uint8_t* __restrict__ Xq, int runs, int64_t total,
                                                      int64_t rows, int places) {
   pdl_enter();
@@ -203,14 +262,13 @@ __global__ void __launch_bounds__(256) swiglu_kernel(const T* __restrict__ G, in
   int64_t n = t / runs;
   int i = static_cast<int>(t - n * runs);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
-  float g[8] = {}, u[8] = {};
+  Raw8<T> g = {}, u = {};
   if (t < total) {
-    load8<T, VEC>(G + n * ldg + 8 * i, g);
-    load8<T, VEC>(U + n * ldu + 8 * i, u);
+    g.template load<VEC>(G + n * ldg + 8 * i);
+    u.template load<VEC>(U + n * ldu + 8 * i);
   }
   while (t - static_cast<int>(threadIdx.x & 31) < total) {   // warp-uniform
-    float v[8];
-    float gn[8] = {}, un[8] = {};
+    Raw8<T> gn = {}, un = {};
     n += rows;
     i += places;
     if (i >= runs) {
@@ -218,18 +276,16 @@ __global__ void __launch_bounds__(256) swiglu_kernel(const T* __restrict__ G, in
       ++n;
     }
     if (t + stride < total) {
-      load8<T, VEC>(G + n * ldg + 8 * i, gn);
-      load8<T, VEC>(U + n * ldu + 8 * i, un);
+      gn.template load<VEC>(G + n * ldg + 8 * i);
+      un.template load<VEC>(U + n * ldu + 8 * i);
     }
+    float v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = swiglu(g[k], u[k]);
     store_q8_block(v, Xq + (t >> 2) * Q8_1_BYTES, t < total);
     t += stride;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      g[k] = gn[k];
-      u[k] = un[k];
-    }
+    g = gn;
+    u = un;
   }
 }
 
@@ -261,7 +317,7 @@ cudaError_t launch_swiglu_t(const void* G, int64_t ldg, const void* U, int64_t l
                             int num_sms, cudaStream_t s) {
   const bool vec = rows16(ldg, sizeof(T)) && rows16(ldu, sizeof(T));
   const int64_t runs = K / 8, total = N * runs;
-  const int64_t blocks = std::min<int64_t>((total + 255) / 256, static_cast<int64_t>(num_sms) * 6);
+  const int64_t blocks = std::min<int64_t>((total + 255) / 256, static_cast<int64_t>(num_sms) * swiglu_ctas<T>());
   const int64_t stride = blocks * 256;
   auto k = vec ? swiglu_kernel<T, true> : swiglu_kernel<T, false>;
   return launch_pdl(k, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, static_cast<const T*>(G), ldg,

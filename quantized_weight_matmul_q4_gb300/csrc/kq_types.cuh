@@ -37,6 +37,24 @@ __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
   }
 }
 
+// Eight elements as loaded, to be converted where they are used.
+template <typename T>
+struct Raw8 {
+  alignas(16) T e[8];
+  template <bool VEC>
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+        reinterpret_cast<uint4*>(e)[i] = reinterpret_cast<const uint4*>(p)[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = p[i];
+    }
+  }
+  __device__ __forceinline__ float operator[](int i) const { return to_f32(e[i]); }
+};
+
 template <typename T, bool VEC>
 __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
   if constexpr (VEC) {
