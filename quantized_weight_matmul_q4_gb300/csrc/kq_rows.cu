@@ -63,57 +63,6 @@ __device__ __forceinline__ void store_q8_block(const float (&v)[8], uint8_t* dst
   }
 }
 
-// Four blocks of a lane quad at once (v[c]: this lane's eight values of block c). The
-// maxima and sums are reduced so that lane j of the quad ends up with block j's: it
-// alone makes that block's scale, its reciprocal and its header. Bit for bit what
-// store_q8_block does, with a quarter of the divisions.
-__device__ __forceinline__ void store_q8_blocks4(const float (&v)[4][8], uint8_t* const (&dst)[4], const bool (&store)[4]) {
-  const int j = threadIdx.x & 3, quad = threadIdx.x & 28;
-  const bool hi = j & 2, lo = j & 1;
-  float m[4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    m[c] = fabsf(v[c][0]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) m[c] = max_nan(m[c], fabsf(v[c][i]));
-  }
-  const float a0 = max_nan(hi ? m[2] : m[0], __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[2], 2));
-  const float a1 = max_nan(hi ? m[3] : m[1], __shfl_xor_sync(0xffffffffu, hi ? m[1] : m[3], 2));
-  const float a = max_nan(lo ? a1 : a0, __shfl_xor_sync(0xffffffffu, lo ? a0 : a1, 1));   // of block j
-  const float d = __fdiv_rn(a, 127.0f);
-  const float di = q8_inv_scale(d);
-  int s[4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const float f = __shfl_sync(0xffffffffu, di, quad + c);
-    uint32_t q[2];
-    s[c] = 0;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      uint32_t u[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) u[k] = __float_as_uint(__fadd_rn(__fmul_rn(v[c][4 * w + k], f), 12582912.0f));
-      q[w] = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
-      s[c] = __dp4a(static_cast<int>(q[w]), 0x01010101, s[c]);
-    }
-    if (store[c]) {   // blocks are 36 bytes apart: 4-byte stores
-      uint32_t* p = reinterpret_cast<uint32_t*>(dst[c] + 4 + 8 * j);
-      p[0] = q[0];
-      p[1] = q[1];
-    }
-  }
-  const int s0 = (hi ? s[2] : s[0]) + __shfl_xor_sync(0xffffffffu, hi ? s[0] : s[2], 2);
-  const int s1 = (hi ? s[3] : s[1]) + __shfl_xor_sync(0xffffffffu, hi ? s[1] : s[3], 2);
-  const int sum = (lo ? s1 : s0) + __shfl_xor_sync(0xffffffffu, lo ? s0 : s1, 1);
-  uint8_t* mine = hi ? (lo ? dst[3] : dst[2]) : (lo ? dst[1] : dst[0]);
-  if (hi ? (lo ? store[3] : store[2]) : (lo ? store[1] : store[0])) {
-    const __half dh = __float2half_rn(d);
-    const __half sh = __float2half_rn(__fmul_rn(__half2float(dh), static_cast<float>(sum)));
-    *reinterpret_cast<uint32_t*>(mine) =
-        static_cast<uint32_t>(__half_as_ushort(dh)) | (static_cast<uint32_t>(__half_as_ushort(sh)) << 16);
-  }
-}
-
 // Sum of v over the CTA, in a fixed order (part: one float per warp).
 __device__ __forceinline__ float block_sum(float v, float* part) {
   v = warp_sum_f(v);
@@ -129,7 +78,7 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
 // together; H may be X or R themselves (an element is read and written by the
 // same thread, the read first).
 template <typename T, bool VEC, int CH>
-__global__ void __launch_bounds__(CH == 1 ? 1024 : 512) add_rmsnorm_reg_kernel(const T* X, int64_t ldx, const T* R, int64_t ldr,
+__global__ void __launch_bounds__(CH == 2 ? 512 : 1024) add_rmsnorm_reg_kernel(const T* X, int64_t ldx, const T* R, int64_t ldr,
                                                               const float* __restrict__ gamma, float eps, T* H,
                                                               int64_t ldh, T* Y, int64_t ldy, uint8_t* __restrict__ Xq,
                                                               int K) {
@@ -170,14 +119,10 @@ __global__ void __launch_bounds__(CH == 1 ? 1024 : 512) add_rmsnorm_reg_kernel(c
   ss = block_sum(ss, part);
   const float rr = __fdiv_rn(1.0f, sqrtf(__fdiv_rn(ss, static_cast<float>(K)) + eps));
   uint8_t* xq = Xq + n * (K >> 5) * Q8_1_BYTES;
-  uint8_t* dst[CH];
-  bool in[CH];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int i = threadIdx.x + c * blockDim.x;
-    in[c] = i < runs;
-    dst[c] = xq + (i >> 2) * Q8_1_BYTES;
-    if (in[c]) {
+    if (i < runs) {
       float w[8];
       load8<float, true>(gamma + 8 * i, w);
 #pragma unroll
@@ -185,8 +130,11 @@ __global__ void __launch_bounds__(CH == 1 ? 1024 : 512) add_rmsnorm_reg_kernel(c
       if (Y) store8<T, VEC>(Y + n * ldy + 8 * i, v[c]);
     }
   }
-  if constexpr (CH == 4) store_q8_blocks4(v, dst, in);
-  else store_q8_block(v[0], dst[0], in[0]);
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i = threadIdx.x + c * blockDim.x;
+    store_q8_block(v[c], xq + (i >> 2) * Q8_1_BYTES, i < runs);
+  }
 }
 
 // The same for rows too long for registers. The row is read twice (the second time from L2): once for the sum of squares
@@ -249,8 +197,8 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 // A thread takes runs of eight values, a grid's threads apart; the next run's
 // loads are in flight while one is computed. Row and place in the row are
 // carried along (no division per run): a step is `rows` rows and `places` places. (Four
-// runs a thread with the divisions shared as above: 35.6 us instead of 32.5 for
-// 2048 x 14336 in bf16, and 2.4 instead of 1.5 for eight rows of 768.)
+// runs a thread, a lane of each quad making one block's scale for all: 35.6 us instead
+// of 32.5 for 2048 x 14336 in bf16, and 2.4 instead of 1.5 for eight rows of 768.)
 template <typename T>
 constexpr int swiglu_ctas() { return sizeof(T) == 4 ? 5 : 6; }   // per SM: what the registers allow
 template <typename T, bool VEC>
@@ -302,12 +250,15 @@ cudaError_t launch_norm_t(const void* X, int64_t ldx, const void* R, int64_t ldr
                       static_cast<const T*>(X), ldx, static_cast<const T*>(R), ldr, gamma, eps, static_cast<T*>(H), ldh,
                       static_cast<T*>(Y), ldy, static_cast<uint8_t*>(Xq), static_cast<int>(K));
   };
-  // Few rows: as many threads as a row has runs, for the latency. Many: four runs a
-  // thread, so that more of a row is in flight per thread and more rows share an SM.
+  // As many threads as a row has runs, for the latency of a row; two runs a thread where
+  // there are many rows, so that more rows share an SM (bf16, K = 4096: 1024 rows 9.7 us
+  // against 10.9, 2048 rows 17.2 against 16.9, 4099 rows 30.5 against 28.9); four where the row is long.
   const int64_t runs = K / 8;
-  if (N <= 2 * num_sms && runs <= 1024)
+  if (N <= 10 * num_sms && runs <= 1024)
     return go(vec ? add_rmsnorm_reg_kernel<T, true, 1> : add_rmsnorm_reg_kernel<T, false, 1>, runs);
-  if (runs <= 4 * 512)
+  if (runs <= 1024)
+    return go(vec ? add_rmsnorm_reg_kernel<T, true, 2> : add_rmsnorm_reg_kernel<T, false, 2>, (runs + 1) / 2);
+  if (runs <= 4096)
     return go(vec ? add_rmsnorm_reg_kernel<T, true, 4> : add_rmsnorm_reg_kernel<T, false, 4>, (runs + 3) / 4);
   return go(vec ? add_rmsnorm_kernel<T, true> : add_rmsnorm_kernel<T, false>, 512);
 }
