@@ -224,19 +224,27 @@ def kq_add_rmsnorm_q8_1(X, R, gamma, eps: float, H=None, Y=False, Xq=None, strea
     N, K = shape
     x, ldx = _rows(X, "X", shape, X.dtype)
     r, ldr = _rows(R, "R", shape, X.dtype) if R is not None else (None, 0)
-    if H is None and R is not None:
-        H = _out((N, K), X.dtype, X.device, stream)
-    h, ldh = _rows(H, "H", shape, X.dtype) if H is not None else (None, 0)
+    h, ldh = None, K
+    if H is not None:
+        h, ldh = _rows(H, "H", shape, X.dtype)
+    elif R is not None:
+        H = _out(shape, X.dtype, X.device, stream)
+        h = H.data_ptr()
+    y, ldy = None, K
     if Y is True:
-        Y = _out((N, K), X.dtype, X.device, stream)
+        Y = _out(shape, X.dtype, X.device, stream)
+        y = Y.data_ptr()
     elif Y is False:
         Y = None
-    y, ldy = _rows(Y, "Y", shape, X.dtype) if Y is not None else (None, 0)
+    elif Y is not None:
+        y, ldy = _rows(Y, "Y", shape, X.dtype)
     if Xq is None:
         Xq = _out((N, K // 32, 36), torch.uint8, X.device, stream)
-    check(lib().kq_add_rmsnorm_q8_1(dt, x, ldx, r, ldr, _sized(gamma, "gamma", K, torch.float32), float(eps), h, ldh,
-                                    y, ldy, _sized(Xq, "Xq", N * (K // 32) * 36, torch.uint8), K, N, _stream(stream)),
-          "kq_add_rmsnorm_q8_1")
+        xq = Xq.data_ptr()
+    else:
+        xq = _sized(Xq, "Xq", N * (K // 32) * 36, torch.uint8)
+    check(lib().kq_add_rmsnorm_q8_1(dt, x, ldx, r, ldr, _sized(gamma, "gamma", K, torch.float32), eps, h, ldh,
+                                    y, ldy, xq, K, N, _stream(stream)), "kq_add_rmsnorm_q8_1")
     return H, Y, Xq
 
 
@@ -252,8 +260,10 @@ def kq_swiglu_q8_1(gate, up, Xq=None, stream=None):
     u, ldu = _rows(up, "up", shape, gate.dtype)
     if Xq is None:
         Xq = _out((N, K // 32, 36), torch.uint8, gate.device, stream)
-    check(lib().kq_swiglu_q8_1(dt, g, ldg, u, ldu, _sized(Xq, "Xq", N * (K // 32) * 36, torch.uint8), K, N,
-                               _stream(stream)), "kq_swiglu_q8_1")
+        xq = Xq.data_ptr()
+    else:
+        xq = _sized(Xq, "Xq", N * (K // 32) * 36, torch.uint8)
+    check(lib().kq_swiglu_q8_1(dt, g, ldg, u, ldu, xq, K, N, _stream(stream)), "kq_swiglu_q8_1")
     return Xq
 
 
@@ -278,11 +288,16 @@ def kq_moe_route(logits, top_k: int, score="softmax", bias=None, n_groups: int =
     top_k = int(top_k)
     if ids is None:
         ids = _out((T, top_k), torch.int32, logits.device, stream)
+        pi = ids.data_ptr()
+    else:
+        pi = _sized(ids, "ids", T * top_k, torch.int32)
     if probs is None:
         probs = _out((T, top_k), torch.float32, logits.device, stream)
+        pp = probs.data_ptr()
+    else:
+        pp = _sized(probs, "probs", T * top_k, torch.float32)
     check(lib().kq_moe_route(dt, x, ld, _sized(bias, "bias", E, torch.float32), sc, n_groups, topk_groups, group_top,
-                             top_k, bool(renormalise), float(scale), _sized(ids, "ids", T * top_k, torch.int32),
-                             _sized(probs, "probs", T * top_k, torch.float32), E, T, _stream(stream)), "kq_moe_route")
+                             top_k, 1 if renormalise else 0, scale, pi, pp, E, T, _stream(stream)), "kq_moe_route")
     return ids, probs
 
 
@@ -314,7 +329,10 @@ def kq_matvec_g4(W, scales, Xq, M: int, K: int, group: int, zeros=None, Y=None, 
     N = _q8_rows(Xq, K)
     if Y is None:
         Y = _out((N, M), torch.float32, Xq.device, stream)
-    check(lib().kq_matvec_g4(*w, xq, _sized(Y, "Y", N * M, torch.float32), M, K, N, _stream(stream)), "kq_matvec_g4")
+        y = Y.data_ptr()
+    else:
+        y = _sized(Y, "Y", N * M, torch.float32)
+    check(lib().kq_matvec_g4(*w, xq, y, M, K, N, _stream(stream)), "kq_matvec_g4")
     return Y
 
 
@@ -333,9 +351,11 @@ def kq_moe_matvec_g4(W, scales, n_experts: int, expert_ids, Xq, M: int, K: int, 
         raise ValueError(f"Xq must hold {T} or {T * top_k} rows, got {n}")
     if Y is None:
         Y = _out((T, top_k, M), torch.float32, Xq.device, stream)
-    check(lib().kq_moe_matvec_g4(*w, n_experts, _dev(expert_ids, "expert_ids", torch.int32), top_k, n != T, xq,
-                                 _sized(Y, "Y", T * top_k * M, torch.float32), M, K, T, _stream(stream)),
-          "kq_moe_matvec_g4")
+        y = Y.data_ptr()
+    else:
+        y = _sized(Y, "Y", T * top_k * M, torch.float32)
+    check(lib().kq_moe_matvec_g4(*w, n_experts, _dev(expert_ids, "expert_ids", torch.int32), top_k, n != T, xq, y, M, K,
+                                 T, _stream(stream)), "kq_moe_matvec_g4")
     return Y
 
 
