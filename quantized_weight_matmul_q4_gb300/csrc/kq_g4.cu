@@ -25,6 +25,7 @@ struct G4Args {
   const int32_t* ids;   // null: one matrix, rows 0..rows-1 of Xq
   int n_experts, top_k;
   bool x_per_slot, by_pair;
+  bool eager;           // nearly every expert has pairs: its weights are asked for before they are known
   int64_t M;
   int64_t rows;         // activation rows, or (token, slot) pairs
   int blocks;           // 32-element blocks per row
@@ -321,36 +322,21 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
   const int rows = static_cast<int>(min(a.M - m0, static_cast<int64_t>(G4_ROWS)));   // of this tile
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // One matrix: its weights are on their way before the previous kernel's end.
-  if (a.ids) asm volatile("griddepcontrol.wait;" ::: "memory");
-  int expert = 0;
+  if (!a.eager) asm volatile("griddepcontrol.wait;" ::: "memory");
+  int expert = a.ids && !a.by_pair ? static_cast<int>(blockIdx.y) : 0;
   int64_t scan = 0;     // next pair to look at
-  if (a.ids) {
-    if (a.by_pair) {
-      // One cluster per pair; the first pair of an expert takes all of its pairs.
-      expert = a.ids[blockIdx.y];
-      if (expert < 0 || expert >= a.n_experts) {
-        if (tid == 0 && blockIdx.x == 0) report_error(a.err, ERR_EXPERT_ID);
-        if (rank == 0 && tid < rows) a.Y[blockIdx.y * a.M + m0 + tid] = 0.f;
-        return;
-      }
-      int earlier = 0;
-      for (int p = tid; p < static_cast<int>(blockIdx.y); p += 128) earlier |= a.ids[p] == expert;
-      if (__syncthreads_or(earlier)) return;
-      scan = blockIdx.y;
-    } else {
-      expert = blockIdx.y;
-      // Invalid ids belong to no expert: expert 0's CTAs write their zeros.
-      if (expert == 0 && rank == 0) {
-        for (int64_t p = tid; p < a.rows; p += 128) {
-          const int e = a.ids[p];
-          if (e < 0 || e >= a.n_experts) {
-            if (blockIdx.x == 0) report_error(a.err, ERR_EXPERT_ID);
-            for (int m = 0; m < rows; ++m) a.Y[p * a.M + m0 + m] = 0.f;
-          }
-        }
-      }
+  if (a.by_pair) {
+    // One cluster per pair; the first pair of an expert takes all of its pairs.
+    expert = a.ids[blockIdx.y];
+    if (expert < 0 || expert >= a.n_experts) {
+      if (tid == 0 && blockIdx.x == 0) report_error(a.err, ERR_EXPERT_ID);
+      if (rank == 0 && tid < rows) a.Y[blockIdx.y * a.M + m0 + tid] = 0.f;
+      return;
     }
+    int earlier = 0;
+    for (int p = tid; p < static_cast<int>(blockIdx.y); p += 128) earlier |= a.ids[p] == expert;
+    if (__syncthreads_or(earlier)) return;
+    scan = blockIdx.y;
   }
   const int64_t row0 = static_cast<int64_t>(expert) * a.M + m0;
   const int64_t row_bytes = static_cast<int64_t>(a.blocks) * 16;
@@ -377,6 +363,77 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
     return a.w.scale_dtype == KQ_F16 ? __half2float(__ushort_as_half(bits)) : __uint_as_float(static_cast<uint32_t>(bits) << 16);
   };
 
+  const uint8_t* wsrc[4];
+  int span_chunk;      // the next chunk whose scales are in a new span
+  // The copies of chunk c (called for c_begin, c_begin + 1, ...) into a slot.
+  auto fill = [&](int c, int slot) {
+    const uint32_t wd = wdst + slot * (32 * 64);
+    if (even || c + 1 < chunks) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) cp_async16(wd + i * 512, wsrc[i], 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {   // blocks past K: zero
+        const bool in = c * G4_CHUNK + t < a.blocks;
+        cp_async16(wd + i * 512, in ? wsrc[i] : a.w.codes, in ? 16 : 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wsrc[i] += 64;
+    // The scales of the next G4_SPAN groups with the first chunk that needs them; the
+    // span before the last is out of use by then.
+    if (c == span_chunk) {
+      const int span = (c * G4_CHUNK >> a.w.group_shift) / G4_SPAN;
+      span_chunk = static_cast<int>(min((static_cast<int64_t>(span + 1) * G4_SPAN << a.w.group_shift) / G4_CHUNK, static_cast<int64_t>(chunks)));
+      const int n = static_cast<int>(min(a.w.groups - span * G4_SPAN, static_cast<int64_t>(G4_SPAN)));
+      const int64_t at = srow + span * G4_SPAN;
+      uint8_t* raw = my.raw[span & 1][lane];
+      const uint16_t* ss = static_cast<const uint16_t*>(a.w.scales) + at;
+      for (int i = n; i < G4_SPAN; ++i) {   // blocks past K get scale 0
+        reinterpret_cast<uint16_t*>(raw)[i] = 0;
+        if (ZEROS) raw[2 * G4_SPAN + i] = 0;
+      }
+      if (a.w.groups % 2 == 0) {
+        cp_async_row(smem_u32(raw), reinterpret_cast<const uint8_t*>(ss), 2 * n, static_cast<int>(2 * a.w.groups & 31));
+      } else {
+        for (int i = 0; i < n; ++i) reinterpret_cast<uint16_t*>(raw)[i] = __ldg(ss + i);
+      }
+      if (ZEROS) {
+        if (a.w.groups % 4 == 0) {
+          cp_async_row(smem_u32(raw) + 2 * G4_SPAN, a.w.zeros + at, n, static_cast<int>(a.w.groups & 31));
+        } else {
+          for (int i = 0; i < n; ++i) raw[2 * G4_SPAN + i] = __ldg(a.w.zeros + at + i);
+        }
+      }
+    }
+  };
+  auto begin = [&] {   // of a pass over K: the first copies
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wsrc[i] = wsrc0[i];
+    span_chunk = c_begin;
+    for (int i = 0; i < G4_STAGES - 1; ++i) {
+      if (c_begin + i < c_end) fill(c_begin + i, i);
+      cp_async_commit();
+    }
+  };
+  // Weights that are surely needed, or nearly so, are on their way before the previous
+  // kernel's end.
+  bool begun = a.eager;
+  if (a.eager) {
+    begin();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
+  // Invalid ids belong to no expert: expert 0's CTAs write their zeros.
+  if (a.ids && !a.by_pair && expert == 0 && rank == 0) {
+    for (int64_t p = tid; p < a.rows; p += 128) {
+      const int e = a.ids[p];
+      if (e < 0 || e >= a.n_experts) {
+        if (blockIdx.x == 0) report_error(a.err, ERR_EXPERT_ID);
+        for (int m = 0; m < rows; ++m) a.Y[p * a.M + m0 + m] = 0.f;
+      }
+    }
+  }
+
   for (;;) {
     int have;
     if (a.ids) {
@@ -384,17 +441,41 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
       __syncthreads();
       if (tid == 0) sm.count = 0;
       __syncthreads();
+      // 512 pairs at a time; where so many are this expert's that the list would overflow,
+      // 128 at a time.
       bool more = scan < a.rows;
+      have = 0;
       while (more) {
+        unsigned mine = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int64_t p = scan + tid + 128 * k;
+          if (p < a.rows && a.ids[p] == expert) mine |= 1u << k;
+        }
+        int at = mine ? atomicAdd(&sm.count, __popc(mine)) : 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if ((mine >> k & 1) && at < G4_LIST) sm.list[at++] = static_cast<int>(scan + tid + 128 * k);
+        __syncthreads();
+        const int now = *reinterpret_cast<volatile int*>(&sm.count);
+        __syncthreads();
+        if (now <= G4_LIST) {
+          have = now;
+          scan += 512;
+          more = scan < a.rows;
+          continue;
+        }
+        if (have > 0) break;   // those are enough for now: these again next time
+        if (tid == 0) sm.count = 0;
+        __syncthreads();
         const int64_t p = scan + tid;
         if (p < a.rows && a.ids[p] == expert) sm.list[atomicAdd(&sm.count, 1)] = static_cast<int>(p);
-        scan += 128;
         __syncthreads();
         have = *reinterpret_cast<volatile int*>(&sm.count);
-        more = scan < a.rows && have + 128 <= G4_LIST;
+        scan += 128;
+        more = scan < a.rows && have == 0;
         __syncthreads();
       }
-      have = *reinterpret_cast<volatile int*>(&sm.count);
       if (a.splits > 1) {
         // The clusters' CTAs use the list of rank 0: theirs may be in another order.
         cluster_sync();
@@ -406,7 +487,10 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
           }
         cluster_sync();
       }
-      if (have == 0) return;
+      if (have == 0) {
+        cp_async_wait<0>();
+        return;
+      }
     } else {
       have = static_cast<int>(min(a.rows - static_cast<int64_t>(blockIdx.y) * TOK, static_cast<int64_t>(TOK)));
     }
@@ -424,52 +508,6 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
         }
         sm.xrow[tid] = p;
       }
-      const uint8_t* wsrc[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) wsrc[i] = wsrc0[i];
-      int span_chunk = c_begin;      // the next chunk whose scales are in a new span
-      // The copies of chunk c (called for c_begin, c_begin + 1, ...) into a slot.
-      auto fill = [&](int c, int slot) {
-        const uint32_t wd = wdst + slot * (32 * 64);
-        if (even || c + 1 < chunks) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) cp_async16(wd + i * 512, wsrc[i], 16);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {   // blocks past K: zero
-            const bool in = c * G4_CHUNK + t < a.blocks;
-            cp_async16(wd + i * 512, in ? wsrc[i] : a.w.codes, in ? 16 : 0);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) wsrc[i] += 64;
-        // The scales of the next G4_SPAN groups with the first chunk that needs them; the
-        // span before the last is out of use by then.
-        if (c == span_chunk) {
-          const int span = (c * G4_CHUNK >> a.w.group_shift) / G4_SPAN;
-          span_chunk = static_cast<int>(min((static_cast<int64_t>(span + 1) * G4_SPAN << a.w.group_shift) / G4_CHUNK, static_cast<int64_t>(chunks)));
-          const int n = static_cast<int>(min(a.w.groups - span * G4_SPAN, static_cast<int64_t>(G4_SPAN)));
-          const int64_t at = srow + span * G4_SPAN;
-          uint8_t* raw = my.raw[span & 1][lane];
-          const uint16_t* ss = static_cast<const uint16_t*>(a.w.scales) + at;
-          for (int i = n; i < G4_SPAN; ++i) {   // blocks past K get scale 0
-            reinterpret_cast<uint16_t*>(raw)[i] = 0;
-            if (ZEROS) raw[2 * G4_SPAN + i] = 0;
-          }
-          if (a.w.groups % 2 == 0) {
-            cp_async_row(smem_u32(raw), reinterpret_cast<const uint8_t*>(ss), 2 * n, static_cast<int>(2 * a.w.groups & 31));
-          } else {
-            for (int i = 0; i < n; ++i) reinterpret_cast<uint16_t*>(raw)[i] = __ldg(ss + i);
-          }
-          if (ZEROS) {
-            if (a.w.groups % 4 == 0) {
-              cp_async_row(smem_u32(raw) + 2 * G4_SPAN, a.w.zeros + at, n, static_cast<int>(a.w.groups & 31));
-            } else {
-              for (int i = 0; i < n; ++i) raw[2 * G4_SPAN + i] = __ldg(a.w.zeros + at + i);
-            }
-          }
-        }
-      };
       // The activations of the panel at chunk c: 16-byte pieces where rows are aligned.
       auto load = [&](int c) {
         const int64_t at = static_cast<int64_t>(c) * (G4_CHUNK * Q8_1_BYTES);
@@ -522,11 +560,8 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
       };
 
       float acc[2][NT][4] = {};
-      for (int i = 0; i < G4_STAGES - 1; ++i) {
-        if (c_begin + i < c_end) fill(c_begin + i, i);
-        cp_async_commit();
-      }
-      if (!a.ids) asm volatile("griddepcontrol.wait;" ::: "memory");
+      if (!begun) begin();
+      begun = false;
       __syncthreads();   // sm.xrow
       load(c_begin);
       cp_async_commit();
@@ -787,7 +822,7 @@ cudaError_t launch_rows(G4Args a, unsigned grid_y, int64_t active_y, int NT, int
 
 cudaError_t launch_matvec_g4(const G4Weights& w, const uint8_t* Xq, float* Y, int64_t M, int64_t K, int64_t N,
                              int num_sms, cudaStream_t s) {
-  G4Args a{w, Xq, Y, nullptr, 0, 1, false, false, M, N, static_cast<int>(K / 32), 1, nullptr};
+  G4Args a{w, Xq, Y, nullptr, 0, 1, false, false, true, M, N, static_cast<int>(K / 32), 1, nullptr};
   if (N <= 2 && g4_dp_smem(N, a.blocks) <= G4_DP_SMEM) {
     return N == 1 ? launch_stream<1>(a, 0, num_sms, s) : launch_stream<2>(a, 0, num_sms, s);
   }
@@ -808,7 +843,7 @@ cudaError_t launch_moe_matvec_g4(const G4Weights& w, int n_experts, const int32_
                                  const uint8_t* Xq, float* Y, int64_t M, int64_t K, int64_t T, int* err, int num_sms,
                                  cudaStream_t s) {
   const int64_t pairs = T * top_k;
-  G4Args a{w, Xq, Y, ids, n_experts, top_k, x_per_slot, pairs <= n_experts, M, pairs, static_cast<int>(K / 32), 1, err};
+  G4Args a{w, Xq, Y, ids, n_experts, top_k, x_per_slot, pairs <= n_experts, pairs >= 2 * n_experts, M, pairs, static_cast<int>(K / 32), 1, err};
   if ((T == 1 || pairs <= n_experts / 2) && pairs <= 65535 && g4_dp_smem(1, a.blocks) <= G4_DP_SMEM)
     return launch_stream<1>(a, pairs, num_sms, s);
   const int64_t y = a.by_pair ? pairs : n_experts;
