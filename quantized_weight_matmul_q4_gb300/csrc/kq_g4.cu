@@ -264,10 +264,13 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
 // multiples of 4, in pieces as large as its alignment allows.
 __device__ __forceinline__ void cp_async_row(uint32_t dst, const uint8_t* src, int bytes, int align) {
   if (align % 16 == 0) {
+#pragma unroll 1
     for (int o = 0; o < bytes; o += 16) cp_async16(dst + o, src + o, 16);
   } else if (align % 8 == 0) {
+#pragma unroll 1
     for (int o = 0; o < bytes; o += 8) cp_async8(dst + o, src + o);
   } else {
+#pragma unroll 1
     for (int o = 0; o < bytes; o += 4) cp_async4(dst + o, src + o, 4);
   }
 }
@@ -389,6 +392,7 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
       const int64_t at = srow + span * G4_SPAN;
       uint8_t* raw = my.raw[span & 1][lane];
       const uint16_t* ss = static_cast<const uint16_t*>(a.w.scales) + at;
+#pragma unroll 1
       for (int i = n; i < G4_SPAN; ++i) {   // blocks past K get scale 0
         reinterpret_cast<uint16_t*>(raw)[i] = 0;
         if (ZEROS) raw[2 * G4_SPAN + i] = 0;
@@ -396,12 +400,14 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
       if (a.w.groups % 2 == 0) {
         cp_async_row(smem_u32(raw), reinterpret_cast<const uint8_t*>(ss), 2 * n, static_cast<int>(2 * a.w.groups & 31));
       } else {
+#pragma unroll 1
         for (int i = 0; i < n; ++i) reinterpret_cast<uint16_t*>(raw)[i] = __ldg(ss + i);
       }
       if (ZEROS) {
         if (a.w.groups % 4 == 0) {
           cp_async_row(smem_u32(raw) + 2 * G4_SPAN, a.w.zeros + at, n, static_cast<int>(a.w.groups & 31));
         } else {
+#pragma unroll 1
           for (int i = 0; i < n; ++i) raw[2 * G4_SPAN + i] = __ldg(a.w.zeros + at + i);
         }
       }
@@ -411,6 +417,7 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
 #pragma unroll
     for (int i = 0; i < 4; ++i) wsrc[i] = wsrc0[i];
     span_chunk = c_begin;
+#pragma unroll 1
     for (int i = 0; i < G4_STAGES - 1; ++i) {
       if (c_begin + i < c_end) fill(c_begin + i, i);
       cp_async_commit();
@@ -522,7 +529,7 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
           }
         } else {
           constexpr int WORDS = PANEL * G4_CHUNK * Q8_1_BYTES / 4;
-#pragma unroll 4
+#pragma unroll 1
           for (int i = tid; i < TOK * WORDS; i += 128) {
             const uint8_t* p = sm.xrow[i / WORDS];
             const int64_t o = at + i % WORDS * 4;

@@ -89,6 +89,58 @@ def test_each_code_and_position():
         assert np.array_equal(got.cpu().double().numpy(), want), n
 
 
+@pytest.mark.parametrize("group", [32, 64, 128, 1 << 20])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_integers_are_exact(group, zeros):
+    """Unit scales: every output is a sum of integers below 2^24, and is exact."""
+    import torch
+    rng = np.random.default_rng(group % 97 + zeros)
+    M, K = 70, 416
+    W, s, z = g4_weights(rng, M, K, group, zeros)
+    W[0], W[1] = 0xff, 0x00
+    if zeros:
+        z[0], z[1] = 0, 255
+    Wd, sd, sr, zd = _dev_weights(W, np.ones_like(s), z, "bf16")
+    for N in (1, 2, 3, 8, 9, 16, 33):
+        Xq = q8_rows(rng, N, K)
+        Xq[..., 0:2] = np.array([np.float16(1.0)]).view(np.uint8)
+        Xq[0, :, 4:] = 0x80
+        got = kq.kq_matvec_g4(Wd, sd, to_dev(Xq, torch), M, K, group, zeros=zd).cpu().double().numpy()
+        ref, _ = deo.g4_matmul(W, sr, z, group, Xq)
+        assert np.array_equal(got, ref), N
+
+
+@pytest.mark.parametrize("N", [1, 9])
+def test_offsets_beyond_32_bits(N):
+    """A matrix of 5.2 GB (its last rows' offsets are past 2^32 bytes)."""
+    import torch
+    M, K, group = 320_000, 32_768, 256
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(N)
+    W = torch.randint(0, 256, (M, K // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    s = (0.02 * torch.rand(M, K // group, generator=gen, device="cuda") + 0.01).half()
+    z = torch.randint(0, 16, (M, K // group), generator=gen, device="cuda", dtype=torch.uint8)
+    Xq = q8_rows(np.random.default_rng(N), N, K)
+    Y = kq.kq_matvec_g4(W, s, to_dev(Xq, torch), M, K, group, zeros=z).cpu().numpy()
+    rows = [0, 1, 131_071, 262_143, 262_144, M - 130, M - 2, M - 1]
+    ref, B = deo.g4_matmul(W[rows].cpu().numpy(), s[rows].cpu().double().numpy(), z[rows].cpu().numpy(), group, Xq)
+    assert_g4(Y[:, rows], ref, B, K, "5.2 GB")
+
+
+def test_more_activation_rows_than_one_launch_takes():
+    import torch
+    N, M, K = 65535 * 32 + 70, 3, 32
+    rng = np.random.default_rng(5)
+    W, s, z = g4_weights(rng, M, K, 32, True)
+    Wd, sd, sr, zd = _dev_weights(W, s, z, "fp16")
+    Xq = torch.from_numpy(q8_rows(rng, 4096, K)).cuda().repeat(N // 4096 + 1, 1, 1)[:N].contiguous()
+    Y = kq.kq_matvec_g4(Wd, sd, Xq, M, K, 32, zeros=zd)
+    at = torch.tensor([0, 31, 4095, 65535 * 32 - 1, 65535 * 32, N - 1], device="cuda")
+    ref, B = deo.g4_matmul(W, sr, z, 32, Xq[at].cpu().numpy())
+    assert_g4(Y[at].cpu().numpy(), ref, B, K, "many rows")
+    assert torch.equal(Y[4096:8192], Y[:4096])
+
+
 def test_non_finite_scales_reach_the_output():
     import torch
     rng = np.random.default_rng(6)
@@ -117,6 +169,8 @@ MOE = [
     (9, 1, 1, 33, 64, 32, True, "fp16", False),
     (200, 6, 3, 40, 288, 32, True, "fp16", False),
     (700, 512, 8, 17, 64, 64, False, "fp16", False),
+    (600, 1, 1, 33, 96, 32, True, "bf16", False),       # more rows to one expert than are collected at once
+    (1100, 3, 1, 20, 128, 64, False, "fp16", True),
 ]
 
 

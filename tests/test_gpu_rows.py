@@ -135,6 +135,23 @@ def test_swiglu_extremes():
     assert d[0, 4] == 0
 
 
+def test_offsets_beyond_32_bits():
+    import torch
+    N, K = 140_000, 16_384                  # 2.3e9 elements
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    X = torch.randn(N, K, generator=gen, device="cuda", dtype=torch.bfloat16)
+    gamma = torch.ones(K, device="cuda")
+    at = [0, 131_071, 131_072, N - 1]
+    H, Y, Xq = kq.kq_add_rmsnorm_q8_1(X, X, gamma, 1e-5, Y=True)
+    want = kq.kq_add_rmsnorm_q8_1(X[at], X[at], gamma, 1e-5, Y=True)
+    for full, part in zip((H, Y, Xq), want):
+        assert torch.equal(full[at], part)
+    del H, Y, Xq
+    got = kq.kq_swiglu_q8_1(X, X)
+    assert torch.equal(got[at], kq.kq_swiglu_q8_1(X[at], X[at]))
+
+
 def test_same_codes_as_the_quantiser():
     """SwiGLU with a gate whose silu is the gate itself: the codes kq_quantize_q8_1 makes."""
     import torch
