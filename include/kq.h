@@ -296,6 +296,7 @@ KQ_API kq_status kq_moe_combine(const float* Y, const float* probs, float* out, 
  * fp32 [K]; Xq: N * (K/32) * 36 bytes, written. R, H and Y may be NULL. H may be
  * X or R itself (the same pointer and ld); outputs overlap nothing else.
  * K % 32 == 0, eps >= 0.
+ * y is within 64 * 2^-24 of its exact value, relative.
  * A block of y with an infinity or a NaN gets an infinite or NaN scale d_h (the
  * block stands for non-finite values); so does one whose maximum is above
  * 127 * 65504.
@@ -308,7 +309,8 @@ KQ_API kq_status kq_add_rmsnorm_q8_1(int dtype, const void* X, int64_t ldx, cons
  * kq_swiglu_q8_1 — v[k] = silu(gate[k]) * up[k], silu(g) = g / (1 + exp(-g)), in
  * fp32, quantised to Q8_1 as above. gate, up: dtype [N][K] (for instance the
  * halves of one [N][2K] buffer, ld = 2K); Xq: N * (K/32) * 36 bytes, written.
- * K % 32 == 0.
+ * K % 32 == 0. v is within 10 * 2^-24 of its exact value, relative (below 2^-126
+ * it may become 0).
  */
 KQ_API kq_status kq_swiglu_q8_1(int dtype, const void* gate, int64_t ldg, const void* up, int64_t ldu, void* Xq,
                                 int64_t K, int64_t N, kq_stream_t stream);
@@ -332,6 +334,8 @@ KQ_API kq_status kq_swiglu_q8_1(int dtype, const void* gate, int64_t ldg, const 
  * fewer available experts than slots gets the lowest-numbered experts not yet
  * chosen for the others, with weight 0 (ids are always valid and distinct).
  * logits: dtype [T][n_experts], rows ld apart; bias: fp32 [n_experts] or NULL;
+ * Each weight is within 120 * 2^-24 of its exact value, relative (for logits within
+ * 60 of the token's largest).
  * ids: int32 [T][top_k], probs: fp32 [T][top_k], written. 1 <= n_experts <= 512,
  * n_experts % n_groups == 0, 1 <= topk_groups <= n_groups,
  * 1 <= top_k <= topk_groups * n_experts / n_groups.
@@ -352,8 +356,15 @@ KQ_API kq_status kq_moe_route(int dtype, const void* logits, int64_t ld, const f
  * stored block sums are not read). Y: fp32 [N][M], written. K % 32 == 0; W,
  * scales, zeros, Xq and Y are 16-byte aligned.
  * A decode operator: made for up to a few dozen rows of Xq; any N is taken.
- * Block dot products are exact integers, scales and sums fp32: no rounding of
- * the operands beside the Q8_1 codes themselves.
+ * Accuracy: the dot products of 32-element blocks are exact integers and are
+ * multiplied with the scales and summed in fp32; |Y - Y_ref| is at most
+ * (K/32 + 12) * 2^-24 times the sum of the blocks' absolute contributions, Y_ref
+ * the exact product of the dequantised operands. Results do not depend on
+ * scheduling; a row's result may differ in the last bits with the number of
+ * rows in the call (the sums are grouped differently).
+ * As in kq_matvec, W, scales and zeros are streamed before the call waits for the
+ * previous kernel on the stream: they must not be written by a still-running
+ * predecessor that allows programmatic dependent launch.
  */
 KQ_API kq_status kq_matvec_g4(const void* W, const void* scales, int scale_dtype, const void* zeros, int64_t group,
                               const void* Xq, float* Y, int64_t M, int64_t K, int64_t N, kq_stream_t stream);
@@ -365,7 +376,8 @@ KQ_API kq_status kq_matvec_g4(const void* W, const void* scales, int scale_dtype
  * matrices one after the other (n_experts * M rows); expert_ids: int32
  * [T][top_k]; Y: fp32 [T][top_k][M], written. n_experts <= 512,
  * top_k <= n_experts. An out-of-range expert id records KQ_DEVERR_EXPERT_ID and
- * that slot's output row is written as zeros.
+ * that slot's output row is written as zeros; ids may repeat within a token.
+ * W, scales and zeros are streamed early as above (for T * top_k >= 2 * n_experts).
  */
 KQ_API kq_status kq_moe_matvec_g4(const void* W, const void* scales, int scale_dtype, const void* zeros, int64_t group,
                                   int32_t n_experts, const int32_t* expert_ids, int32_t top_k, int x_per_slot,
@@ -403,8 +415,8 @@ KQ_API kq_status kq_get_device_error(int32_t* code, kq_stream_t stream);
  * flag is per process and is read when a call queues its launch (a call
  * captured in a CUDA graph keeps the value it saw). Not for production use:
  * hold = 0 (the default) restores normal calls. Always returns KQ_OK.
- * Calls that take other kernels (TQ4_1S, the small-N decode of kq_gemm) are
- * not affected.
+ * Calls that take other kernels (TQ4_1S, the small-N decode of kq_gemm, the
+ * group-scaled products) are not affected.
  */
 KQ_API kq_status kq_test_hold_copies(int hold);
 
