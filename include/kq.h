@@ -309,8 +309,8 @@ KQ_API kq_status kq_add_rmsnorm_q8_1(int dtype, const void* X, int64_t ldx, cons
  * kq_swiglu_q8_1 — v[k] = silu(gate[k]) * up[k], silu(g) = g / (1 + exp(-g)), in
  * fp32, quantised to Q8_1 as above. gate, up: dtype [N][K] (for instance the
  * halves of one [N][2K] buffer, ld = 2K); Xq: N * (K/32) * 36 bytes, written.
- * K % 32 == 0. v is within 10 * 2^-24 of its exact value, relative (below 2^-126
- * it may become 0).
+ * K % 32 == 0. v is within 10 * 2^-24 of its exact value, relative (a silu
+ * below 2^-119 in magnitude may become 0).
  */
 KQ_API kq_status kq_swiglu_q8_1(int dtype, const void* gate, int64_t ldg, const void* up, int64_t ldu, void* Xq,
                                 int64_t K, int64_t N, kq_stream_t stream);
