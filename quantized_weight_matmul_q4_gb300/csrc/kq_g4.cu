@@ -197,14 +197,13 @@ __global__ void __launch_bounds__(G4_DP_WARPS * 32, G4_DP_CTAS) g4_dp_kernel(G4A
 // whose operands are small integers, so that every block's dot product is exact
 // in the fp32 accumulator.
 //
-// Weight codes are not converted: a nibble or-ed into the mantissa of fp16 1024
-// is 1024 + c (low nibbles of a 16-bit field) or 1024 + 16 c (the next ones), one
-// logic operation for two codes. The even k of a block go through one MMA as
-// (1024 + c) * q, the odd k through a second as (1024 + 16 c) * (q / 16), both
-// exact; their sum is Sum c q + 1024 Sum_even q + 64 Sum_odd q, an integer below
-// 32 * 1039 * 128 < 2^24. The excess depends on the activation row alone and is
-// taken off by starting the accumulator at its negative (with 8 Sum q too where
-// there are no zero points).
+// Weight codes become fp16 by one logic operation for two codes: a low nibble of a
+// 16-bit field or-ed into the mantissa of 1024 is 1024 + c, the next nibble in that of
+// 64 is 64 + c. The even k of a block go through one MMA, the odd k through a second.
+// Without zero points the sum is Sum (c - 8) q + 1032 Sum_even q + 72 Sum_odd q, an
+// integer below 32 * 1039 * 128 < 2^24; the excess depends on the activation row alone
+// and is taken off by starting the accumulator at its negative. With zero points
+// 1024 + z and 64 + z are subtracted first (packed fp16, exact).
 //
 // k is permuted within a block: lane (g = lane / 4, t = lane % 4) of a warp
 // takes word t (k = 8t..8t+7) of its rows' 16-byte blocks for A and the same k of
@@ -228,17 +227,17 @@ constexpr int G4_MAX_SPLITS = 8;
 constexpr int G4_LIST = 256;       // rows of one expert collected at a time
 
 struct alignas(16) G4Frag {    // of one block and 8 activation rows
-  uint4 b[32];     // per lane: even k (two registers), odd k / 16 (two registers)
-  float4 init[4];  // per t: start of the accumulators of rows 2t, 2t + 1, 2t, 2t + 1
+  uint4 b[32];     // per lane: even k (two registers), odd k (two registers)
+  float4 init[4];  // per t: start of the accumulators of rows 2t, 2t + 1, 2t, 2t + 1 (without zero points)
   float2 d[4];     // per t: scales of rows 2t, 2t + 1
-  float2 sum[4];   // per t: Sum q of rows 2t, 2t + 1 (with zero points)
-  float4 pad;      // 656 bytes: eight threads that write eight blocks' fragments meet different banks
+  float4 pad[3];   // 656 bytes: eight threads that write eight blocks' fragments meet different banks
 };
 template <bool FINE, bool ZEROS>
 struct alignas(16) G4Warp {    // a warp's own
   uint8_t w[g4_stages(FINE, ZEROS)][32][G4_CHUNK * 16];
   uint8_t raw[2][32][G4_SPAN * (ZEROS ? 3 : 2)];   // as in memory: G4_SPAN scales, then G4_SPAN zero points
-  float2 scale[FINE ? G4_CHUNK : 1][FINE ? 32 : 1];   // scale and zero point of a chunk's blocks (FINE)
+  // Of a chunk's blocks (FINE): the scale, and -(1024 + zero point) as an fp16 pair.
+  float2 scale[FINE ? G4_CHUNK : 1][FINE ? 32 : 1];
 };
 template <int NT, bool FINE, bool ZEROS>
 struct G4Smem {
@@ -294,18 +293,18 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
-// (v & mask) | 0x6400'6400 in one operation.
-__device__ __forceinline__ uint32_t with_1024(uint32_t v, uint32_t mask) {
+// (v & mask) | magic in one operation.
+template <uint32_t MASK, uint32_t MAGIC>
+__device__ __forceinline__ uint32_t codes_f16(uint32_t v) {
   uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(v), "r"(mask), "r"(0x64006400u));
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(v), "r"(MASK), "r"(MAGIC));
   return r;
 }
-constexpr uint32_t H2_M1152 = 0xe480e480u, H2_M72 = 0xd480d480u, H2_SIXTEENTH = 0x2c002c00u;   // fp16 pairs
+__device__ __forceinline__ uint32_t add_f16x2(uint32_t a, uint32_t b) { return half2_bits(__hadd2(bits_half2(a), bits_half2(b))); }
+constexpr uint32_t H2_M1152 = 0xe480e480u, H2_960 = 0x63806380u;   // fp16 pairs
 
-// Byte i of v as fp32, exactly: 2^23 + byte, less 2^23.
-__device__ __forceinline__ float byte_f32(uint32_t v, int i) {
-  return __uint_as_float(__byte_perm(v, 0x4b000000u, 0x7440 + i)) - 8388608.0f;
-}
+// -(1024 + byte i of v) as an fp16 pair.
+__device__ __forceinline__ uint32_t zero_f16x2(uint32_t v, int i) { return __byte_perm(v, 0xe4e4e4e4u, 0x4040 + 0x0101 * i); }
 
 // FINE: a group is shorter than a chunk, so every block has its own scale; else
 // one scale serves a chunk. ZEROS: zero points are given.
@@ -515,20 +514,31 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
         }
         sm.xrow[tid] = p;
       }
-      // The activations of the panel at chunk c: 16-byte pieces where rows are aligned.
-      auto load = [&](int c) {
-        const int64_t at = static_cast<int64_t>(c) * (G4_CHUNK * Q8_1_BYTES);
-        if (even) {
-          constexpr int PIECES = PANEL * G4_CHUNK * Q8_1_BYTES / 16;   // of a row
+      // The activations of the panel at chunk c, in 16-byte pieces where rows are aligned: piece
+      // tid + 128 k is in row `row`, chunk `ch` of the panel.
+      constexpr int PIECES = PANEL * G4_CHUNK * Q8_1_BYTES / 16;   // of a row
+      constexpr int XP = (TOK * PIECES + 127) / 128;
+      __syncthreads();   // sm.xrow
+      const uint8_t* xsrc[XP];
 #pragma unroll
-          for (int i = tid; i < TOK * PIECES; i += 128) {
-            const uint8_t* p = sm.xrow[i / PIECES];
-            const int64_t o = at + i % PIECES * 16;
-            const bool in = p && o < xbytes;
-            cp_async16(smem_u32(sm.x) + i * 16, in ? p + o : a.Xq, in ? 16 : 0);
+      for (int k = 0; k < XP; ++k) {
+        const int i = tid + 128 * k;
+        const uint8_t* p = even && i < TOK * PIECES ? sm.xrow[i / PIECES] : nullptr;
+        xsrc[k] = p ? p + (static_cast<int64_t>(c_begin) * G4_CHUNK * Q8_1_BYTES + i % PIECES * 16) : nullptr;
+      }
+      auto load = [&](int c) {
+        if (even) {
+#pragma unroll
+          for (int k = 0; k < XP; ++k) {
+            const int i = tid + 128 * k;
+            if (i >= TOK * PIECES) break;
+            const bool in = xsrc[k] && c + i % PIECES / 9 < chunks;
+            cp_async16(smem_u32(sm.x) + i * 16, in ? xsrc[k] : a.Xq, in ? 16 : 0);
+            if (xsrc[k]) xsrc[k] += PIECES * 16;
           }
         } else {
           constexpr int WORDS = PANEL * G4_CHUNK * Q8_1_BYTES / 4;
+          const int64_t at = static_cast<int64_t>(c) * (G4_CHUNK * Q8_1_BYTES);
 #pragma unroll 1
           for (int i = tid; i < TOK * WORDS; i += 128) {
             const uint8_t* p = sm.xrow[i / WORDS];
@@ -551,25 +561,26 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
         for (int j = 0; j < 4; ++j) {
           const uint32_t x0 = px[1 + 2 * j], x1 = px[2 + 2 * j];
           const uint32_t ev = __byte_perm(x0, x1, 0x6240), od = __byte_perm(x0, x1, 0x7351);
-          se = __dp4a(static_cast<int>(ev), 0x01010101, se);
-          so = __dp4a(static_cast<int>(od), 0x01010101, so);
-          const uint32_t ue = ev ^ 0x80808080u, uo = od ^ 0x80808080u;    // codes + 128
-          f.b[fg * 4 + j] = make_uint4(
-              half2_bits(__hadd2(bits_half2(__byte_perm(ue, 0x64646464u, 0x4140)), bits_half2(H2_M1152))),
-              half2_bits(__hadd2(bits_half2(__byte_perm(ue, 0x64646464u, 0x4342)), bits_half2(H2_M1152))),
-              half2_bits(__hfma2(bits_half2(__byte_perm(uo, 0x64646464u, 0x4140)), bits_half2(H2_SIXTEENTH), bits_half2(H2_M72))),
-              half2_bits(__hfma2(bits_half2(__byte_perm(uo, 0x64646464u, 0x4342)), bits_half2(H2_SIXTEENTH), bits_half2(H2_M72))));
+          if (!ZEROS) {
+            se = __dp4a(static_cast<int>(ev), 0x01010101, se);
+            so = __dp4a(static_cast<int>(od), 0x01010101, so);
+          }
+          const uint32_t ue = ev ^ 0x80808080u, uo = od ^ 0x80808080u;    // codes + 128, then 1024 + that
+          f.b[fg * 4 + j] = make_uint4(add_f16x2(__byte_perm(ue, 0x64646464u, 0x4140), H2_M1152),
+                                       add_f16x2(__byte_perm(ue, 0x64646464u, 0x4342), H2_M1152),
+                                       add_f16x2(__byte_perm(uo, 0x64646464u, 0x4140), H2_M1152),
+                                       add_f16x2(__byte_perm(uo, 0x64646464u, 0x4342), H2_M1152));
         }
-        float* c = reinterpret_cast<float*>(&f.init[fg >> 1]) + (fg & 1);
-        c[0] = c[2] = static_cast<float>(ZEROS ? -(1024 * se + 64 * so) : -(1032 * se + 72 * so));
+        if (!ZEROS) {
+          float* c = reinterpret_cast<float*>(&f.init[fg >> 1]) + (fg & 1);
+          c[0] = c[2] = static_cast<float>(-(1032 * se + 72 * so));
+        }
         reinterpret_cast<float*>(&f.d[fg >> 1])[fg & 1] = __low2float(bits_half2(px[0]));
-        if (ZEROS) reinterpret_cast<float*>(&f.sum[fg >> 1])[fg & 1] = static_cast<float>(se + so);
       };
 
       float acc[2][NT][4] = {};
       if (!begun) begin();
       begun = false;
-      __syncthreads();   // sm.xrow
       load(c_begin);
       cp_async_commit();
       int slot = 0;   // of chunk c
@@ -595,7 +606,8 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
         cp_async_commit();
         slot = slot == G4_STAGES - 1 ? 0 : slot + 1;
         const G4Frag* pf = &sm.frag[(c - p_begin) * (G4_CHUNK * NT)];
-        float2 s[4];   // scale and zero point of rows g, g + 8, g + 16, g + 24
+        float s[4];       // scales of rows g, g + 8, g + 16, g + 24
+        uint32_t z[4];    // their -(1024 + zero point), fp16 pairs
         if (FINE) {
           // Lane: row; the four blocks' scales converted once. A chunk has four groups or two.
           const int gr = c * G4_CHUNK >> a.w.group_shift;
@@ -612,69 +624,68 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
             sb = make_uint2(__byte_perm(two, 0, 0x1010), __byte_perm(two, 0, 0x3232));
             zb = __byte_perm(zz, 0, 0x1100);
           }
-          my.scale[0][lane] = make_float2(scale_f(sb.x & 0xffff), ZEROS ? byte_f32(zb, 0) : 0.f);
-          my.scale[1][lane] = make_float2(scale_f(sb.x >> 16), ZEROS ? byte_f32(zb, 1) : 0.f);
-          my.scale[2][lane] = make_float2(scale_f(sb.y & 0xffff), ZEROS ? byte_f32(zb, 2) : 0.f);
-          my.scale[3][lane] = make_float2(scale_f(sb.y >> 16), ZEROS ? byte_f32(zb, 3) : 0.f);
+          my.scale[0][lane] = make_float2(scale_f(sb.x & 0xffff), ZEROS ? __uint_as_float(zero_f16x2(zb, 0)) : 0.f);
+          my.scale[1][lane] = make_float2(scale_f(sb.x >> 16), ZEROS ? __uint_as_float(zero_f16x2(zb, 1)) : 0.f);
+          my.scale[2][lane] = make_float2(scale_f(sb.y & 0xffff), ZEROS ? __uint_as_float(zero_f16x2(zb, 2)) : 0.f);
+          my.scale[3][lane] = make_float2(scale_f(sb.y >> 16), ZEROS ? __uint_as_float(zero_f16x2(zb, 3)) : 0.f);
           __syncwarp();
         } else {
           const int gr = (c * G4_CHUNK) >> a.w.group_shift;
           const uint8_t* raw = my.raw[(gr / G4_SPAN) & 1][g];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            s[i] = make_float2(scale_f(reinterpret_cast<const uint16_t*>(raw + i * (8 * sizeof(my.raw[0][0])))[gr % G4_SPAN]),
-                               ZEROS ? byte_f32(raw[i * (8 * sizeof(my.raw[0][0])) + 2 * G4_SPAN + gr % G4_SPAN], 0) : 0.f);
+          for (int i = 0; i < 4; ++i) {
+            const uint8_t* r = raw + i * (8 * sizeof(my.raw[0][0]));
+            s[i] = scale_f(reinterpret_cast<const uint16_t*>(r)[gr % G4_SPAN]);
+            if (ZEROS) z[i] = zero_f16x2(r[2 * G4_SPAN + gr % G4_SPAN], 0);
+          }
         }
         float part[2][NT][4];   // of this chunk, before the chunk's scale (not FINE)
 #pragma unroll
         for (int b = 0; b < G4_CHUNK; ++b) {
           const uint32_t (&w)[4] = wc[b];
-          uint32_t L[2][4], U[2][4];
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const uint32_t v0 = w[2 * m] >> 8, v1 = w[2 * m + 1] >> 8;
-            L[m][0] = with_1024(w[2 * m], 0x000f000fu);
-            L[m][1] = with_1024(w[2 * m + 1], 0x000f000fu);
-            L[m][2] = with_1024(v0, 0x000f000fu);
-            L[m][3] = with_1024(v1, 0x000f000fu);
-            U[m][0] = with_1024(w[2 * m], 0x00f000f0u);
-            U[m][1] = with_1024(w[2 * m + 1], 0x00f000f0u);
-            U[m][2] = with_1024(v0, 0x00f000f0u);
-            U[m][3] = with_1024(v1, 0x00f000f0u);
-          }
           if (FINE) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[i] = my.scale[b][8 * i + g];
+            for (int i = 0; i < 4; ++i) {
+              const float2 v = my.scale[b][8 * i + g];
+              s[i] = v.x;
+              z[i] = __float_as_uint(v.y);
+            }
           }
+          uint32_t L[2][4], U[2][4];
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {   // rows g and g + 8 of the 16
+              const uint32_t v = w[2 * m + h], v8 = v >> 8;
+              L[m][h] = codes_f16<0x000f000fu, 0x64006400u>(v);
+              L[m][h + 2] = codes_f16<0x000f000fu, 0x64006400u>(v8);
+              U[m][h] = codes_f16<0x00f000f0u, 0x54005400u>(v);
+              U[m][h + 2] = codes_f16<0x00f000f0u, 0x54005400u>(v8);
+              if (ZEROS) {
+                const uint32_t zl = z[2 * m + h], zu = add_f16x2(zl, H2_960);
+                L[m][h] = add_f16x2(L[m][h], zl);
+                L[m][h + 2] = add_f16x2(L[m][h + 2], zl);
+                U[m][h] = add_f16x2(U[m][h], zu);
+                U[m][h + 2] = add_f16x2(U[m][h + 2], zu);
+              }
+            }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const G4Frag& f = pf[b * NT + n];
             const uint4 bf = f.b[lane];
-            const float4 c0 = f.init[t];
+            float4 c0 = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (!ZEROS) c0 = f.init[t];
             const float2 d = f.d[t];
-            float2 sq = make_float2(0.f, 0.f);
-            if (ZEROS) sq = f.sum[t];
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
               float r[4];
               mma16816(r, L[m], bf.x, bf.y, c0.x, c0.y, c0.z, c0.w);
               mma16816(r, U[m], bf.z, bf.w, r[0], r[1], r[2], r[3]);
-              if (ZEROS) {
-                r[0] = fmaf(-s[2 * m].y, sq.x, r[0]);
-                r[1] = fmaf(-s[2 * m].y, sq.y, r[1]);
-                r[2] = fmaf(-s[2 * m + 1].y, sq.x, r[2]);
-                r[3] = fmaf(-s[2 * m + 1].y, sq.y, r[3]);
-              }
-              if (FINE) {
-                acc[m][n][0] = fmaf(r[0] * d.x, s[2 * m].x, acc[m][n][0]);
-                acc[m][n][1] = fmaf(r[1] * d.y, s[2 * m].x, acc[m][n][1]);
-                acc[m][n][2] = fmaf(r[2] * d.x, s[2 * m + 1].x, acc[m][n][2]);
-                acc[m][n][3] = fmaf(r[3] * d.y, s[2 * m + 1].x, acc[m][n][3]);
-              } else {
-                part[m][n][0] = b == 0 ? r[0] * d.x : fmaf(r[0], d.x, part[m][n][0]);
-                part[m][n][1] = b == 0 ? r[1] * d.y : fmaf(r[1], d.y, part[m][n][1]);
-                part[m][n][2] = b == 0 ? r[2] * d.x : fmaf(r[2], d.x, part[m][n][2]);
-                part[m][n][3] = b == 0 ? r[3] * d.y : fmaf(r[3], d.y, part[m][n][3]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float v = r[k] * (k & 1 ? d.y : d.x);
+                if (FINE) acc[m][n][k] = fmaf(v, s[2 * m + (k >> 1)], acc[m][n][k]);
+                else part[m][n][k] = b == 0 ? v : fmaf(r[k], k & 1 ? d.y : d.x, part[m][n][k]);
               }
             }
           }
@@ -682,14 +693,10 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
         if (!FINE) {
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
-            const float f0 = s[2 * m].x, f1 = s[2 * m + 1].x;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              acc[m][n][0] = fmaf(part[m][n][0], f0, acc[m][n][0]);
-              acc[m][n][1] = fmaf(part[m][n][1], f0, acc[m][n][1]);
-              acc[m][n][2] = fmaf(part[m][n][2], f1, acc[m][n][2]);
-              acc[m][n][3] = fmaf(part[m][n][3], f1, acc[m][n][3]);
-            }
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) acc[m][n][k] = fmaf(part[m][n][k], s[2 * m + (k >> 1)], acc[m][n][k]);
           }
         }
       }
