@@ -377,7 +377,7 @@ KQ_API kq_status kq_matvec_g4(const void* W, const void* scales, int scale_dtype
  * [T][top_k]; Y: fp32 [T][top_k][M], written. n_experts <= 512,
  * top_k <= n_experts. An out-of-range expert id records KQ_DEVERR_EXPERT_ID and
  * that slot's output row is written as zeros; ids may repeat within a token.
- * W, scales and zeros are streamed early as above (for T * top_k >= 2 * n_experts).
+ * W, scales and zeros are streamed early as above (for T * top_k >= n_experts).
  */
 KQ_API kq_status kq_moe_matvec_g4(const void* W, const void* scales, int scale_dtype, const void* zeros, int64_t group,
                                   int32_t n_experts, const int32_t* expert_ids, int32_t top_k, int x_per_slot,

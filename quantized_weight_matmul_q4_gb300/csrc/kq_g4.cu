@@ -24,7 +24,7 @@ struct G4Args {
   float* Y;
   const int32_t* ids;   // null: one matrix, rows 0..rows-1 of Xq
   int n_experts, top_k;
-  bool x_per_slot, by_pair;
+  bool x_per_slot;
   bool eager;           // nearly every expert has pairs: its weights are asked for before they are known
   int64_t M;
   int64_t rows;         // activation rows, or (token, slot) pairs
@@ -46,7 +46,13 @@ __device__ __forceinline__ float scale_f32(bool fp16, uint16_t bits) {
 // weights: 2^lanes_log2 lanes share a row, each taking every 2^lanes_log2-th 16-byte
 // block of it, U rows at a time, with the next four 16-byte loads of a lane in
 // flight while it works on the last four. What a block costs a lane is 12
-// operations to unpack, 8 dp4a and about 8 for the scales.
+// operations to unpack, 8 dp4a and about 8 for the scales. Unpacking costs less with
+// dp4a than in the tensor-core form below, and without tiles no row is idle.
+//
+// Bound by HBM for large matrices (152064 x 3584: 45.3 us, 281 MB, 6.2 TB/s = 0.91 of the
+// measured copy; issue slots 67 % busy) and by the launch and the first loads' latency for
+// small ones (4096 x 4096: 3.3 us, launch included;
+// eight experts' 1536 x 2048: 5.5 us, 2.4 TB/s).
 constexpr int G4_DP_WARPS = 8;
 constexpr int G4_DP_CTAS = 3;   // per SM
 
@@ -216,6 +222,20 @@ __global__ void __launch_bounds__(G4_DP_WARPS * 32, G4_DP_CTAS) g4_dp_kernel(G4A
 // which keeps filling while fragments are made. Where there are too few row
 // tiles for the SMs, a cluster of CTAs splits K; their sums are added in rank
 // order through distributed shared memory.
+//
+// The legacy MMA form and not tensor memory, since every block's sums are multiplied
+// with two scales: here they are in registers already, from tensor memory the
+// whole accumulator would be read back for every 32 k.
+//
+// Bound by issue and the latency of its dependent steps, not by HBM: some 270
+// instructions per warp and chunk (8 rows, groups of 128 and longer) up to 560 (16 rows, groups of 32 with
+// zero points) at 46 to 58 % of the issue slots, 16 warps to an SM (128 registers a
+// thread). Launch, first copies and the cluster's sum take 4.5 us of every call (4096 x 512,
+// 8 rows: 4.2). 4096 x 4096, 8 rows: 6.6 us; 14336 x 4096, 16 rows, groups of 32 with zero
+// points: 19.4 us (1.8 TB/s); 128 experts' 2048 x 768, 512 (token, slot) rows, the same
+// groups: 42.4 us (2.9 TB/s). Copying by TMA instead of cp.async was slower (the latter
+// 46 -> 49.5 us), and so was a CTA that goes on to the next tile of its expert's rows
+// with its copies running ahead (two tiles: the same, four: 57 us).
 constexpr int G4_CHUNK = 4;        // 32-element blocks per chunk
 // Chunks of weights in flight per warp: as many as leave room for four CTAs on an SM.
 __host__ __device__ constexpr int g4_stages(bool FINE, bool ZEROS) { return FINE || ZEROS ? 3 : 4; }
@@ -325,21 +345,8 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!a.eager) asm volatile("griddepcontrol.wait;" ::: "memory");
-  int expert = a.ids && !a.by_pair ? static_cast<int>(blockIdx.y) : 0;
+  const int expert = a.ids ? static_cast<int>(blockIdx.y) : 0;
   int64_t scan = 0;     // next pair to look at
-  if (a.by_pair) {
-    // One cluster per pair; the first pair of an expert takes all of its pairs.
-    expert = a.ids[blockIdx.y];
-    if (expert < 0 || expert >= a.n_experts) {
-      if (tid == 0 && blockIdx.x == 0) report_error(a.err, ERR_EXPERT_ID);
-      if (rank == 0 && tid < rows) a.Y[blockIdx.y * a.M + m0 + tid] = 0.f;
-      return;
-    }
-    int earlier = 0;
-    for (int p = tid; p < static_cast<int>(blockIdx.y); p += 128) earlier |= a.ids[p] == expert;
-    if (__syncthreads_or(earlier)) return;
-    scan = blockIdx.y;
-  }
   const int64_t row0 = static_cast<int64_t>(expert) * a.M + m0;
   const int64_t row_bytes = static_cast<int64_t>(a.blocks) * 16;
   const int chunks = (a.blocks + G4_CHUNK - 1) / G4_CHUNK;
@@ -430,7 +437,7 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
     asm volatile("griddepcontrol.wait;" ::: "memory");
   }
   // Invalid ids belong to no expert: expert 0's CTAs write their zeros.
-  if (a.ids && !a.by_pair && expert == 0 && rank == 0) {
+  if (a.ids && expert == 0 && rank == 0) {
     for (int64_t p = tid; p < a.rows; p += 128) {
       const int e = a.ids[p];
       if (e < 0 || e >= a.n_experts) {
@@ -700,6 +707,23 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
           }
         }
       }
+      if (a.splits == 1) {
+        // A warp's store writes whole sectors: eight weight rows (g) of four activation rows.
+        const int64_t m = m0 + warp * 32 + g;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int col = n * 8 + 2 * t + k;
+            if (col >= nn) continue;
+            float* y = a.Y + (a.ids ? sm.list[n0 + col] : static_cast<int64_t>(blockIdx.y) * TOK + col) * a.M + m;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (m + 8 * i < a.M) y[8 * i] = acc[i >> 1][n][2 * (i & 1) + k];
+          }
+        if (n0 + TOK < have) __syncthreads();   // before the next rows' fragments
+        continue;
+      }
       cp_async_wait<0>();
       __syncthreads();  // the fragments make room for the sums of this CTA, [activation row][weight row]
       float* red = reinterpret_cast<float*>(sm.frag);
@@ -710,26 +734,23 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             red[(n * 8 + 2 * t + (k & 1)) * G4_ROWS + warp * 32 + m * 16 + g + 8 * (k >> 1)] = acc[m][n][k];
-      if (a.splits > 1) cluster_sync(); else __syncthreads();
+      cluster_sync();
       // Each rank adds up and writes its share of the tile's rows.
       const int sh = 31 - __clz(G4_ROWS / a.splits);
       for (int i = tid; i < nn << sh; i += 128) {
         const int n = i >> sh, m = (rank << sh) + (i & ((1 << sh) - 1));
         if (m >= rows) continue;
-        float v = red[n * G4_ROWS + m];
-        if (a.splits > 1) {
-          float part[G4_MAX_SPLITS];   // all on their way before the first is added
+        float part[G4_MAX_SPLITS];   // all on their way before the first is added
 #pragma unroll
-          for (int r = 0; r < G4_MAX_SPLITS; ++r)
-            part[r] = r < a.splits ? ld_cluster_f32(mapa_shared(red + n * G4_ROWS + m, r)) : 0.f;
-          v = 0.f;
+        for (int r = 0; r < G4_MAX_SPLITS; ++r)
+          part[r] = r < a.splits ? ld_cluster_f32(mapa_shared(red + n * G4_ROWS + m, r)) : 0.f;
+        float v = 0.f;
 #pragma unroll
-          for (int r = 0; r < G4_MAX_SPLITS; ++r) v += part[r];
-        }
+        for (int r = 0; r < G4_MAX_SPLITS; ++r) v += part[r];
         const int64_t out = a.ids ? sm.list[n0 + n] : static_cast<int64_t>(blockIdx.y) * TOK + n;
         a.Y[out * a.M + m0 + m] = v;
       }
-      if (a.splits > 1) cluster_sync(); else __syncthreads();
+      cluster_sync();   // the others have read this CTA's sums
     }
     if (!a.ids || scan >= a.rows) return;
   }
@@ -769,7 +790,9 @@ cudaError_t launch_stream(const G4Args& a, int64_t pairs, int num_sms, cudaStrea
   const int64_t row_warps = (a.M + per - 1) / per * y;   // warps at one row per lane group
   const int64_t slots = static_cast<int64_t>(num_sms) * G4_DP_CTAS * G4_DP_WARPS;
   const int64_t q = best >> lanes_log2;                  // blocks of a lane per row
-  // Rows per lane: as many as fill its four loads, more where the rows are many.
+  // Rows per lane: as many as fill its four loads, and four where the rows are many (of 4096
+  // codes, one activation row: 4096 rows 3.3 us by one and 5.9 by four, 11008 5.8 and 6.3,
+  // 14336 7.1 and 6.7, 28672 12.9 and 11.7, 152064 59 and 51).
   int U = q >= 4 ? 1 : q >= 2 ? 2 : 4;
   if (NX == 1 && 2 * row_warps >= 7 * slots) U = 4;
   if (a.M < per * U) U = 1;
@@ -794,11 +817,15 @@ cudaError_t launch_mma(const G4Args& a, unsigned grid_y, int num_sms, int slot, 
   cfg.blockDim = dim3(128);
   size_t smem = sizeof(G4Smem<NT, FINE, ZEROS>);
   if (a.splits > 1) {
-    // Clusters are packed onto as few SMs as hold them (4096 x 4096, 8 rows, 256 CTAs: 7.1 us
-    // against 6.7 spread). So ask for the shared memory that leaves an SM its even share
+    // Clusters are packed onto as few SMs as hold them (4096 x 4096, 8 rows, 256 CTAs: 7.5 us
+    // against 6.6 spread). So ask for the shared memory that leaves an SM its even share
     // of the CTAs only, if that leaves a tenth of the places free: clusters need places
-    // near one another. (An SM has 228 KB, each CTA's reservation 1 KB.)
-    const int64_t share = (tiles * a.splits * grid_y * 10 + 9 * num_sms - 1) / (9 * num_sms);
+    // near one another. With one place to an SM, clusters of eight need more free (2048 x 4096,
+    // 128 CTAs on 152 SMs: 9.5 us, as they do not all run at once; 5.6 with two places). (An SM has
+    // 228 KB, each CTA's reservation 1 KB.)
+    const int64_t ctas = tiles * a.splits * grid_y;
+    int64_t share = (ctas * 10 + 9 * num_sms - 1) / (9 * num_sms);
+    if (share == 1 && a.splits == 8 && 4 * ctas > 3 * num_sms) share = 2;
     if (share <= 4) smem = std::max<size_t>(smem, std::min<size_t>(227 * 1024, 228 * 1024 / share - 1024) / 16 * 16);
   }
   cfg.dynamicSmemBytes = smem;
@@ -821,12 +848,38 @@ cudaError_t launch_mma_nt(const G4Args& a, unsigned grid_y, int num_sms, int slo
   return zeros ? launch_mma<NT, false, true>(a, grid_y, num_sms, slot + 2, s) : launch_mma<NT, false, false>(a, grid_y, num_sms, slot + 3, s);
 }
 
-// NT: 8-row tiles of activations per CTA; grid_y: token tiles, pairs or experts.
-cudaError_t launch_rows(G4Args a, unsigned grid_y, int64_t active_y, int NT, int num_sms, cudaStream_t s) {
-  const int chunks = (a.blocks + G4_CHUNK - 1) / G4_CHUNK;
-  const int64_t tiles = (a.M + G4_ROWS - 1) / G4_ROWS * active_y;
-  a.splits = 1;
-  while (a.splits < G4_MAX_SPLITS && tiles * a.splits < 2 * num_sms && chunks >= 4 * a.splits) a.splits *= 2;
+// CTAs that run at once (by shared memory and registers).
+int64_t g4_places(int NT, int num_sms) { return static_cast<int64_t>(num_sms) * (NT == 4 ? 3 : 4); }
+
+// K is split while all clusters still run at once, a tenth of the places left free for
+// clusters of four and eight, which need places near one another. (Of 4096 codes a row,
+// without zero points. Eight rows: 4096 x 4096 17.2 us in one part, 10.6 in two, 7.1 in four, 6.4
+// in eight; 9600 x 4096 12.2 in two, 10.2 in four, 13.1 in the eight that no longer run at
+// once; 28672 x 4096 33.6 in one, 21.1 in two, 22.9 in four.) A part keeps two chunks at least.
+int g4_splits(int64_t tiles, int64_t blocks, int NT, int num_sms) {
+  const int64_t chunks = (blocks + G4_CHUNK - 1) / G4_CHUNK, places = g4_places(NT, num_sms);
+  int splits = 1;
+  while (splits < G4_MAX_SPLITS && chunks >= 4 * splits &&
+         (splits == 1 ? tiles * 2 <= places : 20 * tiles * splits <= 9 * places))
+    splits *= 2;
+  return splits;
+}
+
+// rows: activation rows of a product (an expert's, on average); products: how many (experts).
+cudaError_t launch_rows(G4Args a, int64_t rows, int64_t products, int num_sms, cudaStream_t s) {
+  // Rows per CTA: 8, 16 or 32 (14336 x 4096: 16 rows 17.9 us by 16 and 21.8 by 8; 32 rows 31.1
+  // by 16 and 33.8 by 32; 64 rows 51.8 by 16 and 44.6 by 32; 256 rows 152 by 16 and 142
+  // by 32). The 32 cost where they leave places empty (8192 x 4096, 128 rows: 52.0 by 16, 71.7
+  // by 32 on 256 of 456 places; 14336 x 4096, 96 rows, 336 of 456: 72 by either).
+  const int64_t m_tiles = (a.M + G4_ROWS - 1) / G4_ROWS;
+  int NT = rows > 8 ? 2 : 1;
+  if (rows > 32) {
+    const int64_t tiles = m_tiles * ((rows + 31) / 32) * products, places = g4_places(4, num_sms);
+    const int64_t ctas = tiles * g4_splits(tiles, a.blocks, 4, num_sms);
+    if (4 * ctas >= 3 * ((ctas + places - 1) / places * places)) NT = 4;
+  }
+  const unsigned grid_y = static_cast<unsigned>(a.ids ? products : (rows + NT * 8 - 1) / (NT * 8));
+  a.splits = g4_splits(m_tiles * grid_y, a.blocks, NT, num_sms);
   if (NT == 1) return launch_mma_nt<1>(a, grid_y, num_sms, kSmemG4, s);
   if (NT == 2) return launch_mma_nt<2>(a, grid_y, num_sms, kSmemG4 + 4, s);
   return launch_mma_nt<4>(a, grid_y, num_sms, kSmemG4 + 8, s);
@@ -836,18 +889,20 @@ cudaError_t launch_rows(G4Args a, unsigned grid_y, int64_t active_y, int NT, int
 
 cudaError_t launch_matvec_g4(const G4Weights& w, const uint8_t* Xq, float* Y, int64_t M, int64_t K, int64_t N,
                              int num_sms, cudaStream_t s) {
-  G4Args a{w, Xq, Y, nullptr, 0, 1, false, false, true, M, N, static_cast<int>(K / 32), 1, nullptr};
-  if (N <= 2 && g4_dp_smem(N, a.blocks) <= G4_DP_SMEM) {
+  G4Args a{w, Xq, Y, nullptr, 0, 1, false, true, M, N, static_cast<int>(K / 32), 1, nullptr};
+  // One or two rows: the weight stream, where a row's copy leaves three CTAs on an SM (4096 x 4096,
+  // two rows: 4.7 us against 6.0 of the tensor-core form; three rows as a stream took 6.6); two
+  // rows of a matrix that keeps every SM busy go to the tensor cores (28672 x 4096:
+  // 17.4 against 20.3, 57344 x 4096: 32.6 against 35.8, 65536 x 4096: 36.7 against 35.3, 152064 x
+  // 3584: 68.2 against 61.5).
+  if ((N == 1 || (N == 2 && M <= 400 * static_cast<int64_t>(num_sms))) && g4_dp_smem(N, a.blocks) <= G4_DP_SMEM)
     return N == 1 ? launch_stream<1>(a, 0, num_sms, s) : launch_stream<2>(a, 0, num_sms, s);
-  }
-  const int NT = N > 16 ? 4 : N > 8 ? 2 : 1;
-  constexpr int64_t MOST = 65535;   // grid.y
-  for (int64_t n0 = 0; n0 < N; n0 += MOST * NT * 8) {
-    a.rows = std::min(N - n0, MOST * NT * 8);
+  constexpr int64_t MOST = 65535 * 8;   // grid.y
+  for (int64_t n0 = 0; n0 < N; n0 += MOST) {
+    a.rows = std::min(N - n0, MOST);
     a.Xq = Xq + n0 * a.blocks * Q8_1_BYTES;
     a.Y = Y + n0 * M;
-    const int64_t tok = (a.rows + NT * 8 - 1) / (NT * 8);
-    const cudaError_t e = launch_rows(a, static_cast<unsigned>(tok), tok, NT, num_sms, s);
+    const cudaError_t e = launch_rows(a, a.rows, 1, num_sms, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -857,12 +912,19 @@ cudaError_t launch_moe_matvec_g4(const G4Weights& w, int n_experts, const int32_
                                  const uint8_t* Xq, float* Y, int64_t M, int64_t K, int64_t T, int* err, int num_sms,
                                  cudaStream_t s) {
   const int64_t pairs = T * top_k;
-  G4Args a{w, Xq, Y, ids, n_experts, top_k, x_per_slot, pairs <= n_experts, pairs >= 2 * n_experts, M, pairs, static_cast<int>(K / 32), 1, err};
-  if ((T == 1 || pairs <= n_experts / 2) && pairs <= 65535 && g4_dp_smem(1, a.blocks) <= G4_DP_SMEM)
+  G4Args a{w, Xq, Y, ids, n_experts, top_k, x_per_slot, pairs >= n_experts, M, pairs, static_cast<int>(K / 32), 1, err};
+  // Few pairs to an expert: each is a weight stream of its own, although an expert's weights are then read
+  // once per pair (128 experts of 2048 x 768: 64 pairs 19.8 us against 23.1 of the
+  // tensor-core form, 80 pairs 24.5 and 24.6, 128 pairs 37.2 and 30.2; 8 experts of
+  // 4096 x 14336: 12 pairs 60.7 and 63.6, 16 pairs 77.5 and 63.8).
+  const bool few = pairs <= std::max<int64_t>(n_experts / 2, std::min<int64_t>(12, 3 * n_experts / 2));
+  if ((T == 1 || few) && pairs <= 65535 && g4_dp_smem(1, a.blocks) <= G4_DP_SMEM)
     return launch_stream<1>(a, pairs, num_sms, s);
-  const int64_t y = a.by_pair ? pairs : n_experts;
+  // The tensor-core form's CTAs take twice an expert's average rows at once, so that few experts need a
+  // second pass over their weights (128 experts of 2048 x 768, pairs per expert: 4 44.4 us by 8
+  // and 51.1 by 16; 8 62.7 by 8 and 55.9 by 16; 32 127 by 16 and 133 by 32; 64 229 by 16 and 225 by 32).
   const int64_t each = pairs / n_experts;
-  return launch_rows(a, static_cast<unsigned>(y), y, each > 16 ? 4 : each > 4 ? 2 : 1, num_sms, s);
+  return launch_rows(a, each > 32 ? each : 2 * std::min<int64_t>(each, 8), n_experts, num_sms, s);
 }
 
 }  // namespace kq

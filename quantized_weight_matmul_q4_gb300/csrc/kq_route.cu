@@ -14,9 +14,13 @@
 // few experts that it is between get their keys in fp64, one in each lane, and
 // are ordered by those: the chosen experts are those of the 64-bit definition.
 // (All of a row's keys in fp64, chosen one after the other, kept the whole call
-// waiting for such a row: 8192 x 384 in 12 groups took 58 us.) Bound by the latency of one token's chain of decisions, and by issue
-// for many tokens: a lane keeps its two best experts, so that a round costs two
-// warp reductions and a rescan is rare.
+// waiting for such a row: 8192 x 384 in 12 groups took 58 us.)
+//
+// A lane keeps its two best experts, so that a round costs two warp reductions and
+// a rescan is rare. Bound by the latency of one token's chain of decisions (one
+// token of 128 experts, top 8: 2.4 us; 1024 tokens: 3.9) and by issue for many tokens: 8192 x 384 in
+// 12 groups, top 6, sigmoid with bias, bf16 17.5 us, some 1650 instructions per token,
+// 73 % of the slots busy, against 1 us for its 6.7 MB.
 #include <algorithm>
 
 #include <cuda_bf16.h>

@@ -77,6 +77,10 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
 // t, t + blockDim, ... (CH of them). Read once, all loads of a row in flight
 // together; H may be X or R themselves (an element is read and written by the
 // same thread, the read first).
+//
+// Bound by HBM for many rows: 4099 x 4096 bf16 with residual, H and Y 29.1 us, 153 MB,
+// 5.3 TB/s = 0.78 of the measured copy (issue slots 60 % busy, most of it the
+// quantiser). One fp32 row: 2.4 us, a launch, a row's load, the CTA's sum and the quantiser's chain.
 template <typename T, bool VEC, int CH>
 __global__ void __launch_bounds__(CH == 2 ? 512 : 1024) add_rmsnorm_reg_kernel(const T* X, int64_t ldx, const T* R, int64_t ldr,
                                                               const float* __restrict__ gamma, float eps, T* H,
@@ -137,9 +141,9 @@ __global__ void __launch_bounds__(CH == 2 ? 512 : 1024) add_rmsnorm_reg_kernel(c
   }
 }
 
-// The same for rows too long for registers. The row is read twice (the second time from L2): once for the sum of squares
-// and once for the outputs. H may be X or R themselves: an element is read and
-// written by the same thread, the read first.
+// The same for rows too long for registers. The row is read twice (the second time
+// from L2): once for the sum of squares and once for the outputs. H may be X or R
+// themselves: an element is read and written by the same thread, the read first.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(512) add_rmsnorm_kernel(const T* X, int64_t ldx, const T* R, int64_t ldr,
                                                           const float* __restrict__ gamma, float eps, T* H, int64_t ldh,
@@ -199,6 +203,10 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 // carried along (no division per run): a step is `rows` rows and `places` places. (Four
 // runs a thread, a lane of each quad making one block's scale for all: 35.6 us instead
 // of 32.5 for 2048 x 14336 in bf16, and 2.4 instead of 1.5 for eight rows of 768.)
+//
+// Bound by issue: 33 instructions per value (exp, reciprocal, products, rounding
+// to codes), 80 % of the slots busy. 2048 x 14336 bf16 32.3 us, 150 MB, 4.7 TB/s = 0.69 of
+// the measured copy; eight rows of 768 1.5 us, the launch.
 template <typename T>
 constexpr int swiglu_ctas() { return sizeof(T) == 4 ? 5 : 6; }   // per SM: what the registers allow
 template <typename T, bool VEC>

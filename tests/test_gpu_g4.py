@@ -89,6 +89,22 @@ def test_each_code_and_position():
         assert np.array_equal(got.cpu().double().numpy(), want), n
 
 
+# Many weight rows: 32 activation rows to a CTA (which fill the GPU), two rows on the tensor cores;
+# and a split K whose clusters of eight need every second SM.
+@pytest.mark.parametrize("N,M,K,group,zeros,scales", [
+    (33, 45_000, 96, 32, True, "bf16"),
+    (64, 44_001, 160, 64, False, "fp16"),
+    (40, 44_001, 160, 128, True, "fp16"),
+    (70, 30_001, 352, 256, False, "bf16"),
+    (2, 70_001, 96, 32, True, "fp16"),
+    (2, 61_000, 128, 128, False, "bf16"),
+    (5, 2_001, 2048, 128, False, "fp16"),
+    (16, 2_048, 2080, 32, True, "bf16"),
+])
+def test_many_weight_rows(N, M, K, group, zeros, scales):
+    test_matvec_g4(N, M, K, group, zeros, scales)
+
+
 @pytest.mark.parametrize("group", [32, 64, 128, 1 << 20])
 @pytest.mark.parametrize("zeros", [False, True])
 def test_integers_are_exact(group, zeros):
@@ -191,6 +207,12 @@ def test_moe_matvec_g4(T, E, top_k, M, K, group, zeros, scales, per_slot):
     again = kq.kq_moe_matvec_g4(Wd, sd, E, to_dev(ids, torch), to_dev(Xq, torch), M, K, group, zeros=zd)
     assert torch.equal(got, again)
     assert kq.kq_get_device_error() == 0
+
+
+@pytest.mark.parametrize("group,zeros,scales", [(32, True, "bf16"), (64, False, "fp16"), (128, True, "fp16"), (128, False, "bf16")])
+def test_many_rows_per_expert(group, zeros, scales):
+    """Some 40 rows to an expert, 32 at a time."""
+    test_moe_matvec_g4(161, 8, 2, 8_400, 160, group, zeros, scales, False)
 
 
 @pytest.mark.parametrize("T", [1, 30])
