@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(G4_DP_WARPS * 32, G4_DP_CTAS) g4_dp_kernel(G4A
 // Without zero points the sum is Sum (c - 8) q + 1032 Sum_even q + 72 Sum_odd q, an
 // integer below 32 * 1039 * 128 < 2^24; the excess depends on the activation row alone
 // and is taken off by starting the accumulator at its negative. With zero points
-// 1024 + z and 64 + z are subtracted first (packed fp16, exact).
+// 1024 + z and 64 + z are subtracted first (packed fp16, exact), or z Sum q from the sum.
 //
 // k is permuted within a block: lane (g = lane / 4, t = lane % 4) of a warp
 // takes word t (k = 8t..8t+7) of its rows' 16-byte blocks for A and the same k of
@@ -233,9 +233,9 @@ __global__ void __launch_bounds__(G4_DP_WARPS * 32, G4_DP_CTAS) g4_dp_kernel(G4A
 // thread). Launch, first copies and the cluster's sum take 4.5 us of every call (4096 x 512,
 // 8 rows: 4.2). 4096 x 4096, 8 rows: 6.6 us; 14336 x 4096, 16 rows, groups of 32 with zero
 // points: 19.4 us (1.8 TB/s); 128 experts' 2048 x 768, 512 (token, slot) rows, the same
-// groups: 42.4 us (2.9 TB/s). Copying by TMA instead of cp.async was slower (the latter
+// groups: 39.9 us (3.1 TB/s). Copying by TMA instead of cp.async was slower (the latter
 // 46 -> 49.5 us), and so was a CTA that goes on to the next tile of its expert's rows
-// with its copies running ahead (two tiles: the same, four: 57 us).
+// with its copies running ahead (43.2 us with one tile, 43.6 with two, 57.2 with four).
 constexpr int G4_CHUNK = 4;        // 32-element blocks per chunk
 // Chunks of weights in flight per warp: as many as leave room for four CTAs on an SM.
 __host__ __device__ constexpr int g4_stages(bool FINE, bool ZEROS) { return FINE || ZEROS ? 3 : 4; }
@@ -249,8 +249,8 @@ constexpr int G4_LIST = 256;       // rows of one expert collected at a time
 struct alignas(16) G4Frag {    // of one block and 8 activation rows
   uint4 b[32];     // per lane: even k (two registers), odd k (two registers)
   float4 init[4];  // per t: start of the accumulators of rows 2t, 2t + 1, 2t, 2t + 1 (without zero points)
-  float2 d[4];     // per t: scales of rows 2t, 2t + 1
-  float4 pad[3];   // 656 bytes: eight threads that write eight blocks' fragments meet different banks
+  float4 d[4];     // per t: scales of rows 2t, 2t + 1, sums of their codes
+  float4 pad[1];   // 656 bytes: eight threads that write eight blocks' fragments meet different banks
 };
 template <bool FINE, bool ZEROS>
 struct alignas(16) G4Warp {    // a warp's own
@@ -323,6 +323,10 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t v) {
 __device__ __forceinline__ uint32_t add_f16x2(uint32_t a, uint32_t b) { return half2_bits(__hadd2(bits_half2(a), bits_half2(b))); }
 constexpr uint32_t H2_M1152 = 0xe480e480u, H2_960 = 0x63806380u;   // fp16 pairs
 
+// Byte i of v.
+__device__ __forceinline__ float byte_f32(uint32_t v, int i) {
+  return __uint_as_float(__byte_perm(v, 0x4b000000u, 0x7440 + i)) - 8388608.f;
+}
 // -(1024 + byte i of v) as an fp16 pair.
 __device__ __forceinline__ uint32_t zero_f16x2(uint32_t v, int i) { return __byte_perm(v, 0xe4e4e4e4u, 0x4040 + 0x0101 * i); }
 
@@ -338,6 +342,11 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
   constexpr int TOK = NT * 8;
   constexpr int G4_STAGES = g4_stages(FINE, ZEROS);
   constexpr int PANEL = g4_panel(NT) / NT / G4_CHUNK;   // chunks
+  // Zero points times the sum of the activations' codes are taken from the blocks' sums, exactly as well, where
+  // that is cheaper than subtracting them from the codes: with eight rows and a zero point to
+  // a block (128 experts of 2048 x 768, 64 tokens: 39.9 us against 42.6; 16 rows, 14336 x 4096:
+  // 20.4 against 19.4; groups of 128, 8 rows: 13.7 against 13.3).
+  constexpr bool LATE = ZEROS && FINE && NT == 1;
   static_assert(sizeof(sm.frag) >= TOK * G4_ROWS * sizeof(float));   // the sums take the fragments' place
   const int rank = a.splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int64_t m0 = static_cast<int64_t>(blockIdx.x / a.splits) * G4_ROWS;
@@ -370,6 +379,11 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
   for (int b = 0; b < G4_CHUNK; ++b) arow[b] = smem_u32(&my.w[0][lane][(b ^ ((lane >> 1) & 3)) << 4]);
   auto scale_f = [&](uint16_t bits) {
     return a.w.scale_dtype == KQ_F16 ? __half2float(__ushort_as_half(bits)) : __uint_as_float(static_cast<uint32_t>(bits) << 16);
+  };
+
+  // LATE: the zero point; else -(1024 + it) as an fp16 pair.
+  auto zero = [](uint32_t v, int i) {
+    return LATE ? byte_f32(v, i) : ZEROS ? __uint_as_float(zero_f16x2(v, i)) : 0.f;
   };
 
   const uint8_t* wsrc[4];
@@ -568,7 +582,7 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
         for (int j = 0; j < 4; ++j) {
           const uint32_t x0 = px[1 + 2 * j], x1 = px[2 + 2 * j];
           const uint32_t ev = __byte_perm(x0, x1, 0x6240), od = __byte_perm(x0, x1, 0x7351);
-          if (!ZEROS) {
+          if (!ZEROS || LATE) {
             se = __dp4a(static_cast<int>(ev), 0x01010101, se);
             so = __dp4a(static_cast<int>(od), 0x01010101, so);
           }
@@ -578,11 +592,13 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
                                        add_f16x2(__byte_perm(uo, 0x64646464u, 0x4140), H2_M1152),
                                        add_f16x2(__byte_perm(uo, 0x64646464u, 0x4342), H2_M1152));
         }
-        if (!ZEROS) {
+        if (!ZEROS || LATE) {
           float* c = reinterpret_cast<float*>(&f.init[fg >> 1]) + (fg & 1);
-          c[0] = c[2] = static_cast<float>(-(1032 * se + 72 * so));
+          c[0] = c[2] = static_cast<float>(LATE ? -(1024 * se + 64 * so) : -(1032 * se + 72 * so));
         }
-        reinterpret_cast<float*>(&f.d[fg >> 1])[fg & 1] = __low2float(bits_half2(px[0]));
+        float* fd = reinterpret_cast<float*>(&f.d[fg >> 1]) + (fg & 1);
+        fd[0] = __low2float(bits_half2(px[0]));
+        if (LATE) fd[2] = static_cast<float>(se + so);
       };
 
       float acc[2][NT][4] = {};
@@ -631,10 +647,10 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
             sb = make_uint2(__byte_perm(two, 0, 0x1010), __byte_perm(two, 0, 0x3232));
             zb = __byte_perm(zz, 0, 0x1100);
           }
-          my.scale[0][lane] = make_float2(scale_f(sb.x & 0xffff), ZEROS ? __uint_as_float(zero_f16x2(zb, 0)) : 0.f);
-          my.scale[1][lane] = make_float2(scale_f(sb.x >> 16), ZEROS ? __uint_as_float(zero_f16x2(zb, 1)) : 0.f);
-          my.scale[2][lane] = make_float2(scale_f(sb.y & 0xffff), ZEROS ? __uint_as_float(zero_f16x2(zb, 2)) : 0.f);
-          my.scale[3][lane] = make_float2(scale_f(sb.y >> 16), ZEROS ? __uint_as_float(zero_f16x2(zb, 3)) : 0.f);
+          my.scale[0][lane] = make_float2(scale_f(sb.x & 0xffff), zero(zb, 0));
+          my.scale[1][lane] = make_float2(scale_f(sb.x >> 16), zero(zb, 1));
+          my.scale[2][lane] = make_float2(scale_f(sb.y & 0xffff), zero(zb, 2));
+          my.scale[3][lane] = make_float2(scale_f(sb.y >> 16), zero(zb, 3));
           __syncwarp();
         } else {
           const int gr = (c * G4_CHUNK) >> a.w.group_shift;
@@ -643,7 +659,7 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
           for (int i = 0; i < 4; ++i) {
             const uint8_t* r = raw + i * (8 * sizeof(my.raw[0][0]));
             s[i] = scale_f(reinterpret_cast<const uint16_t*>(r)[gr % G4_SPAN]);
-            if (ZEROS) z[i] = zero_f16x2(r[2 * G4_SPAN + gr % G4_SPAN], 0);
+            if (ZEROS) z[i] = __float_as_uint(zero(r[2 * G4_SPAN + gr % G4_SPAN], 0));
           }
         }
         float part[2][NT][4];   // of this chunk, before the chunk's scale (not FINE)
@@ -668,7 +684,7 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
               L[m][h + 2] = codes_f16<0x000f000fu, 0x64006400u>(v8);
               U[m][h] = codes_f16<0x00f000f0u, 0x54005400u>(v);
               U[m][h + 2] = codes_f16<0x00f000f0u, 0x54005400u>(v8);
-              if (ZEROS) {
+              if (ZEROS && !LATE) {
                 const uint32_t zl = z[2 * m + h], zu = add_f16x2(zl, H2_960);
                 L[m][h] = add_f16x2(L[m][h], zl);
                 L[m][h + 2] = add_f16x2(L[m][h + 2], zl);
@@ -681,8 +697,8 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
             const G4Frag& f = pf[b * NT + n];
             const uint4 bf = f.b[lane];
             float4 c0 = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (!ZEROS) c0 = f.init[t];
-            const float2 d = f.d[t];
+            if (!ZEROS || LATE) c0 = f.init[t];
+            const float4 d = f.d[t];
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
               float r[4];
@@ -690,6 +706,7 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
               mma16816(r, U[m], bf.z, bf.w, r[0], r[1], r[2], r[3]);
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
+                if (LATE) r[k] = fmaf(-__uint_as_float(z[2 * m + (k >> 1)]), k & 1 ? d.w : d.z, r[k]);
                 const float v = r[k] * (k & 1 ? d.y : d.x);
                 if (FINE) acc[m][n][k] = fmaf(v, s[2 * m + (k >> 1)], acc[m][n][k]);
                 else part[m][n][k] = b == 0 ? v : fmaf(r[k], k & 1 ? d.y : d.x, part[m][n][k]);
@@ -921,7 +938,7 @@ cudaError_t launch_moe_matvec_g4(const G4Weights& w, int n_experts, const int32_
   if ((T == 1 || few) && pairs <= 65535 && g4_dp_smem(1, a.blocks) <= G4_DP_SMEM)
     return launch_stream<1>(a, pairs, num_sms, s);
   // The tensor-core form's CTAs take twice an expert's average rows at once, so that few experts need a
-  // second pass over their weights (128 experts of 2048 x 768, pairs per expert: 4 44.4 us by 8
+  // second pass over their weights (128 experts of 2048 x 768, pairs per expert: 4 39.8 us by 8
   // and 51.1 by 16; 8 62.7 by 8 and 55.9 by 16; 32 127 by 16 and 133 by 32; 64 229 by 16 and 225 by 32).
   const int64_t each = pairs / n_experts;
   return launch_rows(a, each > 32 ? each : 2 * std::min<int64_t>(each, 8), n_experts, num_sms, s);
