@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(G4_DP_WARPS * 32, G4_DP_CTAS) g4_dp_kernel(G4A
 // whole accumulator would be read back for every 32 k.
 //
 // Bound by issue and the latency of its dependent steps, not by HBM: some 270
-// instructions per warp and chunk (8 rows, groups of 128 and longer) up to 560 (16 rows, groups of 32 with
+// instructions per warp and chunk (8 rows, groups of 128 and longer) up to 620 (16 rows, groups of 32 with
 // zero points) at 46 to 58 % of the issue slots, 16 warps to an SM (128 registers a
 // thread). Launch, first copies and the cluster's sum take 4.5 us of every call (4096 x 512,
 // 8 rows: 4.2). 4096 x 4096, 8 rows: 6.6 us; 14336 x 4096, 16 rows, groups of 32 with zero
