@@ -100,6 +100,8 @@ def test_each_code_and_position():
     (2, 61_000, 128, 128, False, "bf16"),
     (5, 2_001, 2048, 128, False, "fp16"),
     (16, 2_048, 2080, 32, True, "bf16"),
+    (1, 40, 59_072, 64, True, "bf16"),       # an activation row too long for the weight stream
+    (2, 33, 29_600, 128, False, "fp16"),
 ])
 def test_many_weight_rows(N, M, K, group, zeros, scales):
     test_matvec_g4(N, M, K, group, zeros, scales)
@@ -207,6 +209,39 @@ def test_moe_matvec_g4(T, E, top_k, M, K, group, zeros, scales, per_slot):
     again = kq.kq_moe_matvec_g4(Wd, sd, E, to_dev(ids, torch), to_dev(Xq, torch), M, K, group, zeros=zd)
     assert torch.equal(got, again)
     assert kq.kq_get_device_error() == 0
+
+
+@pytest.mark.parametrize("T,E,top_k,M,K,group,zeros,scales,per_slot", [
+    (10, 128, 8, 130, 768, 32, True, "bf16", True),
+    (14, 32, 2, 70, 2048, 128, False, "fp16", False),
+    (13, 40, 3, 129, 416, 64, True, "fp16", False),
+    (1, 6, 4, 40, 59_072, 128, True, "fp16", False),
+    (2, 8, 3, 70, 1056, 32, True, "bf16", True),
+    (6, 8, 2, 257, 768, 128, False, "fp16", False),
+])
+def test_about_one_row_per_expert(T, E, top_k, M, K, group, zeros, scales, per_slot):
+    """Experts without rows beside experts with one or two; rows too long for the weight stream."""
+    test_moe_matvec_g4(T, E, top_k, M, K, group, zeros, scales, per_slot)
+
+
+def test_invalid_ids_where_few_experts_have_rows():
+    import torch
+    T, E, top_k, M, K = 12, 40, 3, 150, 352
+    rng = np.random.default_rng(5)
+    W, s, z = g4_weights(rng, E * M, K, 32, True)
+    Xq = q8_rows(rng, T, K)
+    ids = rng.integers(1, E, (T, top_k)).astype(np.int32)    # expert 0, which writes the zeros, has no rows
+    Wd, sd, sr, zd = _dev_weights(W, s, z, "bf16")
+    ref, B = deo.moe_g4(W, sr, z, 32, E, ids, Xq, M)
+    bad = ids.copy()
+    bad[0, 1], bad[5, 0], bad[11, 2] = -1, E, 2_000_000_000
+    kq.kq_get_device_error()
+    got = kq.kq_moe_matvec_g4(Wd, sd, E, to_dev(bad, torch), to_dev(Xq, torch), M, K, 32, zeros=zd).cpu().numpy()
+    assert kq.kq_get_device_error() == kq.KQ_DEVERR_EXPERT_ID
+    for t, j in ((0, 1), (5, 0), (11, 2)):
+        assert not got[t, j].any()
+        got[t, j] = ref[t, j]
+    assert_g4(got, ref, B, K, "invalid ids")
 
 
 @pytest.mark.parametrize("group,zeros,scales", [(32, True, "bf16"), (64, False, "fp16"), (128, True, "fp16"), (128, False, "bf16")])
