@@ -95,7 +95,8 @@ __global__ void __launch_bounds__(G4_DP_WARPS * 32, G4_DP_CTAS) g4_dp_kernel(G4A
   const int64_t u_codes = static_cast<int64_t>(per) * a.blocks, u_scales = per * a.w.groups;
 
   uint4 wn[U][JU];
-  uint32_t sn[U][JU];   // scale, zero point << 16
+  uint16_t sn[U][JU];
+  uint8_t zn[U][JU];    // apart: nothing here waits for a load
   auto fetch = [&](int64_t row, int step) {
     const uint4* pc = codes + row * a.blocks;
     const int64_t ps = row * a.w.groups;
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(G4_DP_WARPS * 32, G4_DP_CTAS) g4_dp_kernel(G4A
         if (in) {
           wn[u][j] = __ldcs(pc + b + u * u_codes);
           sn[u][j] = __ldg(scales + gr + u * u_scales);
-          if (ZEROS) sn[u][j] |= static_cast<uint32_t>(__ldg(zeros + gr + u * u_scales)) << 16;
+          if (ZEROS) zn[u][j] = __ldg(zeros + gr + u * u_scales);
         }
       }
     }
@@ -145,13 +146,15 @@ __global__ void __launch_bounds__(G4_DP_WARPS * 32, G4_DP_CTAS) g4_dp_kernel(G4A
     float acc[U][NX] = {};
     for (int step = 0; step < steps; ++step) {
       uint4 w[U][JU];
-      uint32_t sc[U][JU];
+      uint16_t sc[U][JU];
+      uint8_t zp[U][JU];
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int j = 0; j < JU; ++j) {
           w[u][j] = wn[u][j];
           sc[u][j] = sn[u][j];
+          zp[u][j] = ZEROS ? zn[u][j] : 8;
         }
       if (step + 1 < steps) {
         fetch(row, step + 1);
@@ -179,8 +182,8 @@ __global__ void __launch_bounds__(G4_DP_WARPS * 32, G4_DP_CTAS) g4_dp_kernel(G4A
             dot2 = dp4a_us((c.z >> 4) & 0x0f0f0f0fu, static_cast<int>(o.z), dot2);
             dot = dp4a_us(c.w & 0x0f0f0f0fu, static_cast<int>(e.w), dot);
             dot2 = dp4a_us((c.w >> 4) & 0x0f0f0f0fu, static_cast<int>(o.w), dot2);
-            const int t = dot + dot2 - (ZEROS ? static_cast<int>(sc[u][j] >> 16) : 8) * sum;
-            acc[u][n] = fmaf(scale_f32(fp16, static_cast<uint16_t>(sc[u][j])) * ds.x, static_cast<float>(t), acc[u][n]);
+            const int t = dot + dot2 - static_cast<int>(zp[u][j]) * sum;
+            acc[u][n] = fmaf(scale_f32(fp16, sc[u][j]) * ds.x, static_cast<float>(t), acc[u][n]);
           }
         }
       }
