@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(G4_DP_WARPS * 32, G4_DP_CTAS) g4_dp_kernel(G4A
 
   uint4 wn[U][JU];
   uint16_t sn[U][JU];
-  uint8_t zn[U][JU];    // apart: nothing here waits for a load
+  uint8_t zn[U][JU] = {};   // apart: nothing here waits for a load
   auto fetch = [&](int64_t row, int step) {
     const uint4* pc = codes + row * a.blocks;
     const int64_t ps = row * a.w.groups;
@@ -818,7 +818,20 @@ cudaError_t launch_stream(const G4Args& a, int64_t pairs, int num_sms, cudaStrea
   if (a.M < per * U) U = 1;
   const int64_t tiles = (a.M + per * U - 1) / (per * U);
   const int64_t ctas = (tiles + G4_DP_WARPS - 1) / G4_DP_WARPS;
-  const int64_t most = std::max<int64_t>(1, static_cast<int64_t>(num_sms) * G4_DP_CTAS / y);
+  // CTAs per pair: as many as run at once, or, where the pairs do not divide those well, as run in
+  // two to four rounds: the first number of rounds that fills nine tenths of its places (384
+  // experts of 2048 x 768, 240 pairs: 70.5 us in one round, 47.9 in two, 44.8 in four; 128
+  // experts of 1536 x 2048, 128 pairs: 47.7 in one, 42.3 in two; 64 pairs, which fit: 22.6
+  // and 25.0).
+  int64_t most = 1;
+  for (int64_t rounds = 1, best_used = 0; rounds <= 4; ++rounds) {
+    const int64_t places = static_cast<int64_t>(num_sms) * G4_DP_CTAS * rounds, each = places / y;
+    const int64_t used = 1000 * each * y / places;
+    if (used <= best_used) continue;
+    best_used = used;
+    most = each;
+    if (used >= 900) break;
+  }
   const unsigned gx = static_cast<unsigned>(std::min(ctas, most)), gy = static_cast<unsigned>(y);
   const int slot = kSmemG4 + 12 + 6 * (NX - 1);
   if (U == 1) return launch_dp<NX, 1>(a, gx, gy, lanes_log2, slot, s);
@@ -933,11 +946,13 @@ cudaError_t launch_moe_matvec_g4(const G4Weights& w, int n_experts, const int32_
                                  cudaStream_t s) {
   const int64_t pairs = T * top_k;
   G4Args a{w, Xq, Y, ids, n_experts, top_k, x_per_slot, pairs >= n_experts, M, pairs, static_cast<int>(K / 32), 1, err};
-  // Few pairs to an expert: each is a weight stream of its own, although an expert's weights are then read
-  // once per pair (128 experts of 2048 x 768: 64 pairs 19.8 us against 23.1 of the
-  // tensor-core form, 80 pairs 24.5 and 24.6, 128 pairs 37.2 and 30.2; 8 experts of
-  // 4096 x 14336: 12 pairs 60.7 and 63.6, 16 pairs 77.5 and 63.8).
-  const bool few = pairs <= std::max<int64_t>(n_experts / 2, std::min<int64_t>(12, 3 * n_experts / 2));
+  // About one pair to an expert: each is a weight stream of its own, although an expert's weights are then read
+  // once per pair (128 experts of 2048 x 768: 64 pairs 15.3 us against 22.1 of the
+  // tensor-core form, 112 pairs 20.8 and 27.4, 128 pairs 26.6 and 28.7; of 1536 x 2048: 64 pairs
+  // 22.5 and 30.6, 96 pairs 34.7 and 35.9, 128 pairs 42.3 and 37.9). The tensor-core form leaves places
+  // empty where the experts are few (4096 x 4096: 8 experts, 8 pairs 16.6 and 21.6, 12 pairs
+  // 21.4 and 21.7, 16 pairs 26.7 and 21.6; 16 experts, 16 pairs 26.9 and 35.6, 24 pairs 36.8 and 35.8).
+  const bool few = pairs <= std::max<int64_t>(7 * n_experts / 8, std::min<int64_t>(24, 3 * n_experts / 2));
   if ((T == 1 || few) && pairs <= 65535 && g4_dp_smem(1, a.blocks) <= G4_DP_SMEM)
     return launch_stream<1>(a, pairs, num_sms, s);
   // The tensor-core form's CTAs take twice an expert's average rows at once, so that few experts need a

@@ -215,6 +215,8 @@ def test_moe_matvec_g4(T, E, top_k, M, K, group, zeros, scales, per_slot):
     (10, 128, 8, 130, 768, 32, True, "bf16", True),
     (14, 32, 2, 70, 2048, 128, False, "fp16", False),
     (13, 40, 3, 129, 416, 64, True, "fp16", False),
+    (15, 128, 8, 130, 768, 32, True, "bf16", True),
+    (30, 256, 8, 40, 768, 64, True, "fp16", True),      # more pairs than a round of CTAs divides by
     (1, 6, 4, 40, 59_072, 128, True, "fp16", False),
     (2, 8, 3, 70, 1056, 32, True, "bf16", True),
     (6, 8, 2, 257, 768, 128, False, "fp16", False),
