@@ -245,9 +245,12 @@ __host__ __device__ constexpr int g4_stages(bool FINE, bool ZEROS) { return FINE
 constexpr int G4_ROWS = 128;       // weight rows of a CTA, 32 per warp
 // Fragments (of one block and 8 activation rows) per panel.
 __host__ __device__ constexpr int g4_panel(int NT) { return NT == 4 ? 32 : 16; }
-constexpr int G4_SPAN = 16;        // groups whose scales are fetched together: a 32-byte sector of a row
+// Groups whose scales are fetched together: a 32-byte sector of a row, or, where a row's scales or
+// zero points begin between two 4-byte words, half of one (the words that hold them).
+constexpr int G4_SPAN = 16;
+constexpr int G4_SPAN_LOG2 = 4;
 constexpr int G4_MAX_SPLITS = 8;
-constexpr int G4_LIST = 256;       // rows of one expert collected at a time
+constexpr int G4_LIST = 192;       // rows of one expert collected at a time (at least 128)
 
 struct alignas(16) G4Frag {    // of one block and 8 activation rows
   uint4 b[32];     // per lane: even k (two registers), odd k (two registers)
@@ -258,7 +261,7 @@ struct alignas(16) G4Frag {    // of one block and 8 activation rows
 template <bool FINE, bool ZEROS>
 struct alignas(16) G4Warp {    // a warp's own
   uint8_t w[g4_stages(FINE, ZEROS)][32][G4_CHUNK * 16];
-  uint8_t raw[2][32][G4_SPAN * (ZEROS ? 3 : 2)];   // as in memory: G4_SPAN scales, then G4_SPAN zero points
+  uint8_t raw[2][32][G4_SPAN * (ZEROS ? 3 : 2)];   // as in memory: scales, from byte 2 * G4_SPAN zero points
   // Of a chunk's blocks (FINE): the scale, and -(1024 + zero point) as an fp16 pair.
   float2 scale[FINE ? G4_CHUNK : 1][FINE ? 32 : 1];
 };
@@ -266,7 +269,8 @@ template <int NT, bool FINE, bool ZEROS>
 struct G4Smem {
   G4Warp<FINE, ZEROS> warp[4];
   G4Frag frag[g4_panel(NT)];
-  uint8_t x[g4_panel(NT) * 8 * Q8_1_BYTES];       // the next panel's activations as in memory, row after row
+  // The next panel's activations as in memory, row after row, from the 16-byte boundary that each begins behind.
+  alignas(16) uint8_t x[g4_panel(NT) * 8 * Q8_1_BYTES + NT * 8 * 16];
   const uint8_t* xrow[NT * 8];                    // activation rows of this pass
   int count, list[G4_LIST];                       // the expert's pairs
 };
@@ -294,6 +298,18 @@ __device__ __forceinline__ void cp_async_row(uint32_t dst, const uint8_t* src, i
   } else {
 #pragma unroll 1
     for (int o = 0; o < bytes; o += 4) cp_async4(dst + o, src + o, 4);
+  }
+}
+// The `bytes` from `src` on, as the WORDS aligned words that hold them (zeros past the end). The bytes
+// before src in its word have to be readable; `any` is an address for copies of nothing.
+template <int WORDS>
+__device__ __forceinline__ void cp_async_words(uint32_t dst, const void* src, int bytes, const void* any) {
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 3);
+  const uint8_t* p = static_cast<const uint8_t*>(src) - off;
+#pragma unroll
+  for (int w = 0; w < WORDS; ++w) {
+    const int n = min(max(bytes + off - 4 * w, 0), 4);
+    cp_async4(dst + 4 * w, n > 0 ? p + 4 * w : any, n);
   }
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -350,6 +366,7 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
   // a block (128 experts of 2048 x 768, 64 tokens: 39.9 us against 42.6; 16 rows, 14336 x 4096:
   // 20.4 against 19.4; groups of 128, 8 rows: 13.7 against 13.3).
   constexpr bool LATE = ZEROS && FINE && NT == 1;
+  static_assert(NT == 4 || sizeof(sm) <= 228 * 1024 / 4 - 1024);   // four CTAs on an SM
   static_assert(sizeof(sm.frag) >= TOK * G4_ROWS * sizeof(float));   // the sums take the fragments' place
   const int rank = a.splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int64_t m0 = static_cast<int64_t>(blockIdx.x / a.splits) * G4_ROWS;
@@ -375,6 +392,11 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
     wsrc0[i] = a.w.codes + (row0 + min(warp * 32 + g + 8 * i, rows - 1)) * row_bytes + t * 16 + static_cast<int64_t>(c_begin) * 64;
   const uint32_t wdst = smem_u32(&my.w[0][g][(t ^ ((g >> 1) & 3)) << 4]);
   const int64_t srow = (row0 + min(tid, rows - 1)) * a.w.groups;
+  // Every row's scales and zero points begin on a 4-byte word; else those of row `lane`, and those of
+  // the rows g + 8 i alike, this many behind one (in the words copied).
+  const bool wide = a.w.groups % 2 == 0 && (!ZEROS || a.w.groups % 4 == 0);
+  const int span_log2 = wide ? G4_SPAN_LOG2 : G4_SPAN_LOG2 - 1;
+  const int off = static_cast<int>(FINE ? srow : (row0 + warp * 32 + g) * a.w.groups) & 3;
   // ldmatrix: lane l gives the address of row l % 8 of matrix l / 8: rows 0-7, 8-15 of
   // the first and then of the second 16-row tile.
   uint32_t arow[G4_CHUNK];   // of each block of a chunk
@@ -406,33 +428,26 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) wsrc[i] += 64;
-    // The scales of the next G4_SPAN groups with the first chunk that needs them; the
-    // span before the last is out of use by then.
+    // The scales of the next span of groups with the first chunk that needs them; the
+    // span before the last is out of use by then (a span is G4_STAGES - 1 chunks at least).
     if (c == span_chunk) {
-      const int span = (c * G4_CHUNK >> a.w.group_shift) / G4_SPAN;
-      span_chunk = static_cast<int>(min((static_cast<int64_t>(span + 1) * G4_SPAN << a.w.group_shift) / G4_CHUNK, static_cast<int64_t>(chunks)));
-      const int n = static_cast<int>(min(a.w.groups - span * G4_SPAN, static_cast<int64_t>(G4_SPAN)));
-      const int64_t at = srow + span * G4_SPAN;
+      const int span = c * G4_CHUNK >> a.w.group_shift >> span_log2;
+      span_chunk = static_cast<int>(min((static_cast<int64_t>(span + 1) << span_log2 << a.w.group_shift) / G4_CHUNK, static_cast<int64_t>(chunks)));
+      const int n = static_cast<int>(min(a.w.groups - (static_cast<int64_t>(span) << span_log2), static_cast<int64_t>(1) << span_log2));
+      const int64_t at = srow + (static_cast<int64_t>(span) << span_log2);
       uint8_t* raw = my.raw[span & 1][lane];
       const uint16_t* ss = static_cast<const uint16_t*>(a.w.scales) + at;
+      if (wide) {
 #pragma unroll 1
-      for (int i = n; i < G4_SPAN; ++i) {   // blocks past K get scale 0
-        reinterpret_cast<uint16_t*>(raw)[i] = 0;
-        if (ZEROS) raw[2 * G4_SPAN + i] = 0;
-      }
-      if (a.w.groups % 2 == 0) {
-        cp_async_row(smem_u32(raw), reinterpret_cast<const uint8_t*>(ss), 2 * n, static_cast<int>(2 * a.w.groups & 31));
-      } else {
-#pragma unroll 1
-        for (int i = 0; i < n; ++i) reinterpret_cast<uint16_t*>(raw)[i] = __ldg(ss + i);
-      }
-      if (ZEROS) {
-        if (a.w.groups % 4 == 0) {
-          cp_async_row(smem_u32(raw) + 2 * G4_SPAN, a.w.zeros + at, n, static_cast<int>(a.w.groups & 31));
-        } else {
-#pragma unroll 1
-          for (int i = 0; i < n; ++i) raw[2 * G4_SPAN + i] = __ldg(a.w.zeros + at + i);
+        for (int i = n; i < G4_SPAN; ++i) {   // blocks past K get scale 0
+          reinterpret_cast<uint16_t*>(raw)[i] = 0;
+          if (ZEROS) raw[2 * G4_SPAN + i] = 0;
         }
+        cp_async_row(smem_u32(raw), reinterpret_cast<const uint8_t*>(ss), 2 * n, static_cast<int>(2 * a.w.groups & 31));
+        if (ZEROS) cp_async_row(smem_u32(raw) + 2 * G4_SPAN, a.w.zeros + at, n, static_cast<int>(a.w.groups & 31));
+      } else {
+        cp_async_words<G4_SPAN / 4 + 1>(smem_u32(raw), ss, 2 * n, a.w.codes);
+        if (ZEROS) cp_async_words<G4_SPAN / 8 + 1>(smem_u32(raw) + 2 * G4_SPAN, a.w.zeros + at, n, a.w.codes);
       }
     }
   };
@@ -538,38 +553,31 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
         }
         sm.xrow[tid] = p;
       }
-      // The activations of the panel at chunk c, in 16-byte pieces where rows are aligned: piece
-      // tid + 128 k is in row `row`, chunk `ch` of the panel.
-      constexpr int PIECES = PANEL * G4_CHUNK * Q8_1_BYTES / 16;   // of a row
-      constexpr int XP = (TOK * PIECES + 127) / 128;
+      // The activations of the panel at chunk c, in 16-byte pieces from the boundary that the row
+      // begins at or behind (`even`: at). Piece tid + 128 k is `xat` bytes behind the panel's first.
+      constexpr int PIECES = PANEL * G4_CHUNK * Q8_1_BYTES / 16;   // of a row, and one more where rows begin between boundaries
+      constexpr int XP = (TOK * (PIECES + 1) + 127) / 128;
+      const int pieces = even ? PIECES : PIECES + 1;
       __syncthreads();   // sm.xrow
       const uint8_t* xsrc[XP];
+      int xat[XP];
 #pragma unroll
       for (int k = 0; k < XP; ++k) {
-        const int i = tid + 128 * k;
-        const uint8_t* p = even && i < TOK * PIECES ? sm.xrow[i / PIECES] : nullptr;
-        xsrc[k] = p ? p + (static_cast<int64_t>(c_begin) * G4_CHUNK * Q8_1_BYTES + i % PIECES * 16) : nullptr;
+        const int i = tid + 128 * k, r = even ? i / PIECES : i / (PIECES + 1);
+        const uint8_t* p = r < TOK ? sm.xrow[r] : nullptr;
+        const int o = (i - r * pieces) * 16 - static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+        xat[k] = p ? o : 1 << 28;
+        xsrc[k] = p ? p + o + static_cast<int64_t>(c_begin) * (G4_CHUNK * Q8_1_BYTES) : a.Xq;
       }
       auto load = [&](int c) {
-        if (even) {
+        const int left = static_cast<int>(min(xbytes - static_cast<int64_t>(c) * (G4_CHUNK * Q8_1_BYTES), static_cast<int64_t>(1) << 24));
 #pragma unroll
-          for (int k = 0; k < XP; ++k) {
-            const int i = tid + 128 * k;
-            if (i >= TOK * PIECES) break;
-            const bool in = xsrc[k] && c + i % PIECES / 9 < chunks;
-            cp_async16(smem_u32(sm.x) + i * 16, in ? xsrc[k] : a.Xq, in ? 16 : 0);
-            if (xsrc[k]) xsrc[k] += PIECES * 16;
-          }
-        } else {
-          constexpr int WORDS = PANEL * G4_CHUNK * Q8_1_BYTES / 4;
-          const int64_t at = static_cast<int64_t>(c) * (G4_CHUNK * Q8_1_BYTES);
-#pragma unroll 1
-          for (int i = tid; i < TOK * WORDS; i += 128) {
-            const uint8_t* p = sm.xrow[i / WORDS];
-            const int64_t o = at + i % WORDS * 4;
-            const bool in = p && o < xbytes;
-            cp_async4(smem_u32(sm.x) + i * 4, in ? p + o : a.Xq, in ? 4 : 0);
-          }
+        for (int k = 0; k < XP; ++k) {
+          const int i = tid + 128 * k;
+          if (i >= TOK * pieces) break;
+          const int n = min(max(left - xat[k], 0), 16);
+          cp_async16(smem_u32(sm.x) + i * 16, n > 0 ? xsrc[k] : a.Xq, n);
+          xsrc[k] += PIECES * 16;
         }
       };
       // A thread makes one (activation row, block) of a panel's fragments, or two.
@@ -577,7 +585,8 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
       auto make = [&](int k) {
         constexpr int PB = PANEL * G4_CHUNK;   // blocks
         const int xn = (tid + 128 * k) / PB, blk = tid % PB;
-        const uint32_t* px = reinterpret_cast<const uint32_t*>(sm.x) + (tid + 128 * k) * 9;
+        const uint32_t* px = reinterpret_cast<const uint32_t*>(sm.x) + blk * (Q8_1_BYTES / 4) + xn * (pieces * 4) +
+                             (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(sm.xrow[xn])) & 15) / 4;
         G4Frag& f = sm.frag[blk * NT + xn / 8];
         const int fg = xn & 7;
         int se = 0, so = 0;
@@ -637,12 +646,19 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
         if (FINE) {
           // Lane: row; the four blocks' scales converted once. A chunk has four groups or two.
           const int gr = c * G4_CHUNK >> a.w.group_shift;
-          const uint8_t* raw = my.raw[(gr / G4_SPAN) & 1][lane];
-          const uint16_t* rs = reinterpret_cast<const uint16_t*>(raw) + gr % G4_SPAN;
-          const uint8_t* rz = raw + 2 * G4_SPAN + gr % G4_SPAN;
+          const uint8_t* raw = my.raw[(gr >> span_log2) & 1][lane];
+          const int at = gr & ((1 << span_log2) - 1);
+          const uint16_t* rs = reinterpret_cast<const uint16_t*>(raw) + at;
+          const uint8_t* rz = raw + 2 * G4_SPAN + at;
           uint2 sb;
           uint32_t zb;
-          if (a.w.group_shift == 0) {
+          if (!wide) {
+            rs += off & 1;
+            rz += off;
+            const int b1 = 1 >> a.w.group_shift, b2 = 2 >> a.w.group_shift, b3 = 3 >> a.w.group_shift;
+            sb = make_uint2(rs[0] | static_cast<uint32_t>(rs[b1]) << 16, rs[b2] | static_cast<uint32_t>(rs[b3]) << 16);
+            zb = ZEROS ? rz[0] | rz[b1] << 8 | rz[b2] << 16 | static_cast<uint32_t>(rz[b3]) << 24 : 0;
+          } else if (a.w.group_shift == 0) {
             sb = *reinterpret_cast<const uint2*>(rs);
             zb = ZEROS ? *reinterpret_cast<const uint32_t*>(rz) : 0;
           } else {
@@ -657,12 +673,14 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
           __syncwarp();
         } else {
           const int gr = (c * G4_CHUNK) >> a.w.group_shift;
-          const uint8_t* raw = my.raw[(gr / G4_SPAN) & 1][g];
+          const int at = gr & ((1 << span_log2) - 1);
+          const uint8_t* raw = my.raw[(gr >> span_log2) & 1][g] + 2 * at + (wide ? 0 : 2 * (off & 1));
+          const int to_zero = 2 * G4_SPAN - at + (wide ? 0 : off - 2 * (off & 1));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint8_t* r = raw + i * (8 * sizeof(my.raw[0][0]));
-            s[i] = scale_f(reinterpret_cast<const uint16_t*>(r)[gr % G4_SPAN]);
-            if (ZEROS) z[i] = __float_as_uint(zero(r[2 * G4_SPAN + gr % G4_SPAN], 0));
+            s[i] = scale_f(*reinterpret_cast<const uint16_t*>(r));
+            if (ZEROS) z[i] = __float_as_uint(zero(r[to_zero], 0));
           }
         }
         float part[2][NT][4];   // of this chunk, before the chunk's scale (not FINE)
