@@ -249,7 +249,7 @@ __host__ __device__ constexpr int g4_panel(int NT) { return NT == 4 ? 32 : 16; }
 // zero points begin between two 4-byte words, half of one (the words that hold them).
 constexpr int G4_SPAN = 16;
 constexpr int G4_SPAN_LOG2 = 4;
-constexpr int G4_MAX_SPLITS = 8;
+constexpr int G4_MAX_SPLITS = 16;
 constexpr int G4_LIST = 192;       // rows of one expert collected at a time (at least 128)
 
 struct alignas(16) G4Frag {    // of one block and 8 activation rows
@@ -778,13 +778,16 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
       for (int i = tid; i < nn << sh; i += 128) {
         const int n = i >> sh, m = (rank << sh) + (i & ((1 << sh) - 1));
         if (m >= rows) continue;
-        float part[G4_MAX_SPLITS];   // all on their way before the first is added
-#pragma unroll
-        for (int r = 0; r < G4_MAX_SPLITS; ++r)
-          part[r] = r < a.splits ? ld_cluster_f32(mapa_shared(red + n * G4_ROWS + m, r)) : 0.f;
         float v = 0.f;
+#pragma unroll 1
+        for (int r0 = 0; r0 < a.splits; r0 += 8) {
+          float part[8];   // all on their way before the first is added
 #pragma unroll
-        for (int r = 0; r < G4_MAX_SPLITS; ++r) v += part[r];
+          for (int r = 0; r < 8; ++r)
+            part[r] = r0 + r < a.splits ? ld_cluster_f32(mapa_shared(red + n * G4_ROWS + m, r0 + r)) : 0.f;
+#pragma unroll
+          for (int r = 0; r < 8; ++r) v += part[r];
+        }
         const int64_t out = a.ids ? sm.list[n0 + n] : static_cast<int64_t>(blockIdx.y) * TOK + n;
         a.Y[out * a.M + m0 + m] = v;
       }
@@ -861,6 +864,8 @@ template <int NT, bool FINE, bool ZEROS>
 cudaError_t launch_mma(const G4Args& a, unsigned grid_y, int num_sms, int slot, cudaStream_t s) {
   void (*k)(G4Args) = g4_mma_kernel<NT, FINE, ZEROS>;
   cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(k), slot);
+  if (e == cudaSuccess && a.splits > 8)
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (a.M + G4_ROWS - 1) / G4_ROWS;
   cudaLaunchConfig_t cfg = {};
@@ -876,7 +881,7 @@ cudaError_t launch_mma(const G4Args& a, unsigned grid_y, int num_sms, int slot, 
     // 228 KB, each CTA's reservation 1 KB.)
     const int64_t ctas = tiles * a.splits * grid_y;
     int64_t share = (ctas * 10 + 9 * num_sms - 1) / (9 * num_sms);
-    if (share == 1 && a.splits == 8 && 4 * ctas > 3 * num_sms) share = 2;
+    if (share == 1 && (a.splits == 16 || (a.splits == 8 && 4 * ctas > 3 * num_sms))) share = 2;
     if (share <= 4) smem = std::max<size_t>(smem, std::min<size_t>(227 * 1024, 228 * 1024 / share - 1024) / 16 * 16);
   }
   cfg.dynamicSmemBytes = smem;
@@ -906,12 +911,16 @@ int64_t g4_places(int NT, int num_sms) { return static_cast<int64_t>(num_sms) * 
 // clusters of four and eight, which need places near one another. (Of 4096 codes a row,
 // without zero points. Eight rows: 4096 x 4096 17.2 us in one part, 10.6 in two, 7.1 in four, 6.4
 // in eight; 9600 x 4096 12.2 in two, 10.2 in four, 13.1 in the eight that no longer run at
-// once; 28672 x 4096 33.6 in one, 21.1 in two, 22.9 in four.) A part keeps two chunks at least.
+// once; 28672 x 4096 33.6 in one, 21.1 in two, 22.9 in four.) Sixteen parts where those CTAs are no
+// more than the SMs (four rows: 512 x 7168 5.8 in eight, 4.7 in sixteen; 1024 x 4096 4.7 and 4.5;
+// 2048 x 4096, 256 CTAs, 5.3 and 8.8). A part keeps two chunks at least.
 int g4_splits(int64_t tiles, int64_t blocks, int NT, int num_sms) {
   const int64_t chunks = (blocks + G4_CHUNK - 1) / G4_CHUNK, places = g4_places(NT, num_sms);
   int splits = 1;
   while (splits < G4_MAX_SPLITS && chunks >= 4 * splits &&
-         (splits == 1 ? tiles * 2 <= places : 20 * tiles * splits <= 9 * places))
+         (splits == 1   ? tiles * 2 <= places
+          : splits == 8 ? tiles * 16 <= num_sms
+                        : 20 * tiles * splits <= 9 * places))
     splits *= 2;
   return splits;
 }
