@@ -233,10 +233,10 @@ __global__ void __launch_bounds__(G4_DP_WARPS * 32, G4_DP_CTAS) g4_dp_kernel(G4A
 // Bound by issue and the latency of its dependent steps, not by HBM: some 270
 // instructions per warp and chunk (8 rows, groups of 128 and longer) up to 620 (16 rows, groups of 32 with
 // zero points) at 46 to 58 % of the issue slots, 16 warps to an SM (128 registers a
-// thread). Launch, first copies and the cluster's sum take 4.5 us of every call (4096 x 512,
-// 8 rows: 4.2). 4096 x 4096, 8 rows: 6.6 us; 14336 x 4096, 16 rows, groups of 32 with zero
-// points: 19.4 us (1.8 TB/s); 128 experts' 2048 x 768, 512 (token, slot) rows, the same
-// groups: 39.9 us (3.1 TB/s). Copying by TMA instead of cp.async was slower (the latter
+// thread). Launch, first copies and the cluster's sum take 4.5 us of every call (4096 x 1024,
+// 8 rows: 4.4). 4096 x 4096, 8 rows: 6.6 us; 14336 x 4096, 16 rows, groups of 32 with zero
+// points: 20.0 us (1.8 TB/s); 128 experts' 2048 x 768, 512 (token, slot) rows, the same
+// groups: 40.5 us (3.0 TB/s). Copying by TMA instead of cp.async was slower (the latter
 // 46 -> 49.5 us), and so was a CTA that goes on to the next tile of its expert's rows
 // with its copies running ahead (43.2 us with one tile, 43.6 with two, 57.2 with four).
 constexpr int G4_CHUNK = 4;        // 32-element blocks per chunk
@@ -582,11 +582,16 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
       };
       // A thread makes one (activation row, block) of a panel's fragments, or two.
       constexpr int MINE = g4_panel(NT) * 8 / 128;
+      int xbyte[MINE];   // its first byte in sm.x
+#pragma unroll
+      for (int k = 0; k < MINE; ++k) {
+        const int xn = (tid + 128 * k) / (PANEL * G4_CHUNK), blk = tid % (PANEL * G4_CHUNK);
+        xbyte[k] = xn * (pieces * 16) + blk * Q8_1_BYTES + static_cast<int>(reinterpret_cast<uintptr_t>(sm.xrow[xn]) & 15);
+      }
       auto make = [&](int k) {
         constexpr int PB = PANEL * G4_CHUNK;   // blocks
         const int xn = (tid + 128 * k) / PB, blk = tid % PB;
-        const uint32_t* px = reinterpret_cast<const uint32_t*>(sm.x) + blk * (Q8_1_BYTES / 4) + xn * (pieces * 4) +
-                             (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(sm.xrow[xn])) & 15) / 4;
+        const uint32_t* px = reinterpret_cast<const uint32_t*>(sm.x + xbyte[k]);
         G4Frag& f = sm.frag[blk * NT + xn / 8];
         const int fg = xn & 7;
         int se = 0, so = 0;
