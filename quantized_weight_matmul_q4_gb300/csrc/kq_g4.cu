@@ -30,6 +30,7 @@ struct G4Args {
   int64_t rows;         // activation rows, or (token, slot) pairs
   int blocks;           // 32-element blocks per row
   int splits;           // CTAs of a cluster, over K
+  int parts;            // clusters that share an expert's rows
   int* err;
 };
 
@@ -272,7 +273,8 @@ struct G4Smem {
   // The next panel's activations as in memory, row after row, from the 16-byte boundary that each begins behind.
   alignas(16) uint8_t x[g4_panel(NT) * 8 * Q8_1_BYTES + NT * 8 * 16];
   const uint8_t* xrow[NT * 8];                    // activation rows of this pass
-  int count, list[G4_LIST];                       // the expert's pairs
+  unsigned counts[4];                             // of a warp's pairs
+  int list[G4_LIST];                              // the expert's pairs
 };
 // cp.async and ldmatrix take 16-byte rows at 16-byte boundaries.
 static_assert(sizeof(G4Warp<true, true>) % 16 == 0 && sizeof(G4Warp<false, false>) % 16 == 0 && sizeof(G4Frag) == 656 && G4_SPAN % 16 == 0);
@@ -374,7 +376,8 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!a.eager) asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int expert = a.ids ? static_cast<int>(blockIdx.y) : 0;
+  const int part = a.ids ? static_cast<int>(blockIdx.y) % a.parts : 0;
+  const int expert = a.ids ? static_cast<int>(blockIdx.y) / a.parts : 0;
   int64_t scan = 0;     // next pair to look at
   const int64_t row0 = static_cast<int64_t>(expert) * a.M + m0;
   const int64_t row_bytes = static_cast<int64_t>(a.blocks) * 16;
@@ -469,7 +472,7 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
     asm volatile("griddepcontrol.wait;" ::: "memory");
   }
   // Invalid ids belong to no expert: expert 0's CTAs write their zeros.
-  if (a.ids && expert == 0 && rank == 0) {
+  if (a.ids && blockIdx.y == 0 && rank == 0) {
     for (int64_t p = tid; p < a.rows; p += 128) {
       const int e = a.ids[p];
       if (e < 0 || e >= a.n_experts) {
@@ -482,56 +485,42 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
   for (;;) {
     int have;
     if (a.ids) {
-      // Collect this expert's pairs (in any order: each output depends on its own pair alone).
-      __syncthreads();
-      if (tid == 0) sm.count = 0;
-      __syncthreads();
-      // 512 pairs at a time; where so many are this expert's that the list would overflow,
-      // 128 at a time.
-      bool more = scan < a.rows;
+      // Collect this expert's pairs in their order, which all CTAs of the expert share: 512 at a time;
+      // where so many are this expert's that the list would overflow, 128 at a time.
       have = 0;
-      while (more) {
-        unsigned mine = 0;
+      while (scan < a.rows) {
+        unsigned mine[4], counts = 0;   // a byte for each 128
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int64_t p = scan + tid + 128 * k;
-          if (p < a.rows && a.ids[p] == expert) mine |= 1u << k;
+          mine[k] = __ballot_sync(FULL_MASK, p < a.rows && a.ids[p] == expert);
+          counts |= static_cast<unsigned>(__popc(mine[k])) << (8 * k);
         }
-        int at = mine ? atomicAdd(&sm.count, __popc(mine)) : 0;
+        __syncthreads();   // the last counts, or the last pass, are done with
+        if (lane == 0) sm.counts[warp] = counts;
+        __syncthreads();
+        unsigned before = 0, all = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if ((mine >> k & 1) && at < G4_LIST) sm.list[at++] = static_cast<int>(scan + tid + 128 * k);
-        __syncthreads();
-        const int now = *reinterpret_cast<volatile int*>(&sm.count);
-        __syncthreads();
-        if (now <= G4_LIST) {
-          have = now;
-          scan += 512;
-          more = scan < a.rows;
-          continue;
+        for (int w = 0; w < 4; ++w) {
+          if (w < warp) before += sm.counts[w];
+          all += sm.counts[w];
         }
-        if (have > 0) break;   // those are enough for now: these again next time
-        if (tid == 0) sm.count = 0;
-        __syncthreads();
-        const int64_t p = scan + tid;
-        if (p < a.rows && a.ids[p] == expert) sm.list[atomicAdd(&sm.count, 1)] = static_cast<int>(p);
-        __syncthreads();
-        have = *reinterpret_cast<volatile int*>(&sm.count);
-        scan += 128;
-        more = scan < a.rows && have == 0;
-        __syncthreads();
+        const int found = static_cast<int>((all & 255) + (all >> 8 & 255) + (all >> 16 & 255) + (all >> 24));
+        const bool fits = have + found <= G4_LIST;
+        if (!fits && have > 0) break;   // those are enough for now: these again next time
+        int at = have;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k > 0 && !fits) break;
+          if (mine[k] >> lane & 1)
+            sm.list[at + (before >> (8 * k) & 255) + __popc(mine[k] & ((1u << lane) - 1))] = static_cast<int>(scan + tid + 128 * k);
+          at += static_cast<int>(all >> (8 * k) & 255);
+        }
+        have = at;
+        scan += fits ? 512 : 128;
+        if (!fits && have > 0) break;
       }
-      if (a.splits > 1) {
-        // The clusters' CTAs use the list of rank 0: theirs may be in another order.
-        cluster_sync();
-        if (rank != 0)
-          for (int i = tid; i < have; i += 128) {
-            int v;
-            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(&sm.list[i], 0)) : "memory");
-            sm.list[i] = v;
-          }
-        cluster_sync();
-      }
+      __syncthreads();
       if (have == 0) {
         cp_async_wait<0>();
         return;
@@ -539,7 +528,7 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
     } else {
       have = static_cast<int>(min(a.rows - static_cast<int64_t>(blockIdx.y) * TOK, static_cast<int64_t>(TOK)));
     }
-    for (int n0 = 0; n0 < have; n0 += TOK) {
+    for (int n0 = part * TOK; n0 < have; n0 += a.parts * TOK) {
       const int nn = min(TOK, have - n0);
       if (tid < TOK) {
         const uint8_t* p = nullptr;
@@ -764,7 +753,7 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
             for (int i = 0; i < 4; ++i)
               if (m + 8 * i < a.M) y[8 * i] = acc[i >> 1][n][2 * (i & 1) + k];
           }
-        if (n0 + TOK < have) __syncthreads();   // before the next rows' fragments
+        if (n0 + a.parts * TOK < have) __syncthreads();   // before the next rows' fragments
         continue;
       }
       cp_async_wait<0>();
@@ -798,7 +787,10 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
       }
       cluster_sync();   // the others have read this CTA's sums
     }
-    if (!a.ids || scan >= a.rows) return;
+    if (!a.ids || scan >= a.rows) {
+      cp_async_wait<0>();   // of a part without rows
+      return;
+    }
   }
 }
 
@@ -936,15 +928,25 @@ cudaError_t launch_rows(G4Args a, int64_t rows, int64_t products, int num_sms, c
   // by 16 and 33.8 by 32; 64 rows 51.8 by 16 and 44.6 by 32; 256 rows 152 by 16 and 142
   // by 32). The 32 cost where they leave places empty (8192 x 4096, 128 rows: 52.0 by 16, 71.7
   // by 32 on 256 of 456 places; 14336 x 4096, 96 rows, 336 of 456: 72 by either).
+  // Experts' CTAs take twice the average at once, so that few experts need a second pass over their
+  // weights (128 experts of 2048 x 768, pairs per expert: 4 39.8 us by 8 and 51.1 by 16; 8 62.7 by
+  // 8 and 55.9 by 16; 32 127 by 16 and 133 by 32; 64 229 by 16 and 225 by 32).
   const int64_t m_tiles = (a.M + G4_ROWS - 1) / G4_ROWS;
-  int NT = rows > 8 ? 2 : 1;
+  int NT = rows > (a.ids ? 4 : 8) ? 2 : 1;
   if (rows > 32) {
     const int64_t tiles = m_tiles * ((rows + 31) / 32) * products, places = g4_places(4, num_sms);
     const int64_t ctas = tiles * g4_splits(tiles, a.blocks, 4, num_sms);
     if (4 * ctas >= 3 * ((ctas + places - 1) / places * places)) NT = 4;
   }
-  const unsigned grid_y = static_cast<unsigned>(a.ids ? products : (rows + NT * 8 - 1) / (NT * 8));
-  a.splits = g4_splits(m_tiles * grid_y, a.blocks, NT, num_sms);
+  int64_t y = a.ids ? products : (rows + NT * 8 - 1) / (NT * 8);
+  a.splits = g4_splits(m_tiles * y, a.blocks, NT, num_sms);
+  if (a.ids) {
+    // An expert's passes side by side where there are places (11 experts of 218 x 800, 41 rows each: 9.4 us against 23.2).
+    const int64_t passes = (2 * rows + NT * 8 - 1) / (NT * 8);
+    a.parts = static_cast<int>(std::max<int64_t>(1, std::min(passes, g4_places(NT, num_sms) * 9 / 10 / (m_tiles * y * a.splits))));
+    y *= a.parts;
+  }
+  const unsigned grid_y = static_cast<unsigned>(y);
   if (NT == 1) return launch_mma_nt<1>(a, grid_y, num_sms, kSmemG4, s);
   if (NT == 2) return launch_mma_nt<2>(a, grid_y, num_sms, kSmemG4 + 4, s);
   return launch_mma_nt<4>(a, grid_y, num_sms, kSmemG4 + 8, s);
@@ -954,7 +956,7 @@ cudaError_t launch_rows(G4Args a, int64_t rows, int64_t products, int num_sms, c
 
 cudaError_t launch_matvec_g4(const G4Weights& w, const uint8_t* Xq, float* Y, int64_t M, int64_t K, int64_t N,
                              int num_sms, cudaStream_t s) {
-  G4Args a{w, Xq, Y, nullptr, 0, 1, false, true, M, N, static_cast<int>(K / 32), 1, nullptr};
+  G4Args a{w, Xq, Y, nullptr, 0, 1, false, true, M, N, static_cast<int>(K / 32), 1, 1, nullptr};
   // One or two rows: the weight stream, where a row's copy leaves three CTAs on an SM (4096 x 4096,
   // two rows: 4.7 us against 6.0 of the tensor-core form; three rows as a stream took 6.6); two
   // rows of a matrix that keeps every SM busy go to the tensor cores (28672 x 4096:
@@ -977,7 +979,7 @@ cudaError_t launch_moe_matvec_g4(const G4Weights& w, int n_experts, const int32_
                                  const uint8_t* Xq, float* Y, int64_t M, int64_t K, int64_t T, int* err, int num_sms,
                                  cudaStream_t s) {
   const int64_t pairs = T * top_k;
-  G4Args a{w, Xq, Y, ids, n_experts, top_k, x_per_slot, pairs >= n_experts, M, pairs, static_cast<int>(K / 32), 1, err};
+  G4Args a{w, Xq, Y, ids, n_experts, top_k, x_per_slot, pairs >= n_experts, M, pairs, static_cast<int>(K / 32), 1, 1, err};
   // About one pair to an expert: each is a weight stream of its own, although an expert's weights are then read
   // once per pair (128 experts of 2048 x 768: 64 pairs 15.3 us against 22.1 of the
   // tensor-core form, 112 pairs 20.8 and 27.4, 128 pairs 26.6 and 28.7; of 1536 x 2048: 64 pairs
@@ -987,11 +989,7 @@ cudaError_t launch_moe_matvec_g4(const G4Weights& w, int n_experts, const int32_
   const bool few = pairs <= std::max<int64_t>(7 * n_experts / 8, std::min<int64_t>(24, 3 * n_experts / 2));
   if ((T == 1 || few) && pairs <= 65535 && g4_dp_smem(1, a.blocks) <= G4_DP_SMEM)
     return launch_stream<1>(a, pairs, num_sms, s);
-  // The tensor-core form's CTAs take twice an expert's average rows at once, so that few experts need a
-  // second pass over their weights (128 experts of 2048 x 768, pairs per expert: 4 39.8 us by 8
-  // and 51.1 by 16; 8 62.7 by 8 and 55.9 by 16; 32 127 by 16 and 133 by 32; 64 229 by 16 and 225 by 32).
-  const int64_t each = pairs / n_experts;
-  return launch_rows(a, each > 32 ? each : 2 * std::min<int64_t>(each, 8), n_experts, num_sms, s);
+  return launch_rows(a, pairs / n_experts, n_experts, num_sms, s);
 }
 
 }  // namespace kq
