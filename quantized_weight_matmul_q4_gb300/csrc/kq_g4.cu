@@ -50,7 +50,7 @@ __device__ __forceinline__ float scale_f32(bool fp16, uint16_t bits) {
 // operations to unpack, 8 dp4a and about 8 for the scales. Unpacking costs less with
 // dp4a than in the tensor-core form below, and without tiles no row is idle.
 //
-// Bound by HBM for large matrices (152064 x 3584: 45.3 us, 281 MB, 6.2 TB/s = 0.91 of the
+// Bound by HBM for large matrices (152064 x 3584: 45.5 us, 281 MB, 6.2 TB/s = 0.91 of the
 // measured copy; issue slots 67 % busy) and by the launch and the first loads' latency for
 // small ones (4096 x 4096: 3.3 us, launch included;
 // eight experts' 1536 x 2048: 5.5 us, 2.4 TB/s).
@@ -235,9 +235,9 @@ __global__ void __launch_bounds__(G4_DP_WARPS * 32, G4_DP_CTAS) g4_dp_kernel(G4A
 // instructions per warp and chunk (8 rows, groups of 128 and longer) up to 620 (16 rows, groups of 32 with
 // zero points) at 46 to 58 % of the issue slots, 16 warps to an SM (128 registers a
 // thread). Launch, first copies and the cluster's sum take 4.5 us of every call (4096 x 1024,
-// 8 rows: 4.4). 4096 x 4096, 8 rows: 6.6 us; 14336 x 4096, 16 rows, groups of 32 with zero
+// 8 rows: 4.4). 4096 x 4096, 8 rows: 6.4 us; 14336 x 4096, 16 rows, groups of 32 with zero
 // points: 20.0 us (1.8 TB/s); 128 experts' 2048 x 768, 512 (token, slot) rows, the same
-// groups: 40.5 us (3.0 TB/s). Copying by TMA instead of cp.async was slower (the latter
+// groups: 40.7 us (3.0 TB/s). Copying by TMA instead of cp.async was slower (the latter
 // 46 -> 49.5 us), and so was a CTA that goes on to the next tile of its expert's rows
 // with its copies running ahead (43.2 us with one tile, 43.6 with two, 57.2 with four).
 constexpr int G4_CHUNK = 4;        // 32-element blocks per chunk
