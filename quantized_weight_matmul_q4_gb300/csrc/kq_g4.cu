@@ -389,10 +389,6 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
   // This lane copies 16-byte piece t of its warp's rows g + 8 i, and fetches the
   // scales of its row `lane` (a row past the tile's last is that row again; its
   // sums are not written).
-  const uint8_t* wsrc0[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    wsrc0[i] = a.w.codes + (row0 + min(warp * 32 + g + 8 * i, rows - 1)) * row_bytes + t * 16 + static_cast<int64_t>(c_begin) * 64;
   const uint32_t wdst = smem_u32(&my.w[0][g][(t ^ ((g >> 1) & 3)) << 4]);
   const int64_t srow = (row0 + min(tid, rows - 1)) * a.w.groups;
   // Every row's scales and zero points begin on a 4-byte word; else those of row `lane`, and those of
@@ -456,7 +452,8 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
   };
   auto begin = [&] {   // of a pass over K: the first copies
 #pragma unroll
-    for (int i = 0; i < 4; ++i) wsrc[i] = wsrc0[i];
+    for (int i = 0; i < 4; ++i)
+      wsrc[i] = a.w.codes + (row0 + min(warp * 32 + g + 8 * i, rows - 1)) * row_bytes + t * 16 + static_cast<int64_t>(c_begin) * 64;
     span_chunk = c_begin;
 #pragma unroll 1
     for (int i = 0; i < G4_STAGES - 1; ++i) {
@@ -941,7 +938,8 @@ cudaError_t launch_rows(G4Args a, int64_t rows, int64_t products, int num_sms, c
   int64_t y = a.ids ? products : (rows + NT * 8 - 1) / (NT * 8);
   a.splits = g4_splits(m_tiles * y, a.blocks, NT, num_sms);
   if (a.ids) {
-    // An expert's passes side by side where there are places (11 experts of 218 x 800, 41 rows each: 9.4 us against 23.2).
+    // An expert's passes side by side where there are places (11 experts of 218 x 800, 41 rows
+    // each: 9.4 us against 23.2).
     const int64_t passes = (2 * rows + NT * 8 - 1) / (NT * 8);
     a.parts = static_cast<int>(std::max<int64_t>(1, std::min(passes, g4_places(NT, num_sms) * 9 / 10 / (m_tiles * y * a.splits))));
     y *= a.parts;

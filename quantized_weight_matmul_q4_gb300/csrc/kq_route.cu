@@ -248,8 +248,9 @@ __global__ void __launch_bounds__(RT_WARPS * 32, 8) route_kernel(const __grid_co
   // key. An e^-x <= 1 is off by 2^-22 + 0.37 * 1.5 * 2^-24. A softmax score is off by that,
   // by the sum's own error (2^-22 and, as the scores' mean x is at most ln 512, 9.4 * 2^-24;
   // E / 32 + 5 roundings of 2^-24) and by three roundings: under 2^-18 of the largest
-  // score, which is 1 / Sum (without a bias the scores are compared as e^-x: 2^-21). A sigmoid s is off by s (1 - s) times its exponential's error
-  // and by two roundings of 2^-23: under 2^-21 of 1. Adding the bias rounds by 2^-24 of the key.
+  // score, which is 1 / Sum (without a bias the scores are compared as e^-x: 2^-21). A sigmoid
+  // s is off by s (1 - s) times its exponential's error and by two roundings of 2^-23: under
+  // 2^-21 of 1. Adding the bias rounds by 2^-24 of the key.
   const bool near = by_score && a.bias;   // else the experts go by the exact logits
   const float tol = 2.f * (softmax && a.bias ? inv * 3.8147e-6f : 4.7684e-7f);
 
