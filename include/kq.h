@@ -364,7 +364,9 @@ KQ_API kq_status kq_moe_route(int dtype, const void* logits, int64_t ld, const f
  * rows in the call (the sums are grouped differently).
  * As in kq_matvec, W, scales and zeros are streamed before the call waits for the
  * previous kernel on the stream: they must not be written by a still-running
- * predecessor that allows programmatic dependent launch.
+ * predecessor that allows programmatic dependent launch, and none of Xq (or expert
+ * ids) that such a predecessor writes may lie in the same 32-byte sector as their
+ * ends (separate allocations never do).
  */
 KQ_API kq_status kq_matvec_g4(const void* W, const void* scales, int scale_dtype, const void* zeros, int64_t group,
                               const void* Xq, float* Y, int64_t M, int64_t K, int64_t N, kq_stream_t stream);
