@@ -333,9 +333,12 @@ KQ_API kq_status kq_swiglu_q8_1(int dtype, const void* gate, int64_t ldg, const 
  * softmax sum. A logit of +inf counts as the largest finite fp32. A token with
  * fewer available experts than slots gets the lowest-numbered experts not yet
  * chosen for the others, with weight 0 (ids are always valid and distinct).
+ * Each weight is within 120 * 2^-24 of its exact value, relative: a renormalised one for
+ * logits within 60 of the token's largest chosen logit (however far those lie below the
+ * largest of all, or below zero), another for logits within 60 of the token's largest
+ * and weights of at least 2^-126. A score that is 0 in 64 bits (a softmax logit some
+ * 745 below the largest, a sigmoid logit below -709.8) has weight 0.
  * logits: dtype [T][n_experts], rows ld apart; bias: fp32 [n_experts] or NULL;
- * Each weight is within 120 * 2^-24 of its exact value, relative (for logits within
- * 60 of the token's largest).
  * ids: int32 [T][top_k], probs: fp32 [T][top_k], written. 1 <= n_experts <= 512,
  * n_experts % n_groups == 0, 1 <= topk_groups <= n_groups,
  * 1 <= top_k <= topk_groups * n_experts / n_groups.

@@ -200,6 +200,39 @@ __device__ __noinline__ double exact_key(const RouteArgs& a, const T* row, int e
   return s + (a.bias ? static_cast<double>(a.bias[e]) : 0.);
 }
 
+// The renormalised weights of a token whose chosen scores are all tiny. Weights are ratios, and only
+// the chosen experts' distances from `top`, the largest chosen logit, count: a softmax score is taken
+// as e^(l - top) (its factor e^(top - mx) / Sum cancels), a sigmoid score as e^(l - top) / (1 + e^l)
+// (top < 0). The largest of them is at least a half, however far the chosen experts lie below mx or
+// below zero. A score that is zero in the 64-bit definition has weight zero.
+template <typename T>
+__device__ __noinline__ void weights_of_tiny_scores(const RouteArgs& a, int64_t t, const int* ids) {
+  const int lane = threadIdx.x & 31;
+  const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+  float* probs = a.probs + t * a.top_k;
+  const bool softmax = a.score == KQ_SCORE_SOFTMAX;
+  float mx = -INFINITY, top = -INFINITY;
+  for (int e = lane; e < a.E; e += 32) mx = fmaxf(mx, logit(row, e));
+  mx = warp_max(mx);
+  for (int j = lane; j < a.top_k; j += 32)
+    if (ids[j] >= 0) top = fmaxf(top, logit(row, ids[j]));
+  top = warp_max(top);
+  float tot = 0.f;
+  for (int j = lane; j < a.top_k; j += 32) {
+    float w = 0.f;
+    if (ids[j] >= 0) {
+      const float v = logit(row, ids[j]);
+      if (softmax ? v - mx >= -745.14f : v >= -709.79f)   // else e^(v - mx) is 0 in fp64, e^-v infinite
+        w = softmax ? expf(v - top) : __fdiv_rn(expf(v - top), 1.0f + expf(v));
+    }
+    tot += w;
+    probs[j] = w;
+  }
+  tot = warp_sum_f(tot);
+  const float f = tot > 0.f ? __fdiv_rn(1.0f, tot) : 0.f;
+  for (int j = lane; j < a.top_k; j += 32) probs[j] = probs[j] * f * a.scale;   // this lane's own
+}
+
 // PER: experts per lane (E <= 32 * PER).
 template <typename T, int PER>
 __global__ void __launch_bounds__(RT_WARPS * 32, 8) route_kernel(const __grid_constant__ RouteArgs a, int warp_bytes) {
@@ -484,10 +517,16 @@ __global__ void __launch_bounds__(RT_WARPS * 32, 8) route_kernel(const __grid_co
   }
   if (a.renorm) {
     tot = warp_sum_f(tot);
-    const float f = tot > 0.f ? __fdiv_rn(1.0f, tot) : 0.f;
-    for (int j = lane; j < a.top_k; j += 32) {
-      if (a.top_k > 32) w = a.probs[t * a.top_k + j];   // this lane's own
-      a.probs[t * a.top_k + j] = w * f * a.scale;
+    // The largest of 512 scores that sum to 2^-30 is at least 2^-39, and a score e^-60 = 2^-87 of
+    // that still a normal number.
+    if (tot >= 0x1p-30f) {
+      const float f = __fdiv_rn(1.0f, tot);
+      for (int j = lane; j < a.top_k; j += 32) {
+        if (a.top_k > 32) w = a.probs[t * a.top_k + j];   // this lane's own
+        a.probs[t * a.top_k + j] = w * f * a.scale;
+      }
+    } else {
+      weights_of_tiny_scores<T>(a, t, ids);
     }
   }
   const bool empty = ids[a.top_k - 1] < 0;
