@@ -305,6 +305,9 @@ __global__ void __launch_bounds__(RT_WARPS * 32, 8) route_kernel(const __grid_co
     int sl = 0;
     while (sl < 5 && (a.n_groups << (sl + 1)) <= 32) ++sl;
     const int step = 1 << sl, sub = lane & (step - 1);
+    // Scores of two keys are held halved: their sum can pass fp32's range (keys next to its end by
+    // their bias).
+    const float half = a.group_top == 2 ? 0.5f : 1.f;
     float mag = 0.f;   // of the keys in the scores
     for (int g0 = 0; g0 < a.n_groups; g0 += 32 >> sl) {
       const int g = g0 + (lane >> sl);
@@ -325,8 +328,8 @@ __global__ void __launch_bounds__(RT_WARPS * 32, 8) route_kernel(const __grid_co
       }
       if (g < a.n_groups && sub == 0) {
         const bool two = a.group_top == 2 && m2 != -INFINITY;
-        gf[g] = two ? m1 + m2 : m1;
-        const float x = fabsf(m1) + (two ? fabsf(m2) : 0.f);
+        gf[g] = two ? half * m1 + half * m2 : half * m1;
+        const float x = half * fabsf(m1) + (two ? half * fabsf(m2) : 0.f);
         if (x < INFINITY) mag = fmaxf(mag, x);
       }
     }
@@ -349,7 +352,7 @@ __global__ void __launch_bounds__(RT_WARPS * 32, 8) route_kernel(const __grid_co
     cut_out = warp_max(cut_out);
     if (cut_out != -INFINITY && by_score) {
       // A group's score is the sum of two keys: twice a key's error, and a rounding.
-      const float gtol = 2.f * tol + 4.7684e-7f * warp_max(mag);
+      const float gtol = 2.f * half * tol + 4.7684e-7f * warp_max(mag);
       cut_in = warp_min(cut_in);
       if (cut_in - cut_out <= gtol) {
         // The groups that could be on either side, and of their experts those that could
@@ -366,9 +369,9 @@ __global__ void __launch_bounds__(RT_WARPS * 32, 8) route_kernel(const __grid_co
             const int e = lane + 32 * i;
             if (e < a.E && static_cast<int>((e * a.recip) >> 20) == g) m = fmaxf(m, key[i]);
           }
-          // With group_top 2 the least key that counts is the score less the largest key.
+          // With group_top 2 the least key that counts is the score (2 v) less the largest key.
           const float top = warp_max(m);
-          const float low = (a.group_top == 2 ? fminf(v - top, top) : top) - gtol;
+          const float low = a.group_top == 2 ? fminf(v + (v - top), top) - 2.f * gtol : top - gtol;
 #pragma unroll
           for (int i = 0; i < PER; ++i) {
             const int e = lane + 32 * i;
