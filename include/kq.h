@@ -296,7 +296,9 @@ KQ_API kq_status kq_moe_combine(const float* Y, const float* probs, float* out, 
  * fp32 [K]; Xq: N * (K/32) * 36 bytes, written. R, H and Y may be NULL. H may be
  * X or R itself (the same pointer and ld); outputs overlap nothing else.
  * K % 32 == 0, eps >= 0.
- * y is within 64 * 2^-24 of its exact value, relative.
+ * y is within 64 * 2^-24 of its exact value, relative, or within fp32's least value, for
+ * every row of finite h (its squares may pass fp32's range or fall below it; a row of
+ * zeros with eps = 0 gives NaN).
  * A block of y with an infinity or a NaN gets an infinite or NaN scale d_h (the
  * block stands for non-finite values); so does one whose maximum is above
  * 127 * 65504.

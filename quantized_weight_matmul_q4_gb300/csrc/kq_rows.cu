@@ -73,6 +73,41 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
   return v;
 }
 
+// Largest v over the CTA (part: one float per warp); a NaN counts for nothing.
+__device__ __forceinline__ float block_max(float v, float* part) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.f;
+  for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) v = fmaxf(v, part[i]);
+  return v;
+}
+
+// 1 / sqrt(Sum h^2 / K + eps) and whether it may be taken from the fp32 sum: no square and no sum has
+// passed the range, and what fell below it (2^-150 a square at most) is far below the mean.
+__device__ __forceinline__ bool rms_scale(float ss, int K, float eps, float& rr) {
+  const float m = __fdiv_rn(ss, static_cast<float>(K)) + eps;
+  rr = __fdiv_rn(1.0f, sqrtf(m));
+  return ss < INFINITY && m >= 0x1p-100f;
+}
+
+// Where it may not, h is taken times s = s1 * s2, a power of two (two factors: it can be beyond
+// 2^127) that brings the larger of max |h| and sqrt(eps) to 2^40 (subnormal ones to 2^18 at least):
+// then the sum of 2^31 squares stays below 2^128, and a product below 2^-126 is under 2^-166 of the
+// largest and gives a y below fp32's least. The result, 1 / sqrt(Sum (s h)^2 / K + s^2 eps), is the
+// factor of s h.
+struct Pow2 {
+  float s1, s2;
+  __device__ __forceinline__ Pow2(float hmax, float eps) {
+    const int e = 40 + 127 - static_cast<int>(__float_as_uint(fmaxf(hmax, sqrtf(eps))) >> 23), e1 = e >> 1;
+    s1 = __uint_as_float(static_cast<uint32_t>(127 + e1) << 23);
+    s2 = __uint_as_float(static_cast<uint32_t>(127 + e - e1) << 23);
+  }
+  __device__ __forceinline__ float operator()(float h) const { return h * s1 * s2; }
+  __device__ __forceinline__ float square(float eps) const { return eps * s1 * s1 * s2 * s2; }
+};
+
 // One row per CTA, held in registers: thread t has the row's runs of eight values
 // t, t + blockDim, ... (CH of them). Read once, all loads of a row in flight
 // together; H may be X or R themselves (an element is read and written by the
@@ -86,7 +121,7 @@ __global__ void __launch_bounds__(CH == 2 ? 512 : 1024) add_rmsnorm_reg_kernel(c
                                                               const float* __restrict__ gamma, float eps, T* H,
                                                               int64_t ldh, T* Y, int64_t ldy, uint8_t* __restrict__ Xq,
                                                               int K) {
-  __shared__ float part[32];
+  __shared__ float part[32], far_max[32], far_sum[32];
   pdl_enter();
   const int64_t n = blockIdx.x;
   const T* x = X + n * ldx;
@@ -121,7 +156,24 @@ __global__ void __launch_bounds__(CH == 2 ? 512 : 1024) add_rmsnorm_reg_kernel(c
     for (int k = 0; k < 8; ++k) ss = fmaf(v[c][k], v[c][k], ss);
   }
   ss = block_sum(ss, part);
-  const float rr = __fdiv_rn(1.0f, sqrtf(__fdiv_rn(ss, static_cast<float>(K)) + eps));
+  float rr;
+  if (!rms_scale(ss, K, eps, rr)) {   // the same for all threads
+    float m = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(v[c][k]));
+    const Pow2 scaled(block_max(m, far_max), eps);
+    ss = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[c][k] = scaled(v[c][k]);
+        ss = fmaf(v[c][k], v[c][k], ss);
+      }
+    rms_scale(block_sum(ss, far_sum), K, scaled.square(eps), rr);
+  }
   uint8_t* xq = Xq + n * (K >> 5) * Q8_1_BYTES;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -148,7 +200,7 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(512) add_rmsnorm_kernel(const T* X, int64_t ldx, const T* R, int64_t ldr,
                                                           const float* __restrict__ gamma, float eps, T* H, int64_t ldh,
                                                           T* Y, int64_t ldy, uint8_t* __restrict__ Xq, int K) {
-  __shared__ float part[16];
+  __shared__ float part[16], far_max[16], far_sum[16];
   pdl_enter();
   const int64_t n = blockIdx.x;
   const T* x = X + n * ldx;
@@ -166,8 +218,32 @@ __global__ void __launch_bounds__(512) add_rmsnorm_kernel(const T* X, int64_t ld
 #pragma unroll
     for (int k = 0; k < 8; ++k) ss = fmaf(v[k], v[k], ss);
   }
-  ss = block_sum(ss, part);
-  const float rr = __fdiv_rn(1.0f, sqrtf(__fdiv_rn(ss, static_cast<float>(K)) + eps));
+  float rr;
+  const bool far = !rms_scale(block_sum(ss, part), K, eps, rr);   // the same for all threads
+  Pow2 scaled(0x1p40f, 0.f);   // by 1
+  if (far) {
+    // Two passes: the largest, then the sum.
+    float m = 0.f;
+    for (int pass = 0; pass < 2; ++pass) {
+      ss = 0.f;
+      for (int i = threadIdx.x; i < runs; i += blockDim.x) {
+        float v[8], w[8];
+        load8<T, VEC>(x + 8 * i, v);
+        if (r) {
+          load8<T, VEC>(r + 8 * i, w);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] += w[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          m = fmaxf(m, fabsf(v[k]));
+          ss = fmaf(scaled(v[k]), scaled(v[k]), ss);
+        }
+      }
+      if (pass == 0) scaled = Pow2(block_max(m, far_max), eps);
+    }
+    rms_scale(block_sum(ss, far_sum), K, scaled.square(eps), rr);
+  }
   uint8_t* xq = Xq + n * (K >> 5) * Q8_1_BYTES;
   for (int i0 = 0; i0 < runs; i0 += blockDim.x) {
     const int i = i0 + threadIdx.x;
@@ -182,6 +258,10 @@ __global__ void __launch_bounds__(512) add_rmsnorm_kernel(const T* X, int64_t ld
       }
       if (H) store8<T, VEC>(H + n * ldh + 8 * i, v);
       load8<float, true>(gamma + 8 * i, w);
+      if (far) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = scaled(v[k]);
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = v[k] * rr * w[k];
       if (Y) store8<T, VEC>(Y + n * ldy + 8 * i, v);
