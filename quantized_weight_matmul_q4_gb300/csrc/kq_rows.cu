@@ -73,6 +73,17 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
   return v;
 }
 
+// A sum of many terms in fp32 with the part that its additions round away (by Knuth's two-sum).
+struct LongSum {
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float v) {
+    const float t = __fadd_rn(hi, v), b = __fsub_rn(t, hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(v, b)));
+    hi = t;
+  }
+  __device__ __forceinline__ float value() const { return hi < INFINITY ? hi + lo : hi; }
+};
+
 // Largest v over the CTA (part: one float per warp); a NaN counts for nothing.
 __device__ __forceinline__ float block_max(float v, float* part) {
 #pragma unroll
@@ -194,7 +205,9 @@ __global__ void __launch_bounds__(CH == 2 ? 512 : 1024) add_rmsnorm_reg_kernel(c
 }
 
 // The same for rows too long for registers. The row is read twice (the second time
-// from L2): once for the sum of squares and once for the outputs. H may be X or R
+// from L2): once for the sum of squares and once for the outputs. A thread has K / 512
+// squares: the runs' sums are added with what each addition rounds away, as one fp32 sum of
+// them all would be off by as many roundings. H may be X or R
 // themselves: an element is read and written by the same thread, the read first.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(512) add_rmsnorm_kernel(const T* X, int64_t ldx, const T* R, int64_t ldr,
@@ -206,9 +219,9 @@ __global__ void __launch_bounds__(512) add_rmsnorm_kernel(const T* X, int64_t ld
   const T* x = X + n * ldx;
   const T* r = R ? R + n * ldr : nullptr;
   const int runs = K >> 3;
-  float ss = 0.f;
+  LongSum ss;
   for (int i = threadIdx.x; i < runs; i += blockDim.x) {
-    float v[8], w[8];
+    float v[8], w[8], s8 = 0.f;
     load8<T, VEC>(x + 8 * i, v);
     if (r) {
       load8<T, VEC>(r + 8 * i, w);
@@ -216,18 +229,19 @@ __global__ void __launch_bounds__(512) add_rmsnorm_kernel(const T* X, int64_t ld
       for (int k = 0; k < 8; ++k) v[k] += w[k];
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) ss = fmaf(v[k], v[k], ss);
+    for (int k = 0; k < 8; ++k) s8 = fmaf(v[k], v[k], s8);
+    ss.add(s8);
   }
   float rr;
-  const bool far = !rms_scale(block_sum(ss, part), K, eps, rr);   // the same for all threads
+  const bool far = !rms_scale(block_sum(ss.value(), part), K, eps, rr);   // the same for all threads
   Pow2 scaled(0x1p40f, 0.f);   // by 1
   if (far) {
     // Two passes: the largest, then the sum.
     float m = 0.f;
     for (int pass = 0; pass < 2; ++pass) {
-      ss = 0.f;
+      ss = LongSum();
       for (int i = threadIdx.x; i < runs; i += blockDim.x) {
-        float v[8], w[8];
+        float v[8], w[8], s8 = 0.f;
         load8<T, VEC>(x + 8 * i, v);
         if (r) {
           load8<T, VEC>(r + 8 * i, w);
@@ -237,12 +251,13 @@ __global__ void __launch_bounds__(512) add_rmsnorm_kernel(const T* X, int64_t ld
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           m = fmaxf(m, fabsf(v[k]));
-          ss = fmaf(scaled(v[k]), scaled(v[k]), ss);
+          s8 = fmaf(scaled(v[k]), scaled(v[k]), s8);
         }
+        ss.add(s8);
       }
       if (pass == 0) scaled = Pow2(block_max(m, far_max), eps);
     }
-    rms_scale(block_sum(ss, far_sum), K, scaled.square(eps), rr);
+    rms_scale(block_sum(ss.value(), far_sum), K, scaled.square(eps), rr);
   }
   uint8_t* xq = Xq + n * (K >> 5) * Q8_1_BYTES;
   for (int i0 = 0; i0 < runs; i0 += blockDim.x) {
