@@ -5,7 +5,8 @@
 //   out[t][m] = Sum_{j < top_k} probs[t][j] * Y[t][j][m]
 //
 // in fp32 with one fused multiply-add per slot in slot order, so the result
-// does not depend on scheduling. Memory-bound: every Y element is read once.
+// does not depend on scheduling. Memory-bound: every Y element is read once, by ordinary
+// loads (the previous kernel may write it after this one began).
 #include <algorithm>
 
 #include "kq_internal.h"
@@ -15,7 +16,7 @@ namespace kq {
 
 // Four consecutive outputs of one token per thread (M % 4 == 0: the rows of Y
 // and out are then 16-byte aligned), grid-strided.
-__global__ void __launch_bounds__(256) moe_combine4_kernel(const float* __restrict__ Y, const float* __restrict__ P,
+__global__ void __launch_bounds__(256) moe_combine4_kernel(const float* Y, const float* P,
                                                            float* __restrict__ out, int64_t M, int64_t T, int top_k) {
   pdl_enter();
   const int64_t m4 = M >> 2;
@@ -27,8 +28,8 @@ __global__ void __launch_bounds__(256) moe_combine4_kernel(const float* __restri
     const float* p = P + t * top_k;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int j = 0; j < top_k; ++j) {
-      const float pj = __ldg(p + j);
-      const float4 v = __ldg(reinterpret_cast<const float4*>(y + j * M));
+      const float pj = p[j];
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(y + j * M));
       acc.x = fmaf(pj, v.x, acc.x);
       acc.y = fmaf(pj, v.y, acc.y);
       acc.z = fmaf(pj, v.z, acc.z);
@@ -39,7 +40,7 @@ __global__ void __launch_bounds__(256) moe_combine4_kernel(const float* __restri
 }
 
 // Any M: one output per thread.
-__global__ void __launch_bounds__(256) moe_combine1_kernel(const float* __restrict__ Y, const float* __restrict__ P,
+__global__ void __launch_bounds__(256) moe_combine1_kernel(const float* Y, const float* P,
                                                            float* __restrict__ out, int64_t M, int64_t T, int top_k) {
   pdl_enter();
   const int64_t total = T * M;
@@ -49,7 +50,7 @@ __global__ void __launch_bounds__(256) moe_combine1_kernel(const float* __restri
     const float* y = Y + t * top_k * M + m;
     const float* p = P + t * top_k;
     float acc = 0.f;
-    for (int j = 0; j < top_k; ++j) acc = fmaf(__ldg(p + j), __ldg(y + j * M), acc);
+    for (int j = 0; j < top_k; ++j) acc = fmaf(p[j], y[j * M], acc);
     out[i] = acc;
   }
 }

@@ -122,7 +122,8 @@ __global__ void __launch_bounds__(G4_DP_WARPS * 32, G4_DP_CTAS) g4_dp_kernel(G4A
   if (first < tiles) fetch(row, 0);
 
   if (!a.ids) asm volatile("griddepcontrol.wait;" ::: "memory");
-  // A thread unpacks a block.
+  // A thread unpacks a block. (Ordinary loads: the previous kernel may have written it after this one
+  // began, which the read-only path does not allow.)
   const int64_t xrow = a.ids ? (a.x_per_slot ? blockIdx.y : blockIdx.y / a.top_k) : 0;
   for (int i = tid; i < NX * a.blocks; i += blockDim.x) {
     const uint32_t* xb = reinterpret_cast<const uint32_t*>(a.Xq + (xrow * a.blocks + i) * Q8_1_BYTES);
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(G4_DP_WARPS * 32, G4_DP_CTAS) g4_dp_kernel(G4A
     int s = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const uint32_t x0 = __ldg(xb + 1 + 2 * k), x1 = __ldg(xb + 2 + 2 * k);
+      const uint32_t x0 = xb[1 + 2 * k], x1 = xb[2 + 2 * k];
       e[k] = __byte_perm(x0, x1, 0x6420);
       o[k] = __byte_perm(x0, x1, 0x7531);
       s = __dp4a(static_cast<int>(x0), 0x01010101, s);
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(G4_DP_WARPS * 32, G4_DP_CTAS) g4_dp_kernel(G4A
     }
     xe[i] = make_uint4(e[0], e[1], e[2], e[3]);
     xo[i] = make_uint4(o[0], o[1], o[2], o[3]);
-    xs[i] = make_float2(__low2float(bits_half2(__ldg(xb))), __int_as_float(s));
+    xs[i] = make_float2(__low2float(bits_half2(xb[0])), __int_as_float(s));
   }
   __syncthreads();
 

@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(RT_WARPS * 32, 8) route_kernel(const __grid_co
   if (by_score) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const float b = a.bias && lane + 32 * i < a.E ? __ldg(a.bias + lane + 32 * i) : 0.f;
+      const float b = a.bias && lane + 32 * i < a.E ? a.bias[lane + 32 * i] : 0.f;
       const float k = (softmax ? fast_exp(key[i] - mx) * kinv : fast_rcp(1.0f + fast_exp(-key[i]))) + b;
       key[i] = key[i] == -INFINITY ? -INFINITY : fmaxf(k, -INFINITY);   // a NaN is -inf
     }

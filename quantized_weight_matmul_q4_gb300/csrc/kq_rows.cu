@@ -1,7 +1,8 @@
 // Row producers with a Q8_1 output: the residual addition with RMSNorm, and
 // SwiGLU. Each reads its rows once, computes in fp32 and quantises the produced
 // fp32 values, so that the activations of the next weight product go to memory
-// as 36 bytes per 32 values.
+// as 36 bytes per 32 values. Inputs are read by ordinary loads: the previous kernel may have
+// written them after this one began, which the read-only path does not allow.
 //
 //   add + RMSNorm:  h = x + r,  y = (h * 1 / sqrt(Sum h^2 / K + eps)) * gamma
 //   SwiGLU:         v = gate / (1 + exp(-gate)) * up
@@ -129,7 +130,7 @@ struct Pow2 {
 // quantiser). One fp32 row: 2.4 us, a launch, a row's load, the CTA's sum and the quantiser's chain.
 template <typename T, bool VEC, int CH>
 __global__ void __launch_bounds__(CH == 2 ? 512 : 1024) add_rmsnorm_reg_kernel(const T* X, int64_t ldx, const T* R, int64_t ldr,
-                                                              const float* __restrict__ gamma, float eps, T* H,
+                                                              const float* gamma, float eps, T* H,
                                                               int64_t ldh, T* Y, int64_t ldy, uint8_t* __restrict__ Xq,
                                                               int K) {
   __shared__ float part[32], far_max[32], far_sum[32];
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(CH == 2 ? 512 : 1024) add_rmsnorm_reg_kernel(c
 // themselves: an element is read and written by the same thread, the read first.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(512) add_rmsnorm_kernel(const T* X, int64_t ldx, const T* R, int64_t ldr,
-                                                          const float* __restrict__ gamma, float eps, T* H, int64_t ldh,
+                                                          const float* gamma, float eps, T* H, int64_t ldh,
                                                           T* Y, int64_t ldy, uint8_t* __restrict__ Xq, int K) {
   __shared__ float part[16], far_max[16], far_sum[16];
   pdl_enter();
@@ -271,8 +272,8 @@ __global__ void __launch_bounds__(512) add_rmsnorm_kernel(const T* X, int64_t ld
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] += w[k];
       }
+      load8<float, true>(gamma + 8 * i, w);   // before the stores, behind which it would wait
       if (H) store8<T, VEC>(H + n * ldh + 8 * i, v);
-      load8<float, true>(gamma + 8 * i, w);
       if (far) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = scaled(v[k]);
@@ -305,7 +306,7 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 template <typename T>
 constexpr int swiglu_ctas() { return sizeof(T) == 4 ? 5 : 6; }   // per SM: what the registers allow
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256, swiglu_ctas<T>()) swiglu_kernel(const T* __restrict__ G, int64_t ldg, const T* __restrict__ U,
+__global__ void __launch_bounds__(256, swiglu_ctas<T>()) swiglu_kernel(const T* G, int64_t ldg, const T* U,
                                                      int64_t ldu, uint8_t* __restrict__ Xq, int runs, int64_t total,
                                                      int64_t rows, int places) {
   pdl_enter();
