@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(OUT_DIR, "libkq.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["kq_api.cu", "kq_quant.cu", "kq_matvec.cu", "kq_gemm.cu", "kq_gemm_noalloc.cu", "kq_combine.cu", "kq_tq4.cu",
-           "kq_rows.cu", "kq_route.cu", "kq_g4.cu"]
+           "kq_decode_api.cu", "kq_rows.cu", "kq_route.cu", "kq_g4.cu"]
 # A measurement aid outside libkq (the tensor-core MMA issue rate), in a library of its own.
 PROBE_SOURCES = ["probe_mma.cu"]
 PROBE_LIB_PATH = os.path.join(OUT_DIR, "libkqprobe.so")

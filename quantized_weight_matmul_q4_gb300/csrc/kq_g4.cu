@@ -9,8 +9,9 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
-#include "kq_internal.h"
+#include "kq_decode.h"
 #include "kq_types.cuh"
 
 namespace kq {
@@ -792,6 +793,23 @@ __global__ void __launch_bounds__(128, NT == 4 ? 3 : 4) g4_mma_kernel(G4Args a) 
   }
 }
 
+// Raises a kernel's dynamic shared-memory limit to the maximum and lets it have clusters of sixteen,
+// once per device: later calls only read a flag. 24 slots: 12 of the tensor-core form, 12 of the
+// weight stream.
+constexpr int G4_SLOTS = 24, G4_DEVICES = 64;
+std::atomic<uint8_t> g_ready[G4_SLOTS][G4_DEVICES];
+cudaError_t prepare(const void* kernel, int slot) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (slot < 0 || slot >= G4_SLOTS || dev < 0 || dev >= G4_DEVICES) return cudaErrorInvalidValue;
+  if (g_ready[slot][dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (e == cudaSuccess && slot < 12) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) g_ready[slot][dev].store(1, std::memory_order_release);
+  return e;
+}
+
 constexpr size_t G4_DP_SMEM = 72 * 1024;   // the activation row that g4_dp_kernel may hold (three CTAs per SM)
 size_t g4_dp_smem(int64_t NX, int64_t blocks) { return static_cast<size_t>(NX * blocks) * 40; }
 
@@ -800,7 +818,7 @@ cudaError_t launch_dp(const G4Args& a, unsigned grid_x, unsigned grid_y, int lan
   auto k = a.w.zeros ? g4_dp_kernel<NX, U, true> : g4_dp_kernel<NX, U, false>;
   const size_t smem = g4_dp_smem(NX, a.blocks);
   if (smem > 48 * 1024) {
-    const cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(k), slot + (a.w.zeros ? 1 : 0));
+    const cudaError_t e = prepare(reinterpret_cast<const void*>(k), slot + (a.w.zeros ? 1 : 0));
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(k, dim3(grid_x, grid_y), dim3(G4_DP_WARPS * 32), smem, s, a, lanes_log2);
@@ -849,7 +867,7 @@ cudaError_t launch_stream(const G4Args& a, int64_t pairs, int num_sms, cudaStrea
     if (used >= 900) break;
   }
   const unsigned gx = static_cast<unsigned>(std::min(ctas, most)), gy = static_cast<unsigned>(y);
-  const int slot = kSmemG4 + 12 + 6 * (NX - 1);
+  const int slot = 12 + 6 * (NX - 1);
   if (U == 1) return launch_dp<NX, 1>(a, gx, gy, lanes_log2, slot, s);
   if (U == 2) return launch_dp<NX, 2>(a, gx, gy, lanes_log2, slot + 2, s);
   return launch_dp<NX, 4>(a, gx, gy, lanes_log2, slot + 4, s);
@@ -858,9 +876,7 @@ cudaError_t launch_stream(const G4Args& a, int64_t pairs, int num_sms, cudaStrea
 template <int NT, bool FINE, bool ZEROS>
 cudaError_t launch_mma(const G4Args& a, unsigned grid_y, int num_sms, int slot, cudaStream_t s) {
   void (*k)(G4Args) = g4_mma_kernel<NT, FINE, ZEROS>;
-  cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(k), slot);
-  if (e == cudaSuccess && a.splits > 8)
-    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  const cudaError_t e = prepare(reinterpret_cast<const void*>(k), slot);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (a.M + G4_ROWS - 1) / G4_ROWS;
   cudaLaunchConfig_t cfg = {};
@@ -946,9 +962,9 @@ cudaError_t launch_rows(G4Args a, int64_t rows, int64_t products, int num_sms, c
     y *= a.parts;
   }
   const unsigned grid_y = static_cast<unsigned>(y);
-  if (NT == 1) return launch_mma_nt<1>(a, grid_y, num_sms, kSmemG4, s);
-  if (NT == 2) return launch_mma_nt<2>(a, grid_y, num_sms, kSmemG4 + 4, s);
-  return launch_mma_nt<4>(a, grid_y, num_sms, kSmemG4 + 8, s);
+  if (NT == 1) return launch_mma_nt<1>(a, grid_y, num_sms, 0, s);
+  if (NT == 2) return launch_mma_nt<2>(a, grid_y, num_sms, 4, s);
+  return launch_mma_nt<4>(a, grid_y, num_sms, 8, s);
 }
 
 }  // namespace

@@ -25,7 +25,7 @@
 
 #include <cuda_bf16.h>
 
-#include "kq_internal.h"
+#include "kq_decode.h"
 #include "kq_types.cuh"
 
 namespace kq {

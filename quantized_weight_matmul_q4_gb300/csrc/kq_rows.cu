@@ -10,7 +10,7 @@
 
 #include <algorithm>
 
-#include "kq_internal.h"
+#include "kq_decode.h"
 #include "kq_quant.cuh"
 #include "kq_types.cuh"
 
