@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
         tmem_ld_32x32b_x32(tmem_base + acc * a.acc_cols + (static_cast<uint32_t>(32 * wq) << 16) + c0, r);
         tmem_ld_wait();
         if (MOE) {
-          const int my_slot = (c0 + lane < T.ncols) ? __ldg(a.entries + T.nbase + c0 + lane) : 0;
+          const int my_slot = (c0 + lane < T.ncols) ? a.entries[T.nbase + c0 + lane] : 0;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             const int slot = __shfl_sync(0xffffffffu, my_slot, j);
@@ -744,15 +744,16 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
 }
 
 // Fixed-order sum of the split-K partials: Y[i] = Sum_s P[s][i] (n elements).
-__global__ void __launch_bounds__(256) splitk_reduce_kernel(const float* __restrict__ P, float* __restrict__ Y,
+__global__ void __launch_bounds__(256) splitk_reduce_kernel(const float* P, float* __restrict__ Y,
                                                             int64_t n, int splits) {
   pdl_enter();
   const int64_t i4 = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
   if (i4 >= n) return;
   if (i4 + 4 <= n && (n & 3) == 0) {
-    float4 acc = __ldg(reinterpret_cast<const float4*>(P + i4));
+    // From L2 (through L1, 4096 x 4096 for 512 tokens: 33.4 us instead of 33.0).
+    float4 acc = __ldcg(reinterpret_cast<const float4*>(P + i4));
     for (int s = 1; s < splits; ++s) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(P + static_cast<int64_t>(s) * n + i4));
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(P + static_cast<int64_t>(s) * n + i4));
       acc.x += v.x;
       acc.y += v.y;
       acc.z += v.z;
@@ -761,8 +762,8 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(const float* __restr
     *reinterpret_cast<float4*>(Y + i4) = acc;
   } else {
     for (int64_t i = i4; i < n && i < i4 + 4; ++i) {
-      float acc = __ldg(P + i);
-      for (int s = 1; s < splits; ++s) acc += __ldg(P + static_cast<int64_t>(s) * n + i);
+      float acc = P[i];
+      for (int s = 1; s < splits; ++s) acc += P[static_cast<int64_t>(s) * n + i];
       Y[i] = acc;
     }
   }
@@ -807,7 +808,7 @@ __device__ __forceinline__ int block_excl_scan_1024(int v, int* wsum, int* total
 
 constexpr int ROUTE_IDS_PER_THREAD = 16;  // ids held in registers between the two passes
 
-__global__ void __launch_bounds__(1024) moe_route_kernel(const int* __restrict__ ids, int n, int top_k, int E,
+__global__ void __launch_bounds__(1024) moe_route_kernel(const int* ids, int n, int top_k, int E,
                                                          int m_tiles, int bn, int* counts, int* offsets,
                                                          int* tile_start, int* tile_queue, int* slot_pos, float* Y,
                                                          int M, int* err) {
@@ -817,19 +818,23 @@ __global__ void __launch_bounds__(1024) moe_route_kernel(const int* __restrict__
   pdl_enter();
   for (int i = threadIdx.x; i < E; i += 1024) cnt[i] = 0;
   __syncthreads();
-  // pass 1: histogram (ids beyond 16 per thread are re-read in pass 2)
+  // pass 1: histogram, the first ids last: they stay in registers for pass 2
+  constexpr int RUN = 1024 * ROUTE_IDS_PER_THREAD;
   int e_reg[ROUTE_IDS_PER_THREAD];
+  auto load = [&](int i0) {
 #pragma unroll
-  for (int j = 0; j < ROUTE_IDS_PER_THREAD; ++j) {
-    const int i = threadIdx.x + 1024 * j;
-    e_reg[j] = (i < n) ? __ldg(ids + i) : -1;
-  }
-  for (int i0 = 0; i0 < n; i0 += 1024 * ROUTE_IDS_PER_THREAD) {
+    for (int j = 0; j < ROUTE_IDS_PER_THREAD; ++j) {
+      const int i = i0 + threadIdx.x + 1024 * j;
+      e_reg[j] = (i < n) ? ids[i] : -1;
+    }
+  };
+  for (int i0 = (n - 1) / RUN * RUN; i0 >= 0; i0 -= RUN) {
+    load(i0);
 #pragma unroll
     for (int j = 0; j < ROUTE_IDS_PER_THREAD; ++j) {
       const int i = i0 + threadIdx.x + 1024 * j;
       if (i >= n) continue;
-      const int e = (i0 == 0) ? e_reg[j] : __ldg(ids + i);
+      const int e = e_reg[j];
       if (e < 0 || e >= E)
         report_error(err, ERR_EXPERT_ID);
       else
@@ -855,12 +860,13 @@ __global__ void __launch_bounds__(1024) moe_route_kernel(const int* __restrict__
   }
   __syncthreads();
   // pass 2: bucket positions (-1 for an invalid id, whose output row is zeroed)
-  for (int i0 = 0; i0 < n; i0 += 1024 * ROUTE_IDS_PER_THREAD) {
+  for (int i0 = 0; i0 < n; i0 += RUN) {
+    if (i0 > 0) load(i0);
 #pragma unroll
     for (int j = 0; j < ROUTE_IDS_PER_THREAD; ++j) {
       const int i = i0 + threadIdx.x + 1024 * j;
       if (i >= n) continue;
-      const int e = (i0 == 0) ? e_reg[j] : __ldg(ids + i);
+      const int e = e_reg[j];
       if (e < 0 || e >= E) {
         slot_pos[i] = -1;
         for (int m = 0; m < M; ++m) Y[static_cast<int64_t>(i) * M + m] = 0.f;

@@ -89,11 +89,11 @@ __device__ __forceinline__ float silu_f(float g) { return g / (1.0f + expf(-g));
 
 // Activations k .. k+3 (k a multiple of 4).
 template <int PROD>
-__device__ __forceinline__ float4 produce4(const float* __restrict__ x, const float* __restrict__ aux, int k,
+__device__ __forceinline__ float4 produce4(const float* x, const float* aux, int k,
                                            float inv_rms) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(x + k));
+  const float4 a = *reinterpret_cast<const float4*>(x + k);
   if (PROD == PROD_X) return a;
-  const float4 b = __ldg(reinterpret_cast<const float4*>(aux + k));
+  const float4 b = *reinterpret_cast<const float4*>(aux + k);
   if (PROD == PROD_SWIGLU)
     return make_float4(silu_f(a.x) * b.x, silu_f(a.y) * b.y, silu_f(a.z) * b.z, silu_f(a.w) * b.w);
   return make_float4(a.x * inv_rms * b.x, a.y * inv_rms * b.y, a.z * inv_rms * b.z, a.w * inv_rms * b.w);
@@ -103,10 +103,10 @@ __device__ __forceinline__ float4 produce4(const float* __restrict__ x, const fl
 // consumer threads of the CTA (named barrier 1) in a fixed order: each thread
 // sums its quads, warps reduce by shuffles, then every thread adds the warp sums
 // in warp order. red: nthreads / 32 floats of shared memory.
-__device__ __forceinline__ float rms_inv(const float* __restrict__ x, int K, float eps, float* red, int nthreads) {
+__device__ __forceinline__ float rms_inv(const float* x, int K, float eps, float* red, int nthreads) {
   float ss = 0.f;
   for (int q = threadIdx.x; q < (K >> 2); q += nthreads) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(x) + q);
+    const float4 v = reinterpret_cast<const float4*>(x)[q];
     ss = fmaf(v.x, v.x, ss);
     ss = fmaf(v.y, v.y, ss);
     ss = fmaf(v.z, v.z, ss);
@@ -1196,7 +1196,7 @@ cudaError_t launch_matvec(int wtype, const void* W, const float* x, const float*
 // {d8, d8 * Sum q} [n_tok][xs_tok]; the arithmetic of the one-token kernel's own
 // quantiser (quantize_oct), so the codes are the same. Task t quantises eight
 // values of token t / (K / 8); a warp's 32 tasks share one token.
-__global__ void __launch_bounds__(256) quantize_split_kernel(const float* __restrict__ X, int n_tok, int K, int xq_tok,
+__global__ void __launch_bounds__(256) quantize_split_kernel(const float* X, int n_tok, int K, int xq_tok,
                                                              int xs_tok, uint8_t* __restrict__ xq_g,
                                                              uint8_t* __restrict__ xs_g) {
   pdl_enter();
@@ -1206,7 +1206,7 @@ __global__ void __launch_bounds__(256) quantize_split_kernel(const float* __rest
        t += static_cast<int64_t>(gridDim.x) * 256) {
     const int tok = static_cast<int>(t / nt), tl = static_cast<int>(t - static_cast<int64_t>(tok) * nt);
     const float4* src = reinterpret_cast<const float4*>(X + static_cast<int64_t>(tok) * K) + 2 * tl;
-    const float4 a = __ldg(src), c = __ldg(src + 1);
+    const float4 a = src[0], c = src[1];
     const float v[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
     const Q8Oct r = quantize_oct(v);
     *reinterpret_cast<uint2*>(xq_g + static_cast<int64_t>(tok) * xq_tok + 8 * tl) = make_uint2(r.q[0], r.q[1]);

@@ -7,14 +7,14 @@ namespace kq {
 
 // X fp32 [nblk * 32] (token-major, K % 32 == 0) -> nblk Q8_1 blocks of 36 bytes
 // laid out as [fp16 d][fp16 s][int8 q[32]].
-__global__ void __launch_bounds__(256) quantize_q8_1_kernel(const float* __restrict__ X, uint8_t* __restrict__ Xq,
+__global__ void __launch_bounds__(256) quantize_q8_1_kernel(const float* X, uint8_t* __restrict__ Xq,
                                                             int64_t nblk) {
   pdl_enter();
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t b = t >> 3;
   const int j = static_cast<int>(t & 7);
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (b < nblk) v = __ldg(reinterpret_cast<const float4*>(X) + t);
+  if (b < nblk) v = reinterpret_cast<const float4*>(X)[t];
   const Q8Quad r = quantize_quad(v);
   if (b < nblk) {
     uint8_t* dst = Xq + b * Q8_1_BYTES;
@@ -42,7 +42,7 @@ constexpr int XH_CTAS_PER_SM = 8;
 // (4 values) are strided over a grid of a few CTAs per SM, XH_UNROLL loads in
 // flight per thread. K / 4 is a multiple of 64 and the stride a multiple of 32,
 // so a warp's 32 quads always lie in one row and take the same path.
-__global__ void __launch_bounds__(256) quantize_xhat_kernel(const float* __restrict__ X, __half* __restrict__ Xh,
+__global__ void __launch_bounds__(256) quantize_xhat_kernel(const float* X, __half* __restrict__ Xh,
                                                             int K, int64_t rows) {
   pdl_enter();
   const int64_t total = rows * (K >> 2);
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(256) quantize_xhat_kernel(const float* __restr
 #pragma unroll
     for (int u = 0; u < XH_UNROLL; ++u) {
       const int64_t t = t0 + u * stride;
-      if (t < total) v[u] = __ldg(reinterpret_cast<const float4*>(X) + t);
+      if (t < total) v[u] = reinterpret_cast<const float4*>(X)[t];
     }
 #pragma unroll
     for (int u = 0; u < XH_UNROLL; ++u) {
@@ -72,9 +72,9 @@ __global__ void __launch_bounds__(256) quantize_xhat_kernel(const float* __restr
 // every bucket row of the token.
 constexpr int QS_WARPS = 8;
 constexpr int QS_ROUNDS = 4;
-__global__ void __launch_bounds__(QS_WARPS * 32) quantize_scatter_kernel(const float* __restrict__ X,
+__global__ void __launch_bounds__(QS_WARPS * 32) quantize_scatter_kernel(const float* X,
                                                                         __half* __restrict__ Xh, int K, int64_t T,
-                                                                        int top_k, const int* __restrict__ slot_pos,
+                                                                        int top_k, const int* slot_pos,
                                                                         int* __restrict__ entries) {
   pdl_enter();
   const int rounds = K >> 7;  // rounds of 32 quads per row
@@ -89,17 +89,18 @@ __global__ void __launch_bounds__(QS_WARPS * 32) quantize_scatter_kernel(const f
   uint2* hrow0 = reinterpret_cast<uint2*>(Xh);
   const int64_t quads = K >> 2;
   const int* sp = slot_pos + p * top_k;
+  const int first = lane < top_k ? sp[lane] : -1;   // of every round
   float4 v[QS_ROUNDS];
 #pragma unroll
   for (int u = 0; u < QS_ROUNDS; ++u)
-    if (run * QS_ROUNDS + u < r1) v[u] = __ldg(xrow + (run * QS_ROUNDS + u) * 32 + lane);
+    if (run * QS_ROUNDS + u < r1) v[u] = xrow[(run * QS_ROUNDS + u) * 32 + lane];
 #pragma unroll
   for (int u = 0; u < QS_ROUNDS; ++u) {
     const int r = run * QS_ROUNDS + u;
     if (r >= r1) break;  // warp-uniform
     const uint2 h = xhat4(quantize_quad(v[u]));
     for (int j0 = 0; j0 < top_k; j0 += 32) {
-      const int my = (j0 + lane < top_k) ? __ldg(sp + j0 + lane) : -1;
+      const int my = j0 == 0 ? first : (j0 + lane < top_k) ? sp[j0 + lane] : -1;
       const int nj = min(32, top_k - j0);
       for (int jj = 0; jj < nj; ++jj) {
         const int pos = __shfl_sync(0xffffffffu, my, jj);

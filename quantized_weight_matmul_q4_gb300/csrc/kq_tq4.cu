@@ -82,11 +82,11 @@ __device__ __forceinline__ void wht32(float (&v)[TQ_BLOCK]) {
 }
 
 // Loads x[32b .. 32b+32) (16-byte aligned) and rotates it.
-__device__ __forceinline__ void load_rotate(const float* __restrict__ x, int b, float (&v)[TQ_BLOCK]) {
+__device__ __forceinline__ void load_rotate(const float* x, int b, float (&v)[TQ_BLOCK]) {
   const float4* src = reinterpret_cast<const float4*>(x) + static_cast<size_t>(b) * 8;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const float4 t = __ldg(src + k);
+    const float4 t = src[k];
     v[4 * k] = t.x;
     v[4 * k + 1] = t.y;
     v[4 * k + 2] = t.z;
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int q = q0 + i * NW;
-      if (q < p.nq) v[i] = __ldg(reinterpret_cast<const float4*>(p.x) + static_cast<size_t>(q) * 32 + lane);
+      if (q < p.nq) v[i] = reinterpret_cast<const float4*>(p.x)[static_cast<size_t>(q) * 32 + lane];
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
 
 // Fallback: warp per row; lane j takes blocks j, j + 32, ... of each K segment.
 __global__ void __launch_bounds__(TQD_WARPS * 32) tq4_direct_kernel(const uint8_t* __restrict__ W,
-                                                                    const float* __restrict__ x, float* __restrict__ y,
+                                                                    const float* x, float* __restrict__ y,
                                                                     int M, int nbt) {
   extern __shared__ __align__(128) float tq_direct_smem[];  // the table (32 floats reserved), then the segment
   float* lut = tq_direct_smem;

@@ -12,7 +12,7 @@ from quantized_weight_matmul_q4_gb300.build import CSRC
 
 # Pointers to weights, their scales and zero points, by their names in the kernels.
 WEIGHTS = {"W", "scales", "zeros", "w4"}
-FILES = ["kq_rows.cu", "kq_route.cu", "kq_g4.cu", "kq_combine.cu", "kq_types.cuh"]
+FILES = sorted(f for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh")))
 
 
 def _source(name):
