@@ -280,13 +280,15 @@ KQ_API kq_status kq_moe_combine(const float* Y, const float* probs, float* out, 
  * activations, kq_moe_route chooses the experts, kq_moe_matvec_g4 multiplies
  * with the chosen experts' matrices (gate and up, then, after kq_swiglu_q8_1,
  * down), kq_moe_combine sums the slots. They are additions of this library; the
- * source pages have no counterpart to them. None needs a workspace.
+ * source pages have no counterpart to them. None needs a workspace. The Q8_1 rows are
+ * operands of the group-scaled products only: kq_matvec, kq_gemm and
+ * kq_moe_grouped_gemm take fp32 activations and quantise them themselves.
  *
  * Rows of floating-point operands are `ld` elements apart and contiguous within
  * a row; dtype is a kq_dtype (KQ_ERR_TYPE otherwise). For inputs ld is 0 (one
  * row read for all) or at least the row's length, for outputs at least the
  * row's length. Base pointers are 16-byte aligned; any ld is taken (rows that
- * are not 16-byte aligned are read element by element).
+ * are not 16-byte aligned are read and written by pairs of elements).
  *
  * kq_add_rmsnorm_q8_1 — residual addition, RMSNorm and quantisation of N rows:
  *   h = x + r (R NULL: h = x),  y[k] = h[k] * (1 / sqrt(Sum_k h[k]^2 / K + eps)) * gamma[k],
@@ -366,7 +368,8 @@ KQ_API kq_status kq_moe_route(int dtype, const void* logits, int64_t ld, const f
  * (K/32 + 12) * 2^-24 times the sum of the blocks' absolute contributions, Y_ref
  * the exact product of the dequantised operands. Results do not depend on
  * scheduling; a row's result may differ in the last bits with the number of
- * rows in the call (the sums are grouped differently).
+ * rows in the call (the sums are grouped differently). The bound is for products of
+ * scales in fp32's normal range.
  * As in kq_matvec, W, scales and zeros are streamed before the call waits for the
  * previous kernel on the stream: they must not be written by a still-running
  * predecessor that allows programmatic dependent launch, and none of Xq (or expert
@@ -384,7 +387,7 @@ KQ_API kq_status kq_matvec_g4(const void* W, const void* scales, int scale_dtype
  * [T][top_k]; Y: fp32 [T][top_k][M], written. n_experts <= 512,
  * top_k <= n_experts. An out-of-range expert id records KQ_DEVERR_EXPERT_ID and
  * that slot's output row is written as zeros; ids may repeat within a token.
- * W, scales and zeros are streamed early as above (for T * top_k >= n_experts).
+ * W, scales and zeros may be streamed early as above when T * top_k >= n_experts.
  */
 KQ_API kq_status kq_moe_matvec_g4(const void* W, const void* scales, int scale_dtype, const void* zeros, int64_t group,
                                   int32_t n_experts, const int32_t* expert_ids, int32_t top_k, int x_per_slot,

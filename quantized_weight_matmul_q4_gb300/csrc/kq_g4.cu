@@ -47,9 +47,10 @@ __device__ __forceinline__ float scale_f32(bool fp16, uint16_t bits) {
 // nibbles pair up), the scale and the sum of the codes. Then its warps stream
 // weights: 2^lanes_log2 lanes share a row, each taking every 2^lanes_log2-th 16-byte
 // block of it, U rows at a time, with the next four 16-byte loads of a lane in
-// flight while it works on the last four. What a block costs a lane is 12
-// operations to unpack, 8 dp4a and about 8 for the scales. Unpacking costs less with
-// dp4a than in the tensor-core form below, and without tiles no row is idle.
+// flight while it works on the last four. A block costs a lane some 68 instructions
+// (counted on 152064 x 3584): 20 to unpack and multiply, the others read the activations from
+// shared memory, convert and apply the scales, and make addresses and bounds. Unpacking costs less
+// with dp4a than in the tensor-core form below, and without tiles no row is idle.
 //
 // Bound by HBM for large matrices (152064 x 3584: 45.5 us, 281 MB, 6.2 TB/s = 0.91 of the
 // measured copy; issue slots 67 % busy) and by the launch and the first loads' latency for
@@ -233,11 +234,15 @@ __global__ void __launch_bounds__(G4_DP_WARPS * 32, G4_DP_CTAS) g4_dp_kernel(G4A
 // with two scales: here they are in registers already, from tensor memory the
 // whole accumulator would be read back for every 32 k.
 //
-// Bound by issue and the latency of its dependent steps, not by HBM: some 270
-// instructions per warp and chunk (8 rows, groups of 128 and longer) up to 620 (16 rows, groups of 32 with
-// zero points) at 46 to 58 % of the issue slots, 16 warps to an SM (128 registers a
-// thread). Launch, first copies and the cluster's sum take 4.5 us of every call (4096 x 1024,
-// 8 rows: 4.4). 4096 x 4096, 8 rows: 6.4 us; 14336 x 4096, 16 rows, groups of 32 with zero
+// Bound by latency, not by HBM nor by a pipe: some 270 instructions per warp and chunk (8 rows,
+// groups of 128 and longer) up to 620 (16 rows, groups of 32 with zero points) at 46 to 59 % of the
+// issue slots. 16 warps to an SM at most (128 registers a thread) wait on their own chains (copies,
+// ldmatrix, unpacking, two MMAs, scales) and on the barriers around the making of fragments; taking one
+// stage out (copies, unpacking, scales, fmas, fragments) took 2 to 12 % off an earlier state. A line
+// through the times over K, launch included, begins at 4.0 us (4096 weight rows, 8 activation
+// rows, K split in eight) or 5.7 (14336, 16 rows) and rises by 0.6 or 3.1 us (3.6 with
+// groups of 32 and zero points) per 1024 of K; 4096 x 128, 8 rows: 2.3 us.
+// 4096 x 4096, 8 rows: 6.4 us; 14336 x 4096, 16 rows, groups of 32 with zero
 // points: 20.0 us (1.8 TB/s); 128 experts' 2048 x 768, 512 (token, slot) rows, the same
 // groups: 40.7 us (3.0 TB/s). Copying by TMA instead of cp.async was slower (the latter
 // 46 -> 49.5 us), and so was a CTA that goes on to the next tile of its expert's rows
