@@ -100,12 +100,20 @@ typedef enum kq_dtype { KQ_F32 = 1, KQ_F16 = 2, KQ_BF16 = 3 } kq_dtype;
 /* Score function of kq_moe_route. */
 typedef enum kq_score { KQ_SCORE_SOFTMAX = 1, KQ_SCORE_SIGMOID = 2 } kq_score;
 
+/* Which elements of a head the position rotation turns together. */
+typedef enum kq_rope {
+  KQ_ROPE_HALF = 1, /* i and i + rot_dim / 2 */
+  KQ_ROPE_PAIRS = 2 /* 2i and 2i + 1 */
+} kq_rope;
+
 typedef enum kq_op { KQ_OP_MATVEC = 1, KQ_OP_GEMM = 2, KQ_OP_MOE = 3 } kq_op;
 
 /* Device error codes reported by kq_get_device_error. */
 #define KQ_DEVERR_NONE 0
 #define KQ_DEVERR_WAIT_TIMEOUT 1 /* a pipeline wait gave up (the kernel returned early) */
 #define KQ_DEVERR_EXPERT_ID 2    /* an expert id was outside [0, n_experts) */
+#define KQ_DEVERR_POSITION 3     /* a position was not below n_positions */
+#define KQ_DEVERR_PAGE 4         /* a place's sequence, table entry or page was out of range */
 
 /*
  * kq_quantize_q8_1 — fp32 activations to Q8_1 blocks ([MMVQ] §2 and §3.2
@@ -392,6 +400,125 @@ KQ_API kq_status kq_matvec_g4(const void* W, const void* scales, int scale_dtype
 KQ_API kq_status kq_moe_matvec_g4(const void* W, const void* scales, int scale_dtype, const void* zeros, int64_t group,
                                   int32_t n_experts, const int32_t* expert_ids, int32_t top_k, int x_per_slot,
                                   const void* Xq, float* Y, int64_t M, int64_t K, int64_t T, kq_stream_t stream);
+
+/*
+ * The operators of a decode step's attention, and the choice of its tokens. They are
+ * additions of this library; the source pages have no counterpart to them. A row of
+ * queries, keys or values holds its heads one after the other, head_dim elements each;
+ * dtypes, rows and ld are as above (base pointers of rows, tables of cosines, gammas,
+ * caches, workspaces and Xq are 16-byte aligned; index and parameter arrays 4-byte).
+ *
+ * kq_qk_norm_rope — the norm of every head of N rows of queries and keys, then the
+ * position rotation:
+ *   y[i] = x[i] * (1 / sqrt(Sum_i x[i]^2 / head_dim + eps)) * gamma[i]   (gamma NULL: y = x),
+ *   (a, b) -> (a cos - b sin, b cos + a sin) for the pairs that `pairing` (kq_rope) makes
+ *   of the first rot_dim elements; the others stay. cos_sin NULL: no rotation.
+ * cos_sin: fp32 [n_positions][rot_dim], a position's rot_dim / 2 cosines, then their sines.
+ * positions: int32 [N], or NULL (row n is at position n). A row with a negative position
+ * is passed over: nothing is read or written for it. So is one whose position is not
+ * in the table, and KQ_DEVERR_POSITION is recorded.
+ * Q: dtype [N][n_q_heads * head_dim]; K likewise with n_k_heads, NULL where that is 0;
+ * Qo, Ko: out_dtype, written; out_dtype is dtype, or any for fp32 inputs. Qo may be Q and
+ * Ko K (the same pointer, ld and type); outputs overlap nothing else. q_gamma, k_gamma:
+ * fp32 [head_dim] or NULL. head_dim: a multiple of 16 from 16 to 256; rot_dim: a multiple of 16
+ * up to head_dim; eps >= 0. All arithmetic is fp32, rounded once to out_dtype; an
+ * unrounded result is within 16 * 2^-24 * (|a cos| + |b sin|) of its exact value (16 * 2^-24 * |y| where
+ * nothing is turned), for every head of finite x (a head of zeros with eps = 0 gives NaN).
+ */
+KQ_API kq_status kq_qk_norm_rope(int dtype, const void* Q, int64_t ldq, int32_t n_q_heads, const void* K, int64_t ldk,
+                                 int32_t n_k_heads, int32_t head_dim, const float* q_gamma, const float* k_gamma,
+                                 float eps, const float* cos_sin, int32_t rot_dim, int64_t n_positions, int pairing,
+                                 const int32_t* positions, int out_dtype, void* Qo, int64_t ldqo, void* Ko, int64_t ldko,
+                                 int64_t N, kq_stream_t stream);
+
+/*
+ * The 4-bit paged cache. Place p of sequence s is place p % page_size of page
+ * block_table[s * ldt + p / page_size]; page_size is a power of two from 16 to 65536.
+ * A head's 32-element blocks are stored as fp16 s and m and 4-bit codes c, standing for
+ * m + s * c:
+ *   m = fp16(min v), s = fp16((max v - min v) * (1 / 15 as fp32)),
+ *   c = clamp(rint((v - m) / s), 0, 15) (0 where s is 0), all in IEEE fp32.
+ * A block with an infinity or a NaN, or whose m or s would not be finite in fp16, has s = NaN and
+ * m = 0 and stands for NaN.
+ * cache: bytes [n_pages][n_heads][page_size / 16][20 * head_dim]: granules of 16 places of
+ * one head, in each, with G = head_dim / 32,
+ *   [16][head_dim / 2] key codes: element r of block g in byte 4G * (r / 8) + 4g + (r % 8) / 2,
+ *   [16][2][G] fp16 key parameters: the blocks' s, then their m,
+ *   [16][head_dim / 2] value codes: element r of block g in byte 2G * (r / 4) + 2g + (r % 4) / 2,
+ *   [16][2][G] fp16 value parameters;
+ *   an even r has the low half of its byte. 5 bits a value; head_dim is 64, 128 or 256.
+ * Memory that no token was written to may hold anything: no operator uses it.
+ *
+ * kq_kv_append_q4 — writes N tokens' keys and values to their places, the keys turned by
+ * their positions on the way (cos_sin NULL: as they are; the table and pairing as in
+ * kq_qk_norm_rope, each product and each sum rounded to fp32).
+ * K, V: dtype [N][n_heads * head_dim]. positions: int32 [N], a token's place in its
+ * sequence and the row of cos_sin; seq_ids: int32 [N], its sequence, or NULL (token n
+ * belongs to sequence n). block_table: int32 [n_seqs][ldt]. A token with a negative position
+ * is passed over; so is one whose sequence, place or page is out of range (KQ_DEVERR_PAGE
+ * is recorded) or whose position is not in the table of cosines (KQ_DEVERR_POSITION). No
+ * two tokens of a call have the same place (the bytes there would be of either).
+ */
+KQ_API kq_status kq_kv_append_q4(int dtype, const void* K, int64_t ldk, const void* V, int64_t ldv, int32_t n_heads,
+                                 int32_t head_dim, const float* cos_sin, int32_t rot_dim, int64_t n_positions,
+                                 int pairing, const int32_t* positions, const int32_t* seq_ids,
+                                 const int32_t* block_table, int64_t ldt, int64_t n_seqs, void* cache, int64_t n_pages,
+                                 int32_t page_size, int64_t N, kq_stream_t stream);
+
+/*
+ * kq_kv_gather_q4 — reads places of the cache back as rows: K, V: dtype
+ * [N][n_heads * head_dim], written with m + s * c, computed in fp32 and rounded once. The
+ * other arguments are those of kq_kv_append_q4; rows that it would pass over are left as they were.
+ */
+KQ_API kq_status kq_kv_gather_q4(const void* cache, int64_t n_pages, int32_t page_size, int32_t n_heads,
+                                 int32_t head_dim, const int32_t* block_table, int64_t ldt, int64_t n_seqs,
+                                 const int32_t* positions, const int32_t* seq_ids, int dtype, void* K, int64_t ldk,
+                                 void* V, int64_t ldv, int64_t N, kq_stream_t stream);
+
+/*
+ * kq_attn_q4 — attention of N rows of queries over the cache. Query head i attends to key
+ * head i / (n_q_heads / n_kv_heads). Sequence b has the rows q_start[b] to q_start[b + 1] - 1
+ * of Q (q_start: int32 [n_seqs + 1], ascending, or NULL: row b, with N = n_seqs) and
+ * kv_len[b] places in the cache, the rows' own among them. Row i of n sees the places below
+ * kv_len[b] - n + 1 + i and, with window > 0, only the last `window` of those:
+ *   o = Sum_t p_t v_t, p = softmax_t(scale * q . k_t); a row that sees no place gives zeros.
+ * Q: dtype; O: dtype [N][n_q_heads * head_dim], or NULL; Xq: N * (n_q_heads * head_dim / 32) * 36
+ * bytes, the Q8_1 blocks of the unrounded o, or NULL; one of the two is given. Rows of Q that belong
+ * to no sequence are not read, and theirs of O and Xq left as they were.
+ * A place whose page is out of range counts as one that no row sees, and KQ_DEVERR_PAGE is recorded.
+ * ws: at least kq_attn_q4_workspace_bytes(...) bytes, whatever they hold; calls that may
+ * overlap need one each.
+ * Scores, softmax statistics and sums are fp32. Made for the rows of decode steps: any number
+ * of new rows is taken, in tiles that each read the cache again.
+ */
+KQ_API size_t kq_attn_q4_workspace_bytes(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int64_t N,
+                                         int64_t n_seqs);
+KQ_API kq_status kq_attn_q4(int dtype, const void* Q, int64_t ldq, int32_t n_q_heads, const void* cache, int64_t n_pages,
+                            int32_t page_size, int32_t n_kv_heads, int32_t head_dim, const int32_t* block_table,
+                            int64_t ldt, int64_t n_seqs, const int32_t* kv_len, const int32_t* q_start, float scale,
+                            int64_t window, void* O, int64_t ldo, void* Xq, int64_t N, void* ws, size_t ws_bytes,
+                            kq_stream_t stream);
+
+/*
+ * kq_sample — the next token of each of N rows of logits, for given random numbers u in [0, 1).
+ * With a row's tokens in descending order of their logits (ties to the lower index) and
+ * weights w = exp((l - max l) / T), three prefixes of that order limit the choice: the
+ * first top_k tokens (top_k <= 0: all); the shortest prefix with at least top_p of the
+ * weight of those (top_p not below 1: all); the tokens with w >= min_p (1 for larger ones). The
+ * shortest is kept; at least one token always is. The token chosen is the first, by index, at
+ * which the sum of the kept weights passes u times their total; its probability is its share of
+ * that total. T not above 0: the first token with the largest logit, with probability 1.
+ * A logit of -inf or NaN is never chosen; +inf counts as the largest finite fp32. A row without
+ * any other gives token 0 with probability 0.
+ * logits: dtype [N][V], rows ld apart, V <= 524288. temperature, top_p, min_p: fp32 [N], or NULL
+ * (1, 1, 0); top_k: int32 [N] or NULL; u: fp32 [N]; ids: int32 [N], probs: fp32 [N] or NULL, written.
+ * Weights are within 2^-30 of theirs, relative (with 2^-43 of the largest); the sums that are
+ * compared are exact sums of them, so the choice is that of the definition unless two sums
+ * that it compares are that close.
+ */
+KQ_API kq_status kq_sample(int dtype, const void* logits, int64_t ld, const float* temperature, const int32_t* top_k,
+                           const float* top_p, const float* min_p, const float* u, int32_t* ids, float* probs, int64_t V,
+                           int64_t N, kq_stream_t stream);
 
 /*
  * kq_workspace_bytes — device workspace needed by an operation (0 for

@@ -10,7 +10,8 @@ from __future__ import annotations
 
 import ctypes
 
-from ._native import (KQ_BF16, KQ_F16, KQ_F32, KQ_SCORE_SIGMOID, KQ_SCORE_SOFTMAX, KQ_DEVERR_EXPERT_ID, KQ_DEVERR_NONE, KQ_DEVERR_WAIT_TIMEOUT, KQ_GEMM_STATIC_WS_BYTES,
+from ._native import (KQ_BF16, KQ_F16, KQ_F32, KQ_SCORE_SIGMOID, KQ_SCORE_SOFTMAX, KQ_ROPE_HALF, KQ_ROPE_PAIRS,
+                      KQ_DEVERR_POSITION, KQ_DEVERR_PAGE, KQ_DEVERR_EXPERT_ID, KQ_DEVERR_NONE, KQ_DEVERR_WAIT_TIMEOUT, KQ_GEMM_STATIC_WS_BYTES,
                       KQ_OP_GEMM, KQ_OP_MATVEC, KQ_OP_MOE, KQ_Q4_K, KQ_Q5_K, KQ_Q6_K, KQ_TQ4_1S, KQError, check, lib)
 
 __all__ = [
@@ -19,6 +20,8 @@ __all__ = [
     "KQ_GEMM_STATIC_WS_BYTES", "kq_quantize_q8_1", "kq_matvec", "kq_matvec_prefetch", "kq_matvec_swiglu", "kq_matvec_rmsnorm",
     "kq_gemm", "kq_gemm_noalloc", "kq_moe_grouped_gemm", "kq_moe_combine", "kq_workspace_bytes",
     "kq_add_rmsnorm_q8_1", "kq_swiglu_q8_1", "kq_moe_route", "kq_matvec_g4", "kq_moe_matvec_g4",
+    "kq_qk_norm_rope", "kq_kv_append_q4", "kq_kv_gather_q4", "kq_attn_q4", "kq_attn_q4_workspace_bytes", "kq_sample",
+    "kv_cache_q4_shape", "KQ_ROPE_HALF", "KQ_ROPE_PAIRS", "KQ_DEVERR_POSITION", "KQ_DEVERR_PAGE",
     "KQ_F32", "KQ_F16", "KQ_BF16", "KQ_SCORE_SOFTMAX", "KQ_SCORE_SIGMOID",
     "kq_get_device_error", "kq_test_hold_copies", "block_bytes", "row_bytes",
 ]
@@ -357,6 +360,200 @@ def kq_moe_matvec_g4(W, scales, n_experts: int, expert_ids, Xq, M: int, K: int, 
     check(lib().kq_moe_matvec_g4(*w, n_experts, _dev(expert_ids, "expert_ids", torch.int32), top_k, n != T, xq, y, M, K,
                                  T, _stream(stream)), "kq_moe_matvec_g4")
     return Y
+
+
+_PAIRINGS = {"half": KQ_ROPE_HALF, "pairs": KQ_ROPE_PAIRS}
+
+
+def _head_rows(t, name: str, shape, dtype):
+    """(device pointer, elements from row to row) of a CUDA tensor [N, heads, D] whose rows are contiguous."""
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor (libkq has no CPU path)")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    N, heads, D = shape
+    ld, head, step = t.stride()
+    if (step != 1 and D != 1) or (head != D and heads != 1):
+        raise ValueError(f"{name}'s heads must follow one another in its rows")
+    return t.data_ptr(), ld if N > 1 else heads * D
+
+
+def _rope(cos_sin, pairing):
+    """(pointer, rot_dim, n_positions, pairing) of a table of cosines and sines, or of none."""
+    if cos_sin is None:
+        return None, 0, 0, KQ_ROPE_HALF
+    p = _dev(cos_sin, "cos_sin", _torch().float32)
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must have shape [n_positions, rot_dim]")
+    n, rot = cos_sin.shape
+    return p, rot, n, _PAIRINGS[pairing] if isinstance(pairing, str) else int(pairing)
+
+
+def kv_cache_q4_shape(n_pages: int, n_heads: int, page_size: int, head_dim: int):
+    """Shape of the uint8 tensor that is a 4-bit cache of n_pages pages."""
+    return n_pages, n_heads, page_size // 16, 20 * head_dim
+
+
+def _kv_cache(cache, block_table):
+    """(cache pointer, pages, page size, heads, head_dim, table pointer, ldt, sequences)."""
+    torch = _torch()
+    p, bt = _dev(cache, "cache", torch.uint8), _dev(block_table, "block_table", torch.int32)
+    if cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("cache must have the shape that kv_cache_q4_shape gives, block_table [sequences, pages]")
+    pages, heads, granules, size = cache.shape
+    seqs, ldt = block_table.shape
+    if size % 20:
+        raise ValueError("cache must have the shape that kv_cache_q4_shape gives")
+    return p, pages, 16 * granules, heads, size // 20, bt, ldt, seqs
+
+
+def kq_qk_norm_rope(Q, K, cos_sin=None, positions=None, q_gamma=None, k_gamma=None, eps: float = 1e-6, pairing="half",
+                    Qo=None, Ko=None, out_dtype=None, stream=None):
+    """The heads of Q [N, Hq, D] and K [N, Hk, D] (or None) normed and turned: (Qo, Ko).
+
+    q_gamma, k_gamma: fp32 [D], None for no norm. cos_sin: fp32 [n_positions, rot], a position's
+    cosines, then its sines; positions: int32 [N] (None: row n is at n; a negative one is passed over). pairing: "half"
+    turns elements i and i + rot / 2 together, "pairs" 2i and 2i + 1. out_dtype: that of Q, or any for fp32.
+    """
+    torch = _torch()
+    dt = _dtype(Q, "Q")
+    if Q.dim() != 3 or (K is not None and K.dim() != 3):
+        raise ValueError("Q and K must have shape [N, heads, head_dim]")
+    shape = Q.shape
+    N, Hq, D = shape
+    q, ldq = _head_rows(Q, "Q", shape, Q.dtype)
+    if out_dtype is None:
+        out_dtype = Qo.dtype if Qo is not None else Q.dtype
+    if Qo is None:
+        Qo = _out(shape, out_dtype, Q.device, stream)
+    qo, ldqo = _head_rows(Qo, "Qo", shape, out_dtype)
+    k, ldk, Hk, ko, ldko = None, 0, 0, None, 0
+    if K is not None:
+        Hk = K.shape[1]
+        kshape = (N, Hk, D)
+        k, ldk = _head_rows(K, "K", kshape, Q.dtype)
+        if Ko is None:
+            Ko = _out(kshape, out_dtype, Q.device, stream)
+        ko, ldko = _head_rows(Ko, "Ko", kshape, out_dtype)
+    table, rot, n_pos, pair = _rope(cos_sin, pairing)
+    check(lib().kq_qk_norm_rope(dt, q, ldq, Hq, k, ldk, Hk, D, _sized(q_gamma, "q_gamma", D, torch.float32),
+                                _sized(k_gamma, "k_gamma", D, torch.float32), eps, table, rot, n_pos, pair,
+                                _sized(positions, "positions", N, torch.int32), _dtype(Qo, "Qo"), qo, ldqo, ko, ldko, N,
+                                _stream(stream)), "kq_qk_norm_rope")
+    return Qo, Ko if K is not None else None
+
+
+def kq_kv_append_q4(K, V, cache, block_table, positions, seq_ids=None, cos_sin=None, pairing="half", stream=None):
+    """Writes keys and values [N, H, D] to their places of a 4-bit cache (a uint8 tensor of
+    kv_cache_q4_shape), the keys turned by the table cos_sin on the way; returns the cache.
+
+    positions: int32 [N], a token's place in its sequence (negative: passed over); seq_ids: int32 [N] (None: token
+    n belongs to sequence n); block_table: int32 [sequences, pages]. See kq_qk_norm_rope for cos_sin and pairing.
+    """
+    torch = _torch()
+    dt = _dtype(K, "K")
+    c, pages, page, H, D, bt, ldt, seqs = _kv_cache(cache, block_table)
+    shape = (K.shape[0], H, D)
+    k, ldk = _head_rows(K, "K", shape, K.dtype)
+    v, ldv = _head_rows(V, "V", shape, K.dtype)
+    N = shape[0]
+    check(lib().kq_kv_append_q4(dt, k, ldk, v, ldv, H, D, *_rope(cos_sin, pairing),
+                                _sized(positions, "positions", N, torch.int32), _sized(seq_ids, "seq_ids", N, torch.int32),
+                                bt, ldt, seqs, c, pages, page, N, _stream(stream)), "kq_kv_append_q4")
+    return cache
+
+
+def kq_kv_gather_q4(cache, block_table, positions, seq_ids=None, dtype=None, K=None, V=None, stream=None):
+    """Keys and values (rows [N, H, D]; bf16 where no dtype is given) that the cache holds at places positions of
+    sequences seq_ids (as in kq_kv_append_q4). Rows of places that there are not are left as they were."""
+    torch = _torch()
+    c, pages, page, H, D, bt, ldt, seqs = _kv_cache(cache, block_table)
+    N = positions.numel()
+    shape = (N, H, D)
+    if dtype is None:
+        dtype = K.dtype if K is not None else V.dtype if V is not None else torch.bfloat16
+    if K is None:
+        K = _out(shape, dtype, cache.device, stream)
+    if V is None:
+        V = _out(shape, dtype, cache.device, stream)
+    k, ldk = _head_rows(K, "K", shape, dtype)
+    v, ldv = _head_rows(V, "V", shape, dtype)
+    check(lib().kq_kv_gather_q4(c, pages, page, H, D, bt, ldt, seqs, _sized(positions, "positions", N, torch.int32),
+                                _sized(seq_ids, "seq_ids", N, torch.int32), _dtype(K, "K"), k, ldk, v, ldv, N,
+                                _stream(stream)), "kq_kv_gather_q4")
+    return K, V
+
+
+def kq_attn_q4_workspace_bytes(n_q_heads: int, n_kv_heads: int, head_dim: int, N: int, n_seqs: int) -> int:
+    return int(lib().kq_attn_q4_workspace_bytes(n_q_heads, n_kv_heads, head_dim, N, n_seqs))
+
+
+def kq_attn_q4(Q, cache, block_table, kv_len, scale=None, q_start=None, window: int = 0, O=None, Xq=False, ws=None,
+               stream=None):
+    """Attention of queries Q [N, Hq, D] over a 4-bit cache: (O, Xq).
+
+    kv_len: int32 [sequences], places of each sequence, its new rows' own among them; q_start: int32 [sequences + 1], where
+    each sequence's rows begin (None: one row each). scale: 1 / sqrt(D) where none is given. O: as Q; False for
+    none. Xq: True for Q8_1 rows uint8 [N, Hq * D / 32, 36] of the output, or a tensor for them.
+    """
+    torch = _torch()
+    dt = _dtype(Q, "Q")
+    if Q.dim() != 3:
+        raise ValueError("Q must have shape [N, heads, head_dim]")
+    c, pages, page, Hk, D, bt, ldt, seqs = _kv_cache(cache, block_table)
+    N, Hq = Q.shape[0], Q.shape[1]
+    shape = (N, Hq, D)
+    q, ldq = _head_rows(Q, "Q", shape, Q.dtype)
+    o, ldo = None, 0
+    if O is False:
+        O = None
+    else:
+        if O is None:
+            O = _out(shape, Q.dtype, Q.device, stream)
+        o, ldo = _head_rows(O, "O", shape, Q.dtype)
+    xq = None
+    if Xq is False:
+        Xq = None
+    elif Xq is True:
+        Xq = _out((N, Hq * D // 32, 36), torch.uint8, Q.device, stream)
+        xq = Xq.data_ptr()
+    elif Xq is not None:
+        xq = _sized(Xq, "Xq", N * (Hq * D // 32) * 36, torch.uint8)
+    if ws is None:
+        ws = _out((max(16, kq_attn_q4_workspace_bytes(Hq, Hk, D, N, seqs)),), torch.uint8, Q.device, stream)
+    check(lib().kq_attn_q4(dt, q, ldq, Hq, c, pages, page, Hk, D, bt, ldt, seqs, _sized(kv_len, "kv_len", seqs, torch.int32),
+                           _sized(q_start, "q_start", seqs + 1, torch.int32), scale if scale is not None else D ** -0.5,
+                           window, o, ldo, xq, N, _dev(ws, "ws", torch.uint8), ws.numel(), _stream(stream)), "kq_attn_q4")
+    return O, Xq
+
+
+def kq_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, ids=None, probs=None, stream=None):
+    """The next token of every row of logits [N, V] for random numbers u fp32 [N], and its probability:
+    (int32 [N], fp32 [N]).
+
+    temperature, top_p, min_p: fp32 [N], top_k: int32 [N]; None for no such limit. A temperature of 0 takes the first
+    token with the largest logit. probs False: None instead of the probabilities.
+    """
+    torch = _torch()
+    dt = _dtype(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must have shape [N, V]")
+    N, V = logits.shape
+    x, ld = _rows(logits, "logits", logits.shape, logits.dtype)
+    f32 = torch.float32
+    if ids is None:
+        ids = _out((N,), torch.int32, logits.device, stream)
+    if probs is None:
+        probs = _out((N,), f32, logits.device, stream)
+    elif probs is False:
+        probs = None
+    check(lib().kq_sample(dt, x, ld, _sized(temperature, "temperature", N, f32), _sized(top_k, "top_k", N, torch.int32),
+                          _sized(top_p, "top_p", N, f32), _sized(min_p, "min_p", N, f32), _sized(u, "u", N, f32),
+                          _sized(ids, "ids", N, torch.int32), _sized(probs, "probs", N, f32), V, N, _stream(stream)),
+          "kq_sample")
+    return ids, probs
 
 
 def kq_workspace_bytes(op: int, wtype, M: int, K: int, N_or_T: int, n_experts: int = 0, top_k: int = 0) -> int:

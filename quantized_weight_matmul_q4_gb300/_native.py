@@ -29,6 +29,8 @@ KQ_F16 = 2
 KQ_BF16 = 3
 KQ_SCORE_SOFTMAX = 1
 KQ_SCORE_SIGMOID = 2
+KQ_ROPE_HALF = 1
+KQ_ROPE_PAIRS = 2
 KQ_OP_MATVEC = 1
 KQ_OP_GEMM = 2
 KQ_OP_MOE = 3
@@ -36,6 +38,8 @@ KQ_OP_MOE = 3
 KQ_DEVERR_NONE = 0
 KQ_DEVERR_WAIT_TIMEOUT = 1
 KQ_DEVERR_EXPERT_ID = 2
+KQ_DEVERR_POSITION = 3
+KQ_DEVERR_PAGE = 4
 
 KQ_GEMM_STATIC_WS_BYTES = 32 << 20
 
@@ -63,6 +67,16 @@ SIGNATURES = {
     "kq_matvec_g4": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _vp]),
     "kq_moe_matvec_g4": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _vp, _i64, _i32, _vp, _i32, ctypes.c_int, _vp, _vp,
                                         _i64, _i64, _i64, _vp]),
+    "kq_qk_norm_rope": (ctypes.c_int, [ctypes.c_int, _vp, _i64, _i32, _vp, _i64, _i32, _i32, _vp, _vp, ctypes.c_float, _vp,
+                                       _i32, _i64, ctypes.c_int, _vp, ctypes.c_int, _vp, _i64, _vp, _i64, _i64, _vp]),
+    "kq_kv_append_q4": (ctypes.c_int, [ctypes.c_int, _vp, _i64, _vp, _i64, _i32, _i32, _vp, _i32, _i64, ctypes.c_int, _vp,
+                                       _vp, _vp, _i64, _i64, _vp, _i64, _i32, _i64, _vp]),
+    "kq_kv_gather_q4": (ctypes.c_int, [_vp, _i64, _i32, _i32, _i32, _vp, _i64, _i64, _vp, _vp, ctypes.c_int, _vp, _i64,
+                                       _vp, _i64, _i64, _vp]),
+    "kq_attn_q4_workspace_bytes": (_sz, [_i32, _i32, _i32, _i64, _i64]),
+    "kq_attn_q4": (ctypes.c_int, [ctypes.c_int, _vp, _i64, _i32, _vp, _i64, _i32, _i32, _i32, _vp, _i64, _i64, _vp, _vp,
+                                  ctypes.c_float, _i64, _vp, _i64, _vp, _i64, _vp, _sz, _vp]),
+    "kq_sample": (ctypes.c_int, [ctypes.c_int, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp]),
     "kq_workspace_bytes": (_sz, [ctypes.c_int, ctypes.c_int, _i64, _i64, _i64, _i32, _i32]),
     "kq_get_device_error": (ctypes.c_int, [ctypes.POINTER(_i32), _vp]),
     "kq_test_hold_copies": (ctypes.c_int, [ctypes.c_int]),
