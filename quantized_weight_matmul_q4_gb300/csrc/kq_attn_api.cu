@@ -147,6 +147,7 @@ kq_status kq_attn_q4(int dtype, const void* Q, int64_t ldq, int32_t n_q_heads, c
   if (st != KQ_OK) return st;
   const int64_t row = static_cast<int64_t>(n_q_heads) * head_dim;
   if (n_q_heads <= 0 || n_q_heads > 65536 || n_q_heads % n_kv_heads != 0 || !valid_size(N) || N * row > kMaxValues ||
+      N * n_q_heads > (int64_t(1) << 30) ||
       (!q_start && N != n_seqs) || !valid_ld_in(ldq, row) || (O && !valid_ld_out(ldo, row)) ||
       !(scale > -1e30f && scale < 1e30f) || window < 0)
     return KQ_ERR_SHAPE;

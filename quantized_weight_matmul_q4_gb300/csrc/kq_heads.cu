@@ -11,6 +11,7 @@
 #include <algorithm>
 
 #include "kq_kv4.cuh"
+#include "kq_q8_rows.cuh"
 #include "kq_types.cuh"
 
 namespace kq {
@@ -172,17 +173,6 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const HeadRows a
       store8<TO, VEC>(p + 8 * lane, v);
     }
   }
-}
-
-__device__ __forceinline__ float max_nan(float a, float b) {   // a NaN stays
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
 }
 
 // The codes of the eight values v of a lane, the block being held by an aligned quad of lanes:
