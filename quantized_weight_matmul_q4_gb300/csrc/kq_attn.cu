@@ -34,12 +34,12 @@
 namespace kq {
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr float kLow = -1e30f;          // the maximum before any score
 constexpr float kAhead = 4.f;           // how far a score may pass the maximum (log2) before it is moved
-constexpr float kTop = 11.f;            // weights are 2^(score - maximum + kTop): 2^15 at most
+constexpr float kTop = 10.f;            // weights are 2^(score - maximum + kTop): 2^14 at most
 constexpr int kSegmentUnits = 4;        // what beginning and ending a segment costs, in granules
-constexpr int kLeastUnits = 12;         // the shortest run of a CTA
+constexpr int kRound = kWarps;          // granules of a CTA's runs within a segment come in such numbers
 
 struct Attn {
   AttnArgs a;
@@ -61,11 +61,23 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same beginning from zero.
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 // The transpose of an 8 x 8 matrix of fp16 held two to a lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
+}
+// Two 8 x 8 matrices of fp16 from shared memory, transposed: lanes 0..7 give the rows of the first, 8..15 of the second.
+__device__ __forceinline__ void load_transposed(uint32_t& x, uint32_t& y, const void* row) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(x), "=r"(y) : "r"(smem_u32(row)));
 }
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) { return half2_bits(__floats2half2_rn(lo, hi)); }
 __device__ __forceinline__ float low_part(float v) { return v - __half2float(__float2half_rn(v)); }
@@ -75,13 +87,17 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// a / b of whole numbers that are seldom beyond 32 bits.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (a | b) >> 32 == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+
+// Where a cut `off` units into a segment of `size` is made: before it, after it, or after a whole number of rounds.
+__device__ __forceinline__ int64_t cut_at(int64_t off, int size) {
+  const int w = static_cast<int>(off) - kSegmentUnits;
+  if (w <= 0) return 0;
+  const int to = kSegmentUnits + (w + kRound - 1) / kRound * kRound;
+  return to + kRound / 2 >= size ? size : to;
 }
 
 // A sequence's rows and the granules that any of them sees.
@@ -121,11 +137,14 @@ template <typename T, int D, int NT>
 struct Shape {
   static constexpr int R = 8 * NT;
   static constexpr bool kSplit = sizeof(T) == 4;
-  static constexpr int kStages = D == 64 ? 5 : D == 128 ? 4 : 3;
-  static constexpr int kCtas = D == 256 ? (kSplit ? 2 : 3) : NT == 2 ? (kSplit ? 2 : 3) : (kSplit ? 3 : 4);
+  static constexpr int kStages = 4;
+  static constexpr int kCtas = D == 256 || kSplit || NT == 2 ? 1 : 2;
   static constexpr int kRing = kWarps * kStages * Granule<D>::kBytes;
-  static constexpr int kPitch = D + 4;                                // of the sums that the warps join
-  static constexpr size_t kSmem = kRing + (R * kPitch + 2 * kWarps * R) * sizeof(float);
+  static constexpr int kPitch = D + 4;                                // of the rows of sums that the warps join, in the ring
+  static constexpr int kQuery = NT * (D / 32) * 32 * 16;              // operands of the queries, in one half
+  static constexpr int kSums = NT * ((D + 127) / 128) * 32 * 8;       // their blocks' sums
+  static constexpr size_t kSmem = kRing + kQuery * (kSplit ? 2 : 1) + kSums + (R + 2 * kWarps * R) * sizeof(float);
+  static_assert(kWarps * R * kPitch * 4 <= kRing, "the warps' sums fit the ring");
 };
 
 template <typename T, int D, int NT>
@@ -135,72 +154,108 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
   constexpr int G = Gr::G, R = Sh::R, S = Sh::kStages;
   constexpr bool kSplit = Sh::kSplit;
   constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u;
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int64_t scan[kWarps + 3];
-  float* joined = reinterpret_cast<float*>(smem + Sh::kRing);         // [R][kPitch]
-  float* stat = joined + R * Sh::kPitch;                              // maxima [kWarps][R], totals [kWarps][R]
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t scan[kWarps + 4];
+  __shared__ int abort;      // a wait gave up
+  __shared__ uint64_t full[kWarps][S];
+  float* joined = reinterpret_cast<float*>(smem);                     // [kWarps][R][kPitch]
+  uint4* q_hi = reinterpret_cast<uint4*>(smem + Sh::kRing);           // [NT][G][32]
+  [[maybe_unused]] uint4* q_lo = q_hi + Sh::kQuery / 16;
+  __half* q_sum = reinterpret_cast<__half*>(smem + Sh::kRing + Sh::kQuery * (kSplit ? 2 : 1));   // [NT][(G + 3) / 4][32][4]
+  float* q_factor = reinterpret_cast<float*>(q_sum) + Sh::kSums / 4;  // [R]
+  float* stat = q_factor + R;                                         // maxima [kWarps][R], totals [kWarps][R]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
-  const uint8_t* ring = smem + warp * (S * Gr::kBytes);
-  const uint32_t ring_u = smem_u32(ring);
+  uint8_t* ring = smem + warp * (S * Gr::kBytes);
+  if (lane == 0) {
+#pragma unroll
+    for (int k = 0; k < S; ++k) mbar_init(&full[warp][k], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  if (threadIdx.x == 0) abort = 0;
+  int stage = 0;             // of this warp's next granule, and its phase
+  uint32_t phase = 0;
   pdl_enter();
 
-  // This CTA's run [u, u1) of the line, and the sequence that it begins in.
-  const int64_t B = p.c.n_seqs;
-  int64_t total = 0, u, u1, per, seq_at = 0, b = 0;
+  // This CTA's run [u, u1) of the line, and the sequence that it begins in. The sum over the sequences comes first; where they
+  // are more than the threads, another pass finds the places.
+  int64_t u, u1, per = 1, seq_at, b;
+  if (threadIdx.x == 0) p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
   {
-    auto block_scan = [&](int64_t v, int64_t& sum) {                  // sum of the threads before this one; of all
-      int64_t x = v;
+    const int64_t n_seqs = p.c.n_seqs;
+    const bool once = n_seqs <= kThreads;
+    int64_t before = 0, x = 0, v = 0;
+    int size = 1;
+    int64_t c0 = 0, c1 = 0;
+#pragma unroll 1
+    for (int pass = once ? 1 : 0; pass < 2; ++pass) {
+      before = 0;
+#pragma unroll 1
+      for (int64_t i0 = 0; i0 < n_seqs; i0 += kThreads) {
+        const int64_t i = i0 + threadIdx.x;
+        v = 0;
+        if (i < n_seqs) {
+          Sequence s;
+          s.load(p, i, R);
+          v = s.units(p.c.heads);
+          size = kSegmentUnits + s.granules;
+        }
+        x = v;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      __syncthreads();
-      if (lane == 31) scan[warp] = x;
-      __syncthreads();
-      int64_t before = 0;
-      sum = 0;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) scan[warp] = x;
+        __syncthreads();
+        x += before - v;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        before += w < warp ? scan[w] : 0;
-        sum += scan[w];
+        for (int w = 0; w < kWarps; ++w) {
+          x += w < warp ? scan[w] : 0;
+          before += scan[w];
+        }
+        if (once || (pass == 0 && i0 + kThreads >= n_seqs)) {
+          per = max(static_cast<int64_t>(kRound), quotient(before + gridDim.x - 1, gridDim.x));
+          c0 = blockIdx.x * per;
+          if (c0 >= before) return;
+          c1 = c0 + per;
+        }
+        if (pass == 1) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int64_t cut = k ? c1 : c0;
+            if (x <= cut && cut < x + v) {
+              const int64_t seg = x + quotient(cut - x, size) * size;
+              if (k == 0) scan[kWarps] = i, scan[kWarps + 1] = x;
+              scan[kWarps + 2 + k] = seg + cut_at(cut - seg, size);
+            }
+          }
+        }
       }
-      return before + x - v;
-    };
-    auto units_of = [&](int64_t i) {
-      if (i >= B) return int64_t(0);
-      Sequence s;
-      s.load(p, i, R);
-      return s.units(p.c.heads);
-    };
-    int64_t sum, mine = 0;
-    for (int64_t i = threadIdx.x; i < B; i += kThreads) mine += units_of(i);
-    block_scan(mine, total);
-    per = max(static_cast<int64_t>(kLeastUnits), (total + gridDim.x - 1) / gridDim.x);
-    u = blockIdx.x * per;
-    u1 = min(u + per, total);
-    if (threadIdx.x == 0) p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    if (u >= u1) return;
-    for (int64_t i = 0, at = 0; i < B; i += kThreads) {
-      const int64_t v = units_of(i + threadIdx.x), x = at + block_scan(v, sum);
-      if (x <= u && u < x + v) {
-        scan[kWarps] = i + threadIdx.x;
-        scan[kWarps + 1] = x;
-      }
-      at += sum;
-      if (at > u) break;
     }
     __syncthreads();
     b = scan[kWarps];
     seq_at = scan[kWarps + 1];
+    u = scan[kWarps + 2];
+    u1 = c1 < before ? scan[kWarps + 3] : before;
   }
+  if (u >= u1) return;
   Sequence q;
   q.load(p, b, R);
+  {                        // a run that begins where the sequence ends
+    int64_t n = q.units(p.c.heads);
+    while (u >= seq_at + n) {
+      seq_at += n;
+      q.load(p, ++b, R);
+      n = q.units(p.c.heads);
+    }
+  }
 
   while (u < u1) {
     // The segment that u lies in: [at, end) of the line.
     const int size = kSegmentUnits + q.granules;
-    const int seg = static_cast<int>((u - seq_at) / size);
+    const int seg = static_cast<int>(quotient(u - seq_at, size));
     const int64_t at = seq_at + static_cast<int64_t>(seg) * size, end = at + size;
     const int h = seg / q.tiles, tile = seg - h * q.tiles;
     const bool begins = u == at, ends = end <= u1;
@@ -223,108 +278,114 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
     g0 = max(g0 + q.first, low_least >> 4);
     g1 = min(g1 + q.first, (seen_most + 15) >> 4);
     const int mine = g1 > g0 + warp ? (g1 - g0 - warp + kWarps - 1) / kWarps : 0;
+    // Granules that all of them see whole.
+    const int whole0 = (low_most + 15) >> 4, wholes = max(0, (seen_least >> 4) - whole0);
 
-    // Copies of this warp's granules g0 + warp + k * kWarps, S - 1 ahead; the page of the next is looked up one ahead.
-    const int per_page = p.c.page_shift - 4;
-    const int64_t head_at = static_cast<int64_t>(h) << per_page;
-    const int32_t* table = p.c.table + b * p.c.ldt;
-    auto page_of = [&](int k) {
-      const int64_t i = static_cast<int64_t>(g0 + warp + k * kWarps) >> per_page;
-      return k < mine && i < p.c.ldt ? table[i] : -1;
-    };
-    int page = page_of(0);
-    uint32_t missing = 0;                                             // bit k % S: granule k has no page
-    auto issue = [&](int k) {
-      if (k < mine) {
-        const int slot = k % S;
-        const bool there = page >= 0 && page < p.c.n_pages;
-        missing = there ? missing & ~(1u << slot) : missing | (1u << slot);
-        if (there) {
-          const int64_t gr = ((static_cast<int64_t>(page) * p.c.heads) << per_page) + head_at +
-                             ((g0 + warp + k * kWarps) & ((1 << per_page) - 1));
-          const uint8_t* src = p.c.data + gr * Gr::kBytes + 16 * lane;
-          const uint32_t dst = ring_u + slot * Gr::kBytes + 16 * lane;
+    // A thread's eight elements of the queries, on their way while the pages are looked up.
+    constexpr int L = D / 8;                                          // lanes of a row
+    static_assert(R * L <= kThreads, "a pass takes all rows");
+    const int qr = threadIdx.x / L, l8 = threadIdx.x % L;
+    float qv[8];
+    {
+      int i, hq;
+      if (qr < R && row_of(qr, i, hq)) {
+        const T* src = static_cast<const T*>(p.a.Q) + (q.n0 + i) * p.a.ldq + static_cast<int64_t>(hq) * D + 8 * l8;
+        if (p.vec) load8<T, true>(src, qv);
+        else load8<T, false>(src, qv);
+      } else {
 #pragma unroll
-          for (int i = 0; i < (Gr::kBytes + 511) / 512; ++i)
-            if (Gr::kBytes % 512 == 0 || 512 * i + 16 * lane < Gr::kBytes) cp_async16(dst + 512 * i, src + 512 * i);
-        } else if (lane == 0) {
-          report_error(p.err, ERR_PAGE);
-        }
-        page = page_of(k + 1);
+        for (int j = 0; j < 8; ++j) qv[j] = 0.f;
       }
-      cp_commit();
+    }
+
+    // Copies of this warp's granules g0 + warp + k * kWarps, S - 1 ahead. Lane k % 32 makes granule k's, and has looked its
+    // page up with those of the 31 beside it. A granule whose page is out of range is passed over.
+    const int per_page = p.c.page_shift - 4;
+    const int32_t* table = p.c.table + b * p.c.ldt;
+    auto source = [&](int k) -> const uint8_t* {
+      const int g = g0 + warp + k * kWarps;
+      const int64_t i = static_cast<int64_t>(g) >> per_page;
+      if (k >= mine || i >= p.c.ldt) return nullptr;
+      const int page = table[i];
+      if (page < 0 || page >= p.c.n_pages) return nullptr;
+      return p.c.data + ((((static_cast<int64_t>(page) * p.c.heads) + h) << per_page) + (g & ((1 << per_page) - 1))) * Gr::kBytes;
     };
-#pragma unroll
-    for (int k = 0; k < S - 1; ++k) issue(k);
+    const uint8_t* src = source(lane);
+    const uint8_t* src_next = mine > 32 ? source(32 + lane) : nullptr;
+    auto issue = [&](int to) {
+      uint64_t* bar = &full[warp][to];
+      if (src) {
+        mbar_expect_tx(bar, Gr::kBytes);
+        bulk_g2s(ring + to * Gr::kBytes, src, Gr::kBytes, bar);
+      } else {
+        report_error(p.err, ERR_PAGE);
+        mbar_arrive(bar);
+      }
+    };
+    if (lane < min(S - 1, mine)) issue((stage + lane) % S);
+    // Bit k % 32: granule k of these 32, of the next 32, has no page.
+    uint32_t gone = __ballot_sync(0xffffffffu, src == nullptr && lane < mine), gone_next = 0;
+    int turn = S - 1;                                                 // the lane whose copy is next
 
     // Queries as operands: lane (gid, tig) has of row gid the elements 32 g + 8 tig + 0..7, times 2^a with the
     // row's largest between 2^14 and 2^15 (so that fp16 and bf16 queries are exact), the odd ones
     // also times 2^-4 for the codes that are four bits higher.
-    uint32_t qb[NT][G][2][2], ql[kSplit ? NT : 1][kSplit ? G : 1][2][2], qs[NT][(G + 3) / 4][2];
+    {
+      const int g = l8 >> 2, t = l8 & 3;
+      float most = 0.f, sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(qv[j]));
+#pragma unroll
+      for (int o = 1; o < L; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+      // 2^e <= most < 2^(e + 1); rows below 2^-86 have scores of nothing, and those beyond 2^118 are NaN all over.
+      const int e = max(-86, min(127, static_cast<int>(__float_as_uint(most) >> 23) - 127));
+      const float up1 = pow2((14 - e) >> 1), up2 = pow2(14 - e - ((14 - e) >> 1));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        qv[j] = qv[j] * up1 * up2;
+        sum += qv[j];
+        if (j & 1) qv[j] *= 0.0625f;
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      if (qr < R) {
+        const int nt = qr >> 3, at = 4 * (qr & 7) + t;
+        q_hi[(nt * G + g) * 32 + at] =
+            make_uint4(pack_half2(qv[0], qv[4]), pack_half2(qv[1], qv[5]), pack_half2(qv[2], qv[6]), pack_half2(qv[3], qv[7]));
+        if constexpr (kSplit) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) qv[j] = low_part(qv[j]);
+          q_lo[(nt * G + g) * 32 + at] =
+              make_uint4(pack_half2(qv[0], qv[4]), pack_half2(qv[1], qv[5]), pack_half2(qv[2], qv[6]), pack_half2(qv[3], qv[7]));
+        }
+        // The block's sum in three parts of fp16, one for each of the lanes t = 0, 1, 2.
+        sum *= 0x1p-6f;
+        if (t > 0) sum = low_part(sum);
+        if (t > 1) sum = low_part(sum);
+        q_sum[((nt * ((G + 3) / 4) + (g >> 2)) * 32 + at) * 4 + (g & 3)] = __float2half_rn(t > 2 ? 0.f : sum);
+        if (l8 == 0) q_factor[qr] = most < 0x1p118f ? p.a.scale * 1.44269504f * pow2(10 + min(e, 117)) : NAN;
+      }
+    }
+    __syncthreads();
+    uint32_t qb[NT][G][2][2], qs[NT][(G + 3) / 4][2];
+    [[maybe_unused]] uint32_t ql[kSplit ? NT : 1][kSplit ? G : 1][2][2];
     float factor[NT][2];                                              // of the scores of columns 2 tig, 2 tig + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      int i, hq;
-      const bool here = row_of(8 * nt + gid, i, hq);
-      const T* src = static_cast<const T*>(p.a.Q) + (q.n0 + i) * p.a.ldq + static_cast<int64_t>(hq) * D + 8 * tig;
-      float v[G][8], top = 0.f, sums[G];
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        if (!here) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[g][j] = 0.f;
-        } else if (p.vec) {
-          load8<T, true>(src + 32 * g, v[g]);
-        } else {
-          load8<T, false>(src + 32 * g, v[g]);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[g][j]));
-      }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // 2^e <= top < 2^(e + 1); rows below 2^-86 have scores of nothing, and those beyond 2^118 are NaN all over.
-      const int e = max(-86, min(127, static_cast<int>(__float_as_uint(top) >> 23) - 127));
-      const float up1 = pow2((14 - e) >> 1), up2 = pow2(14 - e - ((14 - e) >> 1));
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        sums[g] = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          v[g][j] = v[g][j] * up1 * up2;
-          sums[g] += v[g][j];
-        }
-        sums[g] += __shfl_xor_sync(0xffffffffu, sums[g], 1);
-        sums[g] += __shfl_xor_sync(0xffffffffu, sums[g], 2);
-        sums[g] *= 0x1p-6f;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float x0 = v[g][2 * k], x4 = v[g][2 * k + 4], x1 = v[g][2 * k + 1] * 0.0625f, x5 = v[g][2 * k + 5] * 0.0625f;
-          qb[nt][g][k][0] = pack_half2(x0, x4);
-          qb[nt][g][k][1] = pack_half2(x1, x5);
-          if constexpr (kSplit) {
-            ql[nt][g][k][0] = pack_half2(low_part(x0), low_part(x4));
-            ql[nt][g][k][1] = pack_half2(low_part(x1), low_part(x5));
-          }
-        }
-        // The blocks' sums in three parts of fp16, one for each of the lanes tig = 0, 1, 2.
-        float part = sums[g];
-        if (tig > 0) part = low_part(part);
-        if (tig > 1) part = low_part(part);
-        sums[g] = tig > 2 ? 0.f : part;
+        *reinterpret_cast<uint4*>(qb[nt][g]) = q_hi[(nt * G + g) * 32 + lane];
+        if constexpr (kSplit) *reinterpret_cast<uint4*>(ql[nt][g]) = q_lo[(nt * G + g) * 32 + lane];
       }
 #pragma unroll
-      for (int k = 0; k < (G + 3) / 4; ++k) {
-        qs[nt][k][0] = pack_half2(sums[4 * k], sums[4 * k + 1]);
-        qs[nt][k][1] = G > 2 ? pack_half2(sums[(4 * k + 2) % G], sums[(4 * k + 3) % G]) : 0u;
-      }
-      const float f = top < 0x1p118f ? p.a.scale * 1.44269504f * pow2(10 + min(e, 117)) : NAN;
+      for (int k = 0; k < (G + 3) / 4; ++k)
+        *reinterpret_cast<uint2*>(qs[nt][k]) = *reinterpret_cast<const uint2*>(q_sum + ((nt * ((G + 3) / 4) + k) * 32 + lane) * 4);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) factor[nt][c] = __shfl_sync(0xffffffffu, f, 4 * (2 * tig + c));
+      for (int c = 0; c < 2; ++c) factor[nt][c] = q_factor[8 * nt + 2 * tig + c];
     }
 
     float o[NT][G][2][4], om[NT][4], top[NT][2];
-    int sigma = -24;                                                  // weights are relative to 2^sigma
+    int sigma = kSplit ? -24 : 0;                                     // weights are relative to 2^sigma
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       top[nt][0] = top[nt][1] = kLow;
@@ -340,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
     // different banks: row r is place r / 2 + 4 (r % 2), of the lower or upper eight.
     const int ta = (gid >> 1) + 4 * (gid & 1);
     auto granule = [&](auto edge_tag, const uint8_t* gr, int place0) {
-      constexpr bool kEdge = decltype(edge_tag)::value;
+      constexpr bool kEdge = decltype(edge_tag)::value;               // some row does not see all of its places
       float s[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -363,15 +424,11 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
         float sm[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sm[nt][j] = 0.f;
           if constexpr (G == 2) {
-            mma_f16(sm[nt], pa[1], pb[1], 0u, 0u, qs[nt][0][0], 0u);
+            mma_f16_zero(sm[nt], pa[1], pb[1], 0u, 0u, qs[nt][0][0], 0u);
           } else {
-#pragma unroll
-            for (int k = 0; k < G / 4; ++k)
-              mma_f16(sm[nt], pa[G / 2 + 2 * k], pb[G / 2 + 2 * k], pa[G / 2 + 2 * k + 1], pb[G / 2 + 2 * k + 1], qs[nt][k][0],
-                      qs[nt][k][1]);
+            mma_f16_zero(sm[nt], pa[G / 2], pb[G / 2], pa[G / 2 + 1], pb[G / 2 + 1], qs[nt][0][0], qs[nt][0][1]);
+            if constexpr (G == 8) mma_f16(sm[nt], pa[6], pb[6], pa[7], pb[7], qs[nt][1][0], qs[nt][1][1]);
           }
         }
 #pragma unroll
@@ -382,8 +439,8 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
           const uint32_t c0 = (ka[g] >> 8) & M0, c1 = (kb[g] >> 8) & M0, c2 = (ka[g] >> 8) & M1, c3 = (kb[g] >> 8) & M1;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(acc, a0, a1, a2, a3, qb[nt][g][0][0], qb[nt][g][0][1]);
+            float acc[4];
+            mma_f16_zero(acc, a0, a1, a2, a3, qb[nt][g][0][0], qb[nt][g][0][1]);
             mma_f16(acc, c0, c1, c2, c3, qb[nt][g][1][0], qb[nt][g][1][1]);
             if constexpr (kSplit) {
               mma_f16(acc, a0, a1, a2, a3, ql[nt][g][0][0], ql[nt][g][0][1]);
@@ -401,8 +458,6 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[nt][j] = fmaf(sm[nt][j], 0x1p-18f, s[nt][j]) * factor[nt][j & 1];
       }
-      const bool out_a = kEdge && (place0 + ta < low_least || place0 + ta >= seen_most);
-      const bool out_b = kEdge && (place0 + ta + 8 < low_least || place0 + ta + 8 >= seen_most);
       if constexpr (kEdge) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -415,38 +470,88 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
           }
       }
 
-      // Parameters of the values: of places ta and ta + 8 the s, as halves.
+      // The values' parameters, two places a word, in the order of the operand's rows 2 tig, 2 tig + 1: m0 (lower eight places)
+      // and m1 (upper eight) as an operand whose rows g (4 + g for 128 elements) are the blocks' m; for rows of 16 bits also va and
+      // vb, their s. fp32 rows: s of two blocks a word, of places ta and ta + 8. Places that no row of the tile sees: 0.
       const uint8_t* vp = gr + Gr::kValues + Gr::kCodes;
-      uint32_t va[G / 2], vb[G / 2];
-      if constexpr (G == 2) {
-        va[0] = *reinterpret_cast<const uint32_t*>(vp + ta * (4 * G));
-        vb[0] = *reinterpret_cast<const uint32_t*>(vp + (ta + 8) * (4 * G));
-      } else {
-#pragma unroll
-        for (int i = 0; i < G / 4; ++i) {
-          *reinterpret_cast<uint2*>(va + 2 * i) = reinterpret_cast<const uint2*>(vp + ta * (4 * G))[i];
-          *reinterpret_cast<uint2*>(vb + 2 * i) = reinterpret_cast<const uint2*>(vp + (ta + 8) * (4 * G))[i];
-        }
-      }
+      const auto unseen = [&](int place) { return kEdge && (place0 + place < low_least || place0 + place >= seen_most); };
+      uint32_t m0 = 0, m1 = 0, sizes = 0;
+      uint32_t va[kSplit ? G / 2 : G], vb[kSplit ? G / 2 : G];
+      uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
       if constexpr (kEdge) {
+        keep0 = (unseen(tig) ? 0u : 0xffffu) | (unseen(tig + 4) ? 0u : 0xffff0000u);
+        keep1 = (unseen(tig + 8) ? 0u : 0xffffu) | (unseen(tig + 12) ? 0u : 0xffff0000u);
+      }
+      if constexpr (D >= 128) {
+        const uint8_t* row = vp + ((lane & 8) + ((lane >> 1) & 3) + 4 * (lane & 1)) * (4 * G);
+        load_transposed(m0, m1, row + (D == 256 ? 2 * G : 0));
+        m0 &= keep0, m1 &= keep1;
+        if constexpr (!kSplit) {
+          uint32_t s0 = m0, s1 = m1;                                  // of 128 elements: rows 0..3 of the same matrices
+          if constexpr (D == 256) {
+            load_transposed(s0, s1, row);
+            s0 &= keep0, s1 &= keep1;
+          }
+          sizes = gid < G ? s0 | s1 : 0;
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            va[g] = __shfl_sync(0xffffffffu, s0, 4 * g + tig);
+            vb[g] = __shfl_sync(0xffffffffu, s1, 4 * g + tig);
+          }
+        }
+      } else {
+        const auto words = [&](int place) { return *reinterpret_cast<const uint2*>(vp + place * 8); };
+        const uint2 x = words(tig), y = words(tig + 4), z = words(tig + 8), w = words(tig + 12);
+        if constexpr (!kSplit) {
+          va[0] = __byte_perm(x.x, y.x, 0x5410) & keep0, va[1] = __byte_perm(x.x, y.x, 0x7632) & keep0;
+          vb[0] = __byte_perm(z.x, w.x, 0x5410) & keep1, vb[1] = __byte_perm(z.x, w.x, 0x7632) & keep1;
+          sizes = va[0] | va[1] | vb[0] | vb[1];
+        }
+        const uint32_t pick = gid == 0 ? 0x5410u : 0x7632u;
+        m0 = gid < G ? __byte_perm(x.y, y.y, pick) & keep0 : 0u;
+        m1 = gid < G ? __byte_perm(z.y, w.y, pick) & keep1 : 0u;
+      }
+      if constexpr (kSplit) {
 #pragma unroll
         for (int i = 0; i < G / 2; ++i) {
-          if (out_a) va[i] = 0;
-          if (out_b) vb[i] = 0;
+          va[i] = unseen(ta) ? 0u : reinterpret_cast<const uint32_t*>(vp + ta * (4 * G))[i];
+          vb[i] = unseen(ta + 8) ? 0u : reinterpret_cast<const uint32_t*>(vp + (ta + 8) * (4 * G))[i];
         }
       }
-      // The largest s of the granule: a NaN counts for nothing, an infinity as fp16's largest.
-      __half2 big = __habs2(bits_half2(va[0]));
-#pragma unroll
-      for (int i = 0; i < G / 2; ++i) big = __hmax2(big, __hmax2(__habs2(bits_half2(va[i])), __habs2(bits_half2(vb[i]))));
-      const float largest = fminf(fmaxf(__low2float(big), __high2float(big)), 65504.f);
 
-      bool move = largest > pow2(sigma);
+      // Scores less their columns' offset; the maximum is moved where one passes it by kAhead, sigma where an s passes 2^sigma.
+      // Rows of 16 bits have sigma 0 until an s is 2 or more (its exponent's highest bit is set).
+      float x[NT][4], off[NT][2];
+      const auto shift = [&] {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) off[nt][c] = top[nt][c] + (static_cast<float>(sigma) - kTop);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[nt][j] = s[nt][j] - off[nt][j & 1];
+        }
+      };
+      shift();
+      float ahead = x[0][0];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) move |= s[nt][j] > top[nt][j & 1] + kAhead;
-      if (__any_sync(0xffffffffu, move)) {
+        for (int j = 0; j < 4; ++j) ahead = fmaxf(ahead, x[nt][j]);
+      float largest = 0.f;
+      if constexpr (kSplit) {
+        __half2 big = __habs2(bits_half2(va[0]));
+#pragma unroll
+        for (int i = 0; i < G / 2; ++i) big = __hmax2(big, __hmax2(__habs2(bits_half2(va[i])), __habs2(bits_half2(vb[i]))));
+        largest = fminf(fmaxf(__low2float(big), __high2float(big)), 65504.f);   // a NaN counts for nothing
+      }
+      if (__any_sync(0xffffffffu, ahead > kTop + kAhead - static_cast<float>(sigma) || (kSplit ? largest > pow2(sigma) : (sizes & 0x40004000u) != 0))) {
+        if constexpr (!kSplit) {
+          __half2 big = __habs2(bits_half2(va[0]));
+#pragma unroll
+          for (int i = 0; i < G; ++i) big = __hmax2(big, __hmax2(__habs2(bits_half2(va[i])), __habs2(bits_half2(vb[i]))));
+          largest = fminf(fmaxf(__low2float(big), __high2float(big)), 65504.f);
+          if (largest < 2.f) largest = 0.f;
+        }
         const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(largest > 0.f ? largest : 0.f));
         const int want = max(sigma, static_cast<int>((bits + 0x007fffffu) >> 23) - 127);   // the power of two not below it
         const float by = pow2(max(-126, sigma - want));
@@ -462,8 +567,8 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
             m = fmaxf(m, top[nt][c]);
             const float f = exp2_fast(top[nt][c] - m), fs = f * by;
             top[nt][c] = m;
-            om[nt][c] *= f;
-            om[nt][c + 2] *= f;
+            om[nt][c] *= kSplit ? f : fs;
+            om[nt][c + 2] *= kSplit ? f : fs;
 #pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -472,42 +577,37 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
                 o[nt][g][k][c + 2] *= fs;
               }
           }
+        shift();
       }
 
-      // Weights: of the codes' sums relative to 2^sigma.
-      const float up = pow2(sigma);
-      uint32_t pb2[NT][2];
-      [[maybe_unused]] uint32_t pl2[kSplit ? NT : 1][2];
+      // Weights, transposed as operands. Rows of 16 bits: the weights times 2^(kTop - sigma) rounded to fp16, and for each
+      // block's codes their products with s (at most 2^15: s is below 2 with sigma 0, else s / 2^sigma at most 1). fp32
+      // rows: these products taken in fp32, and the weights times 2^kTop, all in two halves.
+      uint32_t pw[NT][2];
+      [[maybe_unused]] uint32_t pl[kSplit ? NT : 1][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float b0 = top[nt][0] + (static_cast<float>(sigma) - kTop), b1 = top[nt][1] + (static_cast<float>(sigma) - kTop);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[nt][j] = exp2_fast(s[nt][j] - (j & 1 ? b1 : b0));
+        for (int j = 0; j < 4; ++j) s[nt][j] = exp2_fast(x[nt][j]);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float x = s[nt][2 * k] * up, y = s[nt][2 * k + 1] * up;
-          pb2[nt][k] = transpose8(pack_half2(x, y));
-          if constexpr (kSplit) pl2[nt][k] = transpose8(pack_half2(low_part(x), low_part(y)));
+          if constexpr (kSplit) {
+            const float up = pow2(sigma), y = s[nt][2 * k] * up, z = s[nt][2 * k + 1] * up;
+            pw[nt][k] = transpose8(pack_half2(y, z));
+            pl[nt][k] = transpose8(pack_half2(low_part(y), low_part(z)));
+          } else {
+            pw[nt][k] = transpose8(pack_half2(s[nt][2 * k], s[nt][2 * k + 1]));
+          }
         }
       }
 
-      // The m of the values and a row of ones: rows g < G are the blocks' m, row 8 (or a row of the lower eight) the ones.
+      // The m, and a row of ones (row 8).
       {
-        uint32_t m0 = 0, m1 = 0;
-        if (gid < G) {
-          const uint8_t* mp = vp + 2 * G + 2 * gid;
-          const auto half_at = [&](int place) -> uint32_t {
-            const uint32_t v = *reinterpret_cast<const uint16_t*>(mp + place * (4 * G));
-            return kEdge && (place0 + place < low_least || place0 + place >= seen_most) ? 0u : v;
-          };
-          m0 = half_at(tig) | half_at(tig + 4) << 16;
-          m1 = half_at(tig + 8) | half_at(tig + 12) << 16;
-        }
         const uint32_t one = gid == 0 ? 0x3c003c00u : 0u;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_f16(om[nt], m0, one, m1, one, pb2[nt][0], pb2[nt][1]);
-          if constexpr (kSplit) mma_f16(om[nt], m0, one, m1, one, pl2[nt][0], pl2[nt][1]);
+          mma_f16(om[nt], m0, one, m1, one, pw[nt][0], pw[nt][1]);
+          if constexpr (kSplit) mma_f16(om[nt], m0, one, m1, one, pl[nt][0], pl[nt][1]);
         }
       }
 
@@ -525,104 +625,125 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
           for (int i = 0; i < G / 4; ++i) *reinterpret_cast<uint2*>(&w[k][2 * i]) = reinterpret_cast<const uint2*>(src)[i];
         }
       }
+      // (A NaN of a place that a row does not see is left out.)
+      {
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const float2 sa2 = __half22float2(bits_half2(va[g / 2])), sb2 = __half22float2(bits_half2(vb[g / 2]));
-        const float sa = g & 1 ? sa2.y : sa2.x, sb = g & 1 ? sb2.y : sb2.x;
-        const uint32_t pick = g & 1 ? 0x7632u : 0x5410u;
-        const uint32_t x = __byte_perm(w[0][g / 2], w[1][g / 2], pick), y = __byte_perm(w[2][g / 2], w[3][g / 2], pick);
-        const uint32_t a0 = x & M0, a1 = x & M1, a2 = y & M0, a3 = y & M1;
-        const uint32_t c0 = (x >> 8) & M0, c1 = (x >> 8) & M1, c2 = (y >> 8) & M0, c3 = (y >> 8) & M1;
+        for (int g = 0; g < G; ++g) {
+          const uint32_t pick = g & 1 ? 0x7632u : 0x5410u;
+          const uint32_t x = __byte_perm(w[0][g / 2], w[1][g / 2], pick), y = __byte_perm(w[2][g / 2], w[3][g / 2], pick);
+          const uint32_t a0 = x & M0, a1 = x & M1, a2 = y & M0, a3 = y & M1;
+          const uint32_t c0 = (x >> 8) & M0, c1 = (x >> 8) & M1, c2 = (y >> 8) & M0, c3 = (y >> 8) & M1;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float t[4] = {s[nt][0] * sa, s[nt][1] * sa, s[nt][2] * sb, s[nt][3] * sb};
-          if constexpr (kEdge) {                                      // a NaN of a place that a row does not see
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (kSplit) {
+              const float2 sa2 = __half22float2(bits_half2(va[g / 2])), sb2 = __half22float2(bits_half2(vb[g / 2]));
+              const float sa = g & 1 ? sa2.y : sa2.x, sb = g & 1 ? sb2.y : sb2.x;
+              float t[4] = {s[nt][0] * sa, s[nt][1] * sa, s[nt][2] * sb, s[nt][3] * sb};
+              if constexpr (kEdge) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) t[j] = s[nt][j] == 0.f ? 0.f : t[j];
-          }
-          const uint32_t b0 = transpose8(pack_half2(t[0], t[1])), b1 = transpose8(pack_half2(t[2], t[3]));
-          mma_f16(o[nt][g][0], a0, a1, a2, a3, b0, b1);
-          mma_f16(o[nt][g][1], c0, c1, c2, c3, b0, b1);
-          if constexpr (kSplit) {
-            const uint32_t l0 = transpose8(pack_half2(low_part(t[0]), low_part(t[1])));
-            const uint32_t l1 = transpose8(pack_half2(low_part(t[2]), low_part(t[3])));
-            mma_f16(o[nt][g][0], a0, a1, a2, a3, l0, l1);
-            mma_f16(o[nt][g][1], c0, c1, c2, c3, l0, l1);
+                for (int j = 0; j < 4; ++j) t[j] = s[nt][j] == 0.f ? 0.f : t[j];
+              }
+              const uint32_t b0 = transpose8(pack_half2(t[0], t[1])), b1 = transpose8(pack_half2(t[2], t[3]));
+              const uint32_t l0 = transpose8(pack_half2(low_part(t[0]), low_part(t[1])));
+              const uint32_t l1 = transpose8(pack_half2(low_part(t[2]), low_part(t[3])));
+              mma_f16(o[nt][g][0], a0, a1, a2, a3, b0, b1);
+              mma_f16(o[nt][g][1], c0, c1, c2, c3, b0, b1);
+              mma_f16(o[nt][g][0], a0, a1, a2, a3, l0, l1);
+              mma_f16(o[nt][g][1], c0, c1, c2, c3, l0, l1);
+            } else {
+              uint32_t b0 = half2_bits(__hmul2(bits_half2(pw[nt][0]), bits_half2(va[g])));
+              uint32_t b1 = half2_bits(__hmul2(bits_half2(pw[nt][1]), bits_half2(vb[g])));
+              if constexpr (kEdge) {
+                b0 &= __hne2_mask(bits_half2(pw[nt][0]), __half2half2(__ushort_as_half(0)));
+                b1 &= __hne2_mask(bits_half2(pw[nt][1]), __half2half2(__ushort_as_half(0)));
+              }
+              mma_f16(o[nt][g][0], a0, a1, a2, a3, b0, b1);
+              mma_f16(o[nt][g][1], c0, c1, c2, c3, b0, b1);
+            }
           }
         }
       }
     };
 
+    if (mine > 32) gone_next = __ballot_sync(0xffffffffu, src_next == nullptr && 32 + lane < mine);
+#pragma unroll 1
     for (int k = 0; k < mine; ++k) {
-      cp_wait<S - 2>();
-      __syncwarp();
-      const bool gone = (missing >> (k % S)) & 1;
-      issue(k + S - 1);
-      if (gone) continue;
-      const int place0 = 16 * (g0 + warp + k * kWarps);
-      const uint8_t* gr = ring + (k % S) * Gr::kBytes;
-      if (place0 >= low_most && place0 + 16 <= seen_least) granule(std::false_type{}, gr, place0);
-      else granule(std::true_type{}, gr, place0);
+      if (!mbar_try_wait(&full[warp][stage], phase)) mbar_wait(&full[warp][stage], phase, &abort, p.err);
+      __syncwarp();                               // every lane is past the granule before this one: its stage is free
+      if (k + S - 1 < mine) {
+        if (turn == 32) {                         // the next 32 pages
+          turn = 0;
+          src = src_next;
+          src_next = source(k + S - 1 + 32 + lane);
+        }
+        if (lane == turn) issue((stage + S - 1) % S);
+        ++turn;
+      }
+      bool skip = false;
+      if (gone | gone_next) {
+        skip = (gone >> (k & 31)) & 1;
+      }
+      if ((k & 31) == 31) {
+        gone = gone_next;
+        gone_next = __ballot_sync(0xffffffffu, src_next == nullptr && k + 33 + lane < mine);
+      }
+      const int g = g0 + warp + k * kWarps;
+      const uint8_t* gr = ring + stage * Gr::kBytes;
+      stage = (stage + 1) % S;
+      phase ^= stage == 0;
+      if (skip) continue;
+      if (static_cast<unsigned>(g - whole0) < static_cast<unsigned>(wholes)) granule(std::false_type{}, gr, 16 * g);
+      else granule(std::true_type{}, gr, 16 * g);
     }
-    cp_wait<0>();
 
-    // The warps' sums joined, one warp after the other.
+    // The warps' sums, beside one another where their copies were.
+    __syncthreads();
+    const float up = kSplit ? 0x1p24f * pow2(sigma) : 0x1p24f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int c = 0; c < 2; ++c) {
+        const int r = 8 * nt + 2 * tig + c;
         if (gid == 0) {
-          stat[warp * R + 8 * nt + 2 * tig + c] = top[nt][c];
-          stat[(kWarps + warp) * R + 8 * nt + 2 * tig + c] = om[nt][c + 2];
+          stat[warp * R + r] = top[nt][c] + (kSplit ? 0.f : static_cast<float>(sigma));
+          stat[(kWarps + warp) * R + r] = om[nt][c + 2];
         }
-    __syncthreads();
-    const float up = 0x1p24f * pow2(sigma);
-#pragma unroll 1
-    for (int turn = 0; turn < kWarps; ++turn) {
-      if (warp == turn) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int r = 8 * nt + 2 * tig + c;
-            float most = stat[r];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) most = fmaxf(most, stat[w * R + r]);
-            const float f = exp2_fast(top[nt][c] - most);
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-              const float m = __shfl_sync(0xffffffffu, om[nt][c], 4 * g + tig);
-              float4 v = make_float4(fmaf(o[nt][g][0][c], up, m) * f, fmaf(o[nt][g][0][c + 2], up * 0.0625f, m) * f,
-                                     fmaf(o[nt][g][1][c], up, m) * f, fmaf(o[nt][g][1][c + 2], up * 0.0625f, m) * f);
-              float4* dst = reinterpret_cast<float4*>(joined + r * Sh::kPitch + 32 * g + 4 * gid);
-              if (turn > 0) {
-                const float4 x = *dst;
-                v = make_float4(x.x + v.x, x.y + v.y, x.z + v.z, x.w + v.w);
-              }
-              *dst = v;
-            }
-          }
+        for (int g = 0; g < G; ++g) {
+          const float m = __shfl_sync(0xffffffffu, om[nt][c], 4 * ((D == 128 ? 4 : 0) + g) + tig);
+          *reinterpret_cast<float4*>(joined + (warp * R + r) * Sh::kPitch + 32 * g + 4 * gid) =
+              make_float4(fmaf(o[nt][g][0][c], up, m), fmaf(o[nt][g][0][c + 2], up * 0.0625f, m),
+                          fmaf(o[nt][g][1][c], up, m), fmaf(o[nt][g][1][c + 2], up * 0.0625f, m));
+        }
       }
-      __syncthreads();
-    }
+    __syncthreads();
 
     // Outputs of a whole segment; else a part for the second kernel.
-    constexpr int L = D / 8;                                          // lanes of a row
     float* part = p.parts + (2 * static_cast<int64_t>(blockIdx.x) + (begins ? 1 : 0)) * kPart<D, R>;
-#pragma unroll 1
-    for (int r0 = 0; r0 < R; r0 += kThreads / L) {
-      const int r = r0 + threadIdx.x / L, l8 = threadIdx.x % L;
+    {
+      const int r = qr;
       int i = 0, hq = 0;
       const bool here = r < R && row_of(r, i, hq);
       float v[8], most = kLow, sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.f;
       if (r < R) {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) most = fmaxf(most, stat[w * R + r]);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum = fmaf(stat[(kWarps + w) * R + r], exp2_fast(stat[w * R + r] - most), sum);
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = exp2_fast(stat[w * R + r] - most);
+          const float* src = joined + (w * R + r) * Sh::kPitch + 8 * l8;
+          sum = fmaf(stat[(kWarps + w) * R + r], f, sum);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          *reinterpret_cast<float4*>(v + 4 * j) = *reinterpret_cast<const float4*>(joined + r * Sh::kPitch + 8 * l8 + 4 * j);
+          for (int j = 0; j < 2; ++j) {
+            const float4 x = reinterpret_cast<const float4*>(src)[j];
+            v[4 * j] = fmaf(x.x, f, v[4 * j]);
+            v[4 * j + 1] = fmaf(x.y, f, v[4 * j + 1]);
+            v[4 * j + 2] = fmaf(x.z, f, v[4 * j + 2]);
+            v[4 * j + 3] = fmaf(x.w, f, v[4 * j + 3]);
+          }
+        }
       }
       if (begins && ends) {
         const float inv = sum == 0.f ? 0.f : __fdiv_rn(1.0f, sum);    // a row that sees nothing
@@ -640,7 +761,13 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
       }
     }
     if (begins && !ends && threadIdx.x == 0)
-      p.meta[blockIdx.x] = make_int4(static_cast<int>(b), h, tile, static_cast<int>((end - 1) / per - blockIdx.x) + 1);
+{
+      // The CTA whose run has the segment's last unit: that of the last cut within it that was not moved to its end.
+      int64_t last = quotient(end - 1, per);
+      while (last > blockIdx.x && cut_at(last * per - at, size) == size) --last;
+      p.meta[blockIdx.x] = make_int4(static_cast<int>(b), h, tile, static_cast<int>(last - blockIdx.x) + 1);
+    }
+    fence_proxy_async_smem();      // the ring is written by copies again
     __syncthreads();
 
     // On to the next segment, in this sequence or the next that has any.
@@ -653,68 +780,108 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
         n = q.units(p.c.heads);
       }
     }
+  }  if (abort) {               // copies that a wait gave up on land before the CTA ends
+    for (int k = 0; k < S; ++k) mbar_wait_bounded(&full[warp][(stage + k) % S], phase ^ (stage + k >= S ? 0 : 1));
   }
 }
 
-// The segments that several CTAs had parts of: for the CTA blockIdx.x that began one, row blockIdx.y of its tile.
+// The segments that several CTAs had parts of. Every CTA makes the list of the CTAs that began one, and takes rows of
+// their tiles: a row by one warp where there are rows enough for all, else by up to eight that share its parts.
+constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps;
+
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(kThreads) attn_q4_join_kernel(const Attn p) {
-  constexpr int L4 = D / 4, P = kThreads / L4;                        // lanes of a row, parts read at a time
-  extern __shared__ float weight[];
-  __shared__ float red[kWarps], sums[P][D];
+__global__ void __launch_bounds__(kJoinThreads) attn_q4_join_kernel(const Attn p, int ctas) {
+  constexpr int E = D / 32;                                           // elements of a lane
+  extern __shared__ int list[];                                       // [ctas]
+  __shared__ float sums[kJoinWarps][D];
+  __shared__ int found[kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_enter();
-  const int4 meta = p.meta[blockIdx.x];
-  if (meta.x < 0) return;
-  const int r = blockIdx.y, rr = meta.z * R + r, i = rr / p.group, hq = meta.y * p.group + rr - i * p.group;
-  Sequence q;
-  q.load(p, meta.x, R);
-  if (rr >= q.rows * p.group) return;
-  const float* base = p.parts + 2 * static_cast<int64_t>(blockIdx.x) * kPart<D, R>;
-  auto part = [&](int k) { return base + (k == 0 ? 1 : 2 * static_cast<int64_t>(k)) * kPart<D, R>; };
-  float most = kLow;
-  for (int k = threadIdx.x; k < meta.w; k += kThreads) most = fmaxf(most, part(k)[R * D + r]);
+  int n = 0;
+  for (int c0 = 0; c0 < ctas; c0 += kJoinThreads) {
+    const int c = c0 + threadIdx.x;
+    const bool there = c < ctas && p.meta[c].x >= 0;
+    const uint32_t all = __ballot_sync(0xffffffffu, there);
+    __syncthreads();
+    if (lane == 0) found[warp] = __popc(all);
+    __syncthreads();
+    int at = n;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = most;
-  __syncthreads();
-  most = red[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) most = fmaxf(most, red[w]);
-  float sum = 0.f;
-  for (int k = threadIdx.x; k < meta.w; k += kThreads) {
-    weight[k] = exp2_fast(part(k)[R * D + r] - most);
-    sum = fmaf(weight[k], part(k)[R * D + R + r], sum);
+    for (int w = 0; w < kJoinWarps; ++w) {
+      if (w < warp) at += found[w];
+      n += found[w];
+    }
+    if (there) list[at + __popc(all & ((1u << lane) - 1))] = c;
   }
-  sum = warp_sum_f(sum);
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
-  __syncthreads();
-  sum = red[0];
+  const int items = n * R;
+  int W = 1;                                                          // warps of a row
+  while (W < kJoinWarps && items * 2 * W <= static_cast<int>(gridDim.x) * kJoinWarps) W *= 2;
+  const int each = kJoinWarps / W, group = warp / W, part0 = warp % W;
+  for (int first = blockIdx.x * each; first < items; first += gridDim.x * each) {
+    const int item = first + group;
+    int i = 0, hq = 0;
+    bool here = false;
+    Sequence q;
+    float sum = 0.f;
+    float acc[E];
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) sum += red[w];
-  const int l4 = threadIdx.x % L4, k0 = threadIdx.x / L4;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    if (item < items) {
+      const int c = list[item / R], r = item % R;
+      const int4 meta = p.meta[c];
+      q.load(p, meta.x, R);
+      const int rr = meta.z * R + r;
+      i = rr / p.group;
+      hq = meta.y * p.group + rr - i * p.group;
+      here = rr < q.rows * p.group;
+      const float* base = p.parts + 2 * static_cast<int64_t>(c) * kPart<D, R>;
+      auto part = [&](int k) { return base + (k == 0 ? 1 : 2 * static_cast<int64_t>(k)) * kPart<D, R>; };
+      if (here) {
+        float most = kLow;
+        for (int k = lane; k < meta.w; k += 32) most = fmaxf(most, part(k)[R * D + r]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        for (int k0 = 0; k0 < meta.w; k0 += 32) {
+          const int k = k0 + lane;
+          const float f = k < meta.w ? exp2_fast(part(k)[R * D + r] - most) : 0.f;
+          if (k < meta.w) sum = fmaf(f, part(k)[R * D + R + r], sum);
+          const int count = min(32, meta.w - k0);
 #pragma unroll 4
-  for (int k = k0; k < meta.w; k += P) {
-    const float4 v = *reinterpret_cast<const float4*>(part(k) + r * D + 4 * l4);
-    const float f = weight[k];
-    acc = make_float4(fmaf(f, v.x, acc.x), fmaf(f, v.y, acc.y), fmaf(f, v.z, acc.z), fmaf(f, v.w, acc.w));
-  }
-  *reinterpret_cast<float4*>(&sums[k0][4 * l4]) = acc;
-  __syncthreads();
-  if (threadIdx.x >= 32) return;
-  const int l8 = threadIdx.x;
-  const bool here = l8 < D / 8;
-  const float inv = sum == 0.f ? 0.f : __fdiv_rn(1.0f, sum);
-  float v[8];
+          for (int t = part0; t < count; t += W) {
+            const float g = __shfl_sync(0xffffffffu, f, t);
+            const float* src = part(k0 + t) + r * D + E * lane;
+            float v[E];
+            if constexpr (E == 2) {
+              *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+            } else {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    v[j] = 0.f;
-    if (here)
-      for (int k = 0; k < P; ++k) v[j] += sums[k][8 * l8 + j];
-    v[j] = sum == 0.f ? 0.f : v[j] * inv;
+              for (int e = 0; e < E / 4; ++e) reinterpret_cast<float4*>(v)[e] = reinterpret_cast<const float4*>(src)[e];
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(g, v[e], acc[e]);
+          }
+        }
+        sum = warp_sum_f(sum);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) sums[warp][E * lane + e] = acc[e];
+    __syncthreads();
+    if (part0 == 0) {
+      const float inv = sum == 0.f ? 0.f : __fdiv_rn(1.0f, sum);
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = 0.f;
+        if (lane < D / 8)
+          for (int w = 0; w < W; ++w) v[j] += sums[warp + w][8 * lane + j];
+        v[j] = sum == 0.f ? 0.f : v[j] * inv;
+      }
+      store_row<T, D>(p, here && lane < D / 8, q.n0 + i, hq, lane, v);
+    }
+    __syncthreads();
   }
-  store_row<T, D>(p, here, q.n0 + i, hq, l8, v);
 }
 
 // Rows of a tile: 8 where a sequence's (row, query head) pairs are 8 or fewer on the average, else 16 (of heads of 256
@@ -736,7 +903,7 @@ cudaError_t run(const Attn& p, int num_sms, cudaStream_t s) {
   const int grid = num_sms * Sh::kCtas;
   e = launch_pdl(attn_q4_kernel<T, D, NT>, dim3(grid), dim3(kThreads), Sh::kSmem, s, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_q4_join_kernel<T, D, Sh::R>, dim3(grid, Sh::R), dim3(kThreads), grid * sizeof(float), s, p);
+  return launch_pdl(attn_q4_join_kernel<T, D, Sh::R>, dim3(num_sms), dim3(kJoinThreads), grid * sizeof(int), s, p, grid);
 }
 
 template <typename T>
@@ -747,7 +914,7 @@ cudaError_t run(const Attn& p, int num_sms, cudaStream_t s) {
   return run<T, 256, 1>(p, num_sms, s);
 }
 
-constexpr int kMostCtas = 4;            // of an SM, of any form
+constexpr int kMostCtas = 2;            // of an SM, of any form
 
 }  // namespace
 
