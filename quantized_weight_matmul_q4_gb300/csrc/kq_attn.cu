@@ -13,14 +13,15 @@
 // The first sum of each is a product of codes per block, scaled after (scores) or before (weights);
 // the second is one more product, of the m themselves, which also gives Sum_t p_t by a row of ones.
 //
-// Scores are exact products summed in fp32. Weights are rounded to fp16 as operands (a relative 2^-12, which
-// 16-bit outputs do not show; fp32 rows have theirs split into two halves, as their queries are); they are
-// taken relative to a power of two near the largest s so far, so that none leaves fp16's range.
+// Scores are exact products summed in fp32. Weights are rounded to fp16 as operands (a relative 2^-12 each time,
+// twice for those of the codes, which 16-bit outputs do not show; fp32 rows have theirs split into two
+// halves, as their queries are); they are taken relative to a power of two not below the largest s so
+// far, so that none leaves fp16's range.
 //
-// Work is shared out evenly whatever the sequences' lengths: the granules of 16 places of all (sequence,
-// key head, tile of rows) segments stand in one line, of which each CTA takes an equal run. A segment that
-// lies in several runs is joined by a second kernel from the parts that the first leaves in the workspace, in
-// their order: results do not depend on scheduling.
+// Work is shared out evenly whatever the sequences' lengths: the steps of 32 places of all (sequence,
+// key head, tile of rows) segments stand in one line, of which each warp takes an equal run. The pieces of a
+// segment in a CTA's warps are joined there; what lies in several CTAs is joined by a second kernel from the
+// parts that the first leaves in the workspace. Both go by the order of the line: results do not depend on scheduling.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -34,17 +35,16 @@
 namespace kq {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr float kLow = -1e30f;          // the maximum before any score
 constexpr float kAhead = 4.f;           // how far a score may pass the maximum (log2) before it is moved
 constexpr float kTop = 10.f;            // weights are 2^(score - maximum + kTop): 2^14 at most
-constexpr int kSegmentUnits = 4;        // what beginning and ending a segment costs, in granules
-constexpr int kRound = kWarps;          // granules of a CTA's runs within a segment come in such numbers
+constexpr int kSegmentUnits = 3;        // what beginning and ending a segment costs, in steps of 32 places
+constexpr int kRound = 2;               // steps that a segment is cut by
 
 struct Attn {
   AttnArgs a;
   KvCache c;
-  float* parts;              // [CTAs][2]: unfinished segments, kPart floats each
+  float* parts;              // [CTAs][2]: pieces of segments that another CTA began, or ends; kPart floats each
   int4* meta;                // [CTAs]: what part 1 is (sequence or -1, key head, tile, parts)
   int group;                 // query heads of a key head
   bool vec;                  // rows of Q (and of O) lie on 16-byte boundaries
@@ -56,7 +56,7 @@ constexpr int kPart = R * D + 2 * R;    // sums [R][D], then maxima [R] and tota
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -64,7 +64,7 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 // The same beginning from zero.
 __device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                              uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
@@ -72,7 +72,7 @@ __device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_
 // The transpose of an 8 x 8 matrix of fp16 held two to a lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 // Two 8 x 8 matrices of fp16 from shared memory, transposed: lanes 0..7 give the rows of the first, 8..15 of the second.
@@ -100,25 +100,25 @@ __device__ __forceinline__ int64_t cut_at(int64_t off, int size) {
   return to + kRound / 2 >= size ? size : to;
 }
 
-// A sequence's rows and the granules that any of them sees.
+// A sequence's rows and the steps of 32 places that any of them sees.
 struct Sequence {
-  int64_t n0, len;
-  int rows;                  // new rows
+  int64_t n0;
+  int len, rows;             // places; new rows
   int tiles;                 // of R rows (row, query head of the key head)
-  int first, granules;       // of 16 places
+  int first, steps;
   __device__ __forceinline__ void load(const Attn& p, int64_t b, int R) {
     n0 = p.a.q_start ? p.a.q_start[b] : b;
     const int64_t n1 = p.a.q_start ? min(static_cast<int64_t>(p.a.q_start[b + 1]), p.a.N) : b + 1;
     rows = n0 < 0 || n1 <= n0 ? 0 : static_cast<int>(n1 - n0);
     len = max(0, p.a.kv_len[b]);
-    tiles = (static_cast<int64_t>(rows) * p.group + R - 1) / R;
+    tiles = (rows * p.group + R - 1) / R;
     // The first row sees the earliest places, the last row the latest.
-    const int64_t begin = p.a.window > 0 ? max(int64_t(0), len - rows + 1 - p.a.window) : 0;
-    first = static_cast<int>(begin >> 4);
-    granules = len > begin ? static_cast<int>((len + 15) >> 4) - first : 0;
+    const int64_t begin = p.a.window > 0 ? max(int64_t(0), static_cast<int64_t>(len) - rows + 1 - p.a.window) : 0;
+    first = static_cast<int>(begin >> 5);
+    steps = len > begin ? ((len - 1) >> 5) + 1 - first : 0;
   }
   __device__ __forceinline__ int64_t units(int heads) const {
-    return static_cast<int64_t>(heads) * tiles * (kSegmentUnits + granules);
+    return static_cast<int64_t>(heads) * tiles * (kSegmentUnits + steps);
   }
 };
 
@@ -137,70 +137,70 @@ template <typename T, int D, int NT>
 struct Shape {
   static constexpr int R = 8 * NT;
   static constexpr bool kSplit = sizeof(T) == 4;
-  static constexpr int kStages = 4;
-  static constexpr int kCtas = D == 256 || kSplit || NT == 2 ? 1 : 2;
-  static constexpr int kRing = kWarps * kStages * Granule<D>::kBytes;
-  static constexpr int kPitch = D + 4;                                // of the rows of sums that the warps join, in the ring
-  static constexpr int kQuery = NT * (D / 32) * 32 * 16;              // operands of the queries, in one half
-  static constexpr int kSums = NT * ((D + 127) / 128) * 32 * 8;       // their blocks' sums
-  static constexpr size_t kSmem = kRing + kQuery * (kSplit ? 2 : 1) + kSums + (R + 2 * kWarps * R) * sizeof(float);
-  static_assert(kWarps * R * kPitch * 4 <= kRing, "the warps' sums fit the ring");
+  static constexpr int kWarps = D == 256 ? 7 : NT == 2 || kSplit ? 8 : 12;      // of a CTA, one to an SM
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kStep = 2 * Granule<D>::kBytes;
+  static constexpr int kPitch = D + 4;                                // of the rows of a piece's sums
+  static constexpr int kHeld = (R * kPitch * 4 + kStep - 1) / kStep;  // stages that a piece takes
+  static constexpr int kStages = kHeld + (D == 64 ? 3 : 2);
+  static constexpr int kRing = kStages * kStep;
+  static constexpr size_t kSmem = static_cast<size_t>(kWarps) * kRing;
+};
+
+// What a warp leaves for its CTA: the piece of a segment that was begun before its run (it may end there), and of
+// one that its run begins and does not end.
+struct Piece {
+  int b, h, tile, parts;     // sequence (-1: no such piece), key head, tile of rows; parts, where it begins a segment
+  bool begins, ends;
 };
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kernel(const Attn p) {
+__global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(const Attn p) {
   using Gr = Granule<D>;
   using Sh = Shape<T, D, NT>;
-  constexpr int G = Gr::G, R = Sh::R, S = Sh::kStages;
+  constexpr int G = Gr::G, R = Sh::R, S = Sh::kStages, kWarps = Sh::kWarps, kThreads = Sh::kThreads, L = D / 8;
   constexpr bool kSplit = Sh::kSplit;
   constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t scan[kWarps + 4];
-  __shared__ int abort;      // a wait gave up
+  __shared__ int64_t scan[kWarps], cut_b[kWarps + 1], cut_seq[kWarps + 1], cut_u[kWarps + 1];
   __shared__ uint64_t full[kWarps][S];
-  float* joined = reinterpret_cast<float*>(smem);                     // [kWarps][R][kPitch]
-  uint4* q_hi = reinterpret_cast<uint4*>(smem + Sh::kRing);           // [NT][G][32]
-  [[maybe_unused]] uint4* q_lo = q_hi + Sh::kQuery / 16;
-  __half* q_sum = reinterpret_cast<__half*>(smem + Sh::kRing + Sh::kQuery * (kSplit ? 2 : 1));   // [NT][(G + 3) / 4][32][4]
-  float* q_factor = reinterpret_cast<float*>(q_sum) + Sh::kSums / 4;  // [R]
-  float* stat = q_factor + R;                                         // maxima [kWarps][R], totals [kWarps][R]
+  __shared__ Piece piece[kWarps][2];
+  __shared__ float stat[kWarps][2][2][R];                             // maxima and totals of the pieces
+  __shared__ int abort;                                               // a wait gave up
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
-  uint8_t* ring = smem + warp * (S * Gr::kBytes);
+  uint8_t* ring = smem + warp * Sh::kRing;
   if (lane == 0) {
 #pragma unroll
     for (int k = 0; k < S; ++k) mbar_init(&full[warp][k], 1);
     fence_mbar_init();
+    piece[warp][0].b = piece[warp][1].b = -1;
   }
-  __syncwarp();
   if (threadIdx.x == 0) abort = 0;
-  int stage = 0;             // of this warp's next granule, and its phase
-  uint32_t phase = 0;
   pdl_enter();
 
-  // This CTA's run [u, u1) of the line, and the sequence that it begins in. The sum over the sequences comes first; where they
-  // are more than the threads, another pass finds the places.
-  int64_t u, u1, per = 1, seq_at, b;
+  // The CTA's runs: run i begins at the cut cut_u[i] of the line, in the sequence cut_b[i], whose first unit is cut_seq[i]. The
+  // sum over the sequences comes first; where they are more than the threads, another pass finds the cuts.
+  int64_t per = 1, total = 0;
   if (threadIdx.x == 0) p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
   {
     const int64_t n_seqs = p.c.n_seqs;
     const bool once = n_seqs <= kThreads;
-    int64_t before = 0, x = 0, v = 0;
-    int size = 1;
-    int64_t c0 = 0, c1 = 0;
+    int64_t c0 = 0;
 #pragma unroll 1
     for (int pass = once ? 1 : 0; pass < 2; ++pass) {
-      before = 0;
+      int64_t before = 0;
 #pragma unroll 1
       for (int64_t i0 = 0; i0 < n_seqs; i0 += kThreads) {
         const int64_t i = i0 + threadIdx.x;
-        v = 0;
+        int64_t v = 0;
+        int size = 1;
         if (i < n_seqs) {
           Sequence s;
           s.load(p, i, R);
           v = s.units(p.c.heads);
-          size = kSegmentUnits + s.granules;
+          size = kSegmentUnits + s.steps;
         }
-        x = v;
+        int64_t x = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
@@ -216,52 +216,57 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
           before += scan[w];
         }
         if (once || (pass == 0 && i0 + kThreads >= n_seqs)) {
-          per = max(static_cast<int64_t>(kRound), quotient(before + gridDim.x - 1, gridDim.x));
-          c0 = blockIdx.x * per;
-          if (c0 >= before) return;
-          c1 = c0 + per;
+          total = before;
+          const int64_t runs = static_cast<int64_t>(gridDim.x) * kWarps;
+          per = max(static_cast<int64_t>(kSegmentUnits + kRound), quotient(total + runs - 1, runs));
+          c0 = static_cast<int64_t>(blockIdx.x) * kWarps * per;
+          if (c0 >= total) return;
         }
-        if (pass == 1) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int64_t cut = k ? c1 : c0;
+        if (pass == 1 && x < c0 + (kWarps + 1) * per && c0 < x + v) {
+#pragma unroll 1
+          for (int k = 0; k <= kWarps; ++k) {
+            const int64_t cut = c0 + k * per;
             if (x <= cut && cut < x + v) {
               const int64_t seg = x + quotient(cut - x, size) * size;
-              if (k == 0) scan[kWarps] = i, scan[kWarps + 1] = x;
-              scan[kWarps + 2 + k] = seg + cut_at(cut - seg, size);
+              cut_b[k] = i;
+              cut_seq[k] = x;
+              cut_u[k] = seg + cut_at(cut - seg, size);
             }
           }
         }
       }
     }
     __syncthreads();
-    b = scan[kWarps];
-    seq_at = scan[kWarps + 1];
-    u = scan[kWarps + 2];
-    u1 = c1 < before ? scan[kWarps + 3] : before;
-  }
-  if (u >= u1) return;
-  Sequence q;
-  q.load(p, b, R);
-  {                        // a run that begins where the sequence ends
-    int64_t n = q.units(p.c.heads);
-    while (u >= seq_at + n) {
-      seq_at += n;
-      q.load(p, ++b, R);
-      n = q.units(p.c.heads);
-    }
+    if (threadIdx.x <= kWarps && c0 + threadIdx.x * per >= total) cut_u[threadIdx.x] = total;
+    __syncthreads();
   }
 
+  int64_t u = cut_u[warp], b = cut_b[warp], seq_at = cut_seq[warp];
+  const int64_t u1 = cut_u[warp + 1];
+  uint32_t phases = 0;       // of each stage's next copy
+  int stages = S;            // that copies go to; a held piece takes the last kHeld
+  Sequence q;
+  if (u < u1) q.load(p, b, R);
+
   while (u < u1) {
+    {                        // a run may begin where a sequence ends, and goes on through others
+      int64_t n = q.units(p.c.heads);
+      while (u >= seq_at + n) {
+        seq_at += n;
+        q.load(p, ++b, R);
+        n = q.units(p.c.heads);
+      }
+    }
     // The segment that u lies in: [at, end) of the line.
-    const int size = kSegmentUnits + q.granules;
+    const int size = kSegmentUnits + q.steps;
     const int seg = static_cast<int>(quotient(u - seq_at, size));
     const int64_t at = seq_at + static_cast<int64_t>(seg) * size, end = at + size;
     const int h = seg / q.tiles, tile = seg - h * q.tiles;
     const bool begins = u == at, ends = end <= u1;
-    int g0 = max(0, static_cast<int>(u - at) - kSegmentUnits), g1 = max(0, static_cast<int>(min(end, u1) - at) - kSegmentUnits);
+    int t0 = q.first + max(0, static_cast<int>(u - at) - kSegmentUnits);
+    int t1 = q.first + max(0, static_cast<int>(min(end, u1) - at) - kSegmentUnits);
 
-    // Row r of the tile: new row i = r' / group, head r' % group, r' = tile * R + r. See [low, seen).
+    // Row r of the tile: new row i = r' / group, head r' % group, r' = tile * R + r. It sees [low, seen).
     const int rows = q.rows * p.group;
     auto row_of = [&](int r, int& i, int& hq) {
       const int rr = tile * R + r;
@@ -269,119 +274,121 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
       hq = h * p.group + rr - i * p.group;
       return rr < rows;
     };
-    auto seen_of = [&](int i) { return static_cast<int>(q.len) - q.rows + 1 + i; };
+    auto seen_of = [&](int i) { return q.len - q.rows + 1 + i; };
     auto low_of = [&](int seen) { return p.a.window > 0 ? static_cast<int>(max(int64_t(0), seen - p.a.window)) : 0; };
-    const int i_first = tile * R / p.group, i_last = min(tile * R + R, rows) - 1 < 0 ? 0 : (min(tile * R + R, rows) - 1) / p.group;
-    const int seen_most = seen_of(i_last), seen_least = seen_of(i_first);
+    const int seen_least = seen_of(tile * R / p.group), seen_most = seen_of((min(tile * R + R, rows) - 1) / p.group);
     const int low_least = low_of(seen_least), low_most = low_of(seen_most);
-    // Granules that a row of this tile sees, of those of the run.
-    g0 = max(g0 + q.first, low_least >> 4);
-    g1 = min(g1 + q.first, (seen_most + 15) >> 4);
-    const int mine = g1 > g0 + warp ? (g1 - g0 - warp + kWarps - 1) / kWarps : 0;
-    // Granules that all of them see whole.
-    const int whole0 = (low_most + 15) >> 4, wholes = max(0, (seen_least >> 4) - whole0);
+    // Steps of the run that a row of this tile sees, and those of them that all of its rows see whole.
+    t0 = max(t0, low_least >> 5);
+    t1 = min(t1, (seen_most + 31) >> 5);
+    const int mine = max(0, t1 - t0);
+    const int whole0 = (low_most + 31) >> 5, wholes = max(0, (seen_least >> 5) - whole0);
 
-    // A thread's eight elements of the queries, on their way while the pages are looked up.
-    constexpr int L = D / 8;                                          // lanes of a row
-    static_assert(R * L <= kThreads, "a pass takes all rows");
-    const int qr = threadIdx.x / L, l8 = threadIdx.x % L;
-    float qv[8];
-    {
-      int i, hq;
-      if (qr < R && row_of(qr, i, hq)) {
-        const T* src = static_cast<const T*>(p.a.Q) + (q.n0 + i) * p.a.ldq + static_cast<int64_t>(hq) * D + 8 * l8;
-        if (p.vec) load8<T, true>(src, qv);
-        else load8<T, false>(src, qv);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) qv[j] = 0.f;
-      }
-    }
-
-    // Copies of this warp's granules g0 + warp + k * kWarps, S - 1 ahead. Lane k % 32 makes granule k's, and has looked its
-    // page up with those of the 31 beside it. A granule whose page is out of range is passed over.
+    // Granules of this warp's steps: lane k % 32 has the two of step t0 + k (-1: none, or its page is out of range), and makes
+    // their copies, as one where they lie side by side.
     const int per_page = p.c.page_shift - 4;
     const int32_t* table = p.c.table + b * p.c.ldt;
-    auto source = [&](int k) -> const uint8_t* {
-      const int g = g0 + warp + k * kWarps;
+    const int last_granule = (seen_most - 1) >> 4;
+    auto granule_at = [&](int g) -> int {
       const int64_t i = static_cast<int64_t>(g) >> per_page;
-      if (k >= mine || i >= p.c.ldt) return nullptr;
-      const int page = table[i];
-      if (page < 0 || page >= p.c.n_pages) return nullptr;
-      return p.c.data + ((((static_cast<int64_t>(page) * p.c.heads) + h) << per_page) + (g & ((1 << per_page) - 1))) * Gr::kBytes;
+      const int page = g <= last_granule && i < p.c.ldt ? table[i] : -1;
+      if (page < 0 || page >= p.c.n_pages) return -1;
+      return static_cast<int>(((static_cast<int64_t>(page) * p.c.heads + h) << per_page) + (g & ((1 << per_page) - 1)));
     };
-    const uint8_t* src = source(lane);
-    const uint8_t* src_next = mine > 32 ? source(32 + lane) : nullptr;
-    auto issue = [&](int to) {
-      uint64_t* bar = &full[warp][to];
-      if (src) {
-        mbar_expect_tx(bar, Gr::kBytes);
-        bulk_g2s(ring + to * Gr::kBytes, src, Gr::kBytes, bar);
-      } else {
-        report_error(p.err, ERR_PAGE);
-        mbar_arrive(bar);
+    int ga = -1, gb = -1;
+    auto look_up = [&](int k) {          // of the steps k + lane
+      ga = gb = -1;
+      if (k + lane < mine) {
+        const int g = 2 * (t0 + k + lane);
+        ga = granule_at(g);
+        gb = per_page > 0 && g < last_granule && ga >= 0 ? ga + 1 : granule_at(g + 1);
+        if (ga < 0 || (gb < 0 && g < last_granule)) report_error(p.err, ERR_PAGE);
       }
     };
-    if (lane < min(S - 1, mine)) issue((stage + lane) % S);
-    // Bit k % 32: granule k of these 32, of the next 32, has no page.
-    uint32_t gone = __ballot_sync(0xffffffffu, src == nullptr && lane < mine), gone_next = 0;
-    int turn = S - 1;                                                 // the lane whose copy is next
+    auto issue = [&](int to) {
+      uint64_t* bar = &full[warp][to];
+      uint8_t* dst = ring + to * Sh::kStep;
+      const uint8_t* a = p.c.data + static_cast<int64_t>(ga) * Gr::kBytes;
+      if (gb == ga + 1 && ga >= 0) {
+        mbar_expect_tx(bar, Sh::kStep);
+        bulk_g2s(dst, a, Sh::kStep, bar);
+      } else {
+        mbar_expect_tx(bar, (ga >= 0 ? Gr::kBytes : 0) + (gb >= 0 ? Gr::kBytes : 0));
+        if (ga >= 0) bulk_g2s(dst, a, Gr::kBytes, bar);
+        if (gb >= 0) bulk_g2s(dst + Gr::kBytes, p.c.data + static_cast<int64_t>(gb) * Gr::kBytes, Gr::kBytes, bar);
+      }
+    };
+    look_up(0);
 
     // Queries as operands: lane (gid, tig) has of row gid the elements 32 g + 8 tig + 0..7, times 2^a with the
     // row's largest between 2^14 and 2^15 (so that fp16 and bf16 queries are exact), the odd ones
     // also times 2^-4 for the codes that are four bits higher.
-    {
-      const int g = l8 >> 2, t = l8 & 3;
-      float most = 0.f, sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(qv[j]));
-#pragma unroll
-      for (int o = 1; o < L; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-      // 2^e <= most < 2^(e + 1); rows below 2^-86 have scores of nothing, and those beyond 2^118 are NaN all over.
-      const int e = max(-86, min(127, static_cast<int>(__float_as_uint(most) >> 23) - 127));
-      const float up1 = pow2((14 - e) >> 1), up2 = pow2(14 - e - ((14 - e) >> 1));
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        qv[j] = qv[j] * up1 * up2;
-        sum += qv[j];
-        if (j & 1) qv[j] *= 0.0625f;
-      }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      if (qr < R) {
-        const int nt = qr >> 3, at = 4 * (qr & 7) + t;
-        q_hi[(nt * G + g) * 32 + at] =
-            make_uint4(pack_half2(qv[0], qv[4]), pack_half2(qv[1], qv[5]), pack_half2(qv[2], qv[6]), pack_half2(qv[3], qv[7]));
-        if constexpr (kSplit) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) qv[j] = low_part(qv[j]);
-          q_lo[(nt * G + g) * 32 + at] =
-              make_uint4(pack_half2(qv[0], qv[4]), pack_half2(qv[1], qv[5]), pack_half2(qv[2], qv[6]), pack_half2(qv[3], qv[7]));
-        }
-        // The block's sum in three parts of fp16, one for each of the lanes t = 0, 1, 2.
-        sum *= 0x1p-6f;
-        if (t > 0) sum = low_part(sum);
-        if (t > 1) sum = low_part(sum);
-        q_sum[((nt * ((G + 3) / 4) + (g >> 2)) * 32 + at) * 4 + (g & 3)] = __float2half_rn(t > 2 ? 0.f : sum);
-        if (l8 == 0) q_factor[qr] = most < 0x1p118f ? p.a.scale * 1.44269504f * pow2(10 + min(e, 117)) : NAN;
-      }
-    }
-    __syncthreads();
     uint32_t qb[NT][G][2][2], qs[NT][(G + 3) / 4][2];
     [[maybe_unused]] uint32_t ql[kSplit ? NT : 1][kSplit ? G : 1][2][2];
     float factor[NT][2];                                              // of the scores of columns 2 tig, 2 tig + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      int i, hq;
+      const bool here = row_of(8 * nt + gid, i, hq);
+      const T* src = static_cast<const T*>(p.a.Q) + (q.n0 + i) * p.a.ldq + static_cast<int64_t>(hq) * D + 8 * tig;
+      Raw8<T> raw[G];
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        *reinterpret_cast<uint4*>(qb[nt][g]) = q_hi[(nt * G + g) * 32 + lane];
-        if constexpr (kSplit) *reinterpret_cast<uint4*>(ql[nt][g]) = q_lo[(nt * G + g) * 32 + lane];
+        if (here) {
+          if (p.vec) raw[g].template load<true>(src + 32 * g);
+          else raw[g].template load<false>(src + 32 * g);
+        }
+      }
+      if (nt == 0) {         // the copies begin while the queries are on their way
+        const int now = min(stages - 1, mine);
+        if (lane < now) issue(lane);
+      }
+      float most = 0.f, sums[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) most = fmaxf(most, here ? fabsf(raw[g][j]) : 0.f);
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      // 2^e <= most < 2^(e + 1); rows below 2^-86 have scores of nothing, and those beyond 2^118 are NaN all over.
+      const int e = max(-86, min(127, static_cast<int>(__float_as_uint(most) >> 23) - 127));
+      const float up1 = pow2((14 - e) >> 1), up2 = pow2(14 - e - ((14 - e) >> 1));
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        float v[8];
+        sums[g] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[j] = here ? raw[g][j] * up1 * up2 : 0.f;
+          sums[g] += v[j];
+          if (j & 1) v[j] *= 0.0625f;
+        }
+        sums[g] += __shfl_xor_sync(0xffffffffu, sums[g], 1);
+        sums[g] += __shfl_xor_sync(0xffffffffu, sums[g], 2);
+        sums[g] *= 0x1p-6f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          qb[nt][g][k][0] = pack_half2(v[2 * k], v[2 * k + 4]);
+          qb[nt][g][k][1] = pack_half2(v[2 * k + 1], v[2 * k + 5]);
+          if constexpr (kSplit) {
+            ql[nt][g][k][0] = pack_half2(low_part(v[2 * k]), low_part(v[2 * k + 4]));
+            ql[nt][g][k][1] = pack_half2(low_part(v[2 * k + 1]), low_part(v[2 * k + 5]));
+          }
+        }
+        // The blocks' sums in three parts of fp16, one for each of the lanes tig = 0, 1, 2.
+        float part = sums[g];
+        if (tig > 0) part = low_part(part);
+        if (tig > 1) part = low_part(part);
+        sums[g] = tig > 2 ? 0.f : part;
       }
 #pragma unroll
-      for (int k = 0; k < (G + 3) / 4; ++k)
-        *reinterpret_cast<uint2*>(qs[nt][k]) = *reinterpret_cast<const uint2*>(q_sum + ((nt * ((G + 3) / 4) + k) * 32 + lane) * 4);
+      for (int k = 0; k < (G + 3) / 4; ++k) {
+        qs[nt][k][0] = pack_half2(sums[4 * k], sums[4 * k + 1]);
+        qs[nt][k][1] = G > 2 ? pack_half2(sums[(4 * k + 2) % G], sums[(4 * k + 3) % G]) : 0u;
+      }
+      const float f = most < 0x1p118f ? p.a.scale * 1.44269504f * pow2(10 + min(e, 117)) : NAN;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) factor[nt][c] = q_factor[8 * nt + 2 * tig + c];
+      for (int c = 0; c < 2; ++c) factor[nt][c] = __shfl_sync(0xffffffffu, f, 4 * (2 * tig + c));
     }
 
     float o[NT][G][2][4], om[NT][4], top[NT][2];
@@ -397,17 +404,18 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
       }
     }
 
-    // Rows 0..15 of the operands are places in this order, so that the value codes of lanes side by side lie in
-    // different banks: row r is place r / 2 + 4 (r % 2), of the lower or upper eight.
+    // A step of 32 places, two granules. Rows 0..15 of the operands are a granule's places in this order, so that the value codes of
+    // lanes side by side lie in different banks: row r is place r / 2 + 4 (r % 2), of the lower or upper eight.
     const int ta = (gid >> 1) + 4 * (gid & 1);
-    auto granule = [&](auto edge_tag, const uint8_t* gr, int place0) {
+    const int k_at = ta * (D / 2) + tig * (4 * G), p_at = Gr::kCodes + ta * (4 * G);
+    const int v_at = Gr::kValues + tig * (D / 2) + gid * (2 * G);
+    const int m_at = Gr::kValues + Gr::kCodes + (D >= 128 ? ((lane & 8) + ((lane >> 1) & 3) + 4 * (lane & 1)) * (4 * G) : tig * (4 * G));
+    auto step = [&](auto edge_tag, const uint8_t* st, int place0, int hide) {
       constexpr bool kEdge = decltype(edge_tag)::value;               // some row does not see all of its places
-      float s[NT][4];
+      float s[2][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[nt][j] = 0.f;
-      {
+      for (int w = 0; w < 2; ++w) {
+        const uint8_t* gr = st + w * Gr::kBytes;
         uint32_t ka[G], kb[G], pa[G], pb[G];                          // pa, pb: G / 2 words of s, then G / 2 of m
         auto words = [](uint32_t (&w)[G], const uint8_t* src) {
           if constexpr (G == 2) {
@@ -417,10 +425,10 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
             for (int i = 0; i < G / 4; ++i) *reinterpret_cast<uint4*>(w + 4 * i) = reinterpret_cast<const uint4*>(src)[i];
           }
         };
-        words(ka, gr + ta * (D / 2) + tig * (4 * G));
-        words(kb, gr + (ta + 8) * (D / 2) + tig * (4 * G));
-        words(pa, gr + Gr::kCodes + ta * (4 * G));
-        words(pb, gr + Gr::kCodes + (ta + 8) * (4 * G));
+        words(ka, gr + k_at);
+        words(kb, gr + k_at + 8 * (D / 2));
+        words(pa, gr + p_at);
+        words(pb, gr + p_at + 8 * (4 * G));
         float sm[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -430,6 +438,8 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
             mma_f16_zero(sm[nt], pa[G / 2], pb[G / 2], pa[G / 2 + 1], pb[G / 2 + 1], qs[nt][0][0], qs[nt][0][1]);
             if constexpr (G == 8) mma_f16(sm[nt], pa[6], pb[6], pa[7], pb[7], qs[nt][1][0], qs[nt][1][1]);
           }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[w][nt][j] = sm[nt][j] * 0x1p-18f;
         }
 #pragma unroll
         for (int g = 0; g < G; ++g) {
@@ -446,113 +456,124 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
               mma_f16(acc, a0, a1, a2, a3, ql[nt][g][0][0], ql[nt][g][0][1]);
               mma_f16(acc, c0, c1, c2, c3, ql[nt][g][1][0], ql[nt][g][1][1]);
             }
-            s[nt][0] = fmaf(sa, acc[0], s[nt][0]);
-            s[nt][1] = fmaf(sa, acc[1], s[nt][1]);
-            s[nt][2] = fmaf(sb, acc[2], s[nt][2]);
-            s[nt][3] = fmaf(sb, acc[3], s[nt][3]);
+            s[w][nt][0] = fmaf(sa, acc[0], s[w][nt][0]);
+            s[w][nt][1] = fmaf(sa, acc[1], s[w][nt][1]);
+            s[w][nt][2] = fmaf(sb, acc[2], s[w][nt][2]);
+            s[w][nt][3] = fmaf(sb, acc[3], s[w][nt][3]);
           }
         }
         // Sum s acc is of 2^(a - 24) q . (k - m), sm of 2^(a - 6) q . m.
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[nt][j] = fmaf(sm[nt][j], 0x1p-18f, s[nt][j]) * factor[nt][j & 1];
-      }
-      if constexpr (kEdge) {
+          for (int j = 0; j < 4; ++j) s[w][nt][j] *= factor[nt][j & 1];
+        if constexpr (kEdge) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            int i, hq;
-            row_of(8 * nt + 2 * tig + (j & 1), i, hq);
-            const int seen = seen_of(i), place = place0 + ta + (j < 2 ? 0 : 8);
-            if (place >= seen || place < low_of(seen)) s[nt][j] = -INFINITY;
-          }
+            for (int j = 0; j < 4; ++j) {
+              int i, hq;
+              row_of(8 * nt + 2 * tig + (j & 1), i, hq);
+              const int seen = seen_of(i), place = place0 + 16 * w + ta + (j < 2 ? 0 : 8);
+              if (place >= seen || place < low_of(seen) || (hide >> w & 1)) s[w][nt][j] = -INFINITY;
+            }
+        }
       }
 
       // The values' parameters, two places a word, in the order of the operand's rows 2 tig, 2 tig + 1: m0 (lower eight places)
       // and m1 (upper eight) as an operand whose rows g (4 + g for 128 elements) are the blocks' m; for rows of 16 bits also va and
       // vb, their s. fp32 rows: s of two blocks a word, of places ta and ta + 8. Places that no row of the tile sees: 0.
-      const uint8_t* vp = gr + Gr::kValues + Gr::kCodes;
-      const auto unseen = [&](int place) { return kEdge && (place0 + place < low_least || place0 + place >= seen_most); };
-      uint32_t m0 = 0, m1 = 0, sizes = 0;
-      uint32_t va[kSplit ? G / 2 : G], vb[kSplit ? G / 2 : G];
-      uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-      if constexpr (kEdge) {
-        keep0 = (unseen(tig) ? 0u : 0xffffu) | (unseen(tig + 4) ? 0u : 0xffff0000u);
-        keep1 = (unseen(tig + 8) ? 0u : 0xffffu) | (unseen(tig + 12) ? 0u : 0xffff0000u);
-      }
-      if constexpr (D >= 128) {
-        const uint8_t* row = vp + ((lane & 8) + ((lane >> 1) & 3) + 4 * (lane & 1)) * (4 * G);
-        load_transposed(m0, m1, row + (D == 256 ? 2 * G : 0));
-        m0 &= keep0, m1 &= keep1;
-        if constexpr (!kSplit) {
-          uint32_t s0 = m0, s1 = m1;                                  // of 128 elements: rows 0..3 of the same matrices
-          if constexpr (D == 256) {
-            load_transposed(s0, s1, row);
-            s0 &= keep0, s1 &= keep1;
-          }
-          sizes = gid < G ? s0 | s1 : 0;
+      uint32_t m0[2], m1[2], sizes = 0;
+      uint32_t va[2][kSplit ? G / 2 : G], vb[2][kSplit ? G / 2 : G];
 #pragma unroll
-          for (int g = 0; g < G; ++g) {
-            va[g] = __shfl_sync(0xffffffffu, s0, 4 * g + tig);
-            vb[g] = __shfl_sync(0xffffffffu, s1, 4 * g + tig);
+      for (int w = 0; w < 2; ++w) {
+        const uint8_t* row = st + w * Gr::kBytes + m_at;
+        const auto unseen = [&](int place) {
+          return kEdge && (place0 + 16 * w + place < low_least || place0 + 16 * w + place >= seen_most || (hide >> w & 1));
+        };
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        if constexpr (kEdge) {
+          keep0 = (unseen(tig) ? 0u : 0xffffu) | (unseen(tig + 4) ? 0u : 0xffff0000u);
+          keep1 = (unseen(tig + 8) ? 0u : 0xffffu) | (unseen(tig + 12) ? 0u : 0xffff0000u);
+        }
+        if constexpr (D >= 128) {
+          load_transposed(m0[w], m1[w], row + (D == 256 ? 2 * G : 0));
+          m0[w] &= keep0, m1[w] &= keep1;
+          if constexpr (!kSplit) {
+            uint32_t s0 = m0[w], s1 = m1[w];                          // of 128 elements: rows 0..3 of the same matrices
+            if constexpr (D == 256) {
+              load_transposed(s0, s1, row);
+              s0 &= keep0, s1 &= keep1;
+            }
+            sizes |= s0 | s1;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              va[w][g] = __shfl_sync(0xffffffffu, s0, 4 * g + tig);
+              vb[w][g] = __shfl_sync(0xffffffffu, s1, 4 * g + tig);
+            }
+          }
+        } else {
+          const auto words = [&](int place) { return *reinterpret_cast<const uint2*>(row + place * 8); };
+          const uint2 x = words(0), y = words(4), z = words(8), t = words(12);
+          if constexpr (!kSplit) {
+            va[w][0] = __byte_perm(x.x, y.x, 0x5410) & keep0, va[w][1] = __byte_perm(x.x, y.x, 0x7632) & keep0;
+            vb[w][0] = __byte_perm(z.x, t.x, 0x5410) & keep1, vb[w][1] = __byte_perm(z.x, t.x, 0x7632) & keep1;
+            sizes |= va[w][0] | va[w][1] | vb[w][0] | vb[w][1];
+          }
+          const uint32_t pick = gid == 0 ? 0x5410u : 0x7632u;
+          m0[w] = gid < G ? __byte_perm(x.y, y.y, pick) & keep0 : 0u;
+          m1[w] = gid < G ? __byte_perm(z.y, t.y, pick) & keep1 : 0u;
+        }
+        if constexpr (kSplit) {
+          const uint8_t* vp = st + w * Gr::kBytes + Gr::kValues + p_at;
+#pragma unroll
+          for (int i = 0; i < G / 2; ++i) {
+            va[w][i] = unseen(ta) ? 0u : reinterpret_cast<const uint32_t*>(vp)[i];
+            vb[w][i] = unseen(ta + 8) ? 0u : reinterpret_cast<const uint32_t*>(vp + 8 * (4 * G))[i];
           }
         }
-      } else {
-        const auto words = [&](int place) { return *reinterpret_cast<const uint2*>(vp + place * 8); };
-        const uint2 x = words(tig), y = words(tig + 4), z = words(tig + 8), w = words(tig + 12);
-        if constexpr (!kSplit) {
-          va[0] = __byte_perm(x.x, y.x, 0x5410) & keep0, va[1] = __byte_perm(x.x, y.x, 0x7632) & keep0;
-          vb[0] = __byte_perm(z.x, w.x, 0x5410) & keep1, vb[1] = __byte_perm(z.x, w.x, 0x7632) & keep1;
-          sizes = va[0] | va[1] | vb[0] | vb[1];
-        }
-        const uint32_t pick = gid == 0 ? 0x5410u : 0x7632u;
-        m0 = gid < G ? __byte_perm(x.y, y.y, pick) & keep0 : 0u;
-        m1 = gid < G ? __byte_perm(z.y, w.y, pick) & keep1 : 0u;
       }
-      if constexpr (kSplit) {
-#pragma unroll
-        for (int i = 0; i < G / 2; ++i) {
-          va[i] = unseen(ta) ? 0u : reinterpret_cast<const uint32_t*>(vp + ta * (4 * G))[i];
-          vb[i] = unseen(ta + 8) ? 0u : reinterpret_cast<const uint32_t*>(vp + (ta + 8) * (4 * G))[i];
-        }
-      }
+      if constexpr (!kSplit && D >= 128) sizes = gid < G ? sizes : 0;
 
       // Scores less their columns' offset; the maximum is moved where one passes it by kAhead, sigma where an s passes 2^sigma.
       // Rows of 16 bits have sigma 0 until an s is 2 or more (its exponent's highest bit is set).
-      float x[NT][4], off[NT][2];
+      float x[2][NT][4];
       const auto shift = [&] {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+          const float off[2] = {top[nt][0] + (static_cast<float>(sigma) - kTop), top[nt][1] + (static_cast<float>(sigma) - kTop)};
 #pragma unroll
-          for (int c = 0; c < 2; ++c) off[nt][c] = top[nt][c] + (static_cast<float>(sigma) - kTop);
+          for (int w = 0; w < 2; ++w)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[nt][j] = s[nt][j] - off[nt][j & 1];
+            for (int j = 0; j < 4; ++j) x[w][nt][j] = s[w][nt][j] - off[j & 1];
         }
       };
       shift();
-      float ahead = x[0][0];
+      float ahead = x[0][0][0];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int w = 0; w < 2; ++w)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) ahead = fmaxf(ahead, x[nt][j]);
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) ahead = fmaxf(ahead, x[w][nt][j]);
       float largest = 0.f;
-      if constexpr (kSplit) {
-        __half2 big = __habs2(bits_half2(va[0]));
+      const auto find_largest = [&] {                                 // a NaN counts for nothing
+        __half2 big = __habs2(bits_half2(va[0][0]));
 #pragma unroll
-        for (int i = 0; i < G / 2; ++i) big = __hmax2(big, __hmax2(__habs2(bits_half2(va[i])), __habs2(bits_half2(vb[i]))));
-        largest = fminf(fmaxf(__low2float(big), __high2float(big)), 65504.f);   // a NaN counts for nothing
-      }
-      if (__any_sync(0xffffffffu, ahead > kTop + kAhead - static_cast<float>(sigma) || (kSplit ? largest > pow2(sigma) : (sizes & 0x40004000u) != 0))) {
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+          for (int i = 0; i < (kSplit ? G / 2 : G); ++i)
+            big = __hmax2(big, __hmax2(__habs2(bits_half2(va[w][i])), __habs2(bits_half2(vb[w][i]))));
+        largest = fminf(fmaxf(fmaxf(__low2float(big), __high2float(big)), 0.f), 65504.f);
+      };
+      if constexpr (kSplit) find_largest();
+      if (__any_sync(0xffffffffu, ahead > kTop + kAhead - static_cast<float>(sigma) ||
+                                      (kSplit ? largest > pow2(sigma) : (sizes & 0x40004000u) != 0))) {
         if constexpr (!kSplit) {
-          __half2 big = __habs2(bits_half2(va[0]));
-#pragma unroll
-          for (int i = 0; i < G; ++i) big = __hmax2(big, __hmax2(__habs2(bits_half2(va[i])), __habs2(bits_half2(vb[i]))));
-          largest = fminf(fmaxf(__low2float(big), __high2float(big)), 65504.f);
+          find_largest();
           if (largest < 2.f) largest = 0.f;
         }
-        const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(largest > 0.f ? largest : 0.f));
+        const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(largest));
         const int want = max(sigma, static_cast<int>((bits + 0x007fffffu) >> 23) - 127);   // the power of two not below it
         const float by = pow2(max(-126, sigma - want));
         sigma = want;
@@ -560,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float m = fmaxf(s[nt][c], s[nt][c + 2]);
+            float m = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -580,68 +601,64 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
         shift();
       }
 
-      // Weights, transposed as operands. Rows of 16 bits: the weights times 2^(kTop - sigma) rounded to fp16, and for each
-      // block's codes their products with s (at most 2^15: s is below 2 with sigma 0, else s / 2^sigma at most 1). fp32
-      // rows: these products taken in fp32, and the weights times 2^kTop, all in two halves.
-      uint32_t pw[NT][2];
-      [[maybe_unused]] uint32_t pl[kSplit ? NT : 1][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int w = 0; w < 2; ++w) {
+        // Weights, transposed as operands. Rows of 16 bits: the weights times 2^(kTop - sigma) rounded to fp16, and for each
+        // block's codes their products with s (at most 2^15: s is below 2 with sigma 0, else s / 2^sigma at most 1). fp32
+        // rows: these products taken in fp32, and the weights times 2^kTop, all in two halves.
+        uint32_t pw[NT][2];
+        [[maybe_unused]] uint32_t pl[kSplit ? NT : 1][2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[nt][j] = exp2_fast(x[nt][j]);
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          if constexpr (kSplit) {
-            const float up = pow2(sigma), y = s[nt][2 * k] * up, z = s[nt][2 * k + 1] * up;
-            pw[nt][k] = transpose8(pack_half2(y, z));
-            pl[nt][k] = transpose8(pack_half2(low_part(y), low_part(z)));
-          } else {
-            pw[nt][k] = transpose8(pack_half2(s[nt][2 * k], s[nt][2 * k + 1]));
+          for (int j = 0; j < 4; ++j) x[w][nt][j] = exp2_fast(x[w][nt][j]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            if constexpr (kSplit) {
+              const float up = pow2(sigma), y = x[w][nt][2 * k] * up, z = x[w][nt][2 * k + 1] * up;
+              pw[nt][k] = transpose8(pack_half2(y, z));
+              pl[nt][k] = transpose8(pack_half2(low_part(y), low_part(z)));
+            } else {
+              pw[nt][k] = transpose8(pack_half2(x[w][nt][2 * k], x[w][nt][2 * k + 1]));
+            }
           }
         }
-      }
-
-      // The m, and a row of ones (row 8).
-      {
+        // The m, and a row of ones (row 8).
         const uint32_t one = gid == 0 ? 0x3c003c00u : 0u;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_f16(om[nt], m0, one, m1, one, pw[nt][0], pw[nt][1]);
-          if constexpr (kSplit) mma_f16(om[nt], m0, one, m1, one, pl[nt][0], pl[nt][1]);
+          mma_f16(om[nt], m0[w], one, m1[w], one, pw[nt][0], pw[nt][1]);
+          if constexpr (kSplit) mma_f16(om[nt], m0[w], one, m1[w], one, pl[nt][0], pl[nt][1]);
         }
-      }
-
-      // The values' codes: of places tig, tig + 4, tig + 8, tig + 12 four elements of each block (row gid of the operand
-      // the first of them, row gid + 8 the second, and so on).
-      const uint8_t* vc = gr + Gr::kValues + gid * (2 * G);
-      uint32_t w[4][G / 2];
+        // The values' codes: of places tig, tig + 4, tig + 8, tig + 12 four elements of each block (row gid of the operand
+        // the first of them, row gid + 8 the second, and so on). A NaN of a place that a row does not see is left out.
+        const uint8_t* vc = st + w * Gr::kBytes + v_at;
+        uint32_t cw[4][G / 2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint8_t* src = vc + (tig + 4 * k) * (D / 2);
-        if constexpr (G == 2) {
-          w[k][0] = *reinterpret_cast<const uint32_t*>(src);
-        } else {
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (G == 2) {
+            cw[k][0] = *reinterpret_cast<const uint32_t*>(vc + 4 * k * (D / 2));
+          } else {
 #pragma unroll
-          for (int i = 0; i < G / 4; ++i) *reinterpret_cast<uint2*>(&w[k][2 * i]) = reinterpret_cast<const uint2*>(src)[i];
+            for (int i = 0; i < G / 4; ++i)
+              *reinterpret_cast<uint2*>(&cw[k][2 * i]) = reinterpret_cast<const uint2*>(vc + 4 * k * (D / 2))[i];
+          }
         }
-      }
-      // (A NaN of a place that a row does not see is left out.)
-      {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           const uint32_t pick = g & 1 ? 0x7632u : 0x5410u;
-          const uint32_t x = __byte_perm(w[0][g / 2], w[1][g / 2], pick), y = __byte_perm(w[2][g / 2], w[3][g / 2], pick);
-          const uint32_t a0 = x & M0, a1 = x & M1, a2 = y & M0, a3 = y & M1;
-          const uint32_t c0 = (x >> 8) & M0, c1 = (x >> 8) & M1, c2 = (y >> 8) & M0, c3 = (y >> 8) & M1;
+          const uint32_t y = __byte_perm(cw[0][g / 2], cw[1][g / 2], pick), z = __byte_perm(cw[2][g / 2], cw[3][g / 2], pick);
+          const uint32_t a0 = y & M0, a1 = y & M1, a2 = z & M0, a3 = z & M1;
+          const uint32_t c0 = (y >> 8) & M0, c1 = (y >> 8) & M1, c2 = (z >> 8) & M0, c3 = (z >> 8) & M1;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             if constexpr (kSplit) {
-              const float2 sa2 = __half22float2(bits_half2(va[g / 2])), sb2 = __half22float2(bits_half2(vb[g / 2]));
+              const float2 sa2 = __half22float2(bits_half2(va[w][g / 2])), sb2 = __half22float2(bits_half2(vb[w][g / 2]));
               const float sa = g & 1 ? sa2.y : sa2.x, sb = g & 1 ? sb2.y : sb2.x;
-              float t[4] = {s[nt][0] * sa, s[nt][1] * sa, s[nt][2] * sb, s[nt][3] * sb};
+              float t[4] = {x[w][nt][0] * sa, x[w][nt][1] * sa, x[w][nt][2] * sb, x[w][nt][3] * sb};
               if constexpr (kEdge) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) t[j] = s[nt][j] == 0.f ? 0.f : t[j];
+                for (int j = 0; j < 4; ++j) t[j] = x[w][nt][j] == 0.f ? 0.f : t[j];
               }
               const uint32_t b0 = transpose8(pack_half2(t[0], t[1])), b1 = transpose8(pack_half2(t[2], t[3]));
               const uint32_t l0 = transpose8(pack_half2(low_part(t[0]), low_part(t[1])));
@@ -651,8 +668,8 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
               mma_f16(o[nt][g][0], a0, a1, a2, a3, l0, l1);
               mma_f16(o[nt][g][1], c0, c1, c2, c3, l0, l1);
             } else {
-              uint32_t b0 = half2_bits(__hmul2(bits_half2(pw[nt][0]), bits_half2(va[g])));
-              uint32_t b1 = half2_bits(__hmul2(bits_half2(pw[nt][1]), bits_half2(vb[g])));
+              uint32_t b0 = half2_bits(__hmul2(bits_half2(pw[nt][0]), bits_half2(va[w][g])));
+              uint32_t b1 = half2_bits(__hmul2(bits_half2(pw[nt][1]), bits_half2(vb[w][g])));
               if constexpr (kEdge) {
                 b0 &= __hne2_mask(bits_half2(pw[nt][0]), __half2half2(__ushort_as_half(0)));
                 b1 &= __hne2_mask(bits_half2(pw[nt][1]), __half2half2(__ushort_as_half(0)));
@@ -665,92 +682,122 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
       }
     };
 
-    if (mine > 32) gone_next = __ballot_sync(0xffffffffu, src_next == nullptr && 32 + lane < mine);
+    // Bit k % 32 of a, b: the first, the second granule of step k has no page (next: of the 32 steps that copies are at).
+    uint32_t hidden_a = __ballot_sync(0xffffffffu, ga < 0 && lane < mine);
+    uint32_t hidden_b = __ballot_sync(0xffffffffu, gb < 0 && lane < mine), next_a = 0, next_b = 0;
+    int stage = 0, to = min(stages - 1, mine) % stages, made = min(stages - 1, mine);
 #pragma unroll 1
     for (int k = 0; k < mine; ++k) {
-      if (!mbar_try_wait(&full[warp][stage], phase)) mbar_wait(&full[warp][stage], phase, &abort, p.err);
-      __syncwarp();                               // every lane is past the granule before this one: its stage is free
-      if (k + S - 1 < mine) {
-        if (turn == 32) {                         // the next 32 pages
-          turn = 0;
-          src = src_next;
-          src_next = source(k + S - 1 + 32 + lane);
+      uint64_t* bar = &full[warp][stage];
+      const uint32_t phase = (phases >> stage) & 1;
+      if (!mbar_try_wait(bar, phase)) mbar_wait(bar, phase, &abort, p.err);
+      __syncwarp();                               // every lane is past the step before this one: its stage is free
+      if ((k & 31) == 0 && k > 0) {
+        hidden_a = next_a;
+        hidden_b = next_b;
+      }
+      const int t = t0 + k, hide = (hidden_a >> (k & 31) & 1) | (hidden_b >> (k & 31) & 1) << 1;
+      if (made < mine) {
+        if ((made & 31) == 0) {                   // the next 32 steps' pages
+          look_up(made);
+          next_a = __ballot_sync(0xffffffffu, ga < 0 && made + lane < mine);
+          next_b = __ballot_sync(0xffffffffu, gb < 0 && made + lane < mine);
         }
-        if (lane == turn) issue((stage + S - 1) % S);
-        ++turn;
+        if (lane == (made & 31)) issue(to);
+        ++made;
+        to = to + 1 == stages ? 0 : to + 1;
       }
-      bool skip = false;
-      if (gone | gone_next) {
-        skip = (gone >> (k & 31)) & 1;
-      }
-      if ((k & 31) == 31) {
-        gone = gone_next;
-        gone_next = __ballot_sync(0xffffffffu, src_next == nullptr && k + 33 + lane < mine);
-      }
-      const int g = g0 + warp + k * kWarps;
-      const uint8_t* gr = ring + stage * Gr::kBytes;
-      stage = (stage + 1) % S;
-      phase ^= stage == 0;
-      if (skip) continue;
-      if (static_cast<unsigned>(g - whole0) < static_cast<unsigned>(wholes)) granule(std::false_type{}, gr, 16 * g);
-      else granule(std::true_type{}, gr, 16 * g);
+      const uint8_t* st = ring + stage * Sh::kStep;
+      phases ^= 1u << stage;
+      stage = stage + 1 == stages ? 0 : stage + 1;
+      if (static_cast<unsigned>(t - whole0) < static_cast<unsigned>(wholes) && hide == 0) step(std::false_type{}, st, 32 * t, 0);
+      else step(std::true_type{}, st, 32 * t, hide);
     }
 
-    // The warps' sums, beside one another where their copies were.
-    __syncthreads();
+    // The piece's sums as rows: where a held piece goes, or over the first stages.
+    const bool first_piece = !begins, whole = begins && ends;
+    float* sums = reinterpret_cast<float*>(ring + (first_piece ? (S - Sh::kHeld) * Sh::kStep : 0));
+    float(&most_of)[R] = stat[warp][first_piece ? 0 : 1][0];
+    float(&total_of)[R] = stat[warp][first_piece ? 0 : 1][1];
     const float up = kSplit ? 0x1p24f * pow2(sigma) : 0x1p24f;
+    __syncwarp();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int r = 8 * nt + 2 * tig + c;
         if (gid == 0) {
-          stat[warp * R + r] = top[nt][c] + (kSplit ? 0.f : static_cast<float>(sigma));
-          stat[(kWarps + warp) * R + r] = om[nt][c + 2];
+          most_of[r] = top[nt][c] + (kSplit ? 0.f : static_cast<float>(sigma));
+          total_of[r] = om[nt][c + 2];
         }
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           const float m = __shfl_sync(0xffffffffu, om[nt][c], 4 * ((D == 128 ? 4 : 0) + g) + tig);
-          *reinterpret_cast<float4*>(joined + (warp * R + r) * Sh::kPitch + 32 * g + 4 * gid) =
+          *reinterpret_cast<float4*>(sums + r * Sh::kPitch + 32 * g + 4 * gid) =
               make_float4(fmaf(o[nt][g][0][c], up, m), fmaf(o[nt][g][0][c + 2], up * 0.0625f, m),
                           fmaf(o[nt][g][1][c], up, m), fmaf(o[nt][g][1][c + 2], up * 0.0625f, m));
         }
       }
-    __syncthreads();
-
-    // Outputs of a whole segment; else a part for the second kernel.
-    float* part = p.parts + (2 * static_cast<int64_t>(blockIdx.x) + (begins ? 1 : 0)) * kPart<D, R>;
-    {
-      const int r = qr;
-      int i = 0, hq = 0;
-      const bool here = r < R && row_of(r, i, hq);
-      float v[8], most = kLow, sum = 0.f;
+    __syncwarp();
+    if (whole) {
+#pragma unroll 1
+      for (int r0 = 0; r0 < R && tile * R + r0 < rows; r0 += 32 / L) {
+        const int r = r0 + lane / L, l8 = lane % L;
+        int i, hq;
+        const bool here = row_of(r, i, hq);
+        const float sum = total_of[r], inv = sum == 0.f ? 0.f : __fdiv_rn(1.0f, sum);    // a row that sees nothing
+        float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.f;
-      if (r < R) {
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) most = fmaxf(most, stat[w * R + r]);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float f = exp2_fast(stat[w * R + r] - most);
-          const float* src = joined + (w * R + r) * Sh::kPitch + 8 * l8;
-          sum = fmaf(stat[(kWarps + w) * R + r], f, sum);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float4 x = reinterpret_cast<const float4*>(src)[j];
-            v[4 * j] = fmaf(x.x, f, v[4 * j]);
-            v[4 * j + 1] = fmaf(x.y, f, v[4 * j + 1]);
-            v[4 * j + 2] = fmaf(x.z, f, v[4 * j + 2]);
-            v[4 * j + 3] = fmaf(x.w, f, v[4 * j + 3]);
-          }
-        }
-      }
-      if (begins && ends) {
-        const float inv = sum == 0.f ? 0.f : __fdiv_rn(1.0f, sum);    // a row that sees nothing
+        for (int j = 0; j < 2; ++j)
+          *reinterpret_cast<float4*>(v + 4 * j) = *reinterpret_cast<const float4*>(sums + r * Sh::kPitch + 8 * l8 + 4 * j);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = sum == 0.f ? 0.f : v[j] * inv;
         store_row<T, D>(p, here, q.n0 + i, hq, l8, v);
-      } else if (r < R) {
+      }
+      fence_proxy_async_smem();      // the stages are written by copies again
+      __syncwarp();
+    } else {
+      if (first_piece) stages = S - Sh::kHeld;
+      if (lane == 0) {
+        int parts = 0;
+        if (begins) {
+          // The CTA whose runs have the segment's last unit: that of the last cut within it that was not moved to its end.
+          int64_t last = quotient(end - 1, per);
+          while (cut_at(last * per - at, size) == size) --last;
+          parts = static_cast<int>(quotient(last, kWarps) - blockIdx.x) + 1;
+        }
+        piece[warp][first_piece ? 0 : 1] = Piece{static_cast<int>(b), h, tile, parts, begins, ends};
+      }
+    }
+    u = min(end, u1);
+  }
+  if (abort) {               // copies that a wait gave up on land before the CTA ends
+    for (int k = 0; k < S; ++k) mbar_wait_bounded(&full[warp][k], ((phases >> k) & 1) ^ 1);
+  }
+  __syncthreads();
+
+  // The pieces of segments that several warps had, in the order of the line; each group of lanes does it for its rows. A segment
+  // that was begun and ended in this CTA is done with; what another CTA began (part 0) or ends (part 1) is left as a part.
+  float* parts = p.parts + 2 * static_cast<int64_t>(blockIdx.x) * kPart<D, R>;
+#pragma unroll 1
+  for (int r0 = warp * (32 / L); r0 < R; r0 += kWarps * (32 / L)) {
+    const int r = r0 + lane / L, l8 = lane % L;
+    float v[8], most = kLow, sum = 0.f;
+    bool open = false, begun = false;
+    Piece now = {-1, 0, 0, 0, false, false};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    auto close = [&](bool ended) {
+      const float inv = sum == 0.f ? 0.f : __fdiv_rn(1.0f, sum);
+      if (begun && ended) {
+        Sequence q;
+        q.load(p, now.b, R);
+        const int rr = now.tile * R + r, i = rr / p.group, hq = now.h * p.group + rr - i * p.group;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = sum == 0.f ? 0.f : v[j] * inv;
+        store_row<T, D>(p, rr < q.rows * p.group, q.n0 + i, hq, l8, v);
+      } else {
+        float* part = parts + (begun ? kPart<D, R> : 0);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           *reinterpret_cast<float4*>(part + r * D + 8 * l8 + 4 * j) = *reinterpret_cast<const float4*>(v + 4 * j);
@@ -758,30 +805,33 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, NT>::kCtas) attn_q4_kern
           part[R * D + r] = most;
           part[R * D + R + r] = sum;
         }
+        if (begun && threadIdx.x == 0) p.meta[blockIdx.x] = make_int4(now.b, now.h, now.tile, now.parts);
       }
-    }
-    if (begins && !ends && threadIdx.x == 0)
-{
-      // The CTA whose run has the segment's last unit: that of the last cut within it that was not moved to its end.
-      int64_t last = quotient(end - 1, per);
-      while (last > blockIdx.x && cut_at(last * per - at, size) == size) --last;
-      p.meta[blockIdx.x] = make_int4(static_cast<int>(b), h, tile, static_cast<int>(last - blockIdx.x) + 1);
-    }
-    fence_proxy_async_smem();      // the ring is written by copies again
-    __syncthreads();
-
-    // On to the next segment, in this sequence or the next that has any.
-    u = min(end, u1);
-    if (u < u1) {
-      int64_t n = q.units(p.c.heads);
-      while (u >= seq_at + n) {
-        seq_at += n;
-        q.load(p, ++b, R);
-        n = q.units(p.c.heads);
+      open = false;
+    };
+#pragma unroll 1
+    for (int w = 0; w < 2 * kWarps; ++w) {
+      const Piece& pc = piece[w >> 1][w & 1];
+      if (pc.b < 0) continue;
+      const float* src = reinterpret_cast<const float*>(smem + (w >> 1) * Sh::kRing + (w & 1 ? 0 : (S - Sh::kHeld) * Sh::kStep)) +
+                         r * Sh::kPitch + 8 * l8;
+      if (!open) {
+        open = true;
+        begun = pc.begins;
+        now = pc;
+        most = kLow;
+        sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
       }
+      const float m = stat[w >> 1][w & 1][0][r], more = fmaxf(most, m), f = exp2_fast(most - more), g = exp2_fast(m - more);
+      sum = fmaf(sum, f, stat[w >> 1][w & 1][1][r] * g);
+      most = more;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = fmaf(v[j], f, src[j] * g);
+      if (pc.ends) close(true);
     }
-  }  if (abort) {               // copies that a wait gave up on land before the CTA ends
-    for (int k = 0; k < S; ++k) mbar_wait_bounded(&full[warp][(stage + k) % S], phase ^ (stage + k >= S ? 0 : 1));
+    if (open) close(false);
   }
 }
 
@@ -900,8 +950,8 @@ cudaError_t run(const Attn& p, int num_sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     allowed.fetch_or(uint64_t(1) << dev, std::memory_order_release);
   }
-  const int grid = num_sms * Sh::kCtas;
-  e = launch_pdl(attn_q4_kernel<T, D, NT>, dim3(grid), dim3(kThreads), Sh::kSmem, s, p);
+  const int grid = num_sms;
+  e = launch_pdl(attn_q4_kernel<T, D, NT>, dim3(grid), dim3(Sh::kThreads), Sh::kSmem, s, p);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_q4_join_kernel<T, D, Sh::R>, dim3(num_sms), dim3(kJoinThreads), grid * sizeof(int), s, p, grid);
 }
@@ -914,13 +964,11 @@ cudaError_t run(const Attn& p, int num_sms, cudaStream_t s) {
   return run<T, 256, 1>(p, num_sms, s);
 }
 
-constexpr int kMostCtas = 2;            // of an SM, of any form
-
 }  // namespace
 
 size_t attn_q4_workspace(int n_q, int n_kv, int D, int64_t N, int64_t n_seqs, int num_sms) {
   const int R = tile_rows(n_q / n_kv, D, N, n_seqs);
-  const size_t ctas = static_cast<size_t>(num_sms) * kMostCtas;
+  const size_t ctas = static_cast<size_t>(num_sms);
   return ctas * (sizeof(int4) + 2 * sizeof(float) * (static_cast<size_t>(R) * D + 2 * R));
 }
 
@@ -928,7 +976,7 @@ cudaError_t launch_attn_q4(int dtype, const AttnArgs& a, const KvCache& c, void*
   const int64_t size = dtype == KQ_F32 ? 4 : 2;
   Attn p = {a, c, nullptr, static_cast<int4*>(ws), a.n_q / c.heads,
             a.ldq * size % 16 == 0 && (!a.O || a.ldo * size % 16 == 0), err};
-  p.parts = reinterpret_cast<float*>(p.meta + static_cast<size_t>(num_sms) * kMostCtas);
+  p.parts = reinterpret_cast<float*>(p.meta + num_sms);
   if (dtype == KQ_F16) return run<__half>(p, num_sms, s);
   if (dtype == KQ_BF16) return run<__nv_bfloat16>(p, num_sms, s);
   return run<float>(p, num_sms, s);
