@@ -41,6 +41,9 @@ constexpr float kTop = 10.f;            // weights are 2^(score - maximum + kTop
 constexpr int kSegmentUnits = 3;        // what beginning and ending a segment costs, in steps of 32 places
 constexpr int kRound = 2;               // steps that a segment is cut by
 
+#ifndef KQ_W
+#define KQ_W 12
+#endif
 struct Attn {
   AttnArgs a;
   KvCache c;
@@ -92,6 +95,11 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return (a | b) >> 32 == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
 }
 
+// a / b for 0 <= a, exactly: (a + 1/2) / b is at least 1 / (2 b) from a whole number, far above its rounding for a < 2^20.
+__device__ __forceinline__ int divide(int a, int b) {
+  return a < (1 << 20) ? static_cast<int>(__fdividef(static_cast<float>(a) + 0.5f, static_cast<float>(b))) : a / b;
+}
+
 // Where a cut `off` units into a segment of `size` is made: before it, after it, or after a whole number of rounds.
 __device__ __forceinline__ int64_t cut_at(int64_t off, int size) {
   const int w = static_cast<int>(off) - kSegmentUnits;
@@ -137,7 +145,7 @@ template <typename T, int D, int NT>
 struct Shape {
   static constexpr int R = 8 * NT;
   static constexpr bool kSplit = sizeof(T) == 4;
-  static constexpr int kWarps = D == 256 ? 7 : NT == 2 || kSplit ? 8 : 12;      // of a CTA, one to an SM
+  static constexpr int kWarps = D == 256 ? 7 : NT == 2 || kSplit ? 8 : KQ_W;      // of a CTA, one to an SM
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kStep = 2 * Granule<D>::kBytes;
   static constexpr int kPitch = D + 4;                                // of the rows of a piece's sums
@@ -150,7 +158,9 @@ struct Shape {
 // What a warp leaves for its CTA: the piece of a segment that was begun before its run (it may end there), and of
 // one that its run begins and does not end.
 struct Piece {
-  int b, h, tile, parts;     // sequence (-1: no such piece), key head, tile of rows; parts, where it begins a segment
+  int64_t n0;                // the sequence's first row
+  int b, h, tile, parts;     // sequence, key head, tile of rows; parts, where it begins a segment
+  int rows;                  // (row, query head) pairs of the sequence and the key head
   bool begins, ends;
 };
 
@@ -162,10 +172,12 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
   constexpr bool kSplit = Sh::kSplit;
   constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t scan[kWarps], cut_b[kWarps + 1], cut_seq[kWarps + 1], cut_u[kWarps + 1];
+  __shared__ int64_t scan[kWarps], cut_b[kWarps + 1], cut_seq[kWarps + 1], cut_u[kWarps + 1], first_unit[kThreads];
+  __shared__ int segment_size[kThreads];
   __shared__ uint64_t full[kWarps][S];
   __shared__ Piece piece[kWarps][2];
   __shared__ float stat[kWarps][2][2][R];                             // maxima and totals of the pieces
+  __shared__ uint32_t there;                                          // bit 2 w, 2 w + 1: warp w's pieces
   __shared__ int abort;                                               // a wait gave up
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
   uint8_t* ring = smem + warp * Sh::kRing;
@@ -173,9 +185,8 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
 #pragma unroll
     for (int k = 0; k < S; ++k) mbar_init(&full[warp][k], 1);
     fence_mbar_init();
-    piece[warp][0].b = piece[warp][1].b = -1;
   }
-  if (threadIdx.x == 0) abort = 0;
+  if (threadIdx.x == 0) abort = 0, there = 0;
   pdl_enter();
 
   // The CTA's runs: run i begins at the cut cut_u[i] of the line, in the sequence cut_b[i], whose first unit is cut_seq[i]. The
@@ -222,16 +233,23 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
           c0 = static_cast<int64_t>(blockIdx.x) * kWarps * per;
           if (c0 >= total) return;
         }
-        if (pass == 1 && x < c0 + (kWarps + 1) * per && c0 < x + v) {
-#pragma unroll 1
-          for (int k = 0; k <= kWarps; ++k) {
-            const int64_t cut = c0 + k * per;
-            if (x <= cut && cut < x + v) {
-              const int64_t seg = x + quotient(cut - x, size) * size;
-              cut_b[k] = i;
-              cut_seq[k] = x;
-              cut_u[k] = seg + cut_at(cut - seg, size);
+        if (pass == 1) {
+          first_unit[threadIdx.x] = x;
+          segment_size[threadIdx.x] = size;
+          __syncthreads();
+          // Threads 0..kWarps look for their cut among these sequences: the last that begins at or before it.
+          const int64_t cut = c0 + threadIdx.x * per;
+          if (threadIdx.x <= kWarps && cut >= first_unit[0] && cut < before) {
+            int lo = 0, hi = kThreads;
+            while (hi - lo > 1) {
+              const int mid = (lo + hi) >> 1;
+              if (first_unit[mid] <= cut) lo = mid;
+              else hi = mid;
             }
+            const int64_t seg = first_unit[lo] + quotient(cut - first_unit[lo], segment_size[lo]) * segment_size[lo];
+            cut_b[threadIdx.x] = i0 + lo;
+            cut_seq[threadIdx.x] = first_unit[lo];
+            cut_u[threadIdx.x] = seg + cut_at(cut - seg, segment_size[lo]);
           }
         }
       }
@@ -261,7 +279,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
     const int size = kSegmentUnits + q.steps;
     const int seg = static_cast<int>(quotient(u - seq_at, size));
     const int64_t at = seq_at + static_cast<int64_t>(seg) * size, end = at + size;
-    const int h = seg / q.tiles, tile = seg - h * q.tiles;
+    const int h = q.tiles == 1 ? seg : divide(seg, q.tiles), tile = seg - h * q.tiles;
     const bool begins = u == at, ends = end <= u1;
     int t0 = q.first + max(0, static_cast<int>(u - at) - kSegmentUnits);
     int t1 = q.first + max(0, static_cast<int>(min(end, u1) - at) - kSegmentUnits);
@@ -270,13 +288,13 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
     const int rows = q.rows * p.group;
     auto row_of = [&](int r, int& i, int& hq) {
       const int rr = tile * R + r;
-      i = rr / p.group;
+      i = divide(rr, p.group);
       hq = h * p.group + rr - i * p.group;
       return rr < rows;
     };
     auto seen_of = [&](int i) { return q.len - q.rows + 1 + i; };
     auto low_of = [&](int seen) { return p.a.window > 0 ? static_cast<int>(max(int64_t(0), seen - p.a.window)) : 0; };
-    const int seen_least = seen_of(tile * R / p.group), seen_most = seen_of((min(tile * R + R, rows) - 1) / p.group);
+    const int seen_least = seen_of(divide(tile * R, p.group)), seen_most = seen_of(divide(min(tile * R + R, rows) - 1, p.group));
     const int low_least = low_of(seen_least), low_most = low_of(seen_most);
     // Steps of the run that a row of this tile sees, and those of them that all of its rows see whole.
     t0 = max(t0, low_least >> 5);
@@ -740,7 +758,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
       }
     __syncwarp();
     if (whole) {
-#pragma unroll 1
+#pragma unroll 2
       for (int r0 = 0; r0 < R && tile * R + r0 < rows; r0 += 32 / L) {
         const int r = r0 + lane / L, l8 = lane % L;
         int i, hq;
@@ -766,7 +784,8 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
           while (cut_at(last * per - at, size) == size) --last;
           parts = static_cast<int>(quotient(last, kWarps) - blockIdx.x) + 1;
         }
-        piece[warp][first_piece ? 0 : 1] = Piece{static_cast<int>(b), h, tile, parts, begins, ends};
+        piece[warp][first_piece ? 0 : 1] = Piece{q.n0, static_cast<int>(b), h, tile, parts, rows, begins, ends};
+        atomicOr(&there, 1u << (2 * warp + (first_piece ? 0 : 1)));
       }
     }
     u = min(end, u1);
@@ -775,6 +794,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
     for (int k = 0; k < S; ++k) mbar_wait_bounded(&full[warp][k], ((phases >> k) & 1) ^ 1);
   }
   __syncthreads();
+  if (there == 0) return;
 
   // The pieces of segments that several warps had, in the order of the line; each group of lanes does it for its rows. A segment
   // that was begun and ended in this CTA is done with; what another CTA began (part 0) or ends (part 1) is left as a part.
@@ -784,18 +804,16 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
     const int r = r0 + lane / L, l8 = lane % L;
     float v[8], most = kLow, sum = 0.f;
     bool open = false, begun = false;
-    Piece now = {-1, 0, 0, 0, false, false};
+    const Piece* now = nullptr;
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 0.f;
     auto close = [&](bool ended) {
       const float inv = sum == 0.f ? 0.f : __fdiv_rn(1.0f, sum);
       if (begun && ended) {
-        Sequence q;
-        q.load(p, now.b, R);
-        const int rr = now.tile * R + r, i = rr / p.group, hq = now.h * p.group + rr - i * p.group;
+        const int rr = now->tile * R + r, i = divide(rr, p.group), hq = now->h * p.group + rr - i * p.group;
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = sum == 0.f ? 0.f : v[j] * inv;
-        store_row<T, D>(p, rr < q.rows * p.group, q.n0 + i, hq, l8, v);
+        store_row<T, D>(p, rr < now->rows, now->n0 + i, hq, l8, v);
       } else {
         float* part = parts + (begun ? kPart<D, R> : 0);
 #pragma unroll
@@ -805,20 +823,20 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
           part[R * D + r] = most;
           part[R * D + R + r] = sum;
         }
-        if (begun && threadIdx.x == 0) p.meta[blockIdx.x] = make_int4(now.b, now.h, now.tile, now.parts);
+        if (begun && threadIdx.x == 0) p.meta[blockIdx.x] = make_int4(now->b, now->h, now->tile, now->parts);
       }
       open = false;
     };
 #pragma unroll 1
-    for (int w = 0; w < 2 * kWarps; ++w) {
+    for (uint32_t left = there; left; left &= left - 1) {
+      const int w = __ffs(left) - 1;
       const Piece& pc = piece[w >> 1][w & 1];
-      if (pc.b < 0) continue;
       const float* src = reinterpret_cast<const float*>(smem + (w >> 1) * Sh::kRing + (w & 1 ? 0 : (S - Sh::kHeld) * Sh::kStep)) +
                          r * Sh::kPitch + 8 * l8;
       if (!open) {
         open = true;
         begun = pc.begins;
-        now = pc;
+        now = &pc;
         most = kLow;
         sum = 0.f;
 #pragma unroll
