@@ -18,10 +18,12 @@
 // halves, as their queries are); they are taken relative to a power of two not below the largest s so
 // far, so that none leaves fp16's range.
 //
-// Work is shared out evenly whatever the sequences' lengths: the steps of 32 places of all (sequence,
-// key head, tile of rows) segments stand in one line, of which each warp takes an equal run. The pieces of a
-// segment in a CTA's warps are joined there; what lies in several CTAs is joined by a second kernel from the
-// parts that the first leaves in the workspace. Both go by the order of the line: results do not depend on scheduling.
+// Work is shared out evenly whatever the sequences' lengths: all (sequence, key head, tile of rows) segments stand
+// in one line, of which each warp takes an equal run. Where segments are few and short, the line is of pieces of so many steps of
+// 32 places that there is at most one for each warp; else of steps, and a warp may have the end of a segment, others whole,
+// and the beginning of one. The pieces of a segment in a CTA's warps are joined there; what lies in several CTAs is
+// joined by a second kernel from the parts that the first leaves in the workspace. Both go by the
+// order of the line: results do not depend on scheduling.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -39,16 +41,14 @@ constexpr float kLow = -1e30f;          // the maximum before any score
 constexpr float kAhead = 4.f;           // how far a score may pass the maximum (log2) before it is moved
 constexpr float kTop = 10.f;            // weights are 2^(score - maximum + kTop): 2^14 at most
 constexpr int kSegmentUnits = 3;        // what beginning and ending a segment costs, in steps of 32 places
-constexpr int kRound = 2;               // steps that a segment is cut by
+constexpr int kLongPiece = 10;          // longer pieces' rounding costs more than runs that have parts of two segments
+constexpr int kRound = 2;               // steps that a segment is cut by, and the fewest of a piece
 
-#ifndef KQ_W
-#define KQ_W 12
-#endif
 struct Attn {
   AttnArgs a;
   KvCache c;
   float* parts;              // [CTAs][2]: pieces of segments that another CTA began, or ends; kPart floats each
-  int4* meta;                // [CTAs]: what part 1 is (sequence or -1, key head, tile, parts)
+  int4* meta;                // [CTAs][2]: what part 1 is (key head or -1, tile, parts; the sequence's first row, its pairs)
   int group;                 // query heads of a key head
   bool vec;                  // rows of Q (and of O) lie on 16-byte boundaries
   int* err;
@@ -100,14 +100,6 @@ __device__ __forceinline__ int divide(int a, int b) {
   return a < (1 << 20) ? static_cast<int>(__fdividef(static_cast<float>(a) + 0.5f, static_cast<float>(b))) : a / b;
 }
 
-// Where a cut `off` units into a segment of `size` is made: before it, after it, or after a whole number of rounds.
-__device__ __forceinline__ int64_t cut_at(int64_t off, int size) {
-  const int w = static_cast<int>(off) - kSegmentUnits;
-  if (w <= 0) return 0;
-  const int to = kSegmentUnits + (w + kRound - 1) / kRound * kRound;
-  return to + kRound / 2 >= size ? size : to;
-}
-
 // A sequence's rows and the steps of 32 places that any of them sees.
 struct Sequence {
   int64_t n0;
@@ -125,8 +117,29 @@ struct Sequence {
     first = static_cast<int>(begin >> 5);
     steps = len > begin ? ((len - 1) >> 5) + 1 - first : 0;
   }
-  __device__ __forceinline__ int64_t units(int heads) const {
-    return static_cast<int64_t>(heads) * tiles * (kSegmentUnits + steps);
+};
+
+// The line's units: pieces of `piece` steps, or (piece 0) steps, and kSegmentUnits for each segment.
+struct Line {
+  int piece;
+  int64_t per;               // units of a run
+  __device__ __forceinline__ int size(const Sequence& s) const {
+    return piece ? max(1, (s.steps + piece - 1) / piece) : kSegmentUnits + s.steps;
+  }
+  __device__ __forceinline__ int64_t units(const Sequence& s, int heads) const {
+    return static_cast<int64_t>(heads) * s.tiles * size(s);
+  }
+  // Where a cut `off` units into a segment of `size` is made: before it, after it, or after a whole number of rounds.
+  __device__ __forceinline__ int64_t cut_at(int64_t off, int size) const {
+    if (piece) return off;
+    const int w = static_cast<int>(off) - kSegmentUnits;
+    if (w <= 0) return 0;
+    const int to = kSegmentUnits + (w + kRound - 1) / kRound * kRound;
+    return to + kRound / 2 >= size ? size : to;
+  }
+  // The segment's steps before its unit `off`.
+  __device__ __forceinline__ int steps_before(int64_t off, const Sequence& s) const {
+    return piece ? static_cast<int>(min(off * piece, static_cast<int64_t>(s.steps))) : max(0, static_cast<int>(off) - kSegmentUnits);
   }
 };
 
@@ -145,7 +158,7 @@ template <typename T, int D, int NT>
 struct Shape {
   static constexpr int R = 8 * NT;
   static constexpr bool kSplit = sizeof(T) == 4;
-  static constexpr int kWarps = D == 256 ? 7 : NT == 2 || kSplit ? 8 : KQ_W;      // of a CTA, one to an SM
+  static constexpr int kWarps = D == 256 ? 7 : NT == 2 || kSplit ? 8 : 12;      // of a CTA, one to an SM
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kStep = 2 * Granule<D>::kBytes;
   static constexpr int kPitch = D + 4;                                // of the rows of a piece's sums
@@ -159,7 +172,7 @@ struct Shape {
 // one that its run begins and does not end.
 struct Piece {
   int64_t n0;                // the sequence's first row
-  int b, h, tile, parts;     // sequence, key head, tile of rows; parts, where it begins a segment
+  int h, tile, parts;        // key head, tile of rows; parts, where it begins a segment
   int rows;                  // (row, query head) pairs of the sequence and the key head
   bool begins, ends;
 };
@@ -189,73 +202,93 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
   if (threadIdx.x == 0) abort = 0, there = 0;
   pdl_enter();
 
-  // The CTA's runs: run i begins at the cut cut_u[i] of the line, in the sequence cut_b[i], whose first unit is cut_seq[i]. The
-  // sum over the sequences comes first; where they are more than the threads, another pass finds the cuts.
-  int64_t per = 1, total = 0;
-  if (threadIdx.x == 0) p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  // The CTA's runs: run i begins at the cut cut_u[i] of the line, in the sequence cut_b[i], whose first unit is cut_seq[i]. A
+  // pass over the sequences adds up their segments and steps; another finds the cuts.
+  Line line = {0, 1};
+  int64_t total = 0;
+  if (threadIdx.x == 0) p.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
   {
-    const int64_t n_seqs = p.c.n_seqs;
-    const bool once = n_seqs <= kThreads;
-    int64_t c0 = 0;
+    const int64_t n_seqs = p.c.n_seqs, runs = static_cast<int64_t>(gridDim.x) * kWarps;
+    int64_t c0 = 0, before = 0;
+    // The sum of v over the threads before this one, added to `before`, which moves on by the sum over all.
+    const auto sum_before = [&](int64_t v) {
+      int64_t x = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) scan[warp] = x;
+      __syncthreads();
+      x += before - v;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        x += w < warp ? scan[w] : 0;
+        before += scan[w];
+      }
+      return x;
+    };
+    Sequence s = {};
 #pragma unroll 1
-    for (int pass = once ? 1 : 0; pass < 2; ++pass) {
-      int64_t before = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+      int64_t segments = 0, steps = 0;
 #pragma unroll 1
       for (int64_t i0 = 0; i0 < n_seqs; i0 += kThreads) {
         const int64_t i = i0 + threadIdx.x;
-        int64_t v = 0;
-        int size = 1;
-        if (i < n_seqs) {
-          Sequence s;
-          s.load(p, i, R);
-          v = s.units(p.c.heads);
-          size = kSegmentUnits + s.steps;
+        if (pass == 0 || n_seqs > kThreads) {
+          s = Sequence{};
+          if (i < n_seqs) s.load(p, i, R);
         }
-        int64_t x = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += y;
+        if (pass == 0) {
+          segments += static_cast<int64_t>(p.c.heads) * s.tiles;
+          steps += static_cast<int64_t>(p.c.heads) * s.tiles * s.steps;
+          continue;
         }
+        const int size = line.size(s);
+        const int64_t x = sum_before(line.units(s, p.c.heads));
+        first_unit[threadIdx.x] = x;
+        segment_size[threadIdx.x] = size;
         __syncthreads();
-        if (lane == 31) scan[warp] = x;
-        __syncthreads();
-        x += before - v;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          x += w < warp ? scan[w] : 0;
-          before += scan[w];
-        }
-        if (once || (pass == 0 && i0 + kThreads >= n_seqs)) {
-          total = before;
-          const int64_t runs = static_cast<int64_t>(gridDim.x) * kWarps;
-          per = max(static_cast<int64_t>(kSegmentUnits + kRound), quotient(total + runs - 1, runs));
-          c0 = static_cast<int64_t>(blockIdx.x) * kWarps * per;
-          if (c0 >= total) return;
-        }
-        if (pass == 1) {
-          first_unit[threadIdx.x] = x;
-          segment_size[threadIdx.x] = size;
-          __syncthreads();
-          // Threads 0..kWarps look for their cut among these sequences: the last that begins at or before it.
-          const int64_t cut = c0 + threadIdx.x * per;
-          if (threadIdx.x <= kWarps && cut >= first_unit[0] && cut < before) {
-            int lo = 0, hi = kThreads;
-            while (hi - lo > 1) {
-              const int mid = (lo + hi) >> 1;
-              if (first_unit[mid] <= cut) lo = mid;
-              else hi = mid;
-            }
-            const int64_t seg = first_unit[lo] + quotient(cut - first_unit[lo], segment_size[lo]) * segment_size[lo];
-            cut_b[threadIdx.x] = i0 + lo;
-            cut_seq[threadIdx.x] = first_unit[lo];
-            cut_u[threadIdx.x] = seg + cut_at(cut - seg, segment_size[lo]);
+        // Threads 0..kWarps look for their cut among these sequences: the last that begins at or before it.
+        const int64_t cut = c0 + threadIdx.x * line.per;
+        if (threadIdx.x <= kWarps && cut >= first_unit[0] && cut < before) {
+          int lo = 0, hi = static_cast<int>(min(static_cast<int64_t>(kThreads), n_seqs - i0));
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (first_unit[mid] <= cut) lo = mid;
+            else hi = mid;
           }
+          const int64_t seg = first_unit[lo] + quotient(cut - first_unit[lo], segment_size[lo]) * segment_size[lo];
+          cut_b[threadIdx.x] = i0 + lo;
+          cut_seq[threadIdx.x] = first_unit[lo];
+          cut_u[threadIdx.x] = seg + line.cut_at(cut - seg, segment_size[lo]);
         }
       }
+      if (pass == 0) {
+        // Pieces of so many steps that with one shorter piece a segment they are no more than the runs.
+        sum_before(segments);
+        segments = before;
+        before = 0;
+        sum_before(steps);
+        steps = before;
+        before = 0;
+        const int64_t piece = 2 * segments <= runs ? quotient(steps + runs - segments - 1, runs - segments) : kLongPiece + 1;
+        if (piece <= kLongPiece) {
+          line.piece = max(kRound, static_cast<int>(piece));
+          total = runs;                          // at most
+        } else {
+          total = steps + kSegmentUnits * segments;
+          line.per = max(static_cast<int64_t>(kSegmentUnits + kRound), quotient(total + runs - 1, runs));
+        }
+        c0 = static_cast<int64_t>(blockIdx.x) * kWarps * line.per;
+        if (c0 >= total) return;
+      }
     }
+    total = before;
+    if (c0 >= total) return;
     __syncthreads();
-    if (threadIdx.x <= kWarps && c0 + threadIdx.x * per >= total) cut_u[threadIdx.x] = total;
+    if (threadIdx.x <= kWarps && c0 + threadIdx.x * line.per >= total) cut_u[threadIdx.x] = total;
     __syncthreads();
   }
 
@@ -268,21 +301,20 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
 
   while (u < u1) {
     {                        // a run may begin where a sequence ends, and goes on through others
-      int64_t n = q.units(p.c.heads);
+      int64_t n = line.units(q, p.c.heads);
       while (u >= seq_at + n) {
         seq_at += n;
         q.load(p, ++b, R);
-        n = q.units(p.c.heads);
+        n = line.units(q, p.c.heads);
       }
     }
     // The segment that u lies in: [at, end) of the line.
-    const int size = kSegmentUnits + q.steps;
+    const int size = line.size(q);
     const int seg = static_cast<int>(quotient(u - seq_at, size));
     const int64_t at = seq_at + static_cast<int64_t>(seg) * size, end = at + size;
     const int h = q.tiles == 1 ? seg : divide(seg, q.tiles), tile = seg - h * q.tiles;
     const bool begins = u == at, ends = end <= u1;
-    int t0 = q.first + max(0, static_cast<int>(u - at) - kSegmentUnits);
-    int t1 = q.first + max(0, static_cast<int>(min(end, u1) - at) - kSegmentUnits);
+    int t0 = q.first + line.steps_before(u - at, q), t1 = q.first + line.steps_before(min(end, u1) - at, q);
 
     // Row r of the tile: new row i = r' / group, head r' % group, r' = tile * R + r. It sees [low, seen).
     const int rows = q.rows * p.group;
@@ -336,7 +368,21 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
         if (gb >= 0) bulk_g2s(dst + Gr::kBytes, p.c.data + static_cast<int64_t>(gb) * Gr::kBytes, Gr::kBytes, bar);
       }
     };
+    Raw8<T> raw[G];          // of the queries: the first rows' are on their way while the pages are looked up
+    auto load_rows = [&](int nt) {
+      int i, hq;
+      if (row_of(8 * nt + gid, i, hq)) {
+        const T* src = static_cast<const T*>(p.a.Q) + (q.n0 + i) * p.a.ldq + static_cast<int64_t>(hq) * D + 8 * tig;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          if (p.vec) raw[g].template load<true>(src + 32 * g);
+          else raw[g].template load<false>(src + 32 * g);
+        }
+      }
+    };
+    load_rows(0);
     look_up(0);
+    if (lane < min(stages - 1, mine)) issue(lane);
 
     // Queries as operands: lane (gid, tig) has of row gid the elements 32 g + 8 tig + 0..7, times 2^a with the
     // row's largest between 2^14 and 2^15 (so that fp16 and bf16 queries are exact), the odd ones
@@ -348,19 +394,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
     for (int nt = 0; nt < NT; ++nt) {
       int i, hq;
       const bool here = row_of(8 * nt + gid, i, hq);
-      const T* src = static_cast<const T*>(p.a.Q) + (q.n0 + i) * p.a.ldq + static_cast<int64_t>(hq) * D + 8 * tig;
-      Raw8<T> raw[G];
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        if (here) {
-          if (p.vec) raw[g].template load<true>(src + 32 * g);
-          else raw[g].template load<false>(src + 32 * g);
-        }
-      }
-      if (nt == 0) {         // the copies begin while the queries are on their way
-        const int now = min(stages - 1, mine);
-        if (lane < now) issue(lane);
-      }
+      if (nt > 0) load_rows(nt);
       float most = 0.f, sums[G];
 #pragma unroll
       for (int g = 0; g < G; ++g)
@@ -780,11 +814,11 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
         int parts = 0;
         if (begins) {
           // The CTA whose runs have the segment's last unit: that of the last cut within it that was not moved to its end.
-          int64_t last = quotient(end - 1, per);
-          while (cut_at(last * per - at, size) == size) --last;
+          int64_t last = quotient(end - 1, line.per);
+          while (line.cut_at(last * line.per - at, size) == size) --last;
           parts = static_cast<int>(quotient(last, kWarps) - blockIdx.x) + 1;
         }
-        piece[warp][first_piece ? 0 : 1] = Piece{q.n0, static_cast<int>(b), h, tile, parts, rows, begins, ends};
+        piece[warp][first_piece ? 0 : 1] = Piece{q.n0, h, tile, parts, rows, begins, ends};
         atomicOr(&there, 1u << (2 * warp + (first_piece ? 0 : 1)));
       }
     }
@@ -823,7 +857,10 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
           part[R * D + r] = most;
           part[R * D + R + r] = sum;
         }
-        if (begun && threadIdx.x == 0) p.meta[blockIdx.x] = make_int4(now->b, now->h, now->tile, now->parts);
+        if (begun && threadIdx.x == 0) {
+          p.meta[2 * blockIdx.x] = make_int4(now->h, now->tile, now->parts, 0);
+          p.meta[2 * blockIdx.x + 1] = make_int4(static_cast<int>(now->n0), now->rows, 0, 0);
+        }
       }
       open = false;
     };
@@ -860,7 +897,7 @@ constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps;
 template <typename T, int D, int R>
 __global__ void __launch_bounds__(kJoinThreads) attn_q4_join_kernel(const Attn p, int ctas) {
   constexpr int E = D / 32;                                           // elements of a lane
-  extern __shared__ int list[];                                       // [ctas]
+  extern __shared__ int4 list[];                                      // [ctas][2]: the CTA, and what it left in meta
   __shared__ float sums[kJoinWarps][D];
   __shared__ int found[kJoinWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -868,9 +905,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_q4_join_kernel(const Attn p
   int n = 0;
   for (int c0 = 0; c0 < ctas; c0 += kJoinThreads) {
     const int c = c0 + threadIdx.x;
-    const bool there = c < ctas && p.meta[c].x >= 0;
-    const uint32_t all = __ballot_sync(0xffffffffu, there);
-    __syncthreads();
+    int4 a = make_int4(-1, 0, 0, 0), b = a;
+    if (c < ctas) a = p.meta[2 * c], b = p.meta[2 * c + 1];
+    const uint32_t all = __ballot_sync(0xffffffffu, a.x >= 0);
+    if (c0 > 0) __syncthreads();
     if (lane == 0) found[warp] = __popc(all);
     __syncthreads();
     int at = n;
@@ -879,8 +917,14 @@ __global__ void __launch_bounds__(kJoinThreads) attn_q4_join_kernel(const Attn p
       if (w < warp) at += found[w];
       n += found[w];
     }
-    if (there) list[at + __popc(all & ((1u << lane) - 1))] = c;
+    if (a.x >= 0) {
+      at += __popc(all & ((1u << lane) - 1));
+      a.w = c;
+      list[2 * at] = a;
+      list[2 * at + 1] = b;
+    }
   }
+  if (n == 0) return;
   __syncthreads();
   const int items = n * R;
   int W = 1;                                                          // warps of a row
@@ -888,35 +932,38 @@ __global__ void __launch_bounds__(kJoinThreads) attn_q4_join_kernel(const Attn p
   const int each = kJoinWarps / W, group = warp / W, part0 = warp % W;
   for (int first = blockIdx.x * each; first < items; first += gridDim.x * each) {
     const int item = first + group;
-    int i = 0, hq = 0;
+    int i = 0, hq = 0, n0 = 0;
     bool here = false;
-    Sequence q;
-    float sum = 0.f;
-    float acc[E];
+    float sum = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
     if (item < items) {
-      const int c = list[item / R], r = item % R;
-      const int4 meta = p.meta[c];
-      q.load(p, meta.x, R);
-      const int rr = meta.z * R + r;
-      i = rr / p.group;
-      hq = meta.y * p.group + rr - i * p.group;
-      here = rr < q.rows * p.group;
-      const float* base = p.parts + 2 * static_cast<int64_t>(c) * kPart<D, R>;
+      const int4 a = list[2 * (item / R)], b = list[2 * (item / R) + 1];
+      const int r = item % R, rr = a.y * R + r, count = a.z;
+      i = divide(rr, p.group);
+      hq = a.x * p.group + rr - i * p.group;
+      n0 = b.x;
+      here = rr < b.y;
+      const float* base = p.parts + 2 * static_cast<int64_t>(a.w) * kPart<D, R>;
       auto part = [&](int k) { return base + (k == 0 ? 1 : 2 * static_cast<int64_t>(k)) * kPart<D, R>; };
       if (here) {
+        // Parts k0 + lane: their maxima and totals; the sums relative to the largest so far.
         float most = kLow;
-        for (int k = lane; k < meta.w; k += 32) most = fmaxf(most, part(k)[R * D + r]);
+        for (int k0 = 0; k0 < count; k0 += 32) {
+          const int k = k0 + lane, some = min(32, count - k0);
+          float m = kLow, t = 0.f;
+          if (k < count) m = part(k)[R * D + r], t = part(k)[R * D + R + r];
+          float more = m;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-        for (int k0 = 0; k0 < meta.w; k0 += 32) {
-          const int k = k0 + lane;
-          const float f = k < meta.w ? exp2_fast(part(k)[R * D + r] - most) : 0.f;
-          if (k < meta.w) sum = fmaf(f, part(k)[R * D + R + r], sum);
-          const int count = min(32, meta.w - k0);
+          for (int o = 16; o > 0; o >>= 1) more = fmaxf(more, __shfl_xor_sync(0xffffffffu, more, o));
+          more = fmaxf(more, most);
+          const float by = exp2_fast(most - more), f = k < count ? exp2_fast(m - more) : 0.f;
+          most = more;
+          sum = sum * by + f * t;
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] *= by;
 #pragma unroll 4
-          for (int t = part0; t < count; t += W) {
+          for (int t = part0; t < some; t += W) {
             const float g = __shfl_sync(0xffffffffu, f, t);
             const float* src = part(k0 + t) + r * D + E * lane;
             float v[E];
@@ -946,7 +993,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_q4_join_kernel(const Attn p
           for (int w = 0; w < W; ++w) v[j] += sums[warp + w][8 * lane + j];
         v[j] = sum == 0.f ? 0.f : v[j] * inv;
       }
-      store_row<T, D>(p, here && lane < D / 8, q.n0 + i, hq, lane, v);
+      store_row<T, D>(p, here && lane < D / 8, static_cast<int64_t>(n0) + i, hq, lane, v);
     }
     __syncthreads();
   }
@@ -971,7 +1018,7 @@ cudaError_t run(const Attn& p, int num_sms, cudaStream_t s) {
   const int grid = num_sms;
   e = launch_pdl(attn_q4_kernel<T, D, NT>, dim3(grid), dim3(Sh::kThreads), Sh::kSmem, s, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_q4_join_kernel<T, D, Sh::R>, dim3(num_sms), dim3(kJoinThreads), grid * sizeof(int), s, p, grid);
+  return launch_pdl(attn_q4_join_kernel<T, D, Sh::R>, dim3(num_sms), dim3(kJoinThreads), grid * 2 * sizeof(int4), s, p, grid);
 }
 
 template <typename T>
@@ -987,14 +1034,14 @@ cudaError_t run(const Attn& p, int num_sms, cudaStream_t s) {
 size_t attn_q4_workspace(int n_q, int n_kv, int D, int64_t N, int64_t n_seqs, int num_sms) {
   const int R = tile_rows(n_q / n_kv, D, N, n_seqs);
   const size_t ctas = static_cast<size_t>(num_sms);
-  return ctas * (sizeof(int4) + 2 * sizeof(float) * (static_cast<size_t>(R) * D + 2 * R));
+  return ctas * (2 * sizeof(int4) + 2 * sizeof(float) * (static_cast<size_t>(R) * D + 2 * R));
 }
 
 cudaError_t launch_attn_q4(int dtype, const AttnArgs& a, const KvCache& c, void* ws, int* err, int num_sms, cudaStream_t s) {
   const int64_t size = dtype == KQ_F32 ? 4 : 2;
   Attn p = {a, c, nullptr, static_cast<int4*>(ws), a.n_q / c.heads,
             a.ldq * size % 16 == 0 && (!a.O || a.ldo * size % 16 == 0), err};
-  p.parts = reinterpret_cast<float*>(p.meta + num_sms);
+  p.parts = reinterpret_cast<float*>(p.meta + 2 * num_sms);
   if (dtype == KQ_F16) return run<__half>(p, num_sms, s);
   if (dtype == KQ_BF16) return run<__nv_bfloat16>(p, num_sms, s);
   return run<float>(p, num_sms, s);

@@ -167,7 +167,7 @@ kq_status kq_sample(int dtype, const void* logits, int64_t ld, const float* temp
                     kq_stream_t stream) {
   if (!valid_dtype(dtype)) return KQ_ERR_TYPE;
   if (!logits || !u || !ids) return KQ_ERR_NULL;
-  if (V <= 0 || V > SAMPLE_MAX_V || !valid_size(N) || !valid_ld_in(ld, V)) return KQ_ERR_SHAPE;
+  if (V <= 0 || V > SAMPLE_MAX_V || !valid_size(N) || N * V > (int64_t(1) << 40) || !valid_ld_in(ld, V)) return KQ_ERR_SHAPE;
   if (!aligned16(logits) || !aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4) ||
       !aligned(u, 4) || !aligned(ids, 4) || !aligned(probs, 4))
     return KQ_ERR_ALIGN;

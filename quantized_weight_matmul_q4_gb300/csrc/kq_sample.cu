@@ -6,12 +6,18 @@
 // shortest of them is kept, and the token is the first, by index, at which the sum of
 // the kept weights passes u times their total.
 //
+// A row is held in the shared memory of a cluster of CTAs. Where top_k or top_p limit it, a histogram over bins of (max l - l) / T
+// of 1/32 of an octave finds the bin that the limit falls into; the tokens that may be kept, if they are
+// few, then go to one CTA, else the cluster goes on. The limit itself is found by histograms of ever
+// finer runs of the logits' bits, until one value is left; of its equals the first by index are kept.
+//
 // Weights are whole numbers, w * 2^43 to within 2^-30 of their size: sums of them are exact in 64
 // bits and the same in any order, so nothing here depends on scheduling, and two sums compare as
 // those of the definition do but for that relative error.
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "kq_attn.h"
 #include "kq_types.cuh"
@@ -21,6 +27,10 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 2048, kPerThread = kBins / kThreads;
+constexpr int kList = 2048;                      // tokens that one CTA takes over
+constexpr int kMostCtas = 16;
+constexpr int kSliceBytes = 128 * 1024;
 constexpr uint64_t kOne = uint64_t(1) << 43;     // the weight of the largest logit
 
 // 2^(31 - j / 64), rounded.
@@ -79,142 +89,212 @@ struct Weigh {
   }
 };
 
-template <typename V>
-__device__ __forceinline__ V block_all(V v, V* part, bool largest) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const V w = __shfl_xor_sync(0xffffffffu, v, o);
-    v = largest ? max(v, w) : v + w;
-  }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = part[0];
-#pragma unroll
-  for (int i = 1; i < kWarps; ++i) v = largest ? max(v, part[i]) : v + part[i];
-  return v;
+__device__ __forceinline__ float value_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
-// A row per CTA, read again for every step: thresholds by bisection over the keys.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_rows_kernel(const SampleArgs a) {
-  __shared__ uint32_t table[64];
-  __shared__ uint64_t part[kWarps];
-  __shared__ uint64_t sums[kThreads + 1];
-  __shared__ uint32_t ties[kThreads + 1];
-  pdl_enter();
-  if (threadIdx.x < 64) table[threadIdx.x] = kPow2[threadIdx.x];
-  const int64_t n = blockIdx.x;
-  const T* x = static_cast<const T*>(a.logits) + n * a.ld;
-  const int V = static_cast<int>(a.V);
-  auto at = [&](int i) { return usable(to_f32(x[i])); };
-  auto sum = [&](auto f) {
-    uint64_t s = 0;
-    for (int i = threadIdx.x; i < V; i += kThreads) s += f(at(i));
-    return block_all<uint64_t>(s, part, false);
-  };
-  uint32_t top = kNone;
-  for (int i = threadIdx.x; i < V; i += kThreads) top = max(top, key_of(at(i)));
-  top = block_all<uint32_t>(top, reinterpret_cast<uint32_t*>(part), true);
-  if (top == kNone) {
-    if (threadIdx.x == 0) {
-      a.ids[n] = 0;
-      if (a.probs) a.probs[n] = 0.f;
-    }
-    return;
+__device__ __forceinline__ uint64_t load_cluster(uint32_t addr) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_cluster(uint32_t addr, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
+// What the CTAs that work on a row share: the row's cluster, or (ctas = 1) one CTA.
+struct Team {
+  int ctas, rank;
+  uint64_t* slots;           // [2]: what this CTA tells the others, in turn
+  uint64_t* part;            // [kWarps + 2]
+  uint64_t* hist;            // [kBins], this CTA's
+  uint64_t* all;             // [kBins], the team's
+  int turn;
+
+  __device__ __forceinline__ void sync() const {
+    if (ctas > 1) cluster_sync();
+    else __syncthreads();
   }
-  float M = -INFINITY;
-  M = __uint_as_float(top & 0x80000000u ? top ^ 0x80000000u : ~top);
-  const float T0 = a.temperature ? a.temperature[n] : 1.f;
-  const bool greedy = !(T0 > 0.f);
+
+  // The value over the team (and over the CTAs before this one, for sums), from each thread's.
+  template <typename Op>
+  __device__ __forceinline__ uint64_t reduce(uint64_t v, Op op, uint64_t zero, uint64_t* before = nullptr) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+    __syncthreads();
+    if (lane == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      v = lane < kWarps ? part[lane] : zero;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+    }
+    if (ctas > 1) {
+      if (threadIdx.x == 0) slots[turn] = v;
+      cluster_sync();
+      if (threadIdx.x < 32) {
+        v = lane < ctas ? load_cluster(mapa_shared(slots + turn, lane)) : zero;
+        uint64_t b = lane < rank ? v : zero;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+          b = op(b, __shfl_xor_sync(0xffffffffu, b, o));
+        }
+        if (lane == 0) part[kWarps + 1] = b;
+      }
+      turn ^= 1;
+    } else if (threadIdx.x == 0) {
+      part[kWarps + 1] = zero;
+    }
+    if (threadIdx.x == 0) part[kWarps] = v;
+    __syncthreads();
+    if (before) *before = part[kWarps + 1];
+    return part[kWarps];
+  }
+  __device__ __forceinline__ uint64_t sum(uint64_t v, uint64_t* before = nullptr) {
+    return reduce(v, [](uint64_t a, uint64_t b) { return a + b; }, 0, before);
+  }
+  __device__ __forceinline__ uint64_t most(uint64_t v) {
+    return reduce(v, [](uint64_t a, uint64_t b) { return max(a, b); }, 0);
+  }
+
+  __device__ __forceinline__ void clear() const {
+    for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0;
+    __syncthreads();
+  }
+  // The team's histogram: each CTA adds up its share of the bins over all, and hands it to all.
+  template <typename Add>
+  __device__ __forceinline__ const uint64_t* gather(Add add) const {
+    sync();
+    if (ctas == 1) return hist;
+    const int share = kBins / ctas;
+    for (int i = threadIdx.x; i < share; i += kThreads) {
+      const int b = rank * share + i;
+      uint64_t v = 0;
+      for (int c = 0; c < ctas; ++c) v = add(v, load_cluster(mapa_shared(hist + b, c)));
+      for (int c = 0; c < ctas; ++c) store_cluster(mapa_shared(all + b, c), v);
+    }
+    cluster_sync();
+    return all;
+  }
+};
+
+// The sum of v over the threads before this one.
+template <typename V>
+__device__ __forceinline__ V sum_before(V v, V* part) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  V x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const V y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) part[warp] = x;
+  __syncthreads();
+  V s = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) s += w < warp ? part[w] : 0;
+  return s + x - v;
+}
+
+struct Row {
+  int k;                     // 0: no limit
+  float p;                   // 1: none
+  double least;              // weights below are not kept
+  float u;
   Weigh w;
-  w.set(M, greedy ? 1.0 : static_cast<double>(T0), table);
-  // Kept: keys above `key`, and the first `extra` tokens, by index, of those with that key.
-  uint32_t key = kNone + 1, extra = 0xffffffffu;
-  if (greedy) {
-    key = top;
-    extra = 1;
-  } else {
-    const int k = a.top_k ? a.top_k[n] : 0;
-    if (k > 0 && k < V) {
-      uint32_t lo = kNone + 1, hi = top;      // the largest key that k tokens reach
-      while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo + 1) / 2;
-        if (sum([&](float l) { return static_cast<uint64_t>(key_of(l) >= mid); }) >= static_cast<uint64_t>(k)) lo = mid;
-        else hi = mid - 1;
+};
+
+// A limit: keys above `key` are within it, and the first `extra`, by index, of the tokens with that key.
+struct Limit {
+  uint32_t key, extra;
+};
+
+// each(f): f(logit, place) for every token of the team, each CTA's by all of its threads.
+//
+// The largest key in [lo, hi] at which a sum over the keys from hi down, by histograms of runs of keys, passes a
+// goal: reached(s) says whether a sum s is enough; above is the sum of keys beyond hi, and of those beyond the key after.
+template <typename Each, typename Weight, typename Reached>
+__device__ __forceinline__ uint32_t search(Team& team, uint32_t lo, uint32_t hi, uint64_t& above, Each each, Weight weight,
+                                           Reached reached) {
+  __shared__ int found;
+  __shared__ uint64_t found_above;
+  for (;;) {
+    const uint32_t span = hi - lo;
+    const int s = span < kBins ? 0 : 21 - __clz(span);
+    team.clear();
+    each([&](float l, int) {
+      const uint32_t k = key_of(l);
+      if (k >= lo && k <= hi) {
+        const uint64_t v = weight(l);
+        if (v) atomicAdd(reinterpret_cast<unsigned long long*>(team.hist + ((hi - k) >> s)), static_cast<unsigned long long>(v));
       }
-      const uint64_t above = sum([&](float l) { return static_cast<uint64_t>(key_of(l) > lo); });
-      key = lo;
-      extra = static_cast<uint32_t>(k - above);
+    });
+    if (threadIdx.x == 0) found = -1;
+    const uint64_t* h = team.gather([](uint64_t a, uint64_t b) { return a + b; });
+    uint64_t bin[kPerThread], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) mine += bin[i] = h[kPerThread * threadIdx.x + i];
+    uint64_t c = above + sum_before<uint64_t>(mine, team.part);
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      if (!reached(c) && reached(c + bin[i])) {
+        found = kPerThread * threadIdx.x + i;
+        found_above = c;
+      }
+      c += bin[i];
     }
-    const float p = a.top_p ? a.top_p[n] : 1.f;
-    if (p < 1.f) {
-      const uint64_t wk = w(__uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key));
-      const uint64_t same = sum([&](float l) { return static_cast<uint64_t>(key_of(l) == key); });
-      const uint64_t some = min(same, static_cast<uint64_t>(extra));
-      const uint64_t all = sum([&](float l) { return key_of(l) > key ? w(l) : 0; }) + some * wk;
-      const double goal = static_cast<double>(p) * static_cast<double>(all);
-      uint32_t lo = key, hi = top;            // the largest key whose prefix has that weight
-      while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo + 1) / 2;
-        const uint64_t s = sum([&](float l) { return key_of(l) >= mid ? w(l) : 0; });
-        if (static_cast<double>(s) >= goal) lo = mid;
-        else hi = mid - 1;
-      }
-      const uint64_t above = sum([&](float l) { return key_of(l) > lo ? w(l) : 0; });
-      const uint64_t one = w(__uint_as_float(lo & 0x80000000u ? lo ^ 0x80000000u : ~lo));
-      // Of the tokens with that key: the fewest that bring the sum to the goal, one at least.
-      uint64_t c = 1;
-      if (one > 0) {
-        const double need = (goal - static_cast<double>(above)) / static_cast<double>(one);
-        c = need > 1.0 ? static_cast<uint64_t>(ceil(need)) : 1;
-      }
-      extra = static_cast<uint32_t>(min(c, static_cast<uint64_t>(lo == key ? extra : 0xffffffffu)));
-      key = lo;
-    }
+    __syncthreads();
+    // Never reached (a goal that rounding has put above the whole sum): the lowest key.
+    if (found < 0) return lo;
+    above = found_above;
+    hi -= static_cast<uint32_t>(found) << s;
+    if (s == 0) return hi;
+    lo = max(lo, hi - ((1u << s) - 1));
+    __syncthreads();
   }
-  const float mp = a.min_p && !greedy ? a.min_p[n] : 0.f;
-  const double least = mp > 0.f ? fmin(static_cast<double>(mp), 1.0) * static_cast<double>(kOne) : 0.0;
-  // The kept weights by index: a run of tokens for each thread.
-  const int run = (V + kThreads - 1) / kThreads, i0 = min(V, static_cast<int>(threadIdx.x) * run), i1 = min(V, i0 + run);
+}
+
+// The choice from the tokens within a limit, `count` in this CTA in the order of their indexes, the ranks' one after the
+// other: at(i) is a token's logit, index(i) its index.
+template <typename At, typename Index>
+__device__ __forceinline__ void choose(Team& team, const SampleArgs& a, const Row& row, int64_t n, int count, Limit limit, At at,
+                                       Index index) {
+  // Runs of tokens by thread: the ties with the limit's key before each, then the kept weights
+  // (an odd number of them, for the banks).
+  const int run = ((count + kThreads - 1) / kThreads) | 1, i0 = min(count, static_cast<int>(threadIdx.x) * run), i1 = min(count, i0 + run);
   uint32_t same = 0;
-  for (int i = i0; i < i1; ++i) same += key_of(at(i)) == key;
-  ties[threadIdx.x + 1] = same;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    ties[0] = 0;
-    for (int i = 0; i < kThreads; ++i) ties[i + 1] += ties[i];
+  uint64_t ties = 0;
+  if (limit.extra != 0xffffffffu) {
+    for (int i = i0; i < i1; ++i) same += key_of(at(i)) == limit.key;
+    const uint64_t mine = sum_before<uint64_t>(same, team.part);
+    uint64_t before;
+    team.sum(same, &before);
+    ties = before + mine;
   }
-  __syncthreads();
-  auto kept = [&](float l, uint32_t& seen) -> uint64_t {
+  auto kept = [&](float l, uint64_t& seen) -> uint64_t {
     const uint32_t k = key_of(l);
-    if (k < key || (k == key && seen++ >= extra)) return 0;
-    const uint64_t v = greedy ? kOne : w(l);
-    return static_cast<double>(v) >= least ? v : 0;
+    if (k < limit.key || (k == limit.key && seen++ >= limit.extra)) return 0;
+    const uint64_t v = row.w(l);
+    return static_cast<double>(v) >= row.least ? v : 0;
   };
-  uint64_t mine = 0;
-  uint32_t seen = ties[threadIdx.x];
+  uint64_t mine = 0, seen = ties;
   for (int i = i0; i < i1; ++i) mine += kept(at(i), seen);
-  sums[threadIdx.x + 1] = mine;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    sums[0] = 0;
-    for (int i = 0; i < kThreads; ++i) sums[i + 1] += sums[i];
-  }
-  __syncthreads();
-  const uint64_t total = sums[kThreads];
-  const float u = a.u[n];
+  uint64_t c = sum_before<uint64_t>(mine, team.part), before;
+  const uint64_t total = team.sum(mine, &before);
+  c += before;
   // The first sum above u * total: at least floor(u * total) + 1, and at most all of it.
-  uint64_t goal = u > 0.f ? static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total)) : 0;
+  uint64_t goal = row.u > 0.f ? static_cast<uint64_t>(static_cast<double>(row.u) * static_cast<double>(total)) : 0;
   goal = min(goal, total - 1);
-  if (sums[threadIdx.x] <= goal && goal < sums[threadIdx.x + 1]) {
-    uint64_t c = sums[threadIdx.x];
-    seen = ties[threadIdx.x];
+  if (c <= goal && goal < c + mine) {
+    seen = ties;
     for (int i = i0; i < i1; ++i) {
       const uint64_t v = kept(at(i), seen);
       c += v;
       if (c > goal) {
-        a.ids[n] = i;
+        a.ids[n] = index(i);
         if (a.probs) a.probs[n] = static_cast<float>(static_cast<double>(v) / static_cast<double>(total));
         break;
       }
@@ -222,13 +302,331 @@ __global__ void __launch_bounds__(kThreads) sample_rows_kernel(const SampleArgs 
   }
 }
 
+// The limits of top_k (the k-th largest key is in [k_lo, k_hi], with k_above tokens beyond it) and of top_p. whole: the
+// weight of all tokens, where top_k does not limit them. window(goal, lo, hi, above): the keys between which the prefix
+// with that weight ends.
+template <typename Each, typename Window>
+__device__ __forceinline__ Limit limits(Team& team, const Row& row, uint32_t k_lo, uint32_t k_hi, uint64_t k_above, uint64_t whole,
+                                        Each each, Window window) {
+  Limit limit = {kNone + 1, 0xffffffffu};
+  if (row.k > 0) {
+    const uint64_t k = row.k;
+    limit.key = search(team, k_lo, k_hi, k_above, each, [](float) -> uint64_t { return 1; }, [&](uint64_t s) { return s >= k; });
+    limit.extra = static_cast<uint32_t>(k - k_above);
+  }
+  if (row.p < 1.f) {
+    if (row.k > 0) {
+      uint64_t mine = 0;
+      each([&](float l, int) { mine += key_of(l) > limit.key ? row.w(l) : 0; });
+      whole = team.sum(mine) + limit.extra * row.w(value_of(limit.key));
+    }
+    const double goal = static_cast<double>(row.p) * static_cast<double>(whole);
+    uint32_t lo = limit.key, hi = 0;
+    uint64_t above = 0;
+    window(goal, lo, hi, above);
+    const uint32_t key = search(team, lo, hi, above, each, [&](float l) { return row.w(l); },
+                                [&](uint64_t s) { return static_cast<double>(s) >= goal; });
+    // Of the tokens with that key: the fewest that bring the sum to the goal, one at least.
+    const uint64_t one = row.w(value_of(key));
+    uint64_t c = 1;
+    if (one > 0) {
+      const double need = (goal - static_cast<double>(above)) / static_cast<double>(one);
+      c = need > 1.0 ? static_cast<uint64_t>(ceil(need)) : 1;
+    }
+    limit.extra = static_cast<uint32_t>(min(c, static_cast<uint64_t>(key == limit.key ? limit.extra : 0xfffffffeu)));
+    limit.key = key;
+  }
+  return limit;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a, int ctas, int per, bool vec) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint32_t table[64];
+  __shared__ uint64_t slots[2], part[kWarps + 2];
+  __shared__ float partf[kWarps];
+  __shared__ int bin_of[3];
+  T* slice = reinterpret_cast<T*>(smem);
+  uint64_t* hist = reinterpret_cast<uint64_t*>(smem + (static_cast<size_t>(per) * sizeof(T) + 15) / 16 * 16);
+  float* list = reinterpret_cast<float*>(hist + 2 * kBins);
+  int* list_at = reinterpret_cast<int*>(list + kList);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_enter();
+  if (threadIdx.x < 64) table[threadIdx.x] = kPow2[threadIdx.x];
+  const int64_t n = blockIdx.x / ctas;
+  Team team = {ctas, static_cast<int>(cluster_ctarank()), slots, part, hist, hist + kBins, 0};
+  const int first = team.rank * per, count = max(0, min(per, static_cast<int>(a.V) - first));
+  const T* x = static_cast<const T*>(a.logits) + n * a.ld + first;
+
+  // The slice, and the row's largest logit.
+  float top = -INFINITY;
+  {
+    constexpr int E = 16 / sizeof(T);
+    const int whole = vec ? count / E : 0;
+    for (int i = threadIdx.x; i < whole; i += kThreads) {
+      const uint4 v = reinterpret_cast<const uint4*>(x)[i];
+      reinterpret_cast<uint4*>(slice)[i] = v;
+      const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+      for (int j = 0; j < E; ++j) top = fmaxf(top, usable(to_f32(e[j])));
+    }
+    for (int i = whole * E + threadIdx.x; i < count; i += kThreads) {
+      const T v = x[i];
+      slice[i] = v;
+      top = fmaxf(top, usable(to_f32(v)));
+    }
+  }
+  Row row;
+  row.k = a.top_k ? a.top_k[n] : 0;
+  row.p = a.top_p ? a.top_p[n] : 1.f;
+  const float T0 = a.temperature ? a.temperature[n] : 1.f, min_p = a.min_p ? a.min_p[n] : 0.f;
+  row.u = a.u[n];
+  if (row.k < 0 || row.k >= a.V) row.k = 0;
+  if (!(row.p < 1.f)) row.p = 1.f;
+  row.least = min_p > 0.f ? fmin(static_cast<double>(min_p), 1.0) * static_cast<double>(kOne) : 0.0;
+  const uint32_t top_key = static_cast<uint32_t>(team.most(key_of(top)));
+  if (top_key == kNone) {    // no token is available
+    if (threadIdx.x == 0 && team.rank == 0) {
+      a.ids[n] = 0;
+      if (a.probs) a.probs[n] = 0.f;
+    }
+    team.sync();             // nobody leaves while its memory is read
+    return;
+  }
+  auto at = [&](int i) { return usable(to_f32(slice[i])); };
+  auto each = [&](auto f) {
+    for (int i = threadIdx.x; i < count; i += kThreads) f(at(i), i);
+  };
+  if (!(T0 > 0.f)) {         // the first token with the largest logit
+    int at_least = 0x7fffffff;
+    each([&](float l, int i) { at_least = min(at_least, key_of(l) == top_key ? first + i : 0x7fffffff); });
+    const int id = 0x7fffffff - static_cast<int>(team.most(static_cast<uint64_t>(0x7fffffff - at_least)));
+    if (threadIdx.x == 0 && team.rank == 0) {
+      a.ids[n] = id;
+      if (a.probs) a.probs[n] = 1.f;
+    }
+    team.sync();
+    return;
+  }
+  row.w.set(value_of(top_key), static_cast<double>(T0), table);
+  auto index = [&](int i) { return first + i; };
+  if (row.k == 0 && row.p == 1.f) {
+    choose(team, a, row, n, count, Limit{kNone + 1, 0xffffffffu}, at, index);
+    team.sync();
+    return;
+  }
+
+  // Histogram by bins of (M - l) log2(e) / T of 1/32: tokens (low words) and, with top_p, weights relative to the bin's largest
+  // possible, in 2^-15 (high words; those of the last bin are below 2^-63). Without top_k the exact weight of all.
+  const float M = value_of(top_key), scale = 32.f * 1.44269504f / T0;
+  auto bin_at = [&](float l, float& frac) {
+    const float d = fminf(__fsub_rn(M, l) * scale, static_cast<float>(kBins - 1));       // a NaN (0 times infinity): 0
+    const float b = floorf(d);
+    frac = d - b;
+    return static_cast<int>(b);
+  };
+  team.clear();
+  uint64_t whole = 0;
+  each([&](float l, int) {
+    if (l == -INFINITY) return;
+    float frac;
+    const int b = l == M ? (frac = 0.f, 0) : bin_at(l, frac);
+    uint32_t* h = reinterpret_cast<uint32_t*>(hist + b);
+    atomicAdd(h, 1u);
+    if (row.p < 1.f) {
+      if (b < kBins - 1) atomicAdd(h + 1, static_cast<uint32_t>(32768.f * exp2f(frac * -0.03125f)));
+      if (row.k == 0) whole += row.w(l);
+    }
+  });
+  if (row.p < 1.f && row.k == 0) whole = team.sum(whole);
+  // Over the cluster: tokens (low words) and weights as fp32 (high words), the latter times 2^(-b / 32) below.
+  const uint64_t* all;
+  if (team.ctas == 1) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBins; i += kThreads)
+      hist[i] = (hist[i] & 0xffffffffu) | static_cast<uint64_t>(__float_as_uint(static_cast<float>(hist[i] >> 32))) << 32;
+    __syncthreads();
+    all = hist;
+  } else {
+    all = team.gather([](uint64_t v, uint64_t h) {
+      const float w = __uint_as_float(static_cast<uint32_t>(v >> 32)) + static_cast<float>(h >> 32);
+      return ((v & 0xffffffffu) + (h & 0xffffffffu)) | static_cast<uint64_t>(__float_as_uint(w)) << 32;
+    });
+  }
+  // Tokens and weights up to each bin.
+  uint32_t tokens[kPerThread], tokens_sum = 0;
+  float weight[kPerThread], weight_sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    const int b = kPerThread * threadIdx.x + i;
+    tokens[i] = tokens_sum += static_cast<uint32_t>(all[b]);
+    weight[i] = weight_sum += __uint_as_float(static_cast<uint32_t>(all[b] >> 32)) * exp2f(b * -0.03125f) * 0x1p-15f;
+  }
+  const uint32_t tokens_before = static_cast<uint32_t>(sum_before<uint64_t>(tokens_sum, part));
+  const float weight_before = sum_before<float>(weight_sum, partf);
+  __shared__ uint32_t tokens_at, tokens_to, available;
+  // The first bin up to which there are `enough` (of tokens or of weight), in bin_of[to]; the last bin if there are never. Tokens
+  // before it and up to it in tokens_at and tokens_to.
+  auto find = [&](int to, auto enough) {
+    __syncthreads();
+    if (threadIdx.x == 0) bin_of[to] = kBins - 1;
+    __syncthreads();
+#pragma unroll
+    for (int i = kPerThread - 1; i >= 0; --i)
+      if (enough(tokens_before + tokens[i], weight_before + weight[i])) atomicMin(&bin_of[to], static_cast<int>(kPerThread * threadIdx.x + i));
+    __syncthreads();
+    const int b = bin_of[to] - kPerThread * static_cast<int>(threadIdx.x);
+    if (b >= 0 && b < kPerThread) {
+      uint32_t t = 0;
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i) {
+        if (i == b) tokens_at = tokens_before + t, tokens_to = tokens_before + tokens[i];
+        t = tokens[i];
+      }
+    }
+    if (threadIdx.x == kThreads - 1) available = tokens_before + tokens_sum;
+    __syncthreads();
+    return bin_of[to];
+  };
+  // The bins' weights are within 2^-14 of the exact ones, and fp32's sums of them: 2^-11 is beyond that on both sides.
+  const float around = 0x1p-11f;
+  const float in_units = 1.f / static_cast<float>(kOne);
+  int last;                  // no token of a later bin is kept
+  if (row.k > 0) last = find(0, [&](uint32_t t, float) { return t >= static_cast<uint32_t>(row.k); });
+  if (row.k > 0 && available <= static_cast<uint32_t>(row.k)) {        // top_k leaves all of them
+    row.k = 0;
+    if (row.p < 1.f) {
+      whole = 0;
+      each([&](float l, int) { whole += row.w(l); });
+      whole = team.sum(whole);
+    }
+  }
+  if (row.k == 0 && row.p == 1.f) {
+    choose(team, a, row, n, count, Limit{kNone + 1, 0xffffffffu}, at, index);
+    team.sync();
+    return;
+  }
+  if (row.k == 0) last = find(0, [&, g = row.p * (static_cast<float>(whole) * in_units) * (1.f + around)](uint32_t, float w) { return w >= g; });
+  const uint32_t some = tokens_to, k_before = tokens_at;
+
+  if (some <= kList) {
+    // Few: to the first CTA, in the order of their indexes. A warp takes a run of tokens.
+    const int run = ((count + kWarps - 1) / kWarps + 31) / 32 * 32, i0 = min(count, warp * run), i1 = min(count, i0 + run);
+    auto may = [&](int i) {
+      if (i >= i1) return false;
+      const float l = at(i);
+      float frac;
+      return l != -INFINITY && (l == M || bin_at(l, frac) <= last);
+    };
+    uint32_t mine = 0;
+    for (int i = i0; i < i1; i += 32) mine += __popc(__ballot_sync(0xffffffffu, may(i + lane)));
+    uint64_t to;
+    const uint64_t there = team.sum(lane == 0 ? mine : 0, &to);
+    to += sum_before<uint64_t>(lane == 0 ? mine : 0, part);
+    to = __shfl_sync(0xffffffffu, to, 0);
+    const uint32_t list0 = mapa_shared(list, 0), at0 = mapa_shared(list_at, 0);
+    for (int i = i0; i < i1; i += 32) {
+      const bool m = may(i + lane);
+      const uint32_t b = __ballot_sync(0xffffffffu, m);
+      if (m) {
+        const uint32_t k = static_cast<uint32_t>(to) + __popc(b & ((1u << lane) - 1));
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(list0 + 4 * k), "f"(at(i + lane)) : "memory");
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at0 + 4 * k), "r"(first + i + lane) : "memory");
+      }
+      to += __popc(b);
+    }
+    team.sync();
+    if (team.rank > 0) return;
+    Team alone = {1, 0, slots, part, hist, hist, 0};
+    const int m = static_cast<int>(there);
+    auto l_at = [&](int i) { return list[i]; };
+    auto l_each = [&](auto f) {
+      for (int i = threadIdx.x; i < m; i += kThreads) f(list[i], i);
+    };
+    uint64_t low = 0;
+    l_each([&](float l, int) { low = max(low, static_cast<uint64_t>(~key_of(l))); });
+    const uint32_t lo = ~static_cast<uint32_t>(alone.most(low));
+    const Limit limit = limits(alone, row, lo, top_key, 0, whole, l_each,
+                               [&](double, uint32_t& k, uint32_t& hi, uint64_t&) { k = max(k, lo), hi = top_key; });
+    choose(alone, a, row, n, m, limit, l_at, [&](int i) { return list_at[i]; });
+    return;
+  }
+
+  // Many: the cluster goes on. The keys of bins b0 to b1 are between lo and hi.
+  auto keys_of_bins = [&](int b0, int b1, uint32_t& lo, uint32_t& hi) {
+    uint64_t low = 0, high = 0;
+    each([&](float l, int) {
+      if (l == -INFINITY) return;
+      float frac;
+      const int b = l == M ? 0 : bin_at(l, frac);
+      if (b >= b0 && b <= b1) low = max(low, static_cast<uint64_t>(~key_of(l))), high = max(high, static_cast<uint64_t>(key_of(l)));
+    });
+    lo = ~static_cast<uint32_t>(team.most(low));
+    hi = static_cast<uint32_t>(team.most(high));
+  };
+  uint32_t k_lo = 0, k_hi = 0;
+  if (row.k > 0) keys_of_bins(last, last, k_lo, k_hi);
+  const Limit limit = limits(team, row, k_lo, k_hi, k_before, whole, each, [&](double goal, uint32_t& lo, uint32_t& hi, uint64_t& above) {
+    const float g = static_cast<float>(goal) * in_units;
+    const int b0 = find(1, [&](uint32_t, float w) { return w >= g * (1.f - around); });
+    const int b1 = max(b0, find(2, [&](uint32_t, float w) { return w >= g * (1.f + around); }));
+    uint32_t w_lo, w_hi;
+    keys_of_bins(b0, b1, w_lo, w_hi);
+    // Tokens beyond the window, and (with top_k) those that are out of reach.
+    lo = max(lo, w_lo);
+    hi = max(lo, w_hi);
+    uint64_t mine = 0;
+    each([&](float l, int) { mine += key_of(l) > hi ? row.w(l) : 0; });
+    above = team.sum(mine);
+  });
+  choose(team, a, row, n, count, limit, at, index);
+  team.sync();
+}
+
+template <typename T>
+cudaError_t sample(const SampleArgs& a, int num_sms, cudaStream_t s) {
+  // CTAs of a row: enough to hold it, and as many as leave 2048 tokens each, while all rows' run at once.
+  constexpr int kMost = kSliceBytes / sizeof(T);
+  int ctas = 1;
+  while (ctas < kMostCtas && (a.V > static_cast<int64_t>(ctas) * kMost ||
+                              (a.V >= 4096 * static_cast<int64_t>(ctas) && a.N * 2 * ctas <= num_sms)))
+    ctas *= 2;
+  const int per = static_cast<int>(((a.V + ctas - 1) / ctas + 7) / 8 * 8);
+  const size_t smem = (static_cast<size_t>(per) * sizeof(T) + 15) / 16 * 16 + 2 * kBins * sizeof(uint64_t) + kList * 8;
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(allowed.load(std::memory_order_acquire) >> dev & 1)) {
+    e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSliceBytes + 2 * kBins * sizeof(uint64_t) + kList * 8 + 64);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) allowed.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.N * ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const bool vec = a.ld * static_cast<int64_t>(sizeof(T)) % 16 == 0;
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a, ctas, per, vec);
+}
+
 }  // namespace
 
-cudaError_t launch_sample(int dtype, const SampleArgs& a, int, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(a.N)), block(kThreads);
-  if (dtype == KQ_F16) return launch_pdl(sample_rows_kernel<__half>, grid, block, 0, s, a);
-  if (dtype == KQ_BF16) return launch_pdl(sample_rows_kernel<__nv_bfloat16>, grid, block, 0, s, a);
-  return launch_pdl(sample_rows_kernel<float>, grid, block, 0, s, a);
+cudaError_t launch_sample(int dtype, const SampleArgs& a, int num_sms, cudaStream_t s) {
+  if (dtype == KQ_F16) return sample<__half>(a, num_sms, s);
+  if (dtype == KQ_BF16) return sample<__nv_bfloat16>(a, num_sms, s);
+  return sample<float>(a, num_sms, s);
 }
 
 }  // namespace kq
