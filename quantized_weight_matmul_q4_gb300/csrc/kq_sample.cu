@@ -33,19 +33,46 @@ constexpr int kMostCtas = 16;
 constexpr int kSliceBytes = 128 * 1024;
 constexpr uint64_t kOne = uint64_t(1) << 43;     // the weight of the largest logit
 
-// 2^(31 - j / 64), rounded.
-__constant__ uint32_t kPow2[64] = {
-    0x80000000u, 0x7e9f0606u, 0x7d41d96eu, 0x7be86fbau, 0x7a92be8bu, 0x7940bb9eu, 0x77f25cceu, 0x76a7980fu,
-    0x75606374u, 0x741cb528u, 0x72dc8374u, 0x719fc4b9u, 0x70666f76u, 0x6f307a41u, 0x6dfddbccu, 0x6cce8ae1u,
-    0x6ba27e65u, 0x6a79ad56u, 0x69540ec9u, 0x683199edu, 0x6712460bu, 0x65f60a7fu, 0x64dcdec3u, 0x63c6ba64u,
-    0x62b39509u, 0x61a3666du, 0x60962665u, 0x5f8bccdbu, 0x5e8451d0u, 0x5d7fad59u, 0x5c7dd7a4u, 0x5b7ec8f2u,
-    0x5a82799au, 0x5988e209u, 0x5891fac1u, 0x579dbc57u, 0x56ac1f75u, 0x55bd1cdbu, 0x54d0ad5au, 0x53e6c9dau,
-    0x52ff6b55u, 0x521a8ad7u, 0x51382182u, 0x50582888u, 0x4f7a9930u, 0x4e9f6cd4u, 0x4dc69cddu, 0x4cf022cau,
-    0x4c1bf829u, 0x4b4a169cu, 0x4a7a77d4u, 0x49ad1598u, 0x48e1e9bau, 0x4818ee22u, 0x47521cc6u, 0x468d6faeu,
-    0x45cae0f2u, 0x450a6abbu, 0x444c0740u, 0x438fb0cbu, 0x42d561b4u, 0x421d1462u, 0x4166c34cu, 0x40b268fau};
+// 2^(31 - j / 256), rounded.
+__constant__ uint32_t kPow2[256] = {
+    0x80000000u, 0x7fa765adu, 0x7f4f08aeu, 0x7ef6e8dau, 0x7e9f0606u, 0x7e476009u, 0x7deff6b6u, 0x7d98c9e6u, 0x7d41d96eu, 0x7ceb2523u,
+    0x7c94acdeu, 0x7c3e7073u, 0x7be86fbau, 0x7b92aa88u, 0x7b3d20b6u, 0x7ae7d21au, 0x7a92be8bu, 0x7a3de5dfu, 0x79e947efu, 0x7994e492u,
+    0x7940bb9eu, 0x78ecccecu, 0x78991854u, 0x78459dacu, 0x77f25cceu, 0x779f5590u, 0x774c87ccu, 0x76f9f359u, 0x76a7980fu, 0x765575c8u,
+    0x76038c5bu, 0x75b1dba2u, 0x75606374u, 0x750f23abu, 0x74be1c20u, 0x746d4cacu, 0x741cb528u, 0x73cc556du, 0x737c2d55u, 0x732c3cbau,
+    0x72dc8374u, 0x728d015du, 0x723db650u, 0x71eea226u, 0x719fc4b9u, 0x71511de4u, 0x7102ad80u, 0x70b47368u, 0x70666f76u, 0x7018a185u,
+    0x6fcb096fu, 0x6f7da710u, 0x6f307a41u, 0x6ee382deu, 0x6e96c0c3u, 0x6e4a33c9u, 0x6dfddbccu, 0x6db1b8a8u, 0x6d65ca38u, 0x6d1a1057u,
+    0x6cce8ae1u, 0x6c8339b2u, 0x6c381ca6u, 0x6bed3399u, 0x6ba27e65u, 0x6b57fce9u, 0x6b0daeffu, 0x6ac39485u, 0x6a79ad56u, 0x6a2ff94fu,
+    0x69e6784du, 0x699d2a2cu, 0x69540ec9u, 0x690b2601u, 0x68c26fb1u, 0x6879ebb6u, 0x683199edu, 0x67e97a34u, 0x67a18c68u, 0x6759d065u,
+    0x6712460bu, 0x66caed35u, 0x6683c5c3u, 0x663ccf92u, 0x65f60a7fu, 0x65af766au, 0x6569132fu, 0x6522e0adu, 0x64dcdec3u, 0x64970d4fu,
+    0x64516c2eu, 0x640bfb41u, 0x63c6ba64u, 0x6381a978u, 0x633cc85bu, 0x62f816ebu, 0x62b39509u, 0x626f4292u, 0x622b1f66u, 0x61e72b65u,
+    0x61a3666du, 0x615fd05eu, 0x611c6919u, 0x60d9307bu, 0x60962665u, 0x60534ab7u, 0x60109d51u, 0x5fce1e12u, 0x5f8bccdbu, 0x5f49a98cu,
+    0x5f07b405u, 0x5ec5ec26u, 0x5e8451d0u, 0x5e42e4e3u, 0x5e01a53fu, 0x5dc092c7u, 0x5d7fad59u, 0x5d3ef4d7u, 0x5cfe6923u, 0x5cbe0a1cu,
+    0x5c7dd7a4u, 0x5c3dd19cu, 0x5bfdf7e5u, 0x5bbe4a61u, 0x5b7ec8f2u, 0x5b3f7377u, 0x5b0049d4u, 0x5ac14beau, 0x5a82799au, 0x5a43d2c6u,
+    0x5a055751u, 0x59c7071cu, 0x5988e209u, 0x594ae7fbu, 0x590d18d3u, 0x58cf7474u, 0x5891fac1u, 0x5854ab9bu, 0x581786e6u, 0x57da8c83u,
+    0x579dbc57u, 0x57611642u, 0x57249a29u, 0x56e847efu, 0x56ac1f75u, 0x567020a0u, 0x56344b52u, 0x55f89f70u, 0x55bd1cdbu, 0x5581c378u,
+    0x55469329u, 0x550b8bd4u, 0x54d0ad5au, 0x5495f7a1u, 0x545b6a8bu, 0x542105fdu, 0x53e6c9dau, 0x53acb607u, 0x5372ca68u, 0x533906e0u,
+    0x52ff6b55u, 0x52c5f7aau, 0x528cabc3u, 0x52538786u, 0x521a8ad7u, 0x51e1b59au, 0x51a907b4u, 0x5170810bu, 0x51382182u, 0x50ffe8feu,
+    0x50c7d765u, 0x508fec9cu, 0x50582888u, 0x50208b0eu, 0x4fe91413u, 0x4fb1c37cu, 0x4f7a9930u, 0x4f439514u, 0x4f0cb70cu, 0x4ed5ff00u,
+    0x4e9f6cd4u, 0x4e69006eu, 0x4e32b9b4u, 0x4dfc988cu, 0x4dc69cddu, 0x4d90c68bu, 0x4d5b157eu, 0x4d25899cu, 0x4cf022cau, 0x4cbae0efu,
+    0x4c85c3f1u, 0x4c50cbb8u, 0x4c1bf829u, 0x4be7492bu, 0x4bb2bea5u, 0x4b7e587eu, 0x4b4a169cu, 0x4b15f8e6u, 0x4ae1ff43u, 0x4aae299bu,
+    0x4a7a77d4u, 0x4a46e9d6u, 0x4a137f88u, 0x49e038d0u, 0x49ad1598u, 0x497a15c4u, 0x4947393fu, 0x49147feeu, 0x48e1e9bau, 0x48af768au,
+    0x487d2646u, 0x484af8d6u, 0x4818ee22u, 0x47e70611u, 0x47b5408cu, 0x47839d7bu, 0x47521cc6u, 0x4720be55u, 0x46ef8210u, 0x46be67e0u,
+    0x468d6faeu, 0x465c9961u, 0x462be4e2u, 0x45fb521au, 0x45cae0f2u, 0x459a9152u, 0x456a6323u, 0x453a564du, 0x450a6abbu, 0x44daa054u,
+    0x44aaf702u, 0x447b6eadu, 0x444c0740u, 0x441cc0a3u, 0x43ed9ac0u, 0x43be957fu, 0x438fb0cbu, 0x4360ec8du, 0x433248aeu, 0x4303c518u,
+    0x42d561b4u, 0x42a71e6cu, 0x4278fb2bu, 0x424af7dau, 0x421d1462u, 0x41ef50aeu, 0x41c1aca7u, 0x41942839u, 0x4166c34cu, 0x41397dccu,
+    0x410c57a2u, 0x40df50b8u, 0x40b268fau, 0x4085a051u, 0x4058f6a8u, 0x402c6be9u};
 
-// The logit as it is used: no NaN (such a token is not available) and no +inf (the largest finite).
-__device__ __forceinline__ float usable(float l) { return l != l ? -INFINITY : fminf(l, 3.402823466e38f); }
+// The logit as it is used: no NaN (such a token is not available: -inf in its place) and no +inf (the largest finite).
+__device__ __forceinline__ float usable(float l) { return fminf(l, 3.402823466e38f); }
+template <typename T>
+__device__ __forceinline__ float take(T& v) {
+  const float l = to_f32(v);
+  if (l != l) {
+    v = from_f32<T>(-INFINITY);
+    return -INFINITY;
+  }
+  return usable(l);
+}
 
 // Whole numbers in the order of the logits; 0 is below all of them.
 __device__ __forceinline__ uint32_t key_of(float l) {
@@ -54,40 +81,44 @@ __device__ __forceinline__ uint32_t key_of(float l) {
 }
 constexpr uint32_t kNone = 0x007fffffu;                        // the key of -inf
 
-// exp((l - M) / T) * 2^43: with x = (M - l) log2(e) / T as e + r, r in [-1/2, 1/2], and r = j / 64 + f,
-// it is 2^(43 - e) 2^(-j / 64) (1 + q), q = 2^-f - 1 by its series (|f| <= 1/128: |q| < 0.0055, so that the
-// rounding of q to fp32 and to 2^-31 leaves an error below 2^-30 with that of the table).
+// Adding it to an fp32 below 2^22 in magnitude rounds that to a whole number, which the sum has in its low bits.
+constexpr float kWhole = 12582912.f;
+constexpr int kWholeBits = 0x4b400000;
+
+// exp((l - M) / T) * 2^43: with x = (M - l) log2(e) / T as e + r, r in [-1/2, 1/2], and r = j / 256 + f,
+// it is 2^(43 - e) 2^(-j / 256) (1 + q), q = 2^-f - 1 by its series (|f| <= 1/512: |q| < 0.00136, so that the
+// rounding of q to 2^-31 and that of the table leave an error below 2^-30).
 struct Weigh {
   float M, ch, cl;                 // log2(e) / T as a sum of two
   const uint32_t* table;           // kPow2 in shared memory
 
-  __device__ __forceinline__ void set(float max, double T, const uint32_t* t) {
-    M = max;
-    const double c = 1.4426950408889634 / T;
-    ch = static_cast<float>(c);
-    cl = ch < INFINITY ? static_cast<float>(c - static_cast<double>(ch)) : 0.f;
-    table = t;
-  }
   __device__ __forceinline__ uint64_t operator()(float l) const {
     const float dh = __fsub_rn(M, l);                          // M - l as dh + dl, exactly
-    if (dh == 0.f) return kOne;
     const float b = __fsub_rn(M, dh), dl = __fadd_rn(__fsub_rn(M, __fadd_rn(dh, b)), __fsub_rn(b, l));
     const float xh = __fmul_rn(dh, ch);
-    if (!(xh < 64.f)) return 0;
+    if (!(xh < 64.f)) return dh == 0.f ? kOne : 0;             // (0 times an infinite 1 / T is a NaN)
     const float xl = __fmaf_rn(dl, ch, __fmaf_rn(dh, cl, __fmaf_rn(dh, ch, -xh)));
-    const float e = rintf(xh), rh = __fsub_rn(xh, e), r = __fadd_rn(rh, xl), rl = __fsub_rn(xl, __fsub_rn(r, rh));
-    const float j = floorf(__fmaf_rn(r, 64.f, 0.5f));
-    const float f = __fadd_rn(__fmaf_rn(j, -0.015625f, r), rl);
+    const float te = __fadd_rn(xh, kWhole), e = __fsub_rn(te, kWhole), rh = __fsub_rn(xh, e);
+    const float r = __fadd_rn(rh, xl), rl = __fsub_rn(xl, __fsub_rn(r, rh));
+    const float tj = __fmaf_rn(r, 256.f, kWhole), j = __fsub_rn(tj, kWhole);
+    const float f = __fadd_rn(__fmaf_rn(j, -0.00390625f, r), rl);
+    // t = -f ln 2 and what its rounding leaves (0.69314718 is 1.904654e-9 above ln 2); q = t + t^2 / 2 + t^3 / 6.
     const float t = f * -0.69314718f;
-    // f * ln 2 to the last bit of its product: the rest of -f ln 2 beyond t, then t^2 / 2 + t^3 / 6 + t^4 / 24.
     const float rest = __fmaf_rn(f, -0.69314718f, -t) + f * 1.904654e-9f;
-    const float q = t + (rest + t * t * __fmaf_rn(t, __fmaf_rn(t, 0.041666667f, 0.16666667f), 0.5f));
-    const int ji = static_cast<int>(j);
-    const int shift = 19 + static_cast<int>(e) + (ji >> 6);     // j may be negative: 2^(-j / 64) = 2^-(j >> 6) 2^-((j & 63) / 64)
-    const uint64_t p = static_cast<uint64_t>(table[ji & 63]) * static_cast<uint32_t>(0x80000000u + __float2int_rn(q * 2147483648.f));
-    return shift >= 64 ? 0 : p >> shift;
+    const float q = t + (rest + t * t * __fmaf_rn(t, 0.16666667f, 0.5f));
+    const int ji = __float_as_int(tj) - kWholeBits;             // 2^(-j / 256) = 2^-(j >> 8) 2^-((j & 255) / 256)
+    const int shift = 19 + (__float_as_int(te) - kWholeBits) + (ji >> 8);
+    const uint32_t u = 0x80000000u + static_cast<uint32_t>(__float_as_int(__fmaf_rn(q, 2147483648.f, kWhole)) - kWholeBits);
+    const uint64_t w = static_cast<uint64_t>(table[ji & 255]) * u;
+    return shift < 64 ? w >> shift : 0;
   }
 };
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
 __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
@@ -202,7 +233,7 @@ __device__ __forceinline__ V sum_before(V v, V* part) {
 struct Row {
   int k;                     // 0: no limit
   float p;                   // 1: none
-  double least;              // weights below are not kept
+  uint64_t least;            // weights below are not kept
   float u;
   Weigh w;
 };
@@ -225,9 +256,10 @@ __device__ __forceinline__ uint32_t search(Team& team, uint32_t lo, uint32_t hi,
     const uint32_t span = hi - lo;
     const int s = span < kBins ? 0 : 21 - __clz(span);
     team.clear();
+    const float l_lo = value_of(lo), l_hi = value_of(hi);
     each([&](float l, int) {
-      const uint32_t k = key_of(l);
-      if (k >= lo && k <= hi) {
+      if (l >= l_lo && l <= l_hi) {
+        const uint32_t k = key_of(l);
         const uint64_t v = weight(l);
         if (v) atomicAdd(reinterpret_cast<unsigned long long*>(team.hist + ((hi - k) >> s)), static_cast<unsigned long long>(v));
       }
@@ -258,47 +290,72 @@ __device__ __forceinline__ uint32_t search(Team& team, uint32_t lo, uint32_t hi,
 }
 
 // The choice from the tokens within a limit, `count` in this CTA in the order of their indexes, the ranks' one after the
-// other: at(i) is a token's logit, index(i) its index.
+// other: at(i) is a token's logit, index(i) its index. A warp has a run of them, 32 at a time.
 template <typename At, typename Index>
 __device__ __forceinline__ void choose(Team& team, const SampleArgs& a, const Row& row, int64_t n, int count, Limit limit, At at,
                                        Index index) {
-  // Runs of tokens by thread: the ties with the limit's key before each, then the kept weights
-  // (an odd number of them, for the banks).
-  const int run = ((count + kThreads - 1) / kThreads) | 1, i0 = min(count, static_cast<int>(threadIdx.x) * run), i1 = min(count, i0 + run);
-  uint32_t same = 0;
-  uint64_t ties = 0;
-  if (limit.extra != 0xffffffffu) {
-    for (int i = i0; i < i1; ++i) same += key_of(at(i)) == limit.key;
-    const uint64_t mine = sum_before<uint64_t>(same, team.part);
+  __shared__ uint64_t goal_of;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int run = ((count + kWarps - 1) / kWarps + 31) / 32 * 32, i0 = min(count, warp * run), i1 = min(count, i0 + run);
+  const float edge = value_of(limit.key);
+  const bool all_ties = limit.extra == 0xffffffffu;
+  uint64_t ties = 0;                             // with the limit's key, before this warp's
+  if (!all_ties) {
+    uint32_t same = 0;
+    for (int i = i0 + lane; i < i1; i += 32) same += at(i) == edge;
     uint64_t before;
     team.sum(same, &before);
-    ties = before + mine;
+    same = __reduce_add_sync(0xffffffffu, same);
+    ties = before + sum_before<uint64_t>(lane == 0 ? same : 0, team.part);
+    ties = __shfl_sync(0xffffffffu, ties, 0);
   }
-  auto kept = [&](float l, uint64_t& seen) -> uint64_t {
-    const uint32_t k = key_of(l);
-    if (k < limit.key || (k == limit.key && seen++ >= limit.extra)) return 0;
+  // The weight of token i if it is kept; seen: tokens with the limit's key so far. All lanes of the warp call it.
+  auto kept = [&](int i, uint64_t& seen) -> uint64_t {
+    const float l = i < i1 ? at(i) : -INFINITY;
+    bool in = l >= edge;
+    if (!all_ties) {
+      const uint32_t equal = __ballot_sync(0xffffffffu, in && l == edge);
+      if (l == edge) in = in && seen + __popc(equal & ((1u << lane) - 1)) < limit.extra;
+      seen += __popc(equal);
+    }
+    if (!in) return 0;
     const uint64_t v = row.w(l);
-    return static_cast<double>(v) >= row.least ? v : 0;
+    return v >= row.least ? v : 0;
   };
   uint64_t mine = 0, seen = ties;
-  for (int i = i0; i < i1; ++i) mine += kept(at(i), seen);
-  uint64_t c = sum_before<uint64_t>(mine, team.part), before;
+  for (int i = i0; i < i1; i += 32) mine += kept(i + lane, seen);
+  uint64_t before, of_warp = mine;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) of_warp += __shfl_xor_sync(0xffffffffu, of_warp, o);
   const uint64_t total = team.sum(mine, &before);
-  c += before;
+  uint64_t c = before + sum_before<uint64_t>(lane == 0 ? of_warp : 0, team.part);
+  c = __shfl_sync(0xffffffffu, c, 0);
   // The first sum above u * total: at least floor(u * total) + 1, and at most all of it.
-  uint64_t goal = row.u > 0.f ? static_cast<uint64_t>(static_cast<double>(row.u) * static_cast<double>(total)) : 0;
-  goal = min(goal, total - 1);
-  if (c <= goal && goal < c + mine) {
-    seen = ties;
-    for (int i = i0; i < i1; ++i) {
-      const uint64_t v = kept(at(i), seen);
-      c += v;
-      if (c > goal) {
-        a.ids[n] = index(i);
-        if (a.probs) a.probs[n] = static_cast<float>(static_cast<double>(v) / static_cast<double>(total));
-        break;
-      }
+  if (threadIdx.x == 0) {
+    const uint64_t goal = row.u > 0.f ? static_cast<uint64_t>(static_cast<double>(row.u) * static_cast<double>(total)) : 0;
+    goal_of = min(goal, total - 1);
+  }
+  __syncthreads();
+  const uint64_t goal = goal_of;
+  if (!(c <= goal && goal < c + of_warp)) return;
+  seen = ties;
+  for (int i = i0; i < i1; i += 32) {
+    const uint64_t v = kept(i + lane, seen);
+    uint64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
+    const uint32_t past = __ballot_sync(0xffffffffu, c + x > goal);
+    if (past) {
+      if (lane == __ffs(past) - 1) {
+        a.ids[n] = index(i + lane);
+        if (a.probs) a.probs[n] = static_cast<float>(static_cast<double>(v) / static_cast<double>(total));
+      }
+      return;
+    }
+    c += __shfl_sync(0xffffffffu, x, 31);
   }
 }
 
@@ -317,22 +374,27 @@ __device__ __forceinline__ Limit limits(Team& team, const Row& row, uint32_t k_l
   if (row.p < 1.f) {
     if (row.k > 0) {
       uint64_t mine = 0;
-      each([&](float l, int) { mine += key_of(l) > limit.key ? row.w(l) : 0; });
-      whole = team.sum(mine) + limit.extra * row.w(value_of(limit.key));
+      const float edge = value_of(limit.key);
+      each([&](float l, int) { mine += l > edge ? row.w(l) : 0; });
+      whole = team.sum(mine) + limit.extra * row.w(edge);
     }
-    const double goal = static_cast<double>(row.p) * static_cast<double>(whole);
+    // The least sum that is enough.
+    __shared__ uint64_t goal_of;
+    if (threadIdx.x == 0) {
+      const double g = static_cast<double>(row.p) * static_cast<double>(whole);
+      goal_of = g > 0.0 ? static_cast<uint64_t>(ceil(g)) : 0;
+    }
+    __syncthreads();
+    const uint64_t goal = goal_of;
     uint32_t lo = limit.key, hi = 0;
     uint64_t above = 0;
     window(goal, lo, hi, above);
     const uint32_t key = search(team, lo, hi, above, each, [&](float l) { return row.w(l); },
-                                [&](uint64_t s) { return static_cast<double>(s) >= goal; });
+                                [&](uint64_t s) { return s >= goal && s > 0; });
     // Of the tokens with that key: the fewest that bring the sum to the goal, one at least.
     const uint64_t one = row.w(value_of(key));
     uint64_t c = 1;
-    if (one > 0) {
-      const double need = (goal - static_cast<double>(above)) / static_cast<double>(one);
-      c = need > 1.0 ? static_cast<uint64_t>(ceil(need)) : 1;
-    }
+    if (one > 0 && goal > above) c = max(static_cast<uint64_t>(1), (goal - above + one - 1) / one);
     limit.extra = static_cast<uint32_t>(min(c, static_cast<uint64_t>(key == limit.key ? limit.extra : 0xfffffffeu)));
     limit.key = key;
   }
@@ -342,7 +404,9 @@ __device__ __forceinline__ Limit limits(Team& team, const Row& row, uint32_t k_l
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a, int ctas, int per, bool vec) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ uint32_t table[64];
+  __shared__ uint32_t table[256];
+  __shared__ float per_T[2];
+  __shared__ uint64_t least;
   __shared__ uint64_t slots[2], part[kWarps + 2];
   __shared__ float partf[kWarps];
   __shared__ int bin_of[3];
@@ -352,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   int* list_at = reinterpret_cast<int*>(list + kList);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_enter();
-  if (threadIdx.x < 64) table[threadIdx.x] = kPow2[threadIdx.x];
+  if (threadIdx.x < 256) table[threadIdx.x] = kPow2[threadIdx.x];
   const int64_t n = blockIdx.x / ctas;
   Team team = {ctas, static_cast<int>(cluster_ctarank()), slots, part, hist, hist + kBins, 0};
   const int first = team.rank * per, count = max(0, min(per, static_cast<int>(a.V) - first));
@@ -364,16 +428,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     constexpr int E = 16 / sizeof(T);
     const int whole = vec ? count / E : 0;
     for (int i = threadIdx.x; i < whole; i += kThreads) {
-      const uint4 v = reinterpret_cast<const uint4*>(x)[i];
-      reinterpret_cast<uint4*>(slice)[i] = v;
-      const T* e = reinterpret_cast<const T*>(&v);
+      uint4 v = reinterpret_cast<const uint4*>(x)[i];
+      T* e = reinterpret_cast<T*>(&v);
 #pragma unroll
-      for (int j = 0; j < E; ++j) top = fmaxf(top, usable(to_f32(e[j])));
+      for (int j = 0; j < E; ++j) top = fmaxf(top, take(e[j]));
+      reinterpret_cast<uint4*>(slice)[i] = v;
     }
     for (int i = whole * E + threadIdx.x; i < count; i += kThreads) {
-      const T v = x[i];
+      T v = x[i];
+      top = fmaxf(top, take(v));
       slice[i] = v;
-      top = fmaxf(top, usable(to_f32(v)));
     }
   }
   Row row;
@@ -383,7 +447,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   row.u = a.u[n];
   if (row.k < 0 || row.k >= a.V) row.k = 0;
   if (!(row.p < 1.f)) row.p = 1.f;
-  row.least = min_p > 0.f ? fmin(static_cast<double>(min_p), 1.0) * static_cast<double>(kOne) : 0.0;
+  if (threadIdx.x == 0) {    // in 64 bits, by one thread
+    const double c = 1.4426950408889634 / static_cast<double>(T0);
+    per_T[0] = static_cast<float>(c);
+    per_T[1] = per_T[0] < INFINITY ? static_cast<float>(c - static_cast<double>(per_T[0])) : 0.f;
+    least = min_p > 0.f ? static_cast<uint64_t>(ceil(fmin(static_cast<double>(min_p), 1.0) * static_cast<double>(kOne))) : 0;
+  }
   const uint32_t top_key = static_cast<uint32_t>(team.most(key_of(top)));
   if (top_key == kNone) {    // no token is available
     if (threadIdx.x == 0 && team.rank == 0) {
@@ -395,11 +464,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   }
   auto at = [&](int i) { return usable(to_f32(slice[i])); };
   auto each = [&](auto f) {
+#pragma unroll 4
     for (int i = threadIdx.x; i < count; i += kThreads) f(at(i), i);
   };
   if (!(T0 > 0.f)) {         // the first token with the largest logit
     int at_least = 0x7fffffff;
-    each([&](float l, int i) { at_least = min(at_least, key_of(l) == top_key ? first + i : 0x7fffffff); });
+    const float most = value_of(top_key);
+    each([&](float l, int i) { at_least = min(at_least, l == most ? first + i : 0x7fffffff); });
     const int id = 0x7fffffff - static_cast<int>(team.most(static_cast<uint64_t>(0x7fffffff - at_least)));
     if (threadIdx.x == 0 && team.rank == 0) {
       a.ids[n] = id;
@@ -408,7 +479,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     team.sync();
     return;
   }
-  row.w.set(value_of(top_key), static_cast<double>(T0), table);
+  row.w = Weigh{value_of(top_key), per_T[0], per_T[1], table};
+  row.least = least;
   auto index = [&](int i) { return first + i; };
   if (row.k == 0 && row.p == 1.f) {
     choose(team, a, row, n, count, Limit{kNone + 1, 0xffffffffu}, at, index);
@@ -420,10 +492,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   // possible, in 2^-15 (high words; those of the last bin are below 2^-63). Without top_k the exact weight of all.
   const float M = value_of(top_key), scale = 32.f * 1.44269504f / T0;
   auto bin_at = [&](float l, float& frac) {
-    const float d = fminf(__fsub_rn(M, l) * scale, static_cast<float>(kBins - 1));       // a NaN (0 times infinity): 0
-    const float b = floorf(d);
-    frac = d - b;
-    return static_cast<int>(b);
+    const float d = fminf(__fsub_rn(M, l) * scale, static_cast<float>(kBins - 1));       // a NaN (0 times infinity): the last
+    const float t = __fadd_rd(d, 8388608.f);                   // the whole number below d in its low bits
+    frac = d - (t - 8388608.f);
+    return __float_as_int(t) - 0x4b000000;
   };
   team.clear();
   uint64_t whole = 0;
@@ -434,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     uint32_t* h = reinterpret_cast<uint32_t*>(hist + b);
     atomicAdd(h, 1u);
     if (row.p < 1.f) {
-      if (b < kBins - 1) atomicAdd(h + 1, static_cast<uint32_t>(32768.f * exp2f(frac * -0.03125f)));
+      if (b < kBins - 1) atomicAdd(h + 1, static_cast<uint32_t>(__float_as_int(__fmaf_rn(exp2_fast(frac * -0.03125f), 32768.f, kWhole)) - kWholeBits));
       if (row.k == 0) whole += row.w(l);
     }
   });
@@ -547,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     l_each([&](float l, int) { low = max(low, static_cast<uint64_t>(~key_of(l))); });
     const uint32_t lo = ~static_cast<uint32_t>(alone.most(low));
     const Limit limit = limits(alone, row, lo, top_key, 0, whole, l_each,
-                               [&](double, uint32_t& k, uint32_t& hi, uint64_t&) { k = max(k, lo), hi = top_key; });
+                               [&](uint64_t, uint32_t& k, uint32_t& hi, uint64_t&) { k = max(k, lo), hi = top_key; });
     choose(alone, a, row, n, m, limit, l_at, [&](int i) { return list_at[i]; });
     return;
   }
@@ -566,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   };
   uint32_t k_lo = 0, k_hi = 0;
   if (row.k > 0) keys_of_bins(last, last, k_lo, k_hi);
-  const Limit limit = limits(team, row, k_lo, k_hi, k_before, whole, each, [&](double goal, uint32_t& lo, uint32_t& hi, uint64_t& above) {
+  const Limit limit = limits(team, row, k_lo, k_hi, k_before, whole, each, [&](uint64_t goal, uint32_t& lo, uint32_t& hi, uint64_t& above) {
     const float g = static_cast<float>(goal) * in_units;
     const int b0 = find(1, [&](uint32_t, float w) { return w >= g * (1.f - around); });
     const int b1 = max(b0, find(2, [&](uint32_t, float w) { return w >= g * (1.f + around); }));
@@ -576,7 +648,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     lo = max(lo, w_lo);
     hi = max(lo, w_hi);
     uint64_t mine = 0;
-    each([&](float l, int) { mine += key_of(l) > hi ? row.w(l) : 0; });
+    const float l_hi = value_of(hi);
+    each([&](float l, int) { mine += l > l_hi ? row.w(l) : 0; });
     above = team.sum(mine);
   });
   choose(team, a, row, n, count, limit, at, index);
@@ -585,11 +658,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
 
 template <typename T>
 cudaError_t sample(const SampleArgs& a, int num_sms, cudaStream_t s) {
-  // CTAs of a row: enough to hold it, and as many as leave 2048 tokens each, while all rows' run at once.
-  constexpr int kMost = kSliceBytes / sizeof(T);
+  // CTAs of a row: enough to hold it by halves of an SM's shared memory, and as many as leave 2048 tokens each while all rows' run
+  // at once, two to an SM.
+  constexpr int kMost = kSliceBytes / 2 / sizeof(T);
   int ctas = 1;
   while (ctas < kMostCtas && (a.V > static_cast<int64_t>(ctas) * kMost ||
-                              (a.V >= 4096 * static_cast<int64_t>(ctas) && a.N * 2 * ctas <= num_sms)))
+                              (a.V >= 4096 * static_cast<int64_t>(ctas) && a.N * ctas <= num_sms)))
     ctas *= 2;
   const int per = static_cast<int>(((a.V + ctas - 1) / ctas + 7) / 8 * 8);
   const size_t smem = (static_cast<size_t>(per) * sizeof(T) + 15) / 16 * 16 + 2 * kBins * sizeof(uint64_t) + kList * 8;
