@@ -80,6 +80,7 @@ __device__ __forceinline__ uint32_t key_of(float l) {
   return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
 constexpr uint32_t kNone = 0x007fffffu;                        // the key of -inf
+constexpr uint32_t kAll = 0xffffffffu;
 
 // Adding it to an fp32 below 2^22 in magnitude rounds that to a whole number, which the sum has in its low bits.
 constexpr float kWhole = 12582912.f;
@@ -211,6 +212,10 @@ struct Team {
   }
 };
 
+__device__ __forceinline__ void add_shared(void* p, uint32_t v) {
+  asm volatile("red.shared::cta.add.u32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
+}
+
 // The sum of v over the threads before this one.
 template <typename V>
 __device__ __forceinline__ V sum_before(V v, V* part) {
@@ -231,104 +236,352 @@ __device__ __forceinline__ V sum_before(V v, V* part) {
 }
 
 struct Row {
-  int k;                     // 0: no limit
+  uint32_t k;                // 0: no limit
   float p;                   // 1: none
   uint64_t least;            // weights below are not kept
   float u;
   Weigh w;
 };
 
-// A limit: keys above `key` are within it, and the first `extra`, by index, of the tokens with that key.
-struct Limit {
-  uint32_t key, extra;
-};
+// A row of logits in the shared memory of a cluster: the largest, and (T not above 0) its first token; else the limits of top_k
+// and top_p, and the choice among the tokens kept. Steps that the weights' sums decide are taken in whole numbers.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a, int ctas, int per, bool vec) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint32_t table[256];
+  __shared__ float per_T[2];
+  __shared__ uint64_t least, slots[2], part[kWarps + 2], goal_of, found_above;
+  __shared__ float partf[kWarps];
+  __shared__ int bin_of, found;
+  __shared__ uint32_t tokens_at, tokens_to, available;
+  T* slice = reinterpret_cast<T*>(smem);
+  uint64_t* hist = reinterpret_cast<uint64_t*>(smem + (static_cast<size_t>(per) * sizeof(T) + 15) / 16 * 16);
+  T* list = reinterpret_cast<T*>(hist + 2 * kBins);
+  int* list_at = reinterpret_cast<int*>(list + kList);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_enter();
+  if (threadIdx.x < 256) table[threadIdx.x] = kPow2[threadIdx.x];
+  const int64_t n = blockIdx.x / ctas;
+  Team team = {ctas, static_cast<int>(cluster_ctarank()), slots, part, hist, hist + kBins, 0};
+  const int first = team.rank * per;
+  // This CTA's tokens, in the order of their indexes: token i is `first` + i, or index[i].
+  int count = max(0, min(per, static_cast<int>(a.V) - first));
+  const T* tokens = slice;
+  const int* index = nullptr;
+  const T* x = static_cast<const T*>(a.logits) + n * a.ld + first;
 
-// each(f): f(logit, place) for every token of the team, each CTA's by all of its threads.
-//
-// The largest key in [lo, hi] at which a sum over the keys from hi down, by histograms of runs of keys, passes a
-// goal: reached(s) says whether a sum s is enough; above is the sum of keys beyond hi, and of those beyond the key after.
-template <typename Each, typename Weight, typename Reached>
-__device__ __forceinline__ uint32_t search(Team& team, uint32_t lo, uint32_t hi, uint64_t& above, Each each, Weight weight,
-                                           Reached reached) {
-  __shared__ int found;
-  __shared__ uint64_t found_above;
-  for (;;) {
-    const uint32_t span = hi - lo;
-    const int s = span < kBins ? 0 : 21 - __clz(span);
+  // The slice, and the row's largest logit.
+  float top = -INFINITY;
+  {
+    constexpr int E = 16 / sizeof(T);
+    const int whole = vec ? count / E : 0;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < whole; i += kThreads) {
+      uint4 v = reinterpret_cast<const uint4*>(x)[i];
+      T* e = reinterpret_cast<T*>(&v);
+#pragma unroll
+      for (int j = 0; j < E; ++j) top = fmaxf(top, take(e[j]));
+      reinterpret_cast<uint4*>(slice)[i] = v;
+    }
+#pragma unroll 4
+    for (int i = whole * E + threadIdx.x; i < count; i += kThreads) {
+      T v = x[i];
+      top = fmaxf(top, take(v));
+      slice[i] = v;
+    }
+  }
+  Row row;
+  const int k = a.top_k ? a.top_k[n] : 0;
+  row.k = k > 0 && k < a.V ? k : 0;
+  row.p = a.top_p ? a.top_p[n] : 1.f;
+  if (!(row.p < 1.f)) row.p = 1.f;
+  const float T0 = a.temperature ? a.temperature[n] : 1.f, min_p = a.min_p ? a.min_p[n] : 0.f;
+  row.u = a.u[n];
+  if (threadIdx.x == 0) {    // in 64 bits, by one thread
+    const double c = 1.4426950408889634 / static_cast<double>(T0);
+    per_T[0] = static_cast<float>(c);
+    per_T[1] = per_T[0] < INFINITY ? static_cast<float>(c - static_cast<double>(per_T[0])) : 0.f;
+    least = min_p > 0.f ? static_cast<uint64_t>(ceil(fmin(static_cast<double>(min_p), 1.0) * static_cast<double>(kOne))) : 0;
+  }
+  const uint32_t top_key = static_cast<uint32_t>(team.most(key_of(top)));
+  auto at = [&](int i) { return usable(to_f32(tokens[i])); };
+  auto each = [&](auto f) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < count; i += kThreads) f(at(i), i);
+  };
+  const float M = value_of(top_key);
+  if (top_key == kNone || !(T0 > 0.f)) {         // no token at all, or the first with the largest logit
+    int id = 0x7fffffff;
+    each([&](float l, int i) { id = min(id, l == M ? first + i : 0x7fffffff); });
+    id = 0x7fffffff - static_cast<int>(team.most(static_cast<uint64_t>(0x7fffffff - id)));
+    if (threadIdx.x == 0 && team.rank == 0) {
+      a.ids[n] = top_key == kNone ? 0 : id;
+      if (a.probs) a.probs[n] = top_key == kNone ? 0.f : 1.f;
+    }
+    team.sync();             // nobody leaves while its memory is read
+    return;
+  }
+  row.w = Weigh{M, per_T[0], per_T[1], table};
+  row.least = least;
+
+  // The limit: keys above limit_key are within it, and the first `extra`, by index, of the tokens with that key.
+  uint32_t limit_key = kNone + 1, extra = kAll;
+  if (row.k > 0 || row.p < 1.f) {
+    // Histogram by bins of (M - l) log2(e) / T of 1/32: tokens (low words) and, with top_p, weights relative to the bin's largest
+    // possible, in 2^-15 (high words; those of the last bin are below 2^-63). Without top_k the exact weight of all.
+    const float scale = 32.f * 1.44269504f / T0;
+    auto bin_at = [&](float l, float& frac) {
+      const float d = l == M ? 0.f : fminf(__fsub_rn(M, l) * scale, static_cast<float>(kBins - 1));   // (a NaN: the last)
+      const float t = __fadd_rd(d, 8388608.f);                 // the whole number below d in its low bits
+      frac = d - (t - 8388608.f);
+      return __float_as_int(t) - 0x4b000000;
+    };
+    const bool by_weight = row.p < 1.f;
+    uint64_t whole = 0;
     team.clear();
-    const float l_lo = value_of(lo), l_hi = value_of(hi);
     each([&](float l, int) {
-      if (l >= l_lo && l <= l_hi) {
-        const uint32_t k = key_of(l);
-        const uint64_t v = weight(l);
-        if (v) atomicAdd(reinterpret_cast<unsigned long long*>(team.hist + ((hi - k) >> s)), static_cast<unsigned long long>(v));
+      if (l == -INFINITY) return;
+      float frac;
+      uint32_t* h = reinterpret_cast<uint32_t*>(hist + bin_at(l, frac));
+      add_shared(h, 1u);
+      if (by_weight) {
+        const float w = exp2_fast(frac * -0.03125f);
+        add_shared(h + 1, static_cast<uint32_t>(__float_as_int(__fmaf_rn(w, 32768.f, kWhole)) - kWholeBits));
+        if (row.k == 0) whole += row.w(l);
       }
     });
-    if (threadIdx.x == 0) found = -1;
-    const uint64_t* h = team.gather([](uint64_t a, uint64_t b) { return a + b; });
-    uint64_t bin[kPerThread], mine = 0;
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) mine += bin[i] = h[kPerThread * threadIdx.x + i];
-    uint64_t c = above + sum_before<uint64_t>(mine, team.part);
+    if (by_weight && row.k == 0) whole = team.sum(whole);
+    // Over the cluster: tokens (low words) and weights as fp32 (high words), the latter times 2^(-b / 32) below.
+    const auto as_float = [](uint64_t h) { return (h & 0xffffffffu) | static_cast<uint64_t>(__float_as_uint(static_cast<float>(h >> 32))) << 32; };
+    const uint64_t* all = team.gather([&](uint64_t v, uint64_t h) {
+      h = as_float(h);
+      const float w = __uint_as_float(static_cast<uint32_t>(v >> 32)) + __uint_as_float(static_cast<uint32_t>(h >> 32));
+      return ((v & 0xffffffffu) + (h & 0xffffffffu)) | static_cast<uint64_t>(__float_as_uint(w)) << 32;
+    });
+    // Tokens and weights up to each bin.
+    uint32_t tokens_to_bin[kPerThread], tokens_sum = 0;
+    float weight_to_bin[kPerThread], weight_sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
-      if (!reached(c) && reached(c + bin[i])) {
-        found = kPerThread * threadIdx.x + i;
-        found_above = c;
-      }
-      c += bin[i];
+      const int b = kPerThread * threadIdx.x + i;
+      const uint64_t h = team.ctas == 1 ? as_float(all[b]) : all[b];
+      tokens_to_bin[i] = tokens_sum += static_cast<uint32_t>(h);
+      weight_to_bin[i] = weight_sum +=
+          b < kBins - 1 ? __uint_as_float(static_cast<uint32_t>(h >> 32)) * exp2_fast(b * -0.03125f) * 0x1p-15f : 0.f;
     }
-    __syncthreads();
-    // Never reached (a goal that rounding has put above the whole sum): the lowest key.
-    if (found < 0) return lo;
-    above = found_above;
-    hi -= static_cast<uint32_t>(found) << s;
-    if (s == 0) return hi;
-    lo = max(lo, hi - ((1u << s) - 1));
-    __syncthreads();
-  }
-}
+    const uint32_t tokens_before = static_cast<uint32_t>(sum_before<uint64_t>(tokens_sum, part));
+    const float weight_before = sum_before<float>(weight_sum, partf);
+    // The first bin up to which there are so many tokens, or (tokens 0) so much weight; the last bin if there are never. Tokens
+    // before it and up to it in tokens_at and tokens_to.
+    auto find = [&](uint32_t least_tokens, float least_weight) {
+      __syncthreads();
+      if (threadIdx.x == 0) bin_of = kBins - 1;
+      __syncthreads();
+#pragma unroll
+      for (int i = kPerThread - 1; i >= 0; --i)
+        if (least_tokens ? tokens_before + tokens_to_bin[i] >= least_tokens : weight_before + weight_to_bin[i] >= least_weight)
+          atomicMin(&bin_of, static_cast<int>(kPerThread * threadIdx.x + i));
+      __syncthreads();
+      const int b = bin_of;
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i)
+        if (b == static_cast<int>(kPerThread * threadIdx.x) + i) {
+          tokens_at = tokens_before + (i > 0 ? tokens_to_bin[i > 0 ? i - 1 : 0] : 0);
+          tokens_to = tokens_before + tokens_to_bin[i];
+        }
+      if (threadIdx.x == kThreads - 1) available = tokens_before + tokens_sum;
+      __syncthreads();
+      return b;
+    };
+    // The bins' weights are within 2^-14 of the exact ones, and fp32's sums of them: 2^-11 is beyond that on both sides.
+    const float around = 0x1p-11f, in_units = 1.f / static_cast<float>(kOne);
+    int last = kBins - 1;    // no token of a later bin is kept
+    if (row.k > 0) {
+      last = find(row.k, 0.f);
+      if (available <= row.k) {                  // top_k leaves all of them
+        row.k = 0;
+        if (by_weight) {
+          whole = 0;
+          each([&](float l, int) { whole += row.w(l); });
+          whole = team.sum(whole);
+        }
+      }
+    }
+    if (row.k == 0 && by_weight) last = find(0, row.p * (static_cast<float>(whole) * in_units) * (1.f + around));
+    const uint32_t some = tokens_to, k_before = tokens_at;
+    // The least key whose bin is b or an earlier one, by 32 tries at a time. Every warp finds it for itself.
+    auto least_key = [&](int b) {
+      uint32_t lo = kNone, hi = top_key;         // the key is in (lo, hi]
+      while (hi - lo > 1) {
+        const uint32_t step = (hi - lo + 31) / 32, at = min(lo + step * (lane + 1), hi);
+        float frac;
+        const uint32_t in = __ballot_sync(0xffffffffu, bin_at(value_of(at), frac) <= b);
+        const int i = __ffs(in) - 1;             // (hi is among the tries)
+        hi = min(lo + step * (i + 1), hi);
+        lo = lo + step * i;
+      }
+      return hi;
+    };
+    uint32_t lo = least_key(last), hi = top_key;
+    uint64_t above = 0;
 
-// The choice from the tokens within a limit, `count` in this CTA in the order of their indexes, the ranks' one after the
-// other: at(i) is a token's logit, index(i) its index. A warp has a run of them, 32 at a time.
-template <typename At, typename Index>
-__device__ __forceinline__ void choose(Team& team, const SampleArgs& a, const Row& row, int64_t n, int count, Limit limit, At at,
-                                       Index index) {
-  __shared__ uint64_t goal_of;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (some <= kList) {
+      // Few: to the first CTA, in the order of their indexes. A warp takes a run of tokens.
+      const float least_kept = value_of(lo);
+      const int run = ((count + kWarps - 1) / kWarps + 31) / 32 * 32, i0 = min(count, warp * run), i1 = min(count, i0 + run);
+      uint32_t mine = 0;
+#pragma unroll 4
+      for (int i = i0 + lane; i < i1; i += 32) mine += at(i) >= least_kept;
+      mine = __reduce_add_sync(0xffffffffu, mine);
+      uint64_t to;
+      const int there = static_cast<int>(team.sum(lane == 0 ? mine : 0, &to));
+      to += sum_before<uint64_t>(lane == 0 ? mine : 0, part);
+      uint32_t place = __shfl_sync(0xffffffffu, static_cast<uint32_t>(to), 0);
+      const uint32_t list0 = mapa_shared(list, 0), at0 = mapa_shared(list_at, 0);
+#pragma unroll 4
+      for (int i = i0; i < i1; i += 32) {
+        const bool m = i + lane < i1 && at(i + lane) >= least_kept;
+        const uint32_t b = __ballot_sync(0xffffffffu, m);
+        if (m) {
+          const uint32_t to_place = place + __popc(b & ((1u << lane) - 1));
+          if constexpr (sizeof(T) == 4)
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(list0 + 4 * to_place), "f"(slice[i + lane]) : "memory");
+          else
+            asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(list0 + 2 * to_place),
+                         "h"(*reinterpret_cast<const uint16_t*>(slice + i + lane)) : "memory");
+          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at0 + 4 * to_place), "r"(first + i + lane) : "memory");
+        }
+        place += __popc(b);
+      }
+      team.sync();
+      if (team.rank > 0) return;
+      team = Team{1, 0, slots, part, hist, hist, 0};
+      tokens = list;
+      index = list_at;
+      count = there;
+    } else if (row.k > 0) {  // Many: the cluster goes on, within the bin of the k-th token
+      hi = last > 0 ? least_key(last - 1) - 1 : top_key;
+      above = k_before;
+    }
+
+    // The limits one after the other: the largest key at which the sum of tokens, or of weights, over the keys from the largest
+    // down reaches its goal. The sum is by histograms of runs of keys in [lo, hi], `above` that of the keys beyond hi.
+#pragma unroll 1
+    for (int what = row.k > 0 ? 0 : 1; what < (by_weight ? 2 : 1); ++what) {
+      uint64_t goal = row.k;
+      if (what == 1) {
+        const float edge = value_of(limit_key);
+        if (row.k > 0) {
+          uint64_t mine = 0;
+          each([&](float l, int) { mine += l > edge ? row.w(l) : 0; });
+          whole = team.sum(mine) + extra * row.w(edge);
+        }
+        if (threadIdx.x == 0) {                  // the least sum that is enough
+          const double g = static_cast<double>(row.p) * static_cast<double>(whole);
+          goal_of = g > 1.0 ? static_cast<uint64_t>(ceil(g)) : 1;
+        }
+        __syncthreads();
+        goal = goal_of;
+        lo = max(lo, limit_key);
+        hi = top_key;
+        above = 0;
+        if (team.ctas > 1) {
+          // Between the bins in which the prefix may end; what lies beyond is added up.
+          const float g = static_cast<float>(goal) * in_units;
+          const int b0 = find(0, g * (1.f - around)), b1 = max(b0, find(0, g * (1.f + around)));
+          lo = max(least_key(b1), limit_key);
+          hi = max(lo, b0 > 0 ? least_key(b0 - 1) - 1 : top_key);
+          const float beyond = value_of(hi);
+          uint64_t mine = 0;
+          each([&](float l, int) { mine += l > beyond ? row.w(l) : 0; });
+          above = team.sum(mine);
+        }
+      }
+      for (;;) {
+        const uint32_t span = hi - lo;
+        const int s = span < kBins ? 0 : 21 - __clz(span);
+        team.clear();
+        const float l_lo = value_of(lo), l_hi = value_of(hi);
+        each([&](float l, int) {
+          if (l >= l_lo && l <= l_hi) {
+            uint64_t* h = hist + ((hi - key_of(l)) >> s);
+            if (what == 0) add_shared(h, 1u);
+            else atomicAdd(reinterpret_cast<unsigned long long*>(h), static_cast<unsigned long long>(row.w(l)));
+          }
+        });
+        if (threadIdx.x == 0) found = -1;
+        const uint64_t* h = team.gather([](uint64_t v, uint64_t w) { return v + w; });
+        uint64_t bin[kPerThread], mine = 0;
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) mine += bin[i] = h[kPerThread * threadIdx.x + i];
+        uint64_t c = above + sum_before<uint64_t>(mine, part);
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) {
+          if (c < goal && c + bin[i] >= goal) {
+            found = kPerThread * threadIdx.x + i;
+            found_above = c;
+          }
+          c += bin[i];
+        }
+        __syncthreads();
+        if (found < 0) {                         // (a goal that rounding has put above the whole sum)
+          hi = lo;
+          break;
+        }
+        above = found_above;
+        hi -= static_cast<uint32_t>(found) << s;
+        if (s == 0) break;
+        lo = max(lo, hi - ((1u << s) - 1));
+        __syncthreads();
+      }
+      if (what == 0) {
+        limit_key = hi;
+        extra = static_cast<uint32_t>(goal - above);
+      } else {
+        // Of the tokens with that key: the fewest that bring the sum to the goal, one at least.
+        const uint64_t one = row.w(value_of(hi));
+        const uint64_t c = one > 0 && goal > above ? (goal - above + one - 1) / one : 1;
+        extra = static_cast<uint32_t>(min(c, static_cast<uint64_t>(hi == limit_key ? extra : kAll - 1)));
+        limit_key = hi;
+      }
+      __syncthreads();
+    }
+  }
+
+  // The choice. A warp has a run of tokens, 32 at a time.
   const int run = ((count + kWarps - 1) / kWarps + 31) / 32 * 32, i0 = min(count, warp * run), i1 = min(count, i0 + run);
-  const float edge = value_of(limit.key);
-  const bool all_ties = limit.extra == 0xffffffffu;
+  const float edge = value_of(limit_key);
   uint64_t ties = 0;                             // with the limit's key, before this warp's
-  if (!all_ties) {
+  if (extra != kAll) {
     uint32_t same = 0;
+#pragma unroll 4
     for (int i = i0 + lane; i < i1; i += 32) same += at(i) == edge;
     uint64_t before;
     team.sum(same, &before);
     same = __reduce_add_sync(0xffffffffu, same);
-    ties = before + sum_before<uint64_t>(lane == 0 ? same : 0, team.part);
+    ties = before + sum_before<uint64_t>(lane == 0 ? same : 0, part);
     ties = __shfl_sync(0xffffffffu, ties, 0);
   }
   // The weight of token i if it is kept; seen: tokens with the limit's key so far. All lanes of the warp call it.
   auto kept = [&](int i, uint64_t& seen) -> uint64_t {
     const float l = i < i1 ? at(i) : -INFINITY;
     bool in = l >= edge;
-    if (!all_ties) {
-      const uint32_t equal = __ballot_sync(0xffffffffu, in && l == edge);
-      if (l == edge) in = in && seen + __popc(equal & ((1u << lane) - 1)) < limit.extra;
+    if (extra != kAll) {
+      const uint32_t equal = __ballot_sync(0xffffffffu, l == edge);
+      if (l == edge) in = seen + __popc(equal & ((1u << lane) - 1)) < extra;
       seen += __popc(equal);
     }
     if (!in) return 0;
     const uint64_t v = row.w(l);
     return v >= row.least ? v : 0;
   };
-  uint64_t mine = 0, seen = ties;
+  uint64_t mine = 0, seen = ties, before;
   for (int i = i0; i < i1; i += 32) mine += kept(i + lane, seen);
-  uint64_t before, of_warp = mine;
+  uint64_t of_warp = mine;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) of_warp += __shfl_xor_sync(0xffffffffu, of_warp, o);
   const uint64_t total = team.sum(mine, &before);
-  uint64_t c = before + sum_before<uint64_t>(lane == 0 ? of_warp : 0, team.part);
+  uint64_t c = before + sum_before<uint64_t>(lane == 0 ? of_warp : 0, part);
   c = __shfl_sync(0xffffffffu, c, 0);
   // The first sum above u * total: at least floor(u * total) + 1, and at most all of it.
   if (threadIdx.x == 0) {
@@ -337,322 +590,27 @@ __device__ __forceinline__ void choose(Team& team, const SampleArgs& a, const Ro
   }
   __syncthreads();
   const uint64_t goal = goal_of;
-  if (!(c <= goal && goal < c + of_warp)) return;
-  seen = ties;
-  for (int i = i0; i < i1; i += 32) {
-    const uint64_t v = kept(i + lane, seen);
-    uint64_t x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    const uint32_t past = __ballot_sync(0xffffffffu, c + x > goal);
-    if (past) {
-      if (lane == __ffs(past) - 1) {
-        a.ids[n] = index(i + lane);
-        if (a.probs) a.probs[n] = static_cast<float>(static_cast<double>(v) / static_cast<double>(total));
-      }
-      return;
-    }
-    c += __shfl_sync(0xffffffffu, x, 31);
-  }
-}
-
-// The limits of top_k (the k-th largest key is in [k_lo, k_hi], with k_above tokens beyond it) and of top_p. whole: the
-// weight of all tokens, where top_k does not limit them. window(goal, lo, hi, above): the keys between which the prefix
-// with that weight ends.
-template <typename Each, typename Window>
-__device__ __forceinline__ Limit limits(Team& team, const Row& row, uint32_t k_lo, uint32_t k_hi, uint64_t k_above, uint64_t whole,
-                                        Each each, Window window) {
-  Limit limit = {kNone + 1, 0xffffffffu};
-  if (row.k > 0) {
-    const uint64_t k = row.k;
-    limit.key = search(team, k_lo, k_hi, k_above, each, [](float) -> uint64_t { return 1; }, [&](uint64_t s) { return s >= k; });
-    limit.extra = static_cast<uint32_t>(k - k_above);
-  }
-  if (row.p < 1.f) {
-    if (row.k > 0) {
-      uint64_t mine = 0;
-      const float edge = value_of(limit.key);
-      each([&](float l, int) { mine += l > edge ? row.w(l) : 0; });
-      whole = team.sum(mine) + limit.extra * row.w(edge);
-    }
-    // The least sum that is enough.
-    __shared__ uint64_t goal_of;
-    if (threadIdx.x == 0) {
-      const double g = static_cast<double>(row.p) * static_cast<double>(whole);
-      goal_of = g > 0.0 ? static_cast<uint64_t>(ceil(g)) : 0;
-    }
-    __syncthreads();
-    const uint64_t goal = goal_of;
-    uint32_t lo = limit.key, hi = 0;
-    uint64_t above = 0;
-    window(goal, lo, hi, above);
-    const uint32_t key = search(team, lo, hi, above, each, [&](float l) { return row.w(l); },
-                                [&](uint64_t s) { return s >= goal && s > 0; });
-    // Of the tokens with that key: the fewest that bring the sum to the goal, one at least.
-    const uint64_t one = row.w(value_of(key));
-    uint64_t c = 1;
-    if (one > 0 && goal > above) c = max(static_cast<uint64_t>(1), (goal - above + one - 1) / one);
-    limit.extra = static_cast<uint32_t>(min(c, static_cast<uint64_t>(key == limit.key ? limit.extra : 0xfffffffeu)));
-    limit.key = key;
-  }
-  return limit;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a, int ctas, int per, bool vec) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ uint32_t table[256];
-  __shared__ float per_T[2];
-  __shared__ uint64_t least;
-  __shared__ uint64_t slots[2], part[kWarps + 2];
-  __shared__ float partf[kWarps];
-  __shared__ int bin_of[3];
-  T* slice = reinterpret_cast<T*>(smem);
-  uint64_t* hist = reinterpret_cast<uint64_t*>(smem + (static_cast<size_t>(per) * sizeof(T) + 15) / 16 * 16);
-  float* list = reinterpret_cast<float*>(hist + 2 * kBins);
-  int* list_at = reinterpret_cast<int*>(list + kList);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  pdl_enter();
-  if (threadIdx.x < 256) table[threadIdx.x] = kPow2[threadIdx.x];
-  const int64_t n = blockIdx.x / ctas;
-  Team team = {ctas, static_cast<int>(cluster_ctarank()), slots, part, hist, hist + kBins, 0};
-  const int first = team.rank * per, count = max(0, min(per, static_cast<int>(a.V) - first));
-  const T* x = static_cast<const T*>(a.logits) + n * a.ld + first;
-
-  // The slice, and the row's largest logit.
-  float top = -INFINITY;
-  {
-    constexpr int E = 16 / sizeof(T);
-    const int whole = vec ? count / E : 0;
-    for (int i = threadIdx.x; i < whole; i += kThreads) {
-      uint4 v = reinterpret_cast<const uint4*>(x)[i];
-      T* e = reinterpret_cast<T*>(&v);
-#pragma unroll
-      for (int j = 0; j < E; ++j) top = fmaxf(top, take(e[j]));
-      reinterpret_cast<uint4*>(slice)[i] = v;
-    }
-    for (int i = whole * E + threadIdx.x; i < count; i += kThreads) {
-      T v = x[i];
-      top = fmaxf(top, take(v));
-      slice[i] = v;
-    }
-  }
-  Row row;
-  row.k = a.top_k ? a.top_k[n] : 0;
-  row.p = a.top_p ? a.top_p[n] : 1.f;
-  const float T0 = a.temperature ? a.temperature[n] : 1.f, min_p = a.min_p ? a.min_p[n] : 0.f;
-  row.u = a.u[n];
-  if (row.k < 0 || row.k >= a.V) row.k = 0;
-  if (!(row.p < 1.f)) row.p = 1.f;
-  if (threadIdx.x == 0) {    // in 64 bits, by one thread
-    const double c = 1.4426950408889634 / static_cast<double>(T0);
-    per_T[0] = static_cast<float>(c);
-    per_T[1] = per_T[0] < INFINITY ? static_cast<float>(c - static_cast<double>(per_T[0])) : 0.f;
-    least = min_p > 0.f ? static_cast<uint64_t>(ceil(fmin(static_cast<double>(min_p), 1.0) * static_cast<double>(kOne))) : 0;
-  }
-  const uint32_t top_key = static_cast<uint32_t>(team.most(key_of(top)));
-  if (top_key == kNone) {    // no token is available
-    if (threadIdx.x == 0 && team.rank == 0) {
-      a.ids[n] = 0;
-      if (a.probs) a.probs[n] = 0.f;
-    }
-    team.sync();             // nobody leaves while its memory is read
-    return;
-  }
-  auto at = [&](int i) { return usable(to_f32(slice[i])); };
-  auto each = [&](auto f) {
-#pragma unroll 4
-    for (int i = threadIdx.x; i < count; i += kThreads) f(at(i), i);
-  };
-  if (!(T0 > 0.f)) {         // the first token with the largest logit
-    int at_least = 0x7fffffff;
-    const float most = value_of(top_key);
-    each([&](float l, int i) { at_least = min(at_least, l == most ? first + i : 0x7fffffff); });
-    const int id = 0x7fffffff - static_cast<int>(team.most(static_cast<uint64_t>(0x7fffffff - at_least)));
-    if (threadIdx.x == 0 && team.rank == 0) {
-      a.ids[n] = id;
-      if (a.probs) a.probs[n] = 1.f;
-    }
-    team.sync();
-    return;
-  }
-  row.w = Weigh{value_of(top_key), per_T[0], per_T[1], table};
-  row.least = least;
-  auto index = [&](int i) { return first + i; };
-  if (row.k == 0 && row.p == 1.f) {
-    choose(team, a, row, n, count, Limit{kNone + 1, 0xffffffffu}, at, index);
-    team.sync();
-    return;
-  }
-
-  // Histogram by bins of (M - l) log2(e) / T of 1/32: tokens (low words) and, with top_p, weights relative to the bin's largest
-  // possible, in 2^-15 (high words; those of the last bin are below 2^-63). Without top_k the exact weight of all.
-  const float M = value_of(top_key), scale = 32.f * 1.44269504f / T0;
-  auto bin_at = [&](float l, float& frac) {
-    const float d = fminf(__fsub_rn(M, l) * scale, static_cast<float>(kBins - 1));       // a NaN (0 times infinity): the last
-    const float t = __fadd_rd(d, 8388608.f);                   // the whole number below d in its low bits
-    frac = d - (t - 8388608.f);
-    return __float_as_int(t) - 0x4b000000;
-  };
-  team.clear();
-  uint64_t whole = 0;
-  each([&](float l, int) {
-    if (l == -INFINITY) return;
-    float frac;
-    const int b = l == M ? (frac = 0.f, 0) : bin_at(l, frac);
-    uint32_t* h = reinterpret_cast<uint32_t*>(hist + b);
-    atomicAdd(h, 1u);
-    if (row.p < 1.f) {
-      if (b < kBins - 1) atomicAdd(h + 1, static_cast<uint32_t>(__float_as_int(__fmaf_rn(exp2_fast(frac * -0.03125f), 32768.f, kWhole)) - kWholeBits));
-      if (row.k == 0) whole += row.w(l);
-    }
-  });
-  if (row.p < 1.f && row.k == 0) whole = team.sum(whole);
-  // Over the cluster: tokens (low words) and weights as fp32 (high words), the latter times 2^(-b / 32) below.
-  const uint64_t* all;
-  if (team.ctas == 1) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kBins; i += kThreads)
-      hist[i] = (hist[i] & 0xffffffffu) | static_cast<uint64_t>(__float_as_uint(static_cast<float>(hist[i] >> 32))) << 32;
-    __syncthreads();
-    all = hist;
-  } else {
-    all = team.gather([](uint64_t v, uint64_t h) {
-      const float w = __uint_as_float(static_cast<uint32_t>(v >> 32)) + static_cast<float>(h >> 32);
-      return ((v & 0xffffffffu) + (h & 0xffffffffu)) | static_cast<uint64_t>(__float_as_uint(w)) << 32;
-    });
-  }
-  // Tokens and weights up to each bin.
-  uint32_t tokens[kPerThread], tokens_sum = 0;
-  float weight[kPerThread], weight_sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int b = kPerThread * threadIdx.x + i;
-    tokens[i] = tokens_sum += static_cast<uint32_t>(all[b]);
-    weight[i] = weight_sum += __uint_as_float(static_cast<uint32_t>(all[b] >> 32)) * exp2f(b * -0.03125f) * 0x1p-15f;
-  }
-  const uint32_t tokens_before = static_cast<uint32_t>(sum_before<uint64_t>(tokens_sum, part));
-  const float weight_before = sum_before<float>(weight_sum, partf);
-  __shared__ uint32_t tokens_at, tokens_to, available;
-  // The first bin up to which there are `enough` (of tokens or of weight), in bin_of[to]; the last bin if there are never. Tokens
-  // before it and up to it in tokens_at and tokens_to.
-  auto find = [&](int to, auto enough) {
-    __syncthreads();
-    if (threadIdx.x == 0) bin_of[to] = kBins - 1;
-    __syncthreads();
-#pragma unroll
-    for (int i = kPerThread - 1; i >= 0; --i)
-      if (enough(tokens_before + tokens[i], weight_before + weight[i])) atomicMin(&bin_of[to], static_cast<int>(kPerThread * threadIdx.x + i));
-    __syncthreads();
-    const int b = bin_of[to] - kPerThread * static_cast<int>(threadIdx.x);
-    if (b >= 0 && b < kPerThread) {
-      uint32_t t = 0;
-#pragma unroll
-      for (int i = 0; i < kPerThread; ++i) {
-        if (i == b) tokens_at = tokens_before + t, tokens_to = tokens_before + tokens[i];
-        t = tokens[i];
-      }
-    }
-    if (threadIdx.x == kThreads - 1) available = tokens_before + tokens_sum;
-    __syncthreads();
-    return bin_of[to];
-  };
-  // The bins' weights are within 2^-14 of the exact ones, and fp32's sums of them: 2^-11 is beyond that on both sides.
-  const float around = 0x1p-11f;
-  const float in_units = 1.f / static_cast<float>(kOne);
-  int last;                  // no token of a later bin is kept
-  if (row.k > 0) last = find(0, [&](uint32_t t, float) { return t >= static_cast<uint32_t>(row.k); });
-  if (row.k > 0 && available <= static_cast<uint32_t>(row.k)) {        // top_k leaves all of them
-    row.k = 0;
-    if (row.p < 1.f) {
-      whole = 0;
-      each([&](float l, int) { whole += row.w(l); });
-      whole = team.sum(whole);
-    }
-  }
-  if (row.k == 0 && row.p == 1.f) {
-    choose(team, a, row, n, count, Limit{kNone + 1, 0xffffffffu}, at, index);
-    team.sync();
-    return;
-  }
-  if (row.k == 0) last = find(0, [&, g = row.p * (static_cast<float>(whole) * in_units) * (1.f + around)](uint32_t, float w) { return w >= g; });
-  const uint32_t some = tokens_to, k_before = tokens_at;
-
-  if (some <= kList) {
-    // Few: to the first CTA, in the order of their indexes. A warp takes a run of tokens.
-    const int run = ((count + kWarps - 1) / kWarps + 31) / 32 * 32, i0 = min(count, warp * run), i1 = min(count, i0 + run);
-    auto may = [&](int i) {
-      if (i >= i1) return false;
-      const float l = at(i);
-      float frac;
-      return l != -INFINITY && (l == M || bin_at(l, frac) <= last);
-    };
-    uint32_t mine = 0;
-    for (int i = i0; i < i1; i += 32) mine += __popc(__ballot_sync(0xffffffffu, may(i + lane)));
-    uint64_t to;
-    const uint64_t there = team.sum(lane == 0 ? mine : 0, &to);
-    to += sum_before<uint64_t>(lane == 0 ? mine : 0, part);
-    to = __shfl_sync(0xffffffffu, to, 0);
-    const uint32_t list0 = mapa_shared(list, 0), at0 = mapa_shared(list_at, 0);
+  if (c <= goal && goal < c + of_warp) {
+    seen = ties;
     for (int i = i0; i < i1; i += 32) {
-      const bool m = may(i + lane);
-      const uint32_t b = __ballot_sync(0xffffffffu, m);
-      if (m) {
-        const uint32_t k = static_cast<uint32_t>(to) + __popc(b & ((1u << lane) - 1));
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(list0 + 4 * k), "f"(at(i + lane)) : "memory");
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at0 + 4 * k), "r"(first + i + lane) : "memory");
+      const uint64_t v = kept(i + lane, seen);
+      uint64_t s = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
       }
-      to += __popc(b);
+      const uint32_t past = __ballot_sync(0xffffffffu, c + s > goal);
+      if (past) {
+        if (lane == __ffs(past) - 1) {
+          a.ids[n] = index ? index[i + lane] : first + i + lane;
+          if (a.probs) a.probs[n] = static_cast<float>(static_cast<double>(v) / static_cast<double>(total));
+        }
+        break;
+      }
+      c += __shfl_sync(0xffffffffu, s, 31);
     }
-    team.sync();
-    if (team.rank > 0) return;
-    Team alone = {1, 0, slots, part, hist, hist, 0};
-    const int m = static_cast<int>(there);
-    auto l_at = [&](int i) { return list[i]; };
-    auto l_each = [&](auto f) {
-      for (int i = threadIdx.x; i < m; i += kThreads) f(list[i], i);
-    };
-    uint64_t low = 0;
-    l_each([&](float l, int) { low = max(low, static_cast<uint64_t>(~key_of(l))); });
-    const uint32_t lo = ~static_cast<uint32_t>(alone.most(low));
-    const Limit limit = limits(alone, row, lo, top_key, 0, whole, l_each,
-                               [&](uint64_t, uint32_t& k, uint32_t& hi, uint64_t&) { k = max(k, lo), hi = top_key; });
-    choose(alone, a, row, n, m, limit, l_at, [&](int i) { return list_at[i]; });
-    return;
   }
-
-  // Many: the cluster goes on. The keys of bins b0 to b1 are between lo and hi.
-  auto keys_of_bins = [&](int b0, int b1, uint32_t& lo, uint32_t& hi) {
-    uint64_t low = 0, high = 0;
-    each([&](float l, int) {
-      if (l == -INFINITY) return;
-      float frac;
-      const int b = l == M ? 0 : bin_at(l, frac);
-      if (b >= b0 && b <= b1) low = max(low, static_cast<uint64_t>(~key_of(l))), high = max(high, static_cast<uint64_t>(key_of(l)));
-    });
-    lo = ~static_cast<uint32_t>(team.most(low));
-    hi = static_cast<uint32_t>(team.most(high));
-  };
-  uint32_t k_lo = 0, k_hi = 0;
-  if (row.k > 0) keys_of_bins(last, last, k_lo, k_hi);
-  const Limit limit = limits(team, row, k_lo, k_hi, k_before, whole, each, [&](uint64_t goal, uint32_t& lo, uint32_t& hi, uint64_t& above) {
-    const float g = static_cast<float>(goal) * in_units;
-    const int b0 = find(1, [&](uint32_t, float w) { return w >= g * (1.f - around); });
-    const int b1 = max(b0, find(2, [&](uint32_t, float w) { return w >= g * (1.f + around); }));
-    uint32_t w_lo, w_hi;
-    keys_of_bins(b0, b1, w_lo, w_hi);
-    // Tokens beyond the window, and (with top_k) those that are out of reach.
-    lo = max(lo, w_lo);
-    hi = max(lo, w_hi);
-    uint64_t mine = 0;
-    const float l_hi = value_of(hi);
-    each([&](float l, int) { mine += l > l_hi ? row.w(l) : 0; });
-    above = team.sum(mine);
-  });
-  choose(team, a, row, n, count, limit, at, index);
   team.sync();
 }
 
