@@ -7,7 +7,7 @@
 // the kept weights passes u times their total.
 //
 // A row is held in the shared memory of a cluster of CTAs. Where top_k or top_p limit it, a histogram over bins of (max l - l) / T
-// of 1/32 of an octave finds the bin that the limit falls into; the tokens that may be kept, if they are
+// of 1/16 of an octave finds the bin that the limit falls into; the tokens that may be kept, if they are
 // few, then go to one CTA, else the cluster goes on. The limit itself is found by histograms of ever
 // finer runs of the logits' bits, until one value is left; of its equals the first by index are kept.
 //
@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048, kPerThread = kBins / kThreads;
+constexpr int kBins = 1024, kPerThread = kBins / kThreads;
 constexpr int kList = 2048;                      // tokens that one CTA takes over
 constexpr int kMostCtas = 16;
 constexpr int kSliceBytes = 128 * 1024;
@@ -137,7 +137,7 @@ __device__ __forceinline__ void store_cluster(uint32_t addr, uint64_t v) {
 // What the CTAs that work on a row share: the row's cluster, or (ctas = 1) one CTA.
 struct Team {
   int ctas, rank;
-  uint64_t* slots;           // [2]: what this CTA tells the others, in turn
+  uint64_t* slots;           // [2]: what this CTA tells the others, in turn; [2], [3]: and with its histogram
   uint64_t* part;            // [kWarps + 2]
   uint64_t* hist;            // [kBins], this CTA's
   uint64_t* all;             // [kBins], the team's
@@ -189,6 +189,31 @@ struct Team {
   }
   __device__ __forceinline__ uint64_t most(uint64_t v) {
     return reduce(v, [](uint64_t a, uint64_t b) { return max(a, b); }, 0);
+  }
+
+  // This CTA's sum, told to the others with its next histogram (word 0 or 1), and the team's once that is gathered.
+  __device__ __forceinline__ void tell(uint64_t v, int word) const {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      v = part[0];
+      for (int w = 1; w < kWarps; ++w) v += part[w];
+      slots[2 + word] = v;
+    }
+  }
+  __device__ __forceinline__ uint64_t told(int word, uint64_t* before = nullptr) const {
+    const int lane = threadIdx.x & 31;
+    uint64_t v = lane < ctas ? load_cluster(mapa_shared(slots + 2 + word, lane)) : 0, b = lane < rank ? v : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      v += __shfl_xor_sync(0xffffffffu, v, o);
+      b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if (before) *before = b;
+    return v;
   }
 
   __device__ __forceinline__ void clear() const {
@@ -250,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint32_t table[256];
   __shared__ float per_T[2];
-  __shared__ uint64_t least, slots[2], part[kWarps + 2], goal_of, found_above;
+  __shared__ uint64_t least, slots[4], part[kWarps + 2], goal_of, found_above;
   __shared__ float partf[kWarps];
   __shared__ int bin_of, found;
   __shared__ uint32_t tokens_at, tokens_to, available;
@@ -327,9 +352,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   // The limit: keys above limit_key are within it, and the first `extra`, by index, of the tokens with that key.
   uint32_t limit_key = kNone + 1, extra = kAll;
   if (row.k > 0 || row.p < 1.f) {
-    // Histogram by bins of (M - l) log2(e) / T of 1/32: tokens (low words) and, with top_p, weights relative to the bin's largest
+    // Histogram by bins of (M - l) log2(e) / T of 1/16: tokens (low words) and, with top_p, weights relative to the bin's largest
     // possible, in 2^-15 (high words; those of the last bin are below 2^-63). Without top_k the exact weight of all.
-    const float scale = 32.f * 1.44269504f / T0;
+    const float scale = 16.f * 1.44269504f / T0;
     auto bin_at = [&](float l, float& frac) {
       const float d = l == M ? 0.f : fminf(__fsub_rn(M, l) * scale, static_cast<float>(kBins - 1));   // (a NaN: the last)
       const float t = __fadd_rd(d, 8388608.f);                 // the whole number below d in its low bits
@@ -345,19 +370,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
       uint32_t* h = reinterpret_cast<uint32_t*>(hist + bin_at(l, frac));
       add_shared(h, 1u);
       if (by_weight) {
-        const float w = exp2_fast(frac * -0.03125f);
+        const float w = exp2_fast(frac * -0.0625f);
         add_shared(h + 1, static_cast<uint32_t>(__float_as_int(__fmaf_rn(w, 32768.f, kWhole)) - kWholeBits));
         if (row.k == 0) whole += row.w(l);
       }
     });
-    if (by_weight && row.k == 0) whole = team.sum(whole);
-    // Over the cluster: tokens (low words) and weights as fp32 (high words), the latter times 2^(-b / 32) below.
+    if (by_weight && row.k == 0) team.tell(whole, 0);
+    // Over the cluster: tokens (low words) and weights as fp32 (high words), the latter times 2^(-b / 16) below.
     const auto as_float = [](uint64_t h) { return (h & 0xffffffffu) | static_cast<uint64_t>(__float_as_uint(static_cast<float>(h >> 32))) << 32; };
     const uint64_t* all = team.gather([&](uint64_t v, uint64_t h) {
       h = as_float(h);
       const float w = __uint_as_float(static_cast<uint32_t>(v >> 32)) + __uint_as_float(static_cast<uint32_t>(h >> 32));
       return ((v & 0xffffffffu) + (h & 0xffffffffu)) | static_cast<uint64_t>(__float_as_uint(w)) << 32;
     });
+    if (by_weight && row.k == 0) whole = team.told(0);
     // Tokens and weights up to each bin.
     uint32_t tokens_to_bin[kPerThread], tokens_sum = 0;
     float weight_to_bin[kPerThread], weight_sum = 0.f;
@@ -367,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
       const uint64_t h = team.ctas == 1 ? as_float(all[b]) : all[b];
       tokens_to_bin[i] = tokens_sum += static_cast<uint32_t>(h);
       weight_to_bin[i] = weight_sum +=
-          b < kBins - 1 ? __uint_as_float(static_cast<uint32_t>(h >> 32)) * exp2_fast(b * -0.03125f) * 0x1p-15f : 0.f;
+          b < kBins - 1 ? __uint_as_float(static_cast<uint32_t>(h >> 32)) * exp2_fast(b * -0.0625f) * 0x1p-15f : 0.f;
     }
     const uint32_t tokens_before = static_cast<uint32_t>(sum_before<uint64_t>(tokens_sum, part));
     const float weight_before = sum_before<float>(weight_sum, partf);
@@ -422,12 +448,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
       }
       return hi;
     };
-    uint32_t lo = least_key(last), hi = top_key;
-    uint64_t above = 0;
+    // The k-th token is in that bin.
+    uint32_t lo = least_key(last), hi = row.k > 0 && last > 0 ? least_key(last - 1) - 1 : top_key;
+    uint64_t above = row.k > 0 ? k_before : 0;
+    const float least_kept = value_of(lo);
 
     if (some <= kList) {
       // Few: to the first CTA, in the order of their indexes. A warp takes a run of tokens.
-      const float least_kept = value_of(lo);
       const int run = ((count + kWarps - 1) / kWarps + 31) / 32 * 32, i0 = min(count, warp * run), i1 = min(count, i0 + run);
       uint32_t mine = 0;
 #pragma unroll 4
@@ -459,16 +486,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
       tokens = list;
       index = list_at;
       count = there;
-    } else if (row.k > 0) {  // Many: the cluster goes on, within the bin of the k-th token
-      hi = last > 0 ? least_key(last - 1) - 1 : top_key;
-      above = k_before;
-    }
+    }                        // Many: the cluster goes on
 
     // The limits one after the other: the largest key at which the sum of tokens, or of weights, over the keys from the largest
     // down reaches its goal. The sum is by histograms of runs of keys in [lo, hi], `above` that of the keys beyond hi.
 #pragma unroll 1
     for (int what = row.k > 0 ? 0 : 1; what < (by_weight ? 2 : 1); ++what) {
       uint64_t goal = row.k;
+      bool beyond_told = false;
       if (what == 1) {
         const float edge = value_of(limit_key);
         if (row.k > 0) {
@@ -482,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         }
         __syncthreads();
         goal = goal_of;
-        lo = max(lo, limit_key);
+        lo = max(least_key(last), limit_key);
         hi = top_key;
         above = 0;
         if (team.ctas > 1) {
@@ -494,12 +519,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
           const float beyond = value_of(hi);
           uint64_t mine = 0;
           each([&](float l, int) { mine += l > beyond ? row.w(l) : 0; });
-          above = team.sum(mine);
+          team.tell(mine, 1);
+          beyond_told = true;
         }
       }
       for (;;) {
         const uint32_t span = hi - lo;
-        const int s = span < kBins ? 0 : 21 - __clz(span);
+        const int s = span < kBins ? 0 : 22 - __clz(span);
         team.clear();
         const float l_lo = value_of(lo), l_hi = value_of(hi);
         each([&](float l, int) {
@@ -511,6 +537,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         });
         if (threadIdx.x == 0) found = -1;
         const uint64_t* h = team.gather([](uint64_t v, uint64_t w) { return v + w; });
+        if (beyond_told) above = team.told(1), beyond_told = false;
         uint64_t bin[kPerThread], mine = 0;
 #pragma unroll
         for (int i = 0; i < kPerThread; ++i) mine += bin[i] = h[kPerThread * threadIdx.x + i];
@@ -551,38 +578,49 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   // The choice. A warp has a run of tokens, 32 at a time.
   const int run = ((count + kWarps - 1) / kWarps + 31) / 32 * 32, i0 = min(count, warp * run), i1 = min(count, i0 + run);
   const float edge = value_of(limit_key);
-  uint64_t ties = 0;                             // with the limit's key, before this warp's
-  if (extra != kAll) {
-    uint32_t same = 0;
-#pragma unroll 4
-    for (int i = i0 + lane; i < i1; i += 32) same += at(i) == edge;
-    uint64_t before;
-    team.sum(same, &before);
-    same = __reduce_add_sync(0xffffffffu, same);
-    ties = before + sum_before<uint64_t>(lane == 0 ? same : 0, part);
-    ties = __shfl_sync(0xffffffffu, ties, 0);
+  // This CTA's tokens with the limit's key, of which those after the first `extra` of the row are not kept, and the weight of the
+  // others that are: told to the other CTAs at once. A weight with the limit's key is `one`.
+  const uint64_t of_edge = extra != kAll ? row.w(edge) : 0, one = of_edge >= row.least ? of_edge : 0;
+  uint32_t same = 0;
+  uint64_t mine = 0;
+#pragma unroll 2
+  for (int i = i0 + lane; i < i1; i += 32) {
+    const float l = at(i);
+    if (extra != kAll && l == edge) {
+      ++same;
+    } else if (l >= edge) {
+      const uint64_t v = row.w(l);
+      mine += v >= row.least ? v : 0;
+    }
   }
+  same = __reduce_add_sync(0xffffffffu, same);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  team.tell(lane == 0 ? same : 0, 0);
+  team.tell(lane == 0 ? mine : 0, 1);
+  team.sync();
+  uint64_t ties, c;
+  const uint64_t all_same = team.told(0, &ties), all_above = team.told(1, &c), limit = extra;
+  const uint64_t total = all_above + min(all_same, limit) * one;
+  c += min(ties, limit) * one;                   // of the CTAs before this one
+  ties += sum_before<uint64_t>(lane == 0 ? same : 0, part);
+  ties = __shfl_sync(0xffffffffu, ties, 0);
+  const uint64_t kept_ties = min(ties + same, limit) - min(ties, limit), of_warp = mine + kept_ties * one;
+  c += sum_before<uint64_t>(lane == 0 ? of_warp : 0, part);
+  c = __shfl_sync(0xffffffffu, c, 0);
   // The weight of token i if it is kept; seen: tokens with the limit's key so far. All lanes of the warp call it.
   auto kept = [&](int i, uint64_t& seen) -> uint64_t {
     const float l = i < i1 ? at(i) : -INFINITY;
-    bool in = l >= edge;
     if (extra != kAll) {
       const uint32_t equal = __ballot_sync(0xffffffffu, l == edge);
-      if (l == edge) in = seen + __popc(equal & ((1u << lane) - 1)) < extra;
+      const bool in = seen + __popc(equal & ((1u << lane) - 1)) < limit;
       seen += __popc(equal);
+      if (l == edge) return in ? one : 0;
     }
-    if (!in) return 0;
+    if (!(l >= edge)) return 0;
     const uint64_t v = row.w(l);
     return v >= row.least ? v : 0;
   };
-  uint64_t mine = 0, seen = ties, before;
-  for (int i = i0; i < i1; i += 32) mine += kept(i + lane, seen);
-  uint64_t of_warp = mine;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) of_warp += __shfl_xor_sync(0xffffffffu, of_warp, o);
-  const uint64_t total = team.sum(mine, &before);
-  uint64_t c = before + sum_before<uint64_t>(lane == 0 ? of_warp : 0, part);
-  c = __shfl_sync(0xffffffffu, c, 0);
   // The first sum above u * total: at least floor(u * total) + 1, and at most all of it.
   if (threadIdx.x == 0) {
     const uint64_t goal = row.u > 0.f ? static_cast<uint64_t>(static_cast<double>(row.u) * static_cast<double>(total)) : 0;
@@ -591,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   __syncthreads();
   const uint64_t goal = goal_of;
   if (c <= goal && goal < c + of_warp) {
-    seen = ties;
+    uint64_t seen = ties;
     for (int i = i0; i < i1; i += 32) {
       const uint64_t v = kept(i + lane, seen);
       uint64_t s = v;
