@@ -575,12 +575,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     }
   }
 
+  // min_p as a least key, where it is beyond the limit: by 32 tries at a time, every warp for itself.
+  if (row.least > 0) {
+    uint32_t lo = kNone, hi = top_key;
+    while (hi - lo > 1) {
+      const uint32_t step = (hi - lo + 31) / 32;
+      const int i = __ffs(__ballot_sync(0xffffffffu, row.w(value_of(min(lo + step * (lane + 1), hi))) >= row.least)) - 1;
+      hi = min(lo + step * (i + 1), hi);
+      lo = lo + step * i;
+    }
+    if (hi > limit_key) limit_key = hi, extra = kAll;
+  }
+
   // The choice. A warp has a run of tokens, 32 at a time.
   const int run = ((count + kWarps - 1) / kWarps + 31) / 32 * 32, i0 = min(count, warp * run), i1 = min(count, i0 + run);
   const float edge = value_of(limit_key);
   // This CTA's tokens with the limit's key, of which those after the first `extra` of the row are not kept, and the weight of the
   // others that are: told to the other CTAs at once. A weight with the limit's key is `one`.
-  const uint64_t of_edge = extra != kAll ? row.w(edge) : 0, one = of_edge >= row.least ? of_edge : 0;
+  const uint64_t one = extra != kAll ? row.w(edge) : 0;
   uint32_t same = 0;
   uint64_t mine = 0;
 #pragma unroll 2
@@ -589,8 +601,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     if (extra != kAll && l == edge) {
       ++same;
     } else if (l >= edge) {
-      const uint64_t v = row.w(l);
-      mine += v >= row.least ? v : 0;
+      mine += row.w(l);
     }
   }
   same = __reduce_add_sync(0xffffffffu, same);
@@ -617,9 +628,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
       seen += __popc(equal);
       if (l == edge) return in ? one : 0;
     }
-    if (!(l >= edge)) return 0;
-    const uint64_t v = row.w(l);
-    return v >= row.least ? v : 0;
+    return l >= edge ? row.w(l) : 0;
   };
   // The first sum above u * total: at least floor(u * total) + 1, and at most all of it.
   if (threadIdx.x == 0) {
@@ -654,9 +663,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
 
 template <typename T>
 cudaError_t sample(const SampleArgs& a, int num_sms, cudaStream_t s) {
-  // CTAs of a row: enough to hold it by halves of an SM's shared memory, and as many as leave 2048 tokens each while all rows' run
-  // at once, two to an SM.
-  constexpr int kMost = kSliceBytes / 2 / sizeof(T);
+  // CTAs of a row: enough to hold it with two on an SM (80 KB of logits each; with 64 KB, and so eight CTAs for 152064 of 16
+  // bits, 64 rows with top-k and top-p took 73 us against 58), and as many as leave 2048 tokens each while all
+  // rows' run at once.
+  constexpr int kMost = 80 * 1024 / sizeof(T);
   int ctas = 1;
   while (ctas < kMostCtas && (a.V > static_cast<int64_t>(ctas) * kMost ||
                               (a.V >= 4096 * static_cast<int64_t>(ctas) && a.N * ctas <= num_sms)))
