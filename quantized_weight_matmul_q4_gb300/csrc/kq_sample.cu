@@ -138,7 +138,7 @@ __device__ __forceinline__ void store_cluster(uint32_t addr, uint64_t v) {
 struct Team {
   int ctas, rank;
   uint64_t* slots;           // [2]: what this CTA tells the others, in turn; [2], [3]: and with its histogram
-  uint64_t* part;            // [kWarps + 2]
+  uint64_t* part;            // [2 * kWarps]
   uint64_t* hist;            // [kBins], this CTA's
   uint64_t* all;             // [kBins], the team's
   int turn;
@@ -191,17 +191,23 @@ struct Team {
     return reduce(v, [](uint64_t a, uint64_t b) { return max(a, b); }, 0);
   }
 
-  // This CTA's sum, told to the others with its next histogram (word 0 or 1), and the team's once that is gathered.
-  __device__ __forceinline__ void tell(uint64_t v, int word) const {
+  // This CTA's sums, told to the others with its next histogram or sync, and the team's once that is done.
+  __device__ __forceinline__ void tell(uint64_t v, uint64_t w) const {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = 16; o > 0; o >>= 1) {
+      v += __shfl_xor_sync(0xffffffffu, v, o);
+      w += __shfl_xor_sync(0xffffffffu, w, o);
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    if (lane == 0) part[warp] = v, part[kWarps + warp] = w;
     __syncthreads();
-    if (threadIdx.x == 0) {
-      v = part[0];
-      for (int w = 1; w < kWarps; ++w) v += part[w];
-      slots[2 + word] = v;
+    if (threadIdx.x < 32) {
+      static_assert(2 * kWarps == 32, "two words of a lane half each");
+      v = part[lane];
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if ((lane & 15) == 0) slots[2 + (lane >> 4)] = v;
     }
   }
   __device__ __forceinline__ uint64_t told(int word, uint64_t* before = nullptr) const {
@@ -241,6 +247,20 @@ __device__ __forceinline__ void add_shared(void* p, uint32_t v) {
   asm volatile("red.shared::cta.add.u32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
 }
 
+// f * v rounded down or up, for 0 < f < 1: f is m * 2^-s with a 24-bit m.
+__device__ __forceinline__ uint64_t share_of(float f, uint64_t v, bool up) {
+  const uint32_t bits = __float_as_uint(f), e = bits >> 23;
+  const uint64_t m = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
+  const int s = 150 - static_cast<int>(e ? e : 1);               // 24 at least
+  uint64_t lo = m * v, hi = __umul64hi(m, v);                  // hi is below 2^24
+  if (up) {                                                     // + 2^s - 1
+    const uint64_t a_lo = s < 64 ? (uint64_t(1) << s) - 1 : ~uint64_t(0), a_hi = s <= 64 ? 0 : s < 128 ? (uint64_t(1) << (s - 64)) - 1 : ~uint64_t(0) >> 1;
+    lo += a_lo;
+    hi += a_hi + (lo < a_lo);
+  }
+  return s < 64 ? lo >> s | hi << (64 - s) : s < 128 ? hi >> (s - 64) : up && m != 0;
+}
+
 // The sum of v over the threads before this one.
 template <typename V>
 __device__ __forceinline__ V sum_before(V v, V* part) {
@@ -260,6 +280,29 @@ __device__ __forceinline__ V sum_before(V v, V* part) {
   return s + x - v;
 }
 
+// The first key up to top at which `in` is true (it is at top, and at all keys from the first on), by 32 tries at a time; guess and
+// around: where it most likely is. Every warp finds it for itself.
+template <typename In>
+__device__ __forceinline__ uint32_t first_key(uint32_t top, float guess, float around, In in) {
+  const int lane = threadIdx.x & 31;
+  uint32_t lo = kNone, hi = top;                 // the key is in (lo, hi]
+  const uint32_t g_lo = guess > -INFINITY ? key_of(guess - around) : kNone, g_hi = guess > -INFINITY ? key_of(guess + around) : top;
+  // Lane 0 tries the lower end of the guess, the others the upper.
+  const uint32_t at = lane == 0 ? g_lo : g_hi;
+  const uint32_t tried = __ballot_sync(0xffffffffu, at > kNone && at < top && in(at));
+  if (tried & 1) hi = g_lo;
+  else if (g_lo > kNone && g_lo < top) lo = g_lo;
+  if (!(tried & 1) && (tried & 2)) hi = g_hi;
+  else if (!(tried & 2) && g_hi > lo && g_hi < top) lo = g_hi;
+  while (hi - lo > 1) {
+    const uint32_t step = (hi - lo + 31) / 32;
+    const int i = __ffs(__ballot_sync(0xffffffffu, in(min(lo + step * (lane + 1), hi)))) - 1;      // (hi is among the tries)
+    hi = min(lo + step * (i + 1), hi);
+    lo = lo + step * i;
+  }
+  return hi;
+}
+
 struct Row {
   uint32_t k;                // 0: no limit
   float p;                   // 1: none
@@ -275,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint32_t table[256];
   __shared__ float per_T[2];
-  __shared__ uint64_t least, slots[4], part[kWarps + 2], goal_of, found_above;
+  __shared__ uint64_t least, slots[4], part[2 * kWarps], found_above;
   __shared__ float partf[kWarps];
   __shared__ int bin_of, found;
   __shared__ uint32_t tokens_at, tokens_to, available;
@@ -435,18 +478,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     }
     if (row.k == 0 && by_weight) last = find(0, row.p * (static_cast<float>(whole) * in_units) * (1.f + around));
     const uint32_t some = tokens_to, k_before = tokens_at;
-    // The least key whose bin is b or an earlier one, by 32 tries at a time. Every warp finds it for itself.
+    // The least key whose bin is b or an earlier one: near M - (b + 1) / scale.
     auto least_key = [&](int b) {
-      uint32_t lo = kNone, hi = top_key;         // the key is in (lo, hi]
-      while (hi - lo > 1) {
-        const uint32_t step = (hi - lo + 31) / 32, at = min(lo + step * (lane + 1), hi);
+      const float frac_at = static_cast<float>(b + 1) / scale;
+      return first_key(top_key, M - frac_at, 0x1p-20f * (fabsf(M) + frac_at), [&](uint32_t k) {
         float frac;
-        const uint32_t in = __ballot_sync(0xffffffffu, bin_at(value_of(at), frac) <= b);
-        const int i = __ffs(in) - 1;             // (hi is among the tries)
-        hi = min(lo + step * (i + 1), hi);
-        lo = lo + step * i;
-      }
-      return hi;
+        return bin_at(value_of(k), frac) <= b;
+      });
     };
     // The k-th token is in that bin.
     uint32_t lo = least_key(last), hi = row.k > 0 && last > 0 ? least_key(last - 1) - 1 : top_key;
@@ -501,12 +539,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
           each([&](float l, int) { mine += l > edge ? row.w(l) : 0; });
           whole = team.sum(mine) + extra * row.w(edge);
         }
-        if (threadIdx.x == 0) {                  // the least sum that is enough
-          const double g = static_cast<double>(row.p) * static_cast<double>(whole);
-          goal_of = g > 1.0 ? static_cast<uint64_t>(ceil(g)) : 1;
-        }
-        __syncthreads();
-        goal = goal_of;
+        goal = row.p > 0.f ? max(share_of(row.p, whole, true), static_cast<uint64_t>(1)) : 1;      // the least sum that is enough
         lo = max(least_key(last), limit_key);
         hi = top_key;
         above = 0;
@@ -519,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
           const float beyond = value_of(hi);
           uint64_t mine = 0;
           each([&](float l, int) { mine += l > beyond ? row.w(l) : 0; });
-          team.tell(mine, 1);
+          team.tell(0, mine);
           beyond_told = true;
         }
       }
@@ -575,16 +608,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     }
   }
 
-  // min_p as a least key, where it is beyond the limit: by 32 tries at a time, every warp for itself.
+  // min_p as a least key, where it is beyond the limit.
   if (row.least > 0) {
-    uint32_t lo = kNone, hi = top_key;
-    while (hi - lo > 1) {
-      const uint32_t step = (hi - lo + 31) / 32;
-      const int i = __ffs(__ballot_sync(0xffffffffu, row.w(value_of(min(lo + step * (lane + 1), hi))) >= row.least)) - 1;
-      hi = min(lo + step * (i + 1), hi);
-      lo = lo + step * i;
-    }
-    if (hi > limit_key) limit_key = hi, extra = kAll;
+    const float below = -logf(fminf(min_p, 1.f)) * T0;
+    const uint32_t least_kept = first_key(top_key, M - below, 0x1p-20f * (fabsf(M) + below), [&](uint32_t k) { return row.w(value_of(k)) >= row.least; });
+    if (least_kept > limit_key) limit_key = least_kept, extra = kAll;
   }
 
   // The choice. A warp has a run of tokens, 32 at a time.
@@ -607,8 +635,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   same = __reduce_add_sync(0xffffffffu, same);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  team.tell(lane == 0 ? same : 0, 0);
-  team.tell(lane == 0 ? mine : 0, 1);
+  team.tell(lane == 0 ? same : 0, lane == 0 ? mine : 0);
   team.sync();
   uint64_t ties, c;
   const uint64_t all_same = team.told(0, &ties), all_above = team.told(1, &c), limit = extra;
@@ -631,12 +658,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     return l >= edge ? row.w(l) : 0;
   };
   // The first sum above u * total: at least floor(u * total) + 1, and at most all of it.
-  if (threadIdx.x == 0) {
-    const uint64_t goal = row.u > 0.f ? static_cast<uint64_t>(static_cast<double>(row.u) * static_cast<double>(total)) : 0;
-    goal_of = min(goal, total - 1);
-  }
-  __syncthreads();
-  const uint64_t goal = goal_of;
+  const uint64_t goal = min(row.u >= 1.f ? total : row.u > 0.f ? share_of(row.u, total, false) : 0, total - 1);
   if (c <= goal && goal < c + of_warp) {
     uint64_t seen = ties;
     for (int i = i0; i < i1; i += 32) {
