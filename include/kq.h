@@ -415,8 +415,8 @@ KQ_API kq_status kq_moe_matvec_g4(const void* W, const void* scales, int scale_d
  *   of the first rot_dim elements; the others stay. cos_sin NULL: no rotation.
  * cos_sin: fp32 [n_positions][rot_dim], a position's rot_dim / 2 cosines, then their sines.
  * positions: int32 [N], or NULL (row n is at position n). A row with a negative position
- * is passed over: nothing is read or written for it. So is one whose position is not
- * in the table, and KQ_DEVERR_POSITION is recorded.
+ * is passed over: nothing is written for it. So is one whose position is not in the
+ * table, and KQ_DEVERR_POSITION is recorded.
  * Q: dtype [N][n_q_heads * head_dim]; K likewise with n_k_heads, NULL where that is 0;
  * Qo, Ko: out_dtype, written; out_dtype is dtype, or any for fp32 inputs. Qo may be Q and
  * Ko K (the same pointer, ld and type); outputs overlap nothing else. q_gamma, k_gamma:

@@ -9,6 +9,7 @@ inline bool aligned(const void* p, unsigned to) { return (reinterpret_cast<uintp
 inline bool aligned16(const void* p) { return aligned(p, 16); }
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxValues = int64_t(1) << 38;
+constexpr int64_t kMaxHeads = int64_t(1) << 30;
 
 kq_status finish(cudaError_t e) { return e == cudaSuccess ? KQ_OK : KQ_ERR_CUDA; }
 
@@ -58,7 +59,7 @@ kq_status kq_qk_norm_rope(int dtype, const void* Q, int64_t ldq, int32_t n_q_hea
   if (!valid_dtype(dtype) || !valid_dtype(out_dtype) || (dtype != KQ_F32 && out_dtype != dtype)) return KQ_ERR_TYPE;
   if (!Q || !Qo || (n_k_heads > 0 && (!K || !Ko))) return KQ_ERR_NULL;
   if (n_q_heads <= 0 || n_q_heads > 65536 || n_k_heads < 0 || n_k_heads > 65536 || head_dim < 16 || head_dim > 256 ||
-      head_dim % 16 != 0 || !valid_size(N) || N * (n_q_heads + n_k_heads) * head_dim > kMaxValues ||
+      head_dim % 16 != 0 || !valid_size(N) || N * (n_q_heads + n_k_heads) > kMaxHeads ||
       !(eps >= 0.f && eps < 1e30f))  // also rejects NaN
     return KQ_ERR_SHAPE;
   const int64_t q = static_cast<int64_t>(n_q_heads) * head_dim, k = static_cast<int64_t>(n_k_heads) * head_dim;
@@ -88,7 +89,7 @@ kq_status kq_kv_append_q4(int dtype, const void* K, int64_t ldk, const void* V, 
   kq_status st = cache_of(cache, n_pages, page_size, n_heads, head_dim, block_table, ldt, n_seqs, &c);
   if (st != KQ_OK) return st;
   const int64_t row = static_cast<int64_t>(n_heads) * head_dim;
-  if (!valid_size(N) || 2 * N * row > kMaxValues || !valid_ld_in(ldk, row) || !valid_ld_in(ldv, row) ||
+  if (!valid_size(N) || 2 * N * n_heads > kMaxHeads || !valid_ld_in(ldk, row) || !valid_ld_in(ldv, row) ||
       (!seq_ids && N > n_seqs))
     return KQ_ERR_SHAPE;
   Rope rope;
@@ -114,7 +115,7 @@ kq_status kq_kv_gather_q4(const void* cache, int64_t n_pages, int32_t page_size,
   const kq_status st = cache_of(cache, n_pages, page_size, n_heads, head_dim, block_table, ldt, n_seqs, &c);
   if (st != KQ_OK) return st;
   const int64_t row = static_cast<int64_t>(n_heads) * head_dim;
-  if (!valid_size(N) || 2 * N * row > kMaxValues || !valid_ld_out(ldk, row) || !valid_ld_out(ldv, row) ||
+  if (!valid_size(N) || 2 * N * n_heads > kMaxHeads || !valid_ld_out(ldk, row) || !valid_ld_out(ldv, row) ||
       (!seq_ids && N > n_seqs))
     return KQ_ERR_SHAPE;
   if (!aligned16(K) || !aligned16(V) || !aligned(positions, 4) || !aligned(seq_ids, 4) || !cache_aligned(c))
