@@ -119,15 +119,16 @@ def read(cache, table_row, page_size, places):
 
 
 def attention(Q, cache, table, page_size, kv_len, q_start=None, scale=None, window=0):
-    """(o, E, S) for queries Q [N, Hq, D]: the output in fp64; E = Sum_t p_t (|s_t| c_t + |m_t|) per element (what
-    rounding errors of p scale with); S [N, Hq] = the largest over t of scale * Sum (|s| c + |m|) |q| (what those of
+    """(o, E, S) for queries Q [N, Hq, D]: the output in fp64; E [2, N, Hq, D] = Sum_t p_t (|s_t| |c_t - 8| + |m_t + 8 s_t|)
+    and Sum_t p_t (|s_t| c_t + |m_t|) per element (what rounding errors of the weights scale with where the codes are taken from
+    their middle, and those of sums of codes as they are); S [N, Hq] = the largest over t of scale * Sum (|s| c + |m|) |q| (what those of
     the scores scale with). Rows of no sequence are NaN."""
     Q = np.asarray(Q, np.float64)
     N, Hq, D = Q.shape
     H = cache.shape[1]
     group = Hq // H
     scale = D ** -0.5 if scale is None else scale
-    o, E, S = np.full((N, Hq, D), np.nan), np.zeros((N, Hq, D)), np.zeros((N, Hq))
+    o, E, S = np.full((N, Hq, D), np.nan), np.zeros((2, N, Hq, D)), np.zeros((N, Hq))
     for b in range(len(kv_len)):
         n0, n1 = (b, b + 1) if q_start is None else (int(q_start[b]), int(q_start[b + 1]))
         if n1 <= n0:
@@ -137,6 +138,7 @@ def attention(Q, cache, table, page_size, kv_len, q_start=None, scale=None, wind
         flat = lambda s, m, c: (m[..., None] + s[..., None] * c).reshape(L, H, D)  # noqa: E731
         k, v = flat(ks, km, kc), flat(vs, vm, vc)
         ka, va = flat(np.abs(ks), np.abs(km), kc), flat(np.abs(vs), np.abs(vm), vc)
+        vd = flat(np.abs(vs), np.abs(vm + 8 * vs), np.abs(vc - 8))
         for n in range(n0, n1):
             end = L - (n1 - n0) + 1 + (n - n0)
             begin = max(0, end - window) if window else 0
@@ -150,7 +152,7 @@ def attention(Q, cache, table, page_size, kv_len, q_start=None, scale=None, wind
                 p = np.exp(x - x.max())
                 p /= p.sum()
                 o[n, i] = p @ v[begin:end, h]
-                E[n, i] = p @ va[begin:end, h]
+                E[0, n, i], E[1, n, i] = p @ vd[begin:end, h], p @ va[begin:end, h]
     return o, E, S
 
 

@@ -9,14 +9,18 @@
 // bits in the low bits of an fp16 are the exact number c * 2^-24 (c * 2^-20 four bits higher), so
 // a word of eight codes becomes four operand registers by masks and one shift. With blocks g of 32 elements,
 //   q . k_t = Sum_g s_tg (c_tg . q_g) + Sum_g m_tg Sum(q_g)
-//   o       = Sum_g Sum_t (p_t s_tg) c_tg + Sum_t p_t m_tg
-// The first sum of each is a product of codes per block, scaled after (scores) or before (weights);
-// the second is one more product, of the m themselves, which also gives Sum_t p_t by a row of ones.
+//   o       = Sum_g Sum_t (p_t s_tg) (c_tg - 8) + Sum_t p_t (m_tg + 8 s_tg)
+// The first sum of each is a product of codes per block, scaled after (scores) or before (weights). Without the 8 both sums of
+// o are many times as large as their difference where many tokens count, and the tensor cores' additions, which cut
+// off, would show (8192 tokens: 1.8e-3 of o); it is one more product, with a constant operand. The second
+// sum is a product of the m + 8 s, which also gives Sum_t p_t by a row of ones; it is taken for each step by itself and
+// added in fp32.
 //
 // Scores are exact products summed in fp32. Weights are rounded to fp16 as operands (a relative 2^-12 each time,
-// twice for those of the codes, which 16-bit outputs do not show; fp32 rows have theirs split into two
-// halves, as their queries are); they are taken relative to a power of two not below the largest s so
-// far, so that none leaves fp16's range.
+// twice for those of the codes, which 16-bit outputs do not show). For fp32 rows, and where Q8_1 rows are asked for (a code
+// that a rounding moves is a whole step), weights are split into two halves, the codes are operands less 8, and sums of a granule
+// are added in fp32; fp32 queries are split as well. Weights are relative to a power of two not below the largest s so far, so that none
+// leaves fp16's range.
 //
 // Work is shared out evenly whatever the sequences' lengths: all (sequence, key head, tile of rows) segments stand
 // in one line, of which each warp takes an equal run. Where segments are few and short, the line is of pieces of so many steps of
@@ -77,6 +81,12 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
+}
+// The codes in bits AT to AT + 3 of both halves less 8, as fp16: in the low bits of 1024 or of 64 they add their value.
+template <int AT>
+__device__ __forceinline__ uint32_t codes_less_8(uint32_t w) {
+  const uint32_t x = AT ? (w & 0x00f000f0u) | 0x54005400u : (w & 0x000f000fu) | 0x64006400u;
+  return half2_bits(__hsub2(bits_half2(x), __float2half2_rn(AT ? 72.f : 1032.f)));
 }
 // Two 8 x 8 matrices of fp16 from shared memory, transposed: lanes 0..7 give the rows of the first, 8..15 of the second.
 __device__ __forceinline__ void load_transposed(uint32_t& x, uint32_t& y, const void* row) {
@@ -154,11 +164,11 @@ __device__ __forceinline__ void store_row(const Attn& p, bool here, int64_t n, i
   if (p.a.Xq) store_q8_block(v, p.a.Xq + ((n * p.a.n_q + hq) * (D / 32) + (lane8 >> 2)) * Q8_1_BYTES, here);
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, bool FINE>
 struct Shape {
   static constexpr int R = 8 * NT;
-  static constexpr bool kSplit = sizeof(T) == 4;
-  static constexpr int kWarps = D == 256 ? 7 : NT == 2 || kSplit ? 8 : 12;      // of a CTA, one to an SM
+  static constexpr bool kSplitQ = sizeof(T) == 4;                     // queries in two halves
+  static constexpr int kWarps = D == 256 ? 7 : NT == 2 || kSplitQ ? 8 : 12;     // of a CTA, one to an SM
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kStep = 2 * Granule<D>::kBytes;
   static constexpr int kPitch = D + 4;                                // of the rows of a piece's sums
@@ -177,13 +187,14 @@ struct Piece {
   bool begins, ends;
 };
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(const Attn p) {
+template <typename T, int D, int NT, bool FINE>
+__global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kernel(const Attn p) {
   using Gr = Granule<D>;
-  using Sh = Shape<T, D, NT>;
+  using Sh = Shape<T, D, NT, FINE>;
   constexpr int G = Gr::G, R = Sh::R, S = Sh::kStages, kWarps = Sh::kWarps, kThreads = Sh::kThreads, L = D / 8;
-  constexpr bool kSplit = Sh::kSplit;
+  constexpr bool kSplitQ = Sh::kSplitQ, kSplit = FINE;                // weights in two halves
   constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u;
+  constexpr uint32_t kEven = 0x80088008u, kOdd = 0x80808080u;         // -8 as the codes are: times 2^-24, times 2^-20
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t scan[kWarps], cut_b[kWarps + 1], cut_seq[kWarps + 1], cut_u[kWarps + 1], first_unit[kThreads];
   __shared__ int segment_size[kThreads];
@@ -388,7 +399,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
     // row's largest between 2^14 and 2^15 (so that fp16 and bf16 queries are exact), the odd ones
     // also times 2^-4 for the codes that are four bits higher.
     uint32_t qb[NT][G][2][2], qs[NT][(G + 3) / 4][2];
-    [[maybe_unused]] uint32_t ql[kSplit ? NT : 1][kSplit ? G : 1][2][2];
+    [[maybe_unused]] uint32_t ql[kSplitQ ? NT : 1][kSplitQ ? G : 1][2][2];
     float factor[NT][2];                                              // of the scores of columns 2 tig, 2 tig + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -422,7 +433,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
         for (int k = 0; k < 2; ++k) {
           qb[nt][g][k][0] = pack_half2(v[2 * k], v[2 * k + 4]);
           qb[nt][g][k][1] = pack_half2(v[2 * k + 1], v[2 * k + 5]);
-          if constexpr (kSplit) {
+          if constexpr (kSplitQ) {
             ql[nt][g][k][0] = pack_half2(low_part(v[2 * k]), low_part(v[2 * k + 4]));
             ql[nt][g][k][1] = pack_half2(low_part(v[2 * k + 1]), low_part(v[2 * k + 5]));
           }
@@ -504,7 +515,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
             float acc[4];
             mma_f16_zero(acc, a0, a1, a2, a3, qb[nt][g][0][0], qb[nt][g][0][1]);
             mma_f16(acc, c0, c1, c2, c3, qb[nt][g][1][0], qb[nt][g][1][1]);
-            if constexpr (kSplit) {
+            if constexpr (kSplitQ) {
               mma_f16(acc, a0, a1, a2, a3, ql[nt][g][0][0], ql[nt][g][0][1]);
               mma_f16(acc, c0, c1, c2, c3, ql[nt][g][1][0], ql[nt][g][1][1]);
             }
@@ -533,9 +544,10 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
       }
 
       // The values' parameters, two places a word, in the order of the operand's rows 2 tig, 2 tig + 1: m0 (lower eight places)
-      // and m1 (upper eight) as an operand whose rows g (4 + g for 128 elements) are the blocks' m; for rows of 16 bits also va and
+      // and m1 (upper eight) as an operand whose rows g (4 + g for 128 elements) are the blocks' m + 8 s; for rows of 16 bits also va and
       // vb, their s. fp32 rows: s of two blocks a word, of places ta and ta + 8. Places that no row of the tile sees: 0.
       uint32_t m0[2], m1[2], sizes = 0;
+      uint32_t s0[2], s1[2];                                          // the s in the places of the m
       uint32_t va[2][kSplit ? G / 2 : G], vb[2][kSplit ? G / 2 : G];
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
@@ -551,19 +563,21 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
         if constexpr (D >= 128) {
           load_transposed(m0[w], m1[w], row + (D == 256 ? 2 * G : 0));
           m0[w] &= keep0, m1[w] &= keep1;
+          uint32_t t0 = m0[w], t1 = m1[w];                            // of 128 elements: rows 0..3 of the same matrices
+          if constexpr (D == 256) {
+            load_transposed(t0, t1, row);
+            t0 &= keep0, t1 &= keep1;
+          }
           if constexpr (!kSplit) {
-            uint32_t s0 = m0[w], s1 = m1[w];                          // of 128 elements: rows 0..3 of the same matrices
-            if constexpr (D == 256) {
-              load_transposed(s0, s1, row);
-              s0 &= keep0, s1 &= keep1;
-            }
-            sizes |= s0 | s1;
+            sizes |= t0 | t1;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-              va[w][g] = __shfl_sync(0xffffffffu, s0, 4 * g + tig);
-              vb[w][g] = __shfl_sync(0xffffffffu, s1, 4 * g + tig);
+              va[w][g] = __shfl_sync(0xffffffffu, t0, 4 * g + tig);
+              vb[w][g] = __shfl_sync(0xffffffffu, t1, 4 * g + tig);
             }
           }
+          s0[w] = D == 256 ? t0 : __shfl_xor_sync(0xffffffffu, t0, 16);
+          s1[w] = D == 256 ? t1 : __shfl_xor_sync(0xffffffffu, t1, 16);
         } else {
           const auto words = [&](int place) { return *reinterpret_cast<const uint2*>(row + place * 8); };
           const uint2 x = words(0), y = words(4), z = words(8), t = words(12);
@@ -575,6 +589,12 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
           const uint32_t pick = gid == 0 ? 0x5410u : 0x7632u;
           m0[w] = gid < G ? __byte_perm(x.y, y.y, pick) & keep0 : 0u;
           m1[w] = gid < G ? __byte_perm(z.y, t.y, pick) & keep1 : 0u;
+          s0[w] = gid < G ? __byte_perm(x.x, y.x, pick) & keep0 : 0u;
+          s1[w] = gid < G ? __byte_perm(z.x, t.x, pick) & keep1 : 0u;
+        }
+        if constexpr (kEdge) {                                        // a NaN (m is 0 there) reaches rows by the codes' weights
+          s0[w] &= __heq2_mask(bits_half2(s0[w]), bits_half2(s0[w]));
+          s1[w] &= __heq2_mask(bits_half2(s1[w]), bits_half2(s1[w]));
         }
         if constexpr (kSplit) {
           const uint8_t* vp = st + w * Gr::kBytes + Gr::kValues + p_at;
@@ -653,6 +673,8 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
         shift();
       }
 
+      float os[NT][4];                                                // this step's sums of m + 8 s, and of the weights
+      const float scale_m = sigma > 0 ? 0.0625f : 0.5f;
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         // Weights, transposed as operands. Rows of 16 bits: the weights times 2^(kTop - sigma) rounded to fp16, and for each
@@ -675,12 +697,38 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
             }
           }
         }
-        // The m, and a row of ones (row 8).
+        // The m + 8 s (times 1/2, or 1/16 where s may be 2 and more: in fp16's range), and a row of ones (row 8).
+        [[maybe_unused]] uint32_t l0 = 0, l1 = 0;                     // what rounding them to fp16 leaves
+        if constexpr (kSplit) {
+          const auto both = [&](uint32_t& m, uint32_t& l, uint32_t s) {
+            const float2 a = __half22float2(bits_half2(m)), b = __half22float2(bits_half2(s));
+            const float u = fmaf(b.x, 8.f, a.x) * scale_m, v = fmaf(b.y, 8.f, a.y) * scale_m;
+            m = pack_half2(u, v);
+            l = pack_half2(low_part(u), low_part(v));
+          };
+          both(m0[w], l0, s0[w]);
+          both(m1[w], l1, s1[w]);
+        } else {
+          const __half2 eight = __float2half2_rn(8.f * scale_m), by = __float2half2_rn(scale_m);
+          m0[w] = half2_bits(__hfma2(bits_half2(s0[w]), eight, __hmul2(bits_half2(m0[w]), by)));
+          m1[w] = half2_bits(__hfma2(bits_half2(s1[w]), eight, __hmul2(bits_half2(m1[w]), by)));
+        }
         const uint32_t one = gid == 0 ? 0x3c003c00u : 0u;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_f16(om[nt], m0[w], one, m1[w], one, pw[nt][0], pw[nt][1]);
-          if constexpr (kSplit) mma_f16(om[nt], m0[w], one, m1[w], one, pl[nt][0], pl[nt][1]);
+          if (w == 0) mma_f16_zero(os[nt], m0[w], one, m1[w], one, pw[nt][0], pw[nt][1]);
+          else mma_f16(os[nt], m0[w], one, m1[w], one, pw[nt][0], pw[nt][1]);
+          if constexpr (kSplit) {
+            mma_f16(os[nt], m0[w], one, m1[w], one, pl[nt][0], pl[nt][1]);
+            mma_f16(os[nt], l0, 0u, l1, 0u, pw[nt][0], pw[nt][1]);
+          }
+          if (w == 1) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              om[nt][j] = fmaf(os[nt][j], sigma > 0 ? 16.f : 2.f, om[nt][j]);
+              om[nt][j + 2] += os[nt][j + 2];
+            }
+          }
         }
         // The values' codes: of places tig, tig + 4, tig + 8, tig + 12 four elements of each block (row gid of the operand
         // the first of them, row gid + 8 the second, and so on). A NaN of a place that a row does not see is left out.
@@ -700,8 +748,10 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
         for (int g = 0; g < G; ++g) {
           const uint32_t pick = g & 1 ? 0x7632u : 0x5410u;
           const uint32_t y = __byte_perm(cw[0][g / 2], cw[1][g / 2], pick), z = __byte_perm(cw[2][g / 2], cw[3][g / 2], pick);
-          const uint32_t a0 = y & M0, a1 = y & M1, a2 = z & M0, a3 = z & M1;
-          const uint32_t c0 = (y >> 8) & M0, c1 = (y >> 8) & M1, c2 = (z >> 8) & M0, c3 = (z >> 8) & M1;
+          const auto even = [](uint32_t w) { return kSplit ? codes_less_8<0>(w) : w & M0; };
+          const auto odd = [](uint32_t w) { return kSplit ? codes_less_8<4>(w) : w & M1; };
+          const uint32_t a0 = even(y), a1 = odd(y), a2 = even(z), a3 = odd(z);
+          const uint32_t c0 = even(y >> 8), c1 = odd(y >> 8), c2 = even(z >> 8), c3 = odd(z >> 8);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             if constexpr (kSplit) {
@@ -713,12 +763,16 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
                 for (int j = 0; j < 4; ++j) t[j] = x[w][nt][j] == 0.f ? 0.f : t[j];
               }
               const uint32_t b0 = transpose8(pack_half2(t[0], t[1])), b1 = transpose8(pack_half2(t[2], t[3]));
-              const uint32_t l0 = transpose8(pack_half2(low_part(t[0]), low_part(t[1])));
-              const uint32_t l1 = transpose8(pack_half2(low_part(t[2]), low_part(t[3])));
-              mma_f16(o[nt][g][0], a0, a1, a2, a3, b0, b1);
-              mma_f16(o[nt][g][1], c0, c1, c2, c3, b0, b1);
-              mma_f16(o[nt][g][0], a0, a1, a2, a3, l0, l1);
-              mma_f16(o[nt][g][1], c0, c1, c2, c3, l0, l1);
+              const uint32_t d0 = transpose8(pack_half2(low_part(t[0]), low_part(t[1])));
+              const uint32_t d1 = transpose8(pack_half2(low_part(t[2]), low_part(t[3])));
+              float of[2][4];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                mma_f16_zero(of[k], k ? c0 : a0, k ? c1 : a1, k ? c2 : a2, k ? c3 : a3, d0, d1);
+                mma_f16(of[k], k ? c0 : a0, k ? c1 : a1, k ? c2 : a2, k ? c3 : a3, b0, b1);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[nt][g][k][j] += of[k][j];
+              }
             } else {
               uint32_t b0 = half2_bits(__hmul2(bits_half2(pw[nt][0]), bits_half2(va[w][g])));
               uint32_t b1 = half2_bits(__hmul2(bits_half2(pw[nt][1]), bits_half2(vb[w][g])));
@@ -726,6 +780,8 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
                 b0 &= __hne2_mask(bits_half2(pw[nt][0]), __half2half2(__ushort_as_half(0)));
                 b1 &= __hne2_mask(bits_half2(pw[nt][1]), __half2half2(__ushort_as_half(0)));
               }
+              mma_f16(o[nt][g][0], kEven, kOdd, kEven, kOdd, b0, b1);
+              mma_f16(o[nt][g][1], kEven, kOdd, kEven, kOdd, b0, b1);
               mma_f16(o[nt][g][0], a0, a1, a2, a3, b0, b1);
               mma_f16(o[nt][g][1], c0, c1, c2, c3, b0, b1);
             }
@@ -771,7 +827,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
     float* sums = reinterpret_cast<float*>(ring + (first_piece ? (S - Sh::kHeld) * Sh::kStep : 0));
     float(&most_of)[R] = stat[warp][first_piece ? 0 : 1][0];
     float(&total_of)[R] = stat[warp][first_piece ? 0 : 1][1];
-    const float up = kSplit ? 0x1p24f * pow2(sigma) : 0x1p24f;
+    const float up = kSplit ? pow2(sigma) : 0x1p24f, up_odd = kSplit ? up : 0x1p20f;
     __syncwarp();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -786,8 +842,8 @@ __global__ void __launch_bounds__(Shape<T, D, NT>::kThreads) attn_q4_kernel(cons
         for (int g = 0; g < G; ++g) {
           const float m = __shfl_sync(0xffffffffu, om[nt][c], 4 * ((D == 128 ? 4 : 0) + g) + tig);
           *reinterpret_cast<float4*>(sums + r * Sh::kPitch + 32 * g + 4 * gid) =
-              make_float4(fmaf(o[nt][g][0][c], up, m), fmaf(o[nt][g][0][c + 2], up * 0.0625f, m),
-                          fmaf(o[nt][g][1][c], up, m), fmaf(o[nt][g][1][c + 2], up * 0.0625f, m));
+              make_float4(fmaf(o[nt][g][0][c], up, m), fmaf(o[nt][g][0][c + 2], up_odd, m),
+                          fmaf(o[nt][g][1][c], up, m), fmaf(o[nt][g][1][c + 2], up_odd, m));
         }
       }
     __syncwarp();
@@ -1003,30 +1059,39 @@ __global__ void __launch_bounds__(kJoinThreads) attn_q4_join_kernel(const Attn p
 // elements always 8: their sums are 128 registers for 16 rows).
 int tile_rows(int group, int D, int64_t N, int64_t n_seqs) { return D == 256 || group * N <= 8 * n_seqs ? 8 : 16; }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, bool FINE>
 cudaError_t run(const Attn& p, int num_sms, cudaStream_t s) {
-  using Sh = Shape<T, D, NT>;
+  using Sh = Shape<T, D, NT, FINE>;
   static std::atomic<uint64_t> allowed{0};                            // devices on which the shared memory is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 64 && !(allowed.load(std::memory_order_acquire) >> dev & 1)) {
-    e = cudaFuncSetAttribute(attn_q4_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+  if (dev >= 64 || !(allowed.load(std::memory_order_acquire) >> dev & 1)) {
+    e = cudaFuncSetAttribute(attn_q4_kernel<T, D, NT, FINE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
     if (e != cudaSuccess) return e;
-    allowed.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+    if (dev < 64) allowed.fetch_or(uint64_t(1) << dev, std::memory_order_release);
   }
   const int grid = num_sms;
-  e = launch_pdl(attn_q4_kernel<T, D, NT>, dim3(grid), dim3(Sh::kThreads), Sh::kSmem, s, p);
+  e = launch_pdl(attn_q4_kernel<T, D, NT, FINE>, dim3(grid), dim3(Sh::kThreads), Sh::kSmem, s, p);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_q4_join_kernel<T, D, Sh::R>, dim3(num_sms), dim3(kJoinThreads), grid * 2 * sizeof(int4), s, p, grid);
 }
 
-template <typename T>
+template <typename T, bool FINE>
 cudaError_t run(const Attn& p, int num_sms, cudaStream_t s) {
   const bool wide = tile_rows(p.group, p.c.D, p.a.N, p.c.n_seqs) == 16;
-  if (p.c.D == 64) return wide ? run<T, 64, 2>(p, num_sms, s) : run<T, 64, 1>(p, num_sms, s);
-  if (p.c.D == 128) return wide ? run<T, 128, 2>(p, num_sms, s) : run<T, 128, 1>(p, num_sms, s);
-  return run<T, 256, 1>(p, num_sms, s);
+  if (p.c.D == 64) return wide ? run<T, 64, 2, FINE>(p, num_sms, s) : run<T, 64, 1, FINE>(p, num_sms, s);
+  if (p.c.D == 128) return wide ? run<T, 128, 2, FINE>(p, num_sms, s) : run<T, 128, 1, FINE>(p, num_sms, s);
+  return run<T, 256, 1, FINE>(p, num_sms, s);
+}
+
+template <typename T>
+cudaError_t run(const Attn& p, int num_sms, cudaStream_t s) {
+  return sizeof(T) == 4 || p.a.Xq ? run<T, true>(p, num_sms, s) : run<T, false>(p, num_sms, s);
+}
+template <>
+cudaError_t run<float>(const Attn& p, int num_sms, cudaStream_t s) {
+  return run<float, true>(p, num_sms, s);
 }
 
 }  // namespace

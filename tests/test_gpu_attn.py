@@ -10,11 +10,11 @@ from oracle import decode_oracle as deo
 
 pytestmark = pytest.mark.gpu
 
-# Relative error of a weight p before it is rounded (but for that of its score), and of the sums over
-# the tokens: exponential 2 ulp, products, and a few dozen additions of a fixed tree, below 2^-18. Rounded
-# to fp16 for the tensor cores where rows are fp16 or bf16: twice half a step (p s and p, for the
-# codes' and the minima's sums and the total), 2^-11 together with the division by the rounded total 2^-10.
-WEIGHT = {"fp32": 2.0 ** -18, "fp16": 2.0 ** -10 + 2.0 ** -18, "bf16": 2.0 ** -10 + 2.0 ** -18}
+# Relative error of a weight p (but for that of its score): exponential 2 ulp and a few products, below 2^-20; rounded to fp16
+# for the tensor cores where rows are fp16 or bf16 (half a step, 2^-12) in the values' sum and in the total (their quotient: 2^-11),
+# the product with s once more, and m + 8 s: 2^-10 in all. Split into two halves in fp32 rows, and where Q8_1 rows are asked
+# for: 2^-23 each time.
+WEIGHT = {"fp32": 2.0 ** -19, "fp16": 2.0 ** -10 + 2.0 ** -19, "bf16": 2.0 ** -10 + 2.0 ** -19}
 # Error of a score, relative to scale * Sum (|s| c + |m|) |q|: exact products, sums in fp32 of at most
 # 256 terms whose additions may each cut off a step (2^-23), most of them within 16 by a tree: 2^-18.
 SCORE = 2.0 ** -18
@@ -25,14 +25,17 @@ def _dev(a):
     return torch.from_numpy(np.ascontiguousarray(a)).cuda()
 
 
-def _bound(o, E, S, dtype):
-    """Largest error of an unrounded output: that of the weights, and scores off by d change them by 2 d at most."""
-    d = SCORE * S[..., None]
-    return (WEIGHT[dtype] + np.expm1(2 * d)) * E + 1e-30
+def _bound(o, E, S, dtype, places, fine=False):
+    """Largest error of an unrounded output: that of the weights; scores off by d change them by 2 d at most; the sums of
+    a granule of 16 places are products with the codes as they are (two or four additions that may cut off a step), and are added up
+    (n granules, one or two additions each)."""
+    d, n = SCORE * S[..., None], places / 16 + 1
+    w = WEIGHT["fp32" if fine else dtype]
+    return (w + np.expm1(2 * d) + n * 2.0 ** -22) * E[0] + 2.0 ** -21 * E[1] + 1e-30
 
 
-def _check(got, o, E, S, dtype, what):
-    tol = _bound(o, E, S, dtype)
+def _check(got, o, E, S, dtype, what, places=4096, fine=False):
+    tol = _bound(o, E, S, dtype, places, fine)
     tol = tol + HALF[dtype] * (np.abs(o) + tol) + (2.0 ** -25 if dtype == "fp16" else 0)
     err = np.abs(got - o)
     assert np.all(err <= tol), f"{what}: {np.nanmax(err / tol)} times the bound"
@@ -78,8 +81,10 @@ def test_one_new_row_each(dtype, D, H, group, P, lens):
     case = _case(D + group + len(lens), D, H, group, P, lens, dtype=dtype)
     O, Xq = _run(*case, Xq=True)
     o, E, S = ao.attention(f64(case[2]), case[0], case[1], P, lens)
-    _check(f64(O), o, E, S, dtype, "O")
-    tol = _bound(o, E, S, dtype)
+    _check(f64(O), o, E, S, dtype, "O", max(lens), True)
+    plain, _ = _run(*case)
+    _check(f64(plain), o, E, S, dtype, "O without Xq", max(lens))
+    tol = _bound(o, E, S, dtype, max(lens), True)
     _check_q8(Xq.cpu().numpy(), o.reshape(len(lens), -1), tol.reshape(len(lens), -1), "Xq")
     assert kq.kq_get_device_error() == 0
 
@@ -191,7 +196,7 @@ def test_queries_of_any_size(dtype, size):
         ok = SCORE * S[..., None] < 0.1
     else:
         ok = np.ones_like(S[..., None], bool)
-    tol = _bound(o, E, np.where(ok[..., 0], S, 0), dtype)
+    tol = _bound(o, E, np.where(ok[..., 0], S, 0), dtype, 200)
     tol = tol + HALF[dtype] * (np.abs(o) + tol)
     assert np.all((np.abs(f64(O) - o) <= tol) | ~ok)
 
@@ -210,7 +215,7 @@ def test_values_of_very_different_sizes():
         # Scales far below the largest seen so far are rounded relative to that one: 2^-38 of it.
         far = 2.0 ** -38 * 65504 * 16
         got, _ = kq.kq_attn_q4(q, _dev(cache), _dev(t), _dev(lens))
-        tol = _bound(o, E, S, dtype) + far
+        tol = _bound(o, E, S, dtype, 100) + far
         assert np.all(np.abs(f64(got) - o) <= tol + HALF[dtype] * (np.abs(o) + tol))
 
 
@@ -287,14 +292,22 @@ def test_two_streams_at_once():
 
 
 def test_long_sequence():
-    """More places than the CTAs' partial results are joined from one after the other; some of its pages far apart."""
-    import torch
+    """A sequence in parts of every CTA; many places that count alike, whose codes' sums are far larger than the output."""
     D, H, P, L = 64, 1, 64, 70001
-    rng = np.random.default_rng(15)
     cache, t, Q, lens, _ = _case(16, D, H, 2, P, [L], dtype="fp32")
-    O, _ = kq.kq_attn_q4(Q, _dev(cache), _dev(t), _dev(lens))
     o, E, S = ao.attention(f64(Q), cache, t, P, [L])
-    _check(f64(O), o, E, S, "fp32", "O")
+    for dtype in ("fp32", "fp16"):
+        q = Q.to(torch_dtype(dtype))
+        if dtype == "fp16":
+            o, E, S = ao.attention(f64(q), cache, t, P, [L])
+        O, Xq = kq.kq_attn_q4(q, _dev(cache), _dev(t), _dev(lens), Xq=True)
+        _check(f64(O), o, E, S, dtype, "O", L, True)
+        tol = _bound(o, E, S, dtype, L, True)
+        _check_q8(Xq.cpu().numpy(), o.reshape(1, -1), tol.reshape(1, -1), "Xq")
+        O, _ = kq.kq_attn_q4(q, _dev(cache), _dev(t), _dev(lens))
+        _check(f64(O), o, E, S, dtype, "O", L)
+        # In norm, far below the bound of each element: the roundings are independent of one another.
+        assert np.linalg.norm(f64(O) - o) <= (4e-6 if dtype == "fp32" else 2.0 ** -11) * np.linalg.norm(o)
 
 
 def test_pages_past_32_bits():
