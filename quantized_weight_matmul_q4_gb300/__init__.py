@@ -367,13 +367,14 @@ _PAIRINGS = {"half": KQ_ROPE_HALF, "pairs": KQ_ROPE_PAIRS}
 
 def _head_rows(t, name: str, shape, dtype):
     """(device pointer, elements from row to row) of a CUDA tensor [N, heads, D] whose rows are contiguous."""
-    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor (libkq has no CPU path)")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     N, heads, D = shape
+    if type(t) is not _TENSOR or not t.is_cuda or t.dtype is not dtype or t.shape != shape:
+        if not isinstance(t, _torch().Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor (libkq has no CPU path)")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     ld, head, step = t.stride()
     if (step != 1 and D != 1) or (head != D and heads != 1):
         raise ValueError(f"{name}'s heads must follow one another in its rows")
@@ -486,6 +487,19 @@ def kq_kv_gather_q4(cache, block_table, positions, seq_ids=None, dtype=None, K=N
     return K, V
 
 
+_ATTN_WS = {}  # sizes of a call, and the device -> bytes of its workspace
+
+
+def _attn_ws(*sizes) -> int:
+    key = (*sizes, _GET_DEVICE())
+    n = _ATTN_WS.get(key)
+    if n is None:
+        if len(_ATTN_WS) > 4096:
+            _ATTN_WS.clear()
+        n = _ATTN_WS[key] = kq_attn_q4_workspace_bytes(*sizes)
+    return n
+
+
 def kq_attn_q4_workspace_bytes(n_q_heads: int, n_kv_heads: int, head_dim: int, N: int, n_seqs: int) -> int:
     return int(lib().kq_attn_q4_workspace_bytes(n_q_heads, n_kv_heads, head_dim, N, n_seqs))
 
@@ -522,7 +536,7 @@ def kq_attn_q4(Q, cache, block_table, kv_len, scale=None, q_start=None, window: 
     elif Xq is not None:
         xq = _sized(Xq, "Xq", N * (Hq * D // 32) * 36, torch.uint8)
     if ws is None:
-        ws = _out((max(16, kq_attn_q4_workspace_bytes(Hq, Hk, D, N, seqs)),), torch.uint8, Q.device, stream)
+        ws = _out((max(16, _attn_ws(Hq, Hk, D, N, seqs)),), torch.uint8, Q.device, stream)
     check(lib().kq_attn_q4(dt, q, ldq, Hq, c, pages, page, Hk, D, bt, ldt, seqs, _sized(kv_len, "kv_len", seqs, torch.int32),
                            _sized(q_start, "q_start", seqs + 1, torch.int32), scale if scale is not None else D ** -0.5,
                            window, o, ldo, xq, N, _dev(ws, "ws", torch.uint8), ws.numel(), _stream(stream)), "kq_attn_q4")
