@@ -18,6 +18,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kq_attn.h"
 #include "kq_types.cuh"
@@ -247,6 +248,33 @@ __device__ __forceinline__ void add_shared(void* p, uint32_t v) {
   asm volatile("red.shared::cta.add.u32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
 }
 
+// The least value of type T that is not below l.
+template <typename T>
+__device__ __forceinline__ T at_least(float l) {
+  if constexpr (sizeof(T) == 4) return l;
+  else if constexpr (std::is_same_v<T, __half>) return __float2half_ru(l);
+  else return __float2bfloat16_ru(l);
+}
+// Bit j: element j of the sixteen bytes v is not below `least`.
+__device__ __forceinline__ uint32_t kept_bits(const uint4& v, float least) {
+  return (__uint_as_float(v.x) >= least) | (__uint_as_float(v.y) >= least) << 1 | (__uint_as_float(v.z) >= least) << 2 |
+         (__uint_as_float(v.w) >= least) << 3;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t kept_bits(const uint4& v, T least) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t b = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t m;
+    if constexpr (std::is_same_v<T, __half>) m = __hge2_mask(*reinterpret_cast<const __half2*>(&w[i]), __half2half2(least));
+    else m = __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), __bfloat162bfloat162(least));
+    b |= (m & 0x00010002u) << (2 * i);           // bit 1 of the lower, bit 16 of the upper
+  }
+  // Lower elements are in bits 1, 3, 5, 7, upper ones in bits 16, 18, 20, 22: to 0, 2, 4, 6 and 1, 3, 5, 7.
+  return (b & 0xffu) >> 1 | (b >> 15 & 0xffu);
+}
+
 // f * v rounded down or up, for 0 < f < 1: f is m * 2^-s with a 24-bit m.
 __device__ __forceinline__ uint64_t share_of(float f, uint64_t v, bool up) {
   const uint32_t bits = __float_as_uint(f), e = bits >> 23;
@@ -314,7 +342,7 @@ struct Row {
 // A row of logits in the shared memory of a cluster: the largest, and (T not above 0) its first token; else the limits of top_k
 // and top_p, and the choice among the tokens kept. Steps that the weights' sums decide are taken in whole numbers.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a, int ctas, int per, bool vec) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a, int ctas, int per) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint32_t table[256];
   __shared__ float per_T[2];
@@ -322,8 +350,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   __shared__ float partf[kWarps];
   __shared__ int bin_of, found;
   __shared__ uint32_t tokens_at, tokens_to, available;
-  T* slice = reinterpret_cast<T*>(smem);
-  uint64_t* hist = reinterpret_cast<uint64_t*>(smem + (static_cast<size_t>(per) * sizeof(T) + 15) / 16 * 16);
+  uint64_t* hist = reinterpret_cast<uint64_t*>(smem + (static_cast<size_t>(per) * sizeof(T) + 31) / 16 * 16);
   T* list = reinterpret_cast<T*>(hist + 2 * kBins);
   int* list_at = reinterpret_cast<int*>(list + kList);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -334,29 +361,31 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   const int first = team.rank * per;
   // This CTA's tokens, in the order of their indexes: token i is `first` + i, or index[i].
   int count = max(0, min(per, static_cast<int>(a.V) - first));
+  const T* x = static_cast<const T*>(a.logits) + n * a.ld + first;
+  // In shared memory the slice lies as far from a 16-byte boundary as in memory: `lead` tokens come before the first one.
+  constexpr int E = 16 / sizeof(T);
+  const int beyond = static_cast<int>(reinterpret_cast<uintptr_t>(x) & 15) / static_cast<int>(sizeof(T));
+  const int lead = min(count, beyond ? E - beyond : 0), runs = (count - lead) / E;
+  T* slice = reinterpret_cast<T*>(smem) + beyond;
   const T* tokens = slice;
   const int* index = nullptr;
-  const T* x = static_cast<const T*>(a.logits) + n * a.ld + first;
 
   // The slice, and the row's largest logit.
   float top = -INFINITY;
-  {
-    constexpr int E = 16 / sizeof(T);
-    const int whole = vec ? count / E : 0;
 #pragma unroll 4
-    for (int i = threadIdx.x; i < whole; i += kThreads) {
-      uint4 v = reinterpret_cast<const uint4*>(x)[i];
-      T* e = reinterpret_cast<T*>(&v);
+  for (int i = threadIdx.x; i < runs; i += kThreads) {
+    uint4 v = reinterpret_cast<const uint4*>(x + lead)[i];
+    T* e = reinterpret_cast<T*>(&v);
 #pragma unroll
-      for (int j = 0; j < E; ++j) top = fmaxf(top, take(e[j]));
-      reinterpret_cast<uint4*>(slice)[i] = v;
-    }
-#pragma unroll 4
-    for (int i = whole * E + threadIdx.x; i < count; i += kThreads) {
-      T v = x[i];
-      top = fmaxf(top, take(v));
-      slice[i] = v;
-    }
+    for (int j = 0; j < E; ++j) top = fmaxf(top, take(e[j]));
+    reinterpret_cast<uint4*>(slice + lead)[i] = v;
+  }
+  // The tokens before the first run and after the last: fewer than 2 E.
+  if (static_cast<int>(threadIdx.x) < count - runs * E) {
+    const int i = static_cast<int>(threadIdx.x) < lead ? threadIdx.x : threadIdx.x + runs * E;
+    T v = x[i];
+    top = fmaxf(top, take(v));
+    slice[i] = v;
   }
   Row row;
   const int k = a.top_k ? a.top_k[n] : 0;
@@ -492,32 +521,59 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     const float least_kept = value_of(lo);
 
     if (some <= kList) {
-      // Few: to the first CTA, in the order of their indexes. A warp takes a run of tokens.
-      const int run = ((count + kWarps - 1) / kWarps + 31) / 32 * 32, i0 = min(count, warp * run), i1 = min(count, i0 + run);
+      // Few: to the first CTA, in the order of their indexes. Tokens go by sixteen bytes, E side by side to a lane, and a warp takes
+      // a stretch of them (the first also those before, the last those after).
+      const int each = ((runs + kWarps - 1) / kWarps + 31) / 32 * 32, w0 = min(runs, warp * each), w1 = min(runs, w0 + each);
+      const int tail = lead + runs * E;
+      const uint4* words = reinterpret_cast<const uint4*>(slice + lead);
+      const T least_T = at_least<T>(least_kept);
+      // Bit j: token j of the run is kept; lanes beyond the stretch have none.
+      const auto bits_of = [&](int i) {
+        uint32_t b = 0;
+        if (i < w1) {
+          const uint4 v = words[i];
+          b = kept_bits(v, least_T);
+        }
+        return b;
+      };
+      const auto single = [&](int i, int end) { return i < end && at(i) >= least_kept; };
       uint32_t mine = 0;
 #pragma unroll 4
-      for (int i = i0 + lane; i < i1; i += 32) mine += at(i) >= least_kept;
+      for (int i = w0 + lane; i < w1; i += 32) mine += __popc(bits_of(i));
+      if (warp == 0) mine += single(lane, lead);
+      if (warp == kWarps - 1) mine += single(tail + lane, count);
       mine = __reduce_add_sync(0xffffffffu, mine);
       uint64_t to;
       const int there = static_cast<int>(team.sum(lane == 0 ? mine : 0, &to));
       to += sum_before<uint64_t>(lane == 0 ? mine : 0, part);
       uint32_t place = __shfl_sync(0xffffffffu, static_cast<uint32_t>(to), 0);
       const uint32_t list0 = mapa_shared(list, 0), at0 = mapa_shared(list_at, 0);
-#pragma unroll 4
-      for (int i = i0; i < i1; i += 32) {
-        const bool m = i + lane < i1 && at(i + lane) >= least_kept;
-        const uint32_t b = __ballot_sync(0xffffffffu, m);
-        if (m) {
-          const uint32_t to_place = place + __popc(b & ((1u << lane) - 1));
+      // Puts the tokens i + j of the bits j, after those of the lanes before.
+      const auto put = [&](int i, uint32_t bits) {
+        if (!__any_sync(0xffffffffu, bits != 0)) return;
+        uint32_t before = __popc(bits);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, before, o);
+          if (lane >= o) before += y;
+        }
+        uint32_t to_place = place + before - __popc(bits);
+        place += __shfl_sync(0xffffffffu, before, 31);
+        for (; bits; bits &= bits - 1, ++to_place) {
+          const int k = i + __ffs(bits) - 1;
           if constexpr (sizeof(T) == 4)
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(list0 + 4 * to_place), "f"(slice[i + lane]) : "memory");
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(list0 + 4 * to_place), "f"(slice[k]) : "memory");
           else
             asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(list0 + 2 * to_place),
-                         "h"(*reinterpret_cast<const uint16_t*>(slice + i + lane)) : "memory");
-          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at0 + 4 * to_place), "r"(first + i + lane) : "memory");
+                         "h"(*reinterpret_cast<const uint16_t*>(slice + k)) : "memory");
+          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at0 + 4 * to_place), "r"(first + k) : "memory");
         }
-        place += __popc(b);
-      }
+        __syncwarp();
+      };
+      if (warp == 0) put(lane, single(lane, lead));
+#pragma unroll 2
+      for (int i = w0; i < w1; i += 32) put(lead + (i + lane) * E, bits_of(i + lane));
+      if (warp == kWarps - 1) put(tail + lane, single(tail + lane, count));
       team.sync();
       if (team.rank > 0) return;
       team = Team{1, 0, slots, part, hist, hist, 0};
@@ -694,7 +750,7 @@ cudaError_t sample(const SampleArgs& a, int num_sms, cudaStream_t s) {
                               (a.V >= 4096 * static_cast<int64_t>(ctas) && a.N * ctas <= num_sms)))
     ctas *= 2;
   const int per = static_cast<int>(((a.V + ctas - 1) / ctas + 7) / 8 * 8);
-  const size_t smem = (static_cast<size_t>(per) * sizeof(T) + 15) / 16 * 16 + 2 * kBins * sizeof(uint64_t) + kList * 8;
+  const size_t smem = (static_cast<size_t>(per) * sizeof(T) + 31) / 16 * 16 + 2 * kBins * sizeof(uint64_t) + kList * 8;
   static std::atomic<uint64_t> allowed{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -719,8 +775,7 @@ cudaError_t sample(const SampleArgs& a, int num_sms, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const bool vec = a.ld * static_cast<int64_t>(sizeof(T)) % 16 == 0;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a, ctas, per, vec);
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a, ctas, per);
 }
 
 }  // namespace
