@@ -87,9 +87,9 @@ constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kWhole = 12582912.f;
 constexpr int kWholeBits = 0x4b400000;
 
-// exp((l - M) / T) * 2^43: with x = (M - l) log2(e) / T as e + r, r in [-1/2, 1/2], and r = j / 256 + f,
-// it is 2^(43 - e) 2^(-j / 256) (1 + q), q = 2^-f - 1 by its series (|f| <= 1/512: |q| < 0.00136, so that the
-// rounding of q to 2^-31 and that of the table leave an error below 2^-30).
+// exp((l - M) / T) * 2^43: with x = (M - l) log2(e) / T as k / 256 + f, |f| little above 1/512, it is
+// 2^(43 - (k >> 8)) 2^(-(k & 255) / 256) (1 + q), q = 2^-f - 1 by its series (|q| < 0.00137: fp32's rounding of f and of the series
+// is below 2^-33, that of q and of the table to 2^-31 below 2^-31 of the weight: in all below 2^-30).
 struct Weigh {
   float M, ch, cl;                 // log2(e) / T as a sum of two
   const uint32_t* table;           // kPow2 in shared memory
@@ -98,21 +98,16 @@ struct Weigh {
     const float dh = __fsub_rn(M, l);                          // M - l as dh + dl, exactly
     const float b = __fsub_rn(M, dh), dl = __fadd_rn(__fsub_rn(M, __fadd_rn(dh, b)), __fsub_rn(b, l));
     const float xh = __fmul_rn(dh, ch);
-    if (!(xh < 64.f)) return dh == 0.f ? kOne : 0;             // (0 times an infinite 1 / T is a NaN)
     const float xl = __fmaf_rn(dl, ch, __fmaf_rn(dh, cl, __fmaf_rn(dh, ch, -xh)));
-    const float te = __fadd_rn(xh, kWhole), e = __fsub_rn(te, kWhole), rh = __fsub_rn(xh, e);
-    const float r = __fadd_rn(rh, xl), rl = __fsub_rn(xl, __fsub_rn(r, rh));
-    const float tj = __fmaf_rn(r, 256.f, kWhole), j = __fsub_rn(tj, kWhole);
-    const float f = __fadd_rn(__fmaf_rn(j, -0.00390625f, r), rl);
-    // t = -f ln 2 and what its rounding leaves (0.69314718 is 1.904654e-9 above ln 2); q = t + t^2 / 2 + t^3 / 6.
-    const float t = f * -0.69314718f;
-    const float rest = __fmaf_rn(f, -0.69314718f, -t) + f * 1.904654e-9f;
-    const float q = t + (rest + t * t * __fmaf_rn(t, 0.16666667f, 0.5f));
-    const int ji = __float_as_int(tj) - kWholeBits;             // 2^(-j / 256) = 2^-(j >> 8) 2^-((j & 255) / 256)
-    const int shift = 19 + (__float_as_int(te) - kWholeBits) + (ji >> 8);
+    const float tk = __fmaf_rn(xh, 256.f, kWhole), k = __fsub_rn(tk, kWhole);
+    const float f = __fadd_rn(__fmaf_rn(k, -0.00390625f, xh), xl);            // (the difference without xl is exact)
+    const float t = f * -0.69314718f, q = __fmaf_rn(t * t, __fmaf_rn(t, 0.16666667f, 0.5f), t);
+    const int ki = __float_as_int(tk) - kWholeBits;
     const uint32_t u = 0x80000000u + static_cast<uint32_t>(__float_as_int(__fmaf_rn(q, 2147483648.f, kWhole)) - kWholeBits);
-    const uint64_t w = static_cast<uint64_t>(table[ji & 255]) * u;
-    return shift < 64 ? w >> shift : 0;
+    const uint64_t w = static_cast<uint64_t>(table[ki & 255]) * u;
+    uint64_t v;
+    asm("shr.b64 %0, %1, %2;" : "=l"(v) : "l"(w), "r"(19 + (ki >> 8)));       // (0 beyond 63)
+    return xh < 64.f ? v : dh == 0.f ? kOne : 0;               // (0 times an infinite 1 / T is a NaN)
   }
 };
 
@@ -349,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   __shared__ uint64_t least, slots[4], part[2 * kWarps], found_above;
   __shared__ float partf[kWarps];
   __shared__ int bin_of, found;
-  __shared__ uint32_t tokens_at, tokens_to, available;
+  __shared__ float up_to, available;
   uint64_t* hist = reinterpret_cast<uint64_t*>(smem + (static_cast<size_t>(per) * sizeof(T) + 31) / 16 * 16);
   T* list = reinterpret_cast<T*>(hist + 2 * kBins);
   int* list_at = reinterpret_cast<int*>(list + kList);
@@ -365,7 +360,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   // In shared memory the slice lies as far from a 16-byte boundary as in memory: `lead` tokens come before the first one.
   constexpr int E = 16 / sizeof(T);
   const int beyond = static_cast<int>(reinterpret_cast<uintptr_t>(x) & 15) / static_cast<int>(sizeof(T));
-  const int lead = min(count, beyond ? E - beyond : 0), runs = (count - lead) / E;
+  int lead = min(count, beyond ? E - beyond : 0);
+  int runs = (count - lead) / E;
   T* slice = reinterpret_cast<T*>(smem) + beyond;
   const T* tokens = slice;
   const int* index = nullptr;
@@ -402,10 +398,49 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   }
   const uint32_t top_key = static_cast<uint32_t>(team.most(key_of(top)));
   auto at = [&](int i) { return usable(to_f32(tokens[i])); };
+  const auto words = [&](int i) { return reinterpret_cast<const uint4*>(tokens + lead)[i]; };
+  // All tokens, by sixteen bytes; those before the first sixteen and after the last, fewer than 2 E, one by one.
   auto each = [&](auto f) {
-#pragma unroll 4
-    for (int i = threadIdx.x; i < count; i += kThreads) f(at(i), i);
+#pragma unroll 1
+    for (int i = threadIdx.x; i < runs; i += kThreads) {
+      uint4 v = words(i);
+      const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+      for (int j = 0; j < E; ++j) f(usable(to_f32(e[j])), lead + i * E + j);
+    }
+    if (static_cast<int>(threadIdx.x) < count - runs * E) {
+      const int i = static_cast<int>(threadIdx.x) < lead ? threadIdx.x : threadIdx.x + runs * E;
+      f(at(i), i);
+    }
   };
+  // Those not below `from`, of the sixteens w0, w0 + by, ... up to w1 and (single) the token that has number `single` among those one
+  // by one: a lane goes over its sixteen bytes' alone, so that few tokens cost few steps. Where many are expected, all of the
+  // tokens i0, i0 + by, ... up to i1 (the same ones, over the warp's or the CTA's lanes), -inf in the place of those below.
+  bool dense = true;
+  auto each_from = [&](float from, int by, int w0, int w1, int single, int i0, int i1, auto f) {
+    if (dense) {
+#pragma unroll 4
+      for (int i = i0; i < i1; i += by) {
+        const float l = at(i);
+        f(l >= from ? l : -INFINITY, i);
+      }
+      return;
+    }
+    const T least_T = at_least<T>(from);
+#pragma unroll 2
+    for (int i = w0; i < w1; i += by)
+#pragma unroll 1
+      for (uint32_t b = kept_bits(words(i), least_T); b; b &= b - 1) {
+        const int k = lead + i * E + __ffs(b) - 1;
+        f(at(k), k);
+      }
+    if (single >= 0 && single < count - runs * E) {
+      const int k = single < lead ? single : single + runs * E;
+      const float l = at(k);
+      if (l >= from) f(l, k);
+    }
+  };
+  auto all_from = [&](float from, auto f) { each_from(from, kThreads, threadIdx.x, runs, threadIdx.x, threadIdx.x, count, f); };
   const float M = value_of(top_key);
   if (top_key == kNone || !(T0 > 0.f)) {         // no token at all, or the first with the largest logit
     int id = 0x7fffffff;
@@ -424,8 +459,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   // The limit: keys above limit_key are within it, and the first `extra`, by index, of the tokens with that key.
   uint32_t limit_key = kNone + 1, extra = kAll;
   if (row.k > 0 || row.p < 1.f) {
-    // Histogram by bins of (M - l) log2(e) / T of 1/16: tokens (low words) and, with top_p, weights relative to the bin's largest
-    // possible, in 2^-15 (high words; those of the last bin are below 2^-63). Without top_k the exact weight of all.
+    // Histogram by bins of (M - l) log2(e) / T of 1/16: with top_k of tokens, else of weights relative to the bin's largest possible,
+    // in 2^-15 (those of the last bin are below 2^-63), and with it the exact weight of all.
     const float scale = 16.f * 1.44269504f / T0;
     auto bin_at = [&](float l, float& frac) {
       const float d = l == M ? 0.f : fminf(__fsub_rn(M, l) * scale, static_cast<float>(kBins - 1));   // (a NaN: the last)
@@ -435,78 +470,69 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     };
     const bool by_weight = row.p < 1.f;
     uint64_t whole = 0;
-    team.clear();
-    each([&](float l, int) {
-      if (l == -INFINITY) return;
-      float frac;
-      uint32_t* h = reinterpret_cast<uint32_t*>(hist + bin_at(l, frac));
-      add_shared(h, 1u);
-      if (by_weight) {
-        const float w = exp2_fast(frac * -0.0625f);
-        add_shared(h + 1, static_cast<uint32_t>(__float_as_int(__fmaf_rn(w, 32768.f, kWhole)) - kWholeBits));
-        if (row.k == 0) whole += row.w(l);
+    // Tokens or weights up to each bin: fp32 has these numbers of tokens exactly.
+    float to_bin[kPerThread], sum_to, before;
+    const auto tally = [&] {
+      team.clear();
+      if (row.k > 0) {
+        each([&](float l, int) {
+          float frac;
+          if (l != -INFINITY) add_shared(hist + bin_at(l, frac), 1u);
+        });
+      } else {
+        each([&](float l, int) {
+          if (l == -INFINITY) return;
+          float frac;
+          uint64_t* h = hist + bin_at(l, frac);
+          add_shared(h, static_cast<uint32_t>(__float_as_int(__fmaf_rn(exp2_fast(frac * -0.0625f), 32768.f, kWhole)) - kWholeBits));
+          whole += row.w(l);
+        });
+        team.tell(whole, 0);
       }
-    });
-    if (by_weight && row.k == 0) team.tell(whole, 0);
-    // Over the cluster: tokens (low words) and weights as fp32 (high words), the latter times 2^(-b / 16) below.
-    const auto as_float = [](uint64_t h) { return (h & 0xffffffffu) | static_cast<uint64_t>(__float_as_uint(static_cast<float>(h >> 32))) << 32; };
-    const uint64_t* all = team.gather([&](uint64_t v, uint64_t h) {
-      h = as_float(h);
-      const float w = __uint_as_float(static_cast<uint32_t>(v >> 32)) + __uint_as_float(static_cast<uint32_t>(h >> 32));
-      return ((v & 0xffffffffu) + (h & 0xffffffffu)) | static_cast<uint64_t>(__float_as_uint(w)) << 32;
-    });
-    if (by_weight && row.k == 0) whole = team.told(0);
-    // Tokens and weights up to each bin.
-    uint32_t tokens_to_bin[kPerThread], tokens_sum = 0;
-    float weight_to_bin[kPerThread], weight_sum = 0.f;
+      const uint64_t* all = team.gather([](uint64_t v, uint64_t w) { return v + w; });
+      if (row.k == 0) whole = team.told(0);
+      sum_to = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      const int b = kPerThread * threadIdx.x + i;
-      const uint64_t h = team.ctas == 1 ? as_float(all[b]) : all[b];
-      tokens_to_bin[i] = tokens_sum += static_cast<uint32_t>(h);
-      weight_to_bin[i] = weight_sum +=
-          b < kBins - 1 ? __uint_as_float(static_cast<uint32_t>(h >> 32)) * exp2_fast(b * -0.0625f) * 0x1p-15f : 0.f;
-    }
-    const uint32_t tokens_before = static_cast<uint32_t>(sum_before<uint64_t>(tokens_sum, part));
-    const float weight_before = sum_before<float>(weight_sum, partf);
-    // The first bin up to which there are so many tokens, or (tokens 0) so much weight; the last bin if there are never. Tokens
-    // before it and up to it in tokens_at and tokens_to.
-    auto find = [&](uint32_t least_tokens, float least_weight) {
+      for (int i = 0; i < kPerThread; ++i) {
+        const int b = kPerThread * threadIdx.x + i;
+        const float h = static_cast<float>(all[b]);
+        to_bin[i] = sum_to += row.k > 0 ? h : b < kBins - 1 ? h * exp2_fast(b * -0.0625f) * 0x1p-15f : 0.f;
+      }
+      before = sum_before<float>(sum_to, partf);
+    };
+    tally();
+    // The first bin up to which there is so much, or the last bin if there never is. What is before it in up_to, and all in available.
+    auto find = [&](float least) {
       __syncthreads();
       if (threadIdx.x == 0) bin_of = kBins - 1;
       __syncthreads();
 #pragma unroll
       for (int i = kPerThread - 1; i >= 0; --i)
-        if (least_tokens ? tokens_before + tokens_to_bin[i] >= least_tokens : weight_before + weight_to_bin[i] >= least_weight)
-          atomicMin(&bin_of, static_cast<int>(kPerThread * threadIdx.x + i));
+        if (before + to_bin[i] >= least) atomicMin(&bin_of, static_cast<int>(kPerThread * threadIdx.x + i));
       __syncthreads();
       const int b = bin_of;
 #pragma unroll
       for (int i = 0; i < kPerThread; ++i)
-        if (b == static_cast<int>(kPerThread * threadIdx.x) + i) {
-          tokens_at = tokens_before + (i > 0 ? tokens_to_bin[i > 0 ? i - 1 : 0] : 0);
-          tokens_to = tokens_before + tokens_to_bin[i];
-        }
-      if (threadIdx.x == kThreads - 1) available = tokens_before + tokens_sum;
+        if (b == static_cast<int>(kPerThread * threadIdx.x) + i) up_to = before + (i > 0 ? to_bin[i > 0 ? i - 1 : 0] : 0.f);
+      if (threadIdx.x == kThreads - 1) available = before + sum_to;
       __syncthreads();
       return b;
     };
     // The bins' weights are within 2^-14 of the exact ones, and fp32's sums of them: 2^-11 is beyond that on both sides.
     const float around = 0x1p-11f, in_units = 1.f / static_cast<float>(kOne);
     int last = kBins - 1;    // no token of a later bin is kept
+    uint32_t k_before = 0;
     if (row.k > 0) {
-      last = find(row.k, 0.f);
-      if (available <= row.k) {                  // top_k leaves all of them
+      last = find(static_cast<float>(row.k));
+      k_before = static_cast<uint32_t>(up_to);
+      if (available <= static_cast<float>(row.k)) {          // top_k leaves all of them
         row.k = 0;
-        if (by_weight) {
-          whole = 0;
-          each([&](float l, int) { whole += row.w(l); });
-          whole = team.sum(whole);
-        }
+        last = kBins - 1;
+        if (by_weight) tally();
       }
     }
-    if (row.k == 0 && by_weight) last = find(0, row.p * (static_cast<float>(whole) * in_units) * (1.f + around));
-    const uint32_t some = tokens_to, k_before = tokens_at;
+    const bool weights = row.k == 0 && by_weight;
+    if (weights) last = find(row.p * (static_cast<float>(whole) * in_units) * (1.f + around));
     // The least key whose bin is b or an earlier one: near M - (b + 1) / scale.
     auto least_key = [&](int b) {
       const float frac_at = static_cast<float>(b + 1) / scale;
@@ -520,31 +546,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     uint64_t above = row.k > 0 ? k_before : 0;
     const float least_kept = value_of(lo);
 
-    if (some <= kList) {
-      // Few: to the first CTA, in the order of their indexes. Tokens go by sixteen bytes, E side by side to a lane, and a warp takes
-      // a stretch of them (the first also those before, the last those after).
-      const int each = ((runs + kWarps - 1) / kWarps + 31) / 32 * 32, w0 = min(runs, warp * each), w1 = min(runs, w0 + each);
-      const int tail = lead + runs * E;
-      const uint4* words = reinterpret_cast<const uint4*>(slice + lead);
-      const T least_T = at_least<T>(least_kept);
-      // Bit j: token j of the run is kept; lanes beyond the stretch have none.
-      const auto bits_of = [&](int i) {
-        uint32_t b = 0;
-        if (i < w1) {
-          const uint4 v = words[i];
-          b = kept_bits(v, least_T);
-        }
-        return b;
-      };
-      const auto single = [&](int i, int end) { return i < end && at(i) >= least_kept; };
-      uint32_t mine = 0;
+    // How many are those. Tokens go by sixteen bytes, E side by side to a lane, and a warp takes a stretch of them (the first also
+    // those before, the last those after).
+    const int stretch = ((runs + kWarps - 1) / kWarps + 31) / 32 * 32, w0 = min(runs, warp * stretch), w1 = min(runs, w0 + stretch);
+    const int tail = lead + runs * E;
+    const T least_T = at_least<T>(least_kept);
+    // Bit j: token j of the run is kept; lanes beyond the stretch have none.
+    const auto bits_of = [&](int i) { return i < w1 ? kept_bits(words(i), least_T) : 0u; };
+    const auto single = [&](int i, int end) { return i < end && at(i) >= least_kept; };
+    uint32_t mine = 0;
 #pragma unroll 4
-      for (int i = w0 + lane; i < w1; i += 32) mine += __popc(bits_of(i));
-      if (warp == 0) mine += single(lane, lead);
-      if (warp == kWarps - 1) mine += single(tail + lane, count);
-      mine = __reduce_add_sync(0xffffffffu, mine);
-      uint64_t to;
-      const int there = static_cast<int>(team.sum(lane == 0 ? mine : 0, &to));
+    for (int i = w0 + lane; i < w1; i += 32) mine += __popc(bits_of(i));
+    if (warp == 0) mine += single(lane, lead);
+    if (warp == kWarps - 1) mine += single(tail + lane, count);
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    uint64_t to;
+    const uint64_t there = team.sum(lane == 0 ? mine : 0, &to);
+    dense = static_cast<int64_t>(there) * 4 > a.V;
+    if (there <= kList) {
+      // Few: to the first CTA, in the order of their indexes.
       to += sum_before<uint64_t>(lane == 0 ? mine : 0, part);
       uint32_t place = __shfl_sync(0xffffffffu, static_cast<uint32_t>(to), 0);
       const uint32_t list0 = mapa_shared(list, 0), at0 = mapa_shared(list_at, 0);
@@ -579,7 +599,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
       team = Team{1, 0, slots, part, hist, hist, 0};
       tokens = list;
       index = list_at;
-      count = there;
+      count = static_cast<int>(there);
+      lead = 0;
+      runs = count / E;
+      dense = true;
     }                        // Many: the cluster goes on
 
     // The limits one after the other: the largest key at which the sum of tokens, or of weights, over the keys from the largest
@@ -592,22 +615,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         const float edge = value_of(limit_key);
         if (row.k > 0) {
           uint64_t mine = 0;
-          each([&](float l, int) { mine += l > edge ? row.w(l) : 0; });
+          all_from(edge, [&](float l, int) { mine += l > edge ? row.w(l) : 0; });
           whole = team.sum(mine) + extra * row.w(edge);
         }
         goal = row.p > 0.f ? max(share_of(row.p, whole, true), static_cast<uint64_t>(1)) : 1;      // the least sum that is enough
         lo = max(least_key(last), limit_key);
         hi = top_key;
         above = 0;
-        if (team.ctas > 1) {
+        if (weights && team.ctas > 1) {
           // Between the bins in which the prefix may end; what lies beyond is added up.
           const float g = static_cast<float>(goal) * in_units;
-          const int b0 = find(0, g * (1.f - around)), b1 = max(b0, find(0, g * (1.f + around)));
+          const int b0 = find(g * (1.f - around)), b1 = max(b0, find(g * (1.f + around)));
           lo = max(least_key(b1), limit_key);
           hi = max(lo, b0 > 0 ? least_key(b0 - 1) - 1 : top_key);
           const float beyond = value_of(hi);
           uint64_t mine = 0;
-          each([&](float l, int) { mine += l > beyond ? row.w(l) : 0; });
+          all_from(beyond, [&](float l, int) { mine += l > beyond ? row.w(l) : 0; });
           team.tell(0, mine);
           beyond_told = true;
         }
@@ -617,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         const int s = span < kBins ? 0 : 22 - __clz(span);
         team.clear();
         const float l_lo = value_of(lo), l_hi = value_of(hi);
-        each([&](float l, int) {
+        all_from(l_lo, [&](float l, int) {
           if (l >= l_lo && l <= l_hi) {
             uint64_t* h = hist + ((hi - key_of(l)) >> s);
             if (what == 0) add_shared(h, 1u);
@@ -668,26 +691,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   if (row.least > 0) {
     const float below = -logf(fminf(min_p, 1.f)) * T0;
     const uint32_t least_kept = first_key(top_key, M - below, 0x1p-20f * (fabsf(M) + below), [&](uint32_t k) { return row.w(value_of(k)) >= row.least; });
+    if (limit_key == kNone + 1) dense = false;   // (alone it leaves few)
     if (least_kept > limit_key) limit_key = least_kept, extra = kAll;
   }
 
-  // The choice. A warp has a run of tokens, 32 at a time.
-  const int run = ((count + kWarps - 1) / kWarps + 31) / 32 * 32, i0 = min(count, warp * run), i1 = min(count, i0 + run);
+  // The choice. A warp has a stretch of sixteens (the first also the tokens before them, the last those after).
+  const int stretch = (runs + kWarps - 1) / kWarps, w0 = min(runs, warp * stretch), w1 = min(runs, w0 + stretch);
+  const int i0 = warp > 0 ? lead + w0 * E : 0, i1 = warp < kWarps - 1 ? lead + w1 * E : count;
   const float edge = value_of(limit_key);
   // This CTA's tokens with the limit's key, of which those after the first `extra` of the row are not kept, and the weight of the
   // others that are: told to the other CTAs at once. A weight with the limit's key is `one`.
   const uint64_t one = extra != kAll ? row.w(edge) : 0;
   uint32_t same = 0;
   uint64_t mine = 0;
-#pragma unroll 2
-  for (int i = i0 + lane; i < i1; i += 32) {
-    const float l = at(i);
-    if (extra != kAll && l == edge) {
-      ++same;
-    } else if (l >= edge) {
-      mine += row.w(l);
-    }
-  }
+  // Of the tokens one by one the first warp has those before, the last those after.
+  const int single = warp == 0 && lane < lead ? lane : warp == kWarps - 1 ? lead + lane : -1;
+  each_from(edge, 32, w0 + lane, w1, single, i0 + lane, i1, [&](float l, int) {
+    if (extra != kAll && l == edge) ++same;
+    else mine += row.w(l);
+  });
   same = __reduce_add_sync(0xffffffffu, same);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
@@ -718,6 +740,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   if (c <= goal && goal < c + of_warp) {
     uint64_t seen = ties;
     for (int i = i0; i < i1; i += 32) {
+      if (!__any_sync(0xffffffffu, i + lane < i1 && at(i + lane) >= edge)) continue;
       const uint64_t v = kept(i + lane, seen);
       uint64_t s = v;
 #pragma unroll
