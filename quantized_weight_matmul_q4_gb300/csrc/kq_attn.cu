@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
   __shared__ int64_t scan[kWarps], cut_b[kWarps + 1], cut_seq[kWarps + 1], cut_u[kWarps + 1], first_unit[kThreads];
   __shared__ int segment_size[kThreads];
   __shared__ uint64_t full[kWarps][S];
+  __shared__ int2 range[kWarps][R];                                   // what the rows of a tile see: [x, y)
   __shared__ Piece piece[kWarps][2];
   __shared__ float stat[kWarps][2][2][R];                             // maxima and totals of the pieces
   __shared__ uint32_t there;                                          // bit 2 w, 2 w + 1: warp w's pieces
@@ -392,6 +393,11 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
       }
     };
     load_rows(0);
+    if (lane < R) {
+      int i, hq;
+      row_of(lane, i, hq);
+      range[warp][lane] = make_int2(low_of(seen_of(i)), seen_of(i));
+    }
     look_up(0);
     if (lane < min(stages - 1, mine)) issue(lane);
 
@@ -473,8 +479,8 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
     const int k_at = ta * (D / 2) + tig * (4 * G), p_at = Gr::kCodes + ta * (4 * G);
     const int v_at = Gr::kValues + tig * (D / 2) + gid * (2 * G);
     const int m_at = Gr::kValues + Gr::kCodes + (D >= 128 ? ((lane & 8) + ((lane >> 1) & 3) + 4 * (lane & 1)) * (4 * G) : tig * (4 * G));
-    auto step = [&](auto edge_tag, const uint8_t* st, int place0, int hide) {
-      constexpr bool kEdge = decltype(edge_tag)::value;               // some row does not see all of its places
+    const auto step = [&](auto edge_tag, const uint8_t* st, int place0, int hide) {
+      const bool kEdge = edge_tag;               // some row does not see all of its places
       float s[2][NT][4];
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
@@ -530,15 +536,15 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[w][nt][j] *= factor[nt][j & 1];
-        if constexpr (kEdge) {
+        if (kEdge) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              int i, hq;
-              row_of(8 * nt + 2 * tig + (j & 1), i, hq);
-              const int seen = seen_of(i), place = place0 + 16 * w + ta + (j < 2 ? 0 : 8);
-              if (place >= seen || place < low_of(seen) || (hide >> w & 1)) s[w][nt][j] = -INFINITY;
+            for (int c = 0; c < 2; ++c) {
+              const int2 sees = range[warp][8 * nt + 2 * tig + c];
+              const int place = place0 + 16 * w + ta, hidden = hide >> w & 1;
+              if (place < sees.x || place >= sees.y || hidden) s[w][nt][c] = -INFINITY;
+              if (place + 8 < sees.x || place + 8 >= sees.y || hidden) s[w][nt][c + 2] = -INFINITY;
             }
         }
       }
@@ -556,7 +562,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
           return kEdge && (place0 + 16 * w + place < low_least || place0 + 16 * w + place >= seen_most || (hide >> w & 1));
         };
         uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-        if constexpr (kEdge) {
+        if (kEdge) {
           keep0 = (unseen(tig) ? 0u : 0xffffu) | (unseen(tig + 4) ? 0u : 0xffff0000u);
           keep1 = (unseen(tig + 8) ? 0u : 0xffffu) | (unseen(tig + 12) ? 0u : 0xffff0000u);
         }
@@ -592,7 +598,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
           s0[w] = gid < G ? __byte_perm(x.x, y.x, pick) & keep0 : 0u;
           s1[w] = gid < G ? __byte_perm(z.x, t.x, pick) & keep1 : 0u;
         }
-        if constexpr (kEdge) {                                        // a NaN (m is 0 there) reaches rows by the codes' weights
+        if (kEdge) {                                        // a NaN (m is 0 there) reaches rows by the codes' weights
           s0[w] &= __heq2_mask(bits_half2(s0[w]), bits_half2(s0[w]));
           s1[w] &= __heq2_mask(bits_half2(s1[w]), bits_half2(s1[w]));
         }
@@ -758,7 +764,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
               const float2 sa2 = __half22float2(bits_half2(va[w][g / 2])), sb2 = __half22float2(bits_half2(vb[w][g / 2]));
               const float sa = g & 1 ? sa2.y : sa2.x, sb = g & 1 ? sb2.y : sb2.x;
               float t[4] = {x[w][nt][0] * sa, x[w][nt][1] * sa, x[w][nt][2] * sb, x[w][nt][3] * sb};
-              if constexpr (kEdge) {
+              if (kEdge) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) t[j] = x[w][nt][j] == 0.f ? 0.f : t[j];
               }
@@ -776,7 +782,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
             } else {
               uint32_t b0 = half2_bits(__hmul2(bits_half2(pw[nt][0]), bits_half2(va[w][g])));
               uint32_t b1 = half2_bits(__hmul2(bits_half2(pw[nt][1]), bits_half2(vb[w][g])));
-              if constexpr (kEdge) {
+              if (kEdge) {
                 b0 &= __hne2_mask(bits_half2(pw[nt][0]), __half2half2(__ushort_as_half(0)));
                 b1 &= __hne2_mask(bits_half2(pw[nt][1]), __half2half2(__ushort_as_half(0)));
               }
@@ -818,8 +824,16 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
       const uint8_t* st = ring + stage * Sh::kStep;
       phases ^= 1u << stage;
       stage = stage + 1 == stages ? 0 : stage + 1;
-      if (static_cast<unsigned>(t - whole0) < static_cast<unsigned>(wholes) && hide == 0) step(std::false_type{}, st, 32 * t, 0);
-      else step(std::true_type{}, st, 32 * t, hide);
+      const bool edge = static_cast<unsigned>(t - whole0) >= static_cast<unsigned>(wholes) || hide != 0;
+      // One copy of the step's code, or one more for the steps that all rows see whole. With many short sequences the code that a
+      // CTA runs through bounds rows of 16 bits (256 of up to 900 places: 37.5 us with one copy, 42.8 with two; 32 of up to
+      // 32768: 74.2 and 73.5). Where a step has more registers at work, the branches cost more (16 of 64 fp32 elements: 60 and 51).
+      if constexpr (!FINE && NT == 1) {
+        step(edge, st, 32 * t, hide);
+      } else {
+        if (edge) step(std::true_type{}, st, 32 * t, hide);
+        else step(std::false_type{}, st, 32 * t, 0);
+      }
     }
 
     // The piece's sums as rows: where a held piece goes, or over the first stages.
