@@ -342,9 +342,9 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
     const int low_least = low_of(seen_least), low_most = low_of(seen_most);
     // Steps of the run that a row of this tile sees, and those of them that all of its rows see whole.
     t0 = max(t0, low_least >> 5);
-    t1 = min(t1, (seen_most + 31) >> 5);
+    t1 = min(t1, ((seen_most - 1) >> 5) + 1);            // (a sum of 31 could pass 2^31)
     const int mine = max(0, t1 - t0);
-    const int whole0 = (low_most + 31) >> 5, wholes = max(0, (seen_least >> 5) - whole0);
+    const int whole0 = ((low_most - 1) >> 5) + 1, wholes = max(0, (seen_least >> 5) - whole0);
 
     // Granules of this warp's steps: lane k % 32 has the two of step t0 + k (-1: none, or its page is out of range), and makes
     // their copies, as one where they lie side by side.

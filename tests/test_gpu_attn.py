@@ -335,3 +335,18 @@ def test_many_sequences():
     O, _ = _run(*case)
     o, E, S = ao.attention(f64(case[2]), case[0], case[1], 16, lens)
     _check(f64(O), o, E, S, "bf16", "O")
+
+
+def test_places_next_to_the_last_of_32_bits():
+    """Sequences of up to 2^31 - 1 places, all in one page that the table repeats, of which a window is seen."""
+    import torch
+    D, H, P = 64, 1, 65536
+    rng = np.random.default_rng(20)
+    page = random_cache(rng, 1, H, P, D)
+    lens = [2 ** 31 - 1, 2 ** 31 - 20, 2 ** 31 - 32]
+    Q = torch.randn(3, 4, D, device="cuda", dtype=torch.bfloat16)
+    O, _ = kq.kq_attn_q4(Q, _dev(page), torch.zeros(3, 2 ** 31 // P, dtype=torch.int32, device="cuda"),
+                         torch.tensor(lens, dtype=torch.int32, device="cuda"), window=100)
+    # The same places in a short sequence: 2^31 is a multiple of the page, so that these are its last ones.
+    o, E, S = ao.attention(f64(Q), page, np.zeros((3, 1), np.int32), P, [n % P for n in lens], window=100)
+    _check(f64(O), o, E, S, "bf16", "O")
