@@ -120,6 +120,29 @@ def test_masked_rows(dtype):
         assert ids[3] == 0 and ids[4] == 0 and ids[5] == 2999
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("masked", [0.5, 0.99])
+def test_masked_rows_of_many_tokens(dtype, masked):
+    """Rows that several CTAs share, of odd length: limits above what the mask leaves, few and many tokens left."""
+    rng = np.random.default_rng(8)
+    N, V = 6, 40003
+    L = (2 * rng.standard_normal((N, V))).astype(np.float32)
+    L[rng.random((N, V)) < masked] = -np.inf
+    L[4, 7] = 30.0
+    L[5, :-1] = -np.inf
+    t = _dev(L).to(torch_dtype(dtype))
+    u = rng.random(N).astype(np.float32)
+    for k in (3, 300, 2048, 3000, 30000):
+        K = np.full(N, k, np.int32)
+        _check(t, u, top_k=K)
+        for p in (0.3, 0.9, 0.999):
+            _check(t, u, top_k=K, top_p=np.full(N, p, np.float32), temperature=np.full(N, 1.7, np.float32))
+    for p in (0.5, 0.95):
+        _check(t, u, top_p=np.full(N, p, np.float32), min_p=np.full(N, 0.01, np.float32))
+    _check(t, u, min_p=np.full(N, 0.05, np.float32))
+    _check(t, u)
+
+
 def test_limits_at_their_ends():
     import torch
     rng = np.random.default_rng(6)
