@@ -421,7 +421,7 @@ KQ_API kq_status kq_moe_matvec_g4(const void* W, const void* scales, int scale_d
  * Qo, Ko: out_dtype, written; out_dtype is dtype, or any for fp32 inputs. Qo may be Q and
  * Ko K (the same pointer, ld and type); outputs overlap nothing else. q_gamma, k_gamma:
  * fp32 [head_dim] or NULL. head_dim: a multiple of 16 from 16 to 256; rot_dim: a multiple of 16
- * up to head_dim; eps >= 0. All arithmetic is fp32, rounded once to out_dtype; an
+ * up to head_dim; eps >= 0; N * (n_q_heads + n_k_heads) <= 2^30. All arithmetic is fp32, rounded once to out_dtype; an
  * unrounded result is within 16 * 2^-24 * (|a cos| + |b sin|) of its exact value (16 * 2^-24 * |y| where
  * nothing is turned), for every head of finite x (a head of zeros with eps = 0 gives NaN).
  */
@@ -457,7 +457,7 @@ KQ_API kq_status kq_qk_norm_rope(int dtype, const void* Q, int64_t ldq, int32_t 
  * belongs to sequence n). block_table: int32 [n_seqs][ldt]. A token with a negative position
  * is passed over; so is one whose sequence, place or page is out of range (KQ_DEVERR_PAGE
  * is recorded) or whose position is not in the table of cosines (KQ_DEVERR_POSITION). No
- * two tokens of a call have the same place (the bytes there would be of either).
+ * two tokens of a call have the same place (the bytes there would be of either). 2 * N * n_heads <= 2^30.
  */
 KQ_API kq_status kq_kv_append_q4(int dtype, const void* K, int64_t ldk, const void* V, int64_t ldv, int32_t n_heads,
                                  int32_t head_dim, const float* cos_sin, int32_t rot_dim, int64_t n_positions,
@@ -484,12 +484,14 @@ KQ_API kq_status kq_kv_gather_q4(const void* cache, int64_t n_pages, int32_t pag
  *   o = Sum_t p_t v_t, p = softmax_t(scale * q . k_t); a row that sees no place gives zeros.
  * Q: dtype; O: dtype [N][n_q_heads * head_dim], or NULL; Xq: N * (n_q_heads * head_dim / 32) * 36
  * bytes, the Q8_1 blocks of the unrounded o, or NULL; one of the two is given. Rows of Q that belong
- * to no sequence are not read, and theirs of O and Xq left as they were.
+ * to no sequence are not read, and theirs of O and Xq left as they were. O, Xq and ws overlap neither the inputs nor one another.
  * A place whose page is out of range counts as one that no row sees, and KQ_DEVERR_PAGE is recorded.
  * A query head with an infinity, a NaN or a value of 2^118 or more gives NaN. N * n_q_heads <= 2^30.
  * ws: at least kq_attn_q4_workspace_bytes(...) bytes, whatever they hold; calls that may
  * overlap need one each.
- * Scores, softmax statistics and sums are fp32. Made for the rows of decode steps: any number
+ * Scores, softmax statistics and sums are fp32; a score is a sum of exact products of q and the codes (fp32 q: of its first 22 bits).
+ * The softmax's weights are rounded for the tensor cores: to fp16 (relative 2^-12; the rows o are then rounded to 16 bits
+ * themselves), or, for fp32 rows and wherever Xq is asked for, to two fp16 halves (2^-23). Made for the rows of decode steps: any number
  * of new rows is taken, in tiles that each read the cache again.
  */
 KQ_API size_t kq_attn_q4_workspace_bytes(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int64_t N,
@@ -515,7 +517,8 @@ KQ_API kq_status kq_attn_q4(int dtype, const void* Q, int64_t ldq, int32_t n_q_h
  * (1, 1, 0); top_k: int32 [N] or NULL; u: fp32 [N]; ids: int32 [N], probs: fp32 [N] or NULL, written.
  * Weights are within 2^-30 of theirs, relative (with 2^-43 of the largest); the sums that are
  * compared are exact sums of them, so the choice is that of the definition unless two sums
- * that it compares are that close.
+ * that it compares are that close. Logits further apart than fp32's largest number count as infinitely far.
+ * N * V <= 2^40.
  */
 KQ_API kq_status kq_sample(int dtype, const void* logits, int64_t ld, const float* temperature, const int32_t* top_k,
                            const float* top_p, const float* min_p, const float* u, int32_t* ids, float* probs, int64_t V,

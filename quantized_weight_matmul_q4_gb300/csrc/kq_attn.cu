@@ -28,6 +28,15 @@
 // and the beginning of one. The pieces of a segment in a CTA's warps are joined there; what lies in several CTAs is
 // joined by a second kernel from the parts that the first leaves in the workspace. Both go by the
 // order of the line: results do not depend on scheduling.
+//
+// What bounds it (one GB300, calls in a graph over caches larger than L2, both kernels): at many places the issue of instructions. A
+// granule of 16 places of a head of 128 costs a warp 336 for up to 8 rows,
+// nearly twice that where weights are split: 32 sequences of up to 32768 places, 64 query heads on 8 of 128, 74 us (0.66 of
+// the copy bandwidth), one of 131072 with 32 heads on 8, 44 us (0.57). Below some 4000 places a sequence the ends bound it:
+// finding the runs, pages and queries 4 us before the first step, 3 us for outputs and the second kernel. One sequence of
+// 1000 places 15 us, 256 of up to 900 37 us (0.28). Tensor cores are a third busy, with mma.sync: the codes are
+// operands as they lie in the cache's bytes, in registers; tcgen05 would take them from shared memory as 16-bit numbers, four times
+// what was loaded to write and to read again, for tiles of which 8 of 128 rows are used.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -45,7 +54,8 @@ constexpr float kLow = -1e30f;          // the maximum before any score
 constexpr float kAhead = 4.f;           // how far a score may pass the maximum (log2) before it is moved
 constexpr float kTop = 10.f;            // weights are 2^(score - maximum + kTop): 2^14 at most
 constexpr int kSegmentUnits = 3;        // what beginning and ending a segment costs, in steps of 32 places
-constexpr int kLongPiece = 10;          // longer pieces' rounding costs more than runs that have parts of two segments
+constexpr int kLongPiece = 10;          // longer pieces' rounding costs more than runs that have parts of two segments (drafts of
+                                        // 5 rows for 32 heads of 64: 23.6 us, with 5 steps 24.8; 64 sequences with 20: 34.3 for 32.3)
 constexpr int kRound = 2;               // steps that a segment is cut by, and the fewest of a piece
 
 struct Attn {
@@ -168,7 +178,9 @@ template <typename T, int D, int NT, bool FINE>
 struct Shape {
   static constexpr int R = 8 * NT;
   static constexpr bool kSplitQ = sizeof(T) == 4;                     // queries in two halves
-  static constexpr int kWarps = D == 256 ? 7 : NT == 2 || kSplitQ ? 8 : 12;     // of a CTA, one to an SM
+  // Of a CTA, one to an SM: as many as have the registers that they need (8 heads of 128, 32 sequences of up to 32768
+  // places: 12 warps 68 us, 10 warps 75, 14 warps of 144 registers 87).
+  static constexpr int kWarps = D == 256 ? 7 : NT == 2 || kSplitQ ? 8 : 12;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kStep = 2 * Granule<D>::kBytes;
   static constexpr int kPitch = D + 4;                                // of the rows of a piece's sums
@@ -1069,9 +1081,12 @@ __global__ void __launch_bounds__(kJoinThreads) attn_q4_join_kernel(const Attn p
   }
 }
 
-// Rows of a tile: 8 where a sequence's (row, query head) pairs are 8 or fewer on the average, else 16 (of heads of 256
-// elements always 8: their sums are 128 registers for 16 rows).
-int tile_rows(int group, int D, int64_t N, int64_t n_seqs) { return D == 256 || group * N <= 8 * n_seqs ? 8 : 16; }
+// Rows of a tile: 8, or 16 where a sequence has more than 64 (row, query head) pairs of a key head on the average. 16 unpack a
+// step once for two columns of operands, but leave a warp more registers and so eight warps in place of twelve. us with 8 and 16
+// rows, 8 key heads of 128: 64 sequences of up to 4096 places with 12 pairs 38.0 and 46.1, 16 of up to 8192 with 32 pairs 41.5
+// and 43.8, with 64 pairs 57.3 and 57.2 (fp32 rows 83 and 100), 4 with 256 pairs 102 and 88 (fp32 160 and 151). Heads of
+// 256 elements always 8: their sums are 128 registers for 16 rows.
+int tile_rows(int group, int D, int64_t N, int64_t n_seqs) { return D == 256 || group * N <= 64 * n_seqs ? 8 : 16; }
 
 template <typename T, int D, int NT, bool FINE>
 cudaError_t run(const Attn& p, int num_sms, cudaStream_t s) {

@@ -6,6 +6,12 @@
 //   norm:      y = (x * 1 / sqrt(Sum x^2 / D + eps)) * gamma
 //   rotation:  (a, b) -> (a cos - b sin, b cos + a sin), each product and each sum rounded to fp32
 //   block:     m = fp16(min v), s = fp16((max v - min v) * (1 / 15)), c = clamp(rint((v - m) / s), 0, 15)
+//
+// What bounds it (one GB300, in a graph, inputs larger than L2): of many rows half memory, half the issue of
+// instructions. 4099 rows of 32 + 8 bf16 heads of 128, normed and turned: 25 us (0.51 of the copy bandwidth), of which the exchange of
+// halves and the sum of squares between lanes are a third of the instructions; 8191 tokens of 8 heads
+// written to the cache: 22 us, two thirds of them the codes; read back: 13 us (0.52). One row: 2 us, the launch and three loads
+// one after the other.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -378,7 +384,9 @@ bool even_rows(int64_t ld) {
   return ld * static_cast<int64_t>(sizeof(T)) % 16 == 0;
 }
 
-// Heads that a group takes: one until groups of four would fill every SM's threads.
+// Heads that a group takes: one until groups of four would fill every SM's threads. us with one, two, four and eight heads for 4099
+// rows of 40 heads 32.8, 27.0, 24.6, 23.9; 8191 tokens of 8 heads written 29.5, 24.8, 22.2, 25.8 and read 19.1, 14.7, 13.0, 17.7.
+// With one and four for 256 rows of 40 heads 3.4 and 4.9, 1024 tokens written 5.6 and 6.7.
 int heads_per_item(int64_t N, int rows, int lanes, int num_sms) {
   return N * rows * lanes >= static_cast<int64_t>(num_sms) * 2048 * 4 ? 4 : 1;
 }
