@@ -101,6 +101,21 @@ def test_several_new_rows(dtype, window, D, H, group, P, lens, new):
     _check(f64(O), o, E, S, dtype, "O")
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("D,H,group,P,lens,new,window", [
+    (128, 2, 4, 16, [250, 70, 3], [40, 33, 3], 0), (64, 1, 65, 32, [333], [1], 0), (128, 1, 16, 64, [65, 0, 900], [9, 0, 7], 50),
+    (128, 1, 33, 16, [2000, 2001], [2, 3], 0), (64, 3, 5, 16, [90, 17, 64, 1], [60, 17, 1, 1], 30), (128, 8, 8, 128, [700], [9], 0)])
+def test_many_pairs_of_row_and_head(dtype, D, H, group, P, lens, new, window):
+    """More than 64 (row, query head) pairs of a key head: tiles of 16; with one sequence whose tiles several CTAs share."""
+    case = _case(D + group, D, H, group, P, lens, new, dtype=dtype)
+    o, E, S = ao.attention(f64(case[2]), case[0], case[1], P, lens, q_start=case[4], window=window)
+    O, Xq = _run(*case, window=window, Xq=True)
+    _check(f64(O), o, E, S, dtype, "O", max(lens), True)
+    tol = _bound(o, E, S, dtype, max(lens), True)
+    _check_q8(Xq.cpu().numpy(), o.reshape(sum(new), -1), tol.reshape(sum(new), -1), "Xq")
+    _check(f64(_run(*case, window=window)[0]), o, E, S, dtype, "O without Xq", max(lens))
+
+
 def test_rows_that_see_nothing():
     """Sequences without places, with fewer places than new rows, and of negative length: zeros in both outputs."""
     lens, new = [0, 2, 5, -3, 40], [2, 4, 1, 1, 2]
