@@ -8,8 +8,7 @@
 //   block:     m = fp16(min v), s = fp16((max v - min v) * (1 / 15)), c = clamp(rint((v - m) / s), 0, 15)
 //
 // What bounds it (one GB300, in a graph, inputs larger than L2): of many rows half memory, half the issue of
-// instructions. 4099 rows of 32 + 8 bf16 heads of 128, normed and turned: 25 us (0.51 of the copy bandwidth), of which the exchange of
-// halves and the sum of squares between lanes are a third of the instructions; 8191 tokens of 8 heads
+// instructions. 4099 rows of 32 + 8 bf16 heads of 128, normed and turned: 21.6 us (0.60 of the copy bandwidth); 8191 tokens of 8 heads
 // written to the cache: 22 us, two thirds of them the codes; read back: 13 us (0.52). One row: 2 us, the launch and three loads
 // one after the other.
 #include <cuda_bf16.h>
@@ -95,18 +94,45 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
+// A lane's eight gammas (row null: none): loaded once for several heads, or where they are used (held for one head they are
+// eight registers more: 256 rows of 40 heads 4.0 us, 3.1 so).
+template <bool HELD>
+struct Gamma {
+  const float* row;
+  float held[8];
+  __device__ __forceinline__ Gamma(const float* gamma, int lane, bool mine) : row(gamma ? gamma + 8 * lane : nullptr) {
+    if constexpr (HELD) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) held[i] = 0.f;
+      if (row && mine) load(held);
+    }
+  }
+  __device__ __forceinline__ void load(float (&g)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) *reinterpret_cast<float4*>(g + 4 * i) = *reinterpret_cast<const float4*>(row + 4 * i);
+  }
+  __device__ __forceinline__ void get(float (&g)[8]) const {
+    if constexpr (HELD) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] = held[i];
+    } else {
+      load(g);
+    }
+  }
+};
+
 // v = (v * r) * gamma (gamma null: v), r = 1 / sqrt(Sum v^2 / D + eps). Where squares leave fp32's range, or are so small that
 // their sum loses bits, the head is taken times the power of two that brings the larger of max |v| and sqrt(eps) to between 1 and
 // 2 (in two factors: it can be beyond 2^127), and r is that of those values. (In 64 bits instead, and so for every
 // head since the compiler ran them beside the usual path: 120 us for 4099 x 40 heads of 128, against 17.)
-template <int LANES>
-__device__ __forceinline__ void norm_head(float (&v)[8], const float* gamma, bool mine, int lane, float inv_D, float eps) {
+template <int LANES, typename Gammas>
+__device__ __forceinline__ void norm_head(float (&v)[8], const Gammas& gamma, bool mine, float inv_D, float eps) {
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
   ss = group_sum<LANES>(ss);
   float m = fmaf(ss, inv_D, eps);
-  const bool far = !(ss < INFINITY && m >= 0x1p-90f) && gamma;
+  const bool far = !(ss < INFINITY && m >= 0x1p-90f) && gamma.row;
   if (__any_sync(0xffffffffu, far)) {
     float most = sqrtf(eps), sum = 0.f;
 #pragma unroll
@@ -128,16 +154,12 @@ __device__ __forceinline__ void norm_head(float (&v)[8], const float* gamma, boo
       for (int i = 0; i < 8; ++i) v[i] = w[i];
     }
   }
-  if (!mine || !gamma) return;
+  if (!mine || !gamma.row) return;
   const float r = rsqrtf(m);
+  float g[8];
+  gamma.get(g);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float4 g = *reinterpret_cast<const float4*>(gamma + 8 * lane + 4 * i);
-    v[4 * i] = v[4 * i] * r * g.x;
-    v[4 * i + 1] = v[4 * i + 1] * r * g.y;
-    v[4 * i + 2] = v[4 * i + 2] * r * g.z;
-    v[4 * i + 3] = v[4 * i + 3] * r * g.w;
-  }
+  for (int i = 0; i < 8; ++i) v[i] = v[i] * r * g[i];
 }
 
 struct HeadRows {
@@ -156,48 +178,43 @@ struct HeadRows {
   int* err;
 };
 
-// LANES: a power of two >= D / 8; HPI: heads of one token that a group takes.
+// LANES: a power of two >= D / 8; HPI: heads of one token, of queries or of keys, that a group takes.
 template <typename T, typename TO, bool VEC, int LANES, int HPI>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const HeadRows a) {
   pdl_enter();
   const int lane = threadIdx.x & (LANES - 1), base = threadIdx.x & 31 & ~(LANES - 1);
-  const int heads = a.n_q + a.n_k, chunks = (heads + HPI - 1) / HPI;
+  const int q_chunks = (a.n_q + HPI - 1) / HPI, chunks = q_chunks + (a.n_k + HPI - 1) / HPI;
   const float inv_D = __fdividef(1.0f, static_cast<float>(a.D));
   const uint32_t item = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;      // (host: below 2^31)
   const uint32_t n = item / static_cast<uint32_t>(chunks);
-  const int h0 = static_cast<int>(item - n * chunks) * HPI;
+  const int chunk = static_cast<int>(item - n * chunks);
+  const bool key = chunk >= q_chunks;
+  const int h0 = (key ? chunk - q_chunks : chunk) * HPI, some = min(HPI, (key ? a.n_k : a.n_q) - h0);
   bool ok = n < a.N;
   // The heads are on their way while the position and its row of the table are looked up.
   const bool lanes = ok && 8 * lane < a.D;
+  const int64_t at = static_cast<int64_t>(h0) * a.D + 8 * lane;
+  const T* x = (key ? static_cast<const T*>(a.K) + n * a.ldk : static_cast<const T*>(a.Q) + n * a.ldq) + at;
   Raw8<T> raw[HPI];
 #pragma unroll
-  for (int i = 0; i < HPI; ++i) {
-    const int h = h0 + i;
-    if (lanes && h < heads) {
-      const T* p = h < a.n_q ? static_cast<const T*>(a.Q) + n * a.ldq + static_cast<int64_t>(h) * a.D
-                             : static_cast<const T*>(a.K) + n * a.ldk + static_cast<int64_t>(h - a.n_q) * a.D;
-      raw[i].template load<VEC>(p + 8 * lane);
-    }
-  }
+  for (int i = 0; i < HPI; ++i)
+    if (lanes && i < some) raw[i].template load<VEC>(x + i * a.D);
   const int64_t pos = !ok ? 0 : a.positions ? a.positions[n] : n;
   ok = ok && pos >= 0;
   Turn turn;
   turn.load(table_row(a.rope, pos, ok, a.err), a.rope.rot, a.rope.pairs, lane);
   const bool mine = ok && lanes;
+  const Gamma<(HPI > 1)> gamma(key ? a.k_gamma : a.q_gamma, lane, mine);
+  TO* y = (key ? static_cast<TO*>(a.Ko) + n * a.ldko : static_cast<TO*>(a.Qo) + n * a.ldqo) + at;
 #pragma unroll
   for (int i = 0; i < HPI; ++i) {
-    const int h = h0 + i;
-    const bool here = mine && h < heads;
+    const bool here = mine && i < some;
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = here ? raw[i][j] : 0.f;
-    if (a.q_gamma || a.k_gamma) norm_head<LANES>(v, h < a.n_q ? a.q_gamma : a.k_gamma, here, lane, inv_D, a.eps);
+    if (a.q_gamma || a.k_gamma) norm_head<LANES>(v, gamma, here, inv_D, a.eps);
     if (a.rope.cos_sin) turn.apply(v, a.rope.pairs, base);
-    if (here) {
-      TO* p = h < a.n_q ? static_cast<TO*>(a.Qo) + n * a.ldqo + static_cast<int64_t>(h) * a.D
-                        : static_cast<TO*>(a.Ko) + n * a.ldko + static_cast<int64_t>(h - a.n_q) * a.D;
-      store8<TO, VEC>(p + 8 * lane, v);
-    }
+    if (here) store8<TO, VEC>(y + i * a.D, v);
   }
 }
 
@@ -384,11 +401,11 @@ bool even_rows(int64_t ld) {
   return ld * static_cast<int64_t>(sizeof(T)) % 16 == 0;
 }
 
-// Heads that a group takes: one until groups of four would fill every SM's threads. us with one, two, four and eight heads for 4099
-// rows of 40 heads 32.8, 27.0, 24.6, 23.9; 8191 tokens of 8 heads written 29.5, 24.8, 22.2, 25.8 and read 19.1, 14.7, 13.0, 17.7.
-// With one and four for 256 rows of 40 heads 3.4 and 4.9, 1024 tokens written 5.6 and 6.7.
+// Heads that a group takes: one until groups of one would fill every SM's threads. us with one, two, four and eight heads for
+// 8191 tokens of 8 heads written 29.5, 24.8, 22.2, 25.8 and read 19.1, 14.7, 13.0, 17.7; with one and four for 4099 rows of 40 heads 28
+// and 21.6, 512 rows 5.0 and 4.7, 256 rows 3.1 and 4.9; 2048 tokens of 8 heads written 10.7 and 8.6, 1024 tokens 5.6 and 6.7.
 int heads_per_item(int64_t N, int rows, int lanes, int num_sms) {
-  return N * rows * lanes >= static_cast<int64_t>(num_sms) * 2048 * 4 ? 4 : 1;
+  return N * rows * lanes >= static_cast<int64_t>(num_sms) * 2048 ? 4 : 1;
 }
 
 unsigned blocks_of(int64_t items, int lanes) {
@@ -400,7 +417,7 @@ template <typename T, typename TO, bool VEC, int LANES>
 cudaError_t norm_rope(const HeadRows& a, int num_sms, cudaStream_t s) {
   const int heads = a.n_q + a.n_k;
   if (heads_per_item(a.N, heads, LANES, num_sms) == 4)
-    return launch_pdl(qk_norm_rope_kernel<T, TO, VEC, LANES, 4>, dim3(blocks_of(a.N * ((heads + 3) / 4), LANES)),
+    return launch_pdl(qk_norm_rope_kernel<T, TO, VEC, LANES, 4>, dim3(blocks_of(a.N * ((a.n_q + 3) / 4 + (a.n_k + 3) / 4), LANES)),
                       dim3(kThreads), 0, s, a);
   return launch_pdl(qk_norm_rope_kernel<T, TO, VEC, LANES, 1>, dim3(blocks_of(a.N * heads, LANES)), dim3(kThreads), 0, s, a);
 }
