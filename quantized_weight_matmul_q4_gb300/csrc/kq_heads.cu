@@ -219,9 +219,9 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const HeadRows a
 }
 
 // The codes of the eight values v of a lane, the block being held by an aligned quad of lanes:
-// code i in bits 4i. s and m are as stored. The quotient is that of IEEE division: the product
-// with 1 / s is within 32 * 2^-23 of it (|quotient| <= 22: s is at least the true step less half
-// of fp16's least value), so only where it is that near a half is the division made.
+// code i in bits 4i. s and m are as stored. The quotient is that of IEEE division: 15 times the product
+// with 1 / (15 s), held to 0 .. 1 by the multiplication itself, is within 15 * 4 * 2^-24 < 10^-5 of it held to 0 .. 15, so only
+// where it is that near a half is the division made.
 __device__ __forceinline__ uint32_t block_codes(const float (&v)[8], __half& sh, __half& mh) {
   float lo = v[0], hi = v[0];
 #pragma unroll
@@ -240,7 +240,7 @@ __device__ __forceinline__ uint32_t block_codes(const float (&v)[8], __half& sh,
     return 0;
   }
   if (s == 0.f) return 0;
-  const float inv = __fdiv_rn(1.0f, s);
+  const float inv = __fdiv_rn(1.0f, s) * (1.0f / 15.0f);
   // The whole number nearest to a quotient (the even one of two) is in the low bits of its sum with 1.5 * 2^23; the sum
   // of these words times 16^i is the codes' word and a constant.
   constexpr float kWhole = 12582912.f;
@@ -248,9 +248,10 @@ __device__ __forceinline__ uint32_t block_codes(const float (&v)[8], __half& sh,
   float worst = 0.f;
 #pragma unroll
   for (int i = 7; i >= 0; --i) {
-    const float t = fminf(fmaxf(__fmul_rn(__fsub_rn(v[i], m), inv), 0.f), 15.f);
-    const float c = __fadd_rn(t, kWhole);
-    worst = fmaxf(worst, fabsf(t - __fsub_rn(c, kWhole)));
+    float t;
+    asm("mul.rn.sat.f32 %0, %1, %2;" : "=f"(t) : "f"(__fsub_rn(v[i], m)), "f"(inv));
+    const float c = __fmaf_rn(t, 15.f, kWhole);
+    worst = fmaxf(worst, fabsf(__fmaf_rn(t, 15.f, -__fsub_rn(c, kWhole))));
     w = (w << 4) + __float_as_uint(c);
   }
   if (worst > 0.49999f) {
