@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const HeadRows a
 
 // The codes of the eight values v of a lane, the block being held by an aligned quad of lanes:
 // code i in bits 4i. s and m are as stored. The quotient is that of IEEE division: 15 times the product
-// with 1 / (15 s), held to 0 .. 1 by the multiplication itself, is within 15 * 4 * 2^-24 < 10^-5 of it held to 0 .. 15, so only
+// with 1 / (15 s), held to 0 .. 1 by the multiplication itself, is within 15 * 6 * 2^-24 < 10^-5 of it held to 0 .. 15, so only
 // where it is that near a half is the division made.
 __device__ __forceinline__ uint32_t block_codes(const float (&v)[8], __half& sh, __half& mh) {
   float lo = v[0], hi = v[0];
@@ -234,13 +234,15 @@ __device__ __forceinline__ uint32_t block_codes(const float (&v)[8], __half& sh,
   mh = __float2half_rn(lo);
   sh = __float2half_rn(__fmul_rn(__fsub_rn(hi, lo), 1.0f / 15.0f));
   const float m = __half2float(mh), s = __half2float(sh);
-  if (!(fabsf(m) < INFINITY && s < INFINITY)) {      // a value that fp16 cannot hold, an infinity or a NaN
+  const bool numbers = fabsf(m) < INFINITY && s < INFINITY, codes = numbers && s > 0.f;
+  if (!numbers) {            // a value that fp16 cannot hold, an infinity or a NaN
     sh = __ushort_as_half(static_cast<unsigned short>(0x7fff));
     mh = __ushort_as_half(static_cast<unsigned short>(0));
-    return 0;
   }
-  if (s == 0.f) return 0;
-  const float inv = __fdiv_rn(1.0f, s) * (1.0f / 15.0f);
+  // Without codes all are 0: a NaN held to 0 .. 1 is 0 too.
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  inv = codes ? inv * (1.0f / 15.0f) : 0.f;
   // The whole number nearest to a quotient (the even one of two) is in the low bits of its sum with 1.5 * 2^23; the sum
   // of these words times 16^i is the codes' word and a constant.
   constexpr float kWhole = 12582912.f;
@@ -254,7 +256,7 @@ __device__ __forceinline__ uint32_t block_codes(const float (&v)[8], __half& sh,
     worst = fmaxf(worst, fabsf(__fmaf_rn(t, 15.f, -__fsub_rn(c, kWhole))));
     w = (w << 4) + __float_as_uint(c);
   }
-  if (worst > 0.49999f) {
+  if (codes && worst > 0.49999f) {
     w = 0;
 #pragma unroll
     for (int i = 7; i >= 0; --i) {
