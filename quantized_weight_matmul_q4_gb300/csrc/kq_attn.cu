@@ -33,8 +33,8 @@
 // granule of 16 places of a head of 128 costs a warp 336 for up to 8 rows,
 // nearly twice that where weights are split: 32 sequences of up to 32768 places, 64 query heads on 8 of 128, 74 us (0.66 of
 // the copy bandwidth), one of 131072 with 32 heads on 8, 44 us (0.57). Below some 4000 places a sequence the ends bound it:
-// finding the runs, pages and queries 4 us before the first step, 3 us for outputs and the second kernel. One sequence of
-// 1000 places 15 us, 256 of up to 900 37 us (0.28). Tensor cores are a third busy, with mma.sync: the codes are
+// finding the runs, pages and queries 3 to 4 us before the first step, 3 us for outputs and the second kernel. One sequence of
+// 1000 places 14 us, 256 of up to 900 37 us (0.28). Tensor cores are a third busy, with mma.sync: the codes are
 // operands as they lie in the cache's bytes, in registers; tcgen05 would take them from shared memory as 16-bit numbers, four times
 // what was loaded to write and to read again, for tiles of which 8 of 128 rows are used.
 #include <cuda_bf16.h>
@@ -229,11 +229,60 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
   // The CTA's runs: run i begins at the cut cut_u[i] of the line, in the sequence cut_b[i], whose first unit is cut_seq[i]. A
   // pass over the sequences adds up their segments and steps; another finds the cuts.
   Line line = {0, 1};
-  int64_t total = 0;
+  int64_t total = 0, c0 = 0, u, u1, b, seq_at;
   if (threadIdx.x == 0) p.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
-  {
-    const int64_t n_seqs = p.c.n_seqs, runs = static_cast<int64_t>(gridDim.x) * kWarps;
-    int64_t c0 = 0, before = 0;
+  const int64_t n_seqs = p.c.n_seqs, runs = static_cast<int64_t>(gridDim.x) * kWarps;
+  // The line of so many segments with so many steps in all, and this CTA's first cut; `total` is at most what it says then.
+  const auto lay = [&](int64_t segments, int64_t steps) {
+    // Pieces of so many steps that with one shorter piece a segment they are no more than the runs.
+    const int64_t piece = 2 * segments <= runs ? quotient(steps + runs - segments - 1, runs - segments) : kLongPiece + 1;
+    if (piece <= kLongPiece) {
+      line.piece = max(kRound, static_cast<int>(piece));
+      total = runs;
+    } else {
+      total = steps + kSegmentUnits * segments;
+      line.per = max(static_cast<int64_t>(kSegmentUnits + kRound), quotient(total + runs - 1, runs));
+    }
+    c0 = static_cast<int64_t>(blockIdx.x) * kWarps * line.per;
+  };
+  if (n_seqs <= 32) {
+    // Every warp for itself, a sequence to a lane: 37 places 9.9 us, one sequence of 1000 14.3, where the passes below with their
+    // eight barriers take 10.7 and 15.2.
+    Sequence s = {};
+    if (lane < n_seqs) s.load(p, lane, R);
+    int64_t segments = static_cast<int64_t>(p.c.heads) * s.tiles, steps = segments * s.steps;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      segments += __shfl_xor_sync(0xffffffffu, segments, o);
+      steps += __shfl_xor_sync(0xffffffffu, steps, o);
+    }
+    lay(segments, steps);
+    if (c0 >= total) return;
+    const int size = line.size(s);
+    int64_t x = line.units(s, p.c.heads), first = -x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    first += x;
+    total = __shfl_sync(0xffffffffu, x, 31);
+    if (c0 >= total) return;
+    // The cuts of this warp's run, by lanes 0 and 1: in the last sequence that begins at or before them.
+    const int64_t cut0 = c0 + warp * line.per, cut = cut0 + (lane & 1) * line.per;
+    const int at0 = 31 - __clz(__ballot_sync(0xffffffffu, lane < n_seqs && first <= cut0));
+    const int at1 = 31 - __clz(__ballot_sync(0xffffffffu, lane < n_seqs && first <= cut0 + line.per));
+    const int at = lane & 1 ? at1 : at0;
+    const int64_t from = __shfl_sync(0xffffffffu, first, at);
+    const int of = __shfl_sync(0xffffffffu, size, at);
+    const int64_t seg = from + quotient(cut - from, of) * of, cut_u = cut >= total ? total : seg + line.cut_at(cut - seg, of);
+    u = __shfl_sync(0xffffffffu, cut_u, 0);
+    u1 = __shfl_sync(0xffffffffu, cut_u, 1);
+    b = at0;
+    seq_at = __shfl_sync(0xffffffffu, first, at0);
+    __syncthreads();         // (what thread 0 has cleared)
+  } else {
+    int64_t before = 0;
     // The sum of v over the threads before this one, added to `before`, which moves on by the sum over all.
     const auto sum_before = [&](int64_t v) {
       int64_t x = v;
@@ -290,22 +339,13 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
         }
       }
       if (pass == 0) {
-        // Pieces of so many steps that with one shorter piece a segment they are no more than the runs.
         sum_before(segments);
         segments = before;
         before = 0;
         sum_before(steps);
         steps = before;
         before = 0;
-        const int64_t piece = 2 * segments <= runs ? quotient(steps + runs - segments - 1, runs - segments) : kLongPiece + 1;
-        if (piece <= kLongPiece) {
-          line.piece = max(kRound, static_cast<int>(piece));
-          total = runs;                          // at most
-        } else {
-          total = steps + kSegmentUnits * segments;
-          line.per = max(static_cast<int64_t>(kSegmentUnits + kRound), quotient(total + runs - 1, runs));
-        }
-        c0 = static_cast<int64_t>(blockIdx.x) * kWarps * line.per;
+        lay(segments, steps);
         if (c0 >= total) return;
       }
     }
@@ -314,10 +354,10 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
     __syncthreads();
     if (threadIdx.x <= kWarps && c0 + threadIdx.x * line.per >= total) cut_u[threadIdx.x] = total;
     __syncthreads();
+    u = cut_u[warp], b = cut_b[warp], seq_at = cut_seq[warp];
+    u1 = cut_u[warp + 1];
   }
 
-  int64_t u = cut_u[warp], b = cut_b[warp], seq_at = cut_seq[warp];
-  const int64_t u1 = cut_u[warp + 1];
   uint32_t phases = 0;       // of each stage's next copy
   int stages = S;            // that copies go to; a held piece takes the last kHeld
   Sequence q;
