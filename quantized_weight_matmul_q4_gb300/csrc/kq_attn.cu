@@ -30,9 +30,9 @@
 // order of the line: results do not depend on scheduling.
 //
 // What bounds it (one GB300, calls in a graph over caches larger than L2, both kernels): at many places the issue of instructions. A
-// granule of 16 places of a head of 128 costs a warp 336 for up to 8 rows,
-// nearly twice that where weights are split: 32 sequences of up to 32768 places, 64 query heads on 8 of 128, 74 us (0.66 of
-// the copy bandwidth), one of 131072 with 32 heads on 8, 44 us (0.57). Below some 4000 places a sequence the ends bound it:
+// granule of 16 places of a head of 128 costs a warp 363 for up to 8 rows,
+// nearly twice that where weights are split: 32 sequences of up to 32768 places, 64 query heads on 8 of 128, 73 us (0.67 of
+// the copy bandwidth), one of 131072 with 32 heads on 8, 43 us (0.58). Below some 4000 places a sequence the ends bound it:
 // finding the runs, pages and queries 3 to 4 us before the first step, 3 us for outputs and the second kernel. One sequence of
 // 1000 places 14 us, 256 of up to 900 37 us (0.28). Tensor cores are a third busy, with mma.sync: the codes are
 // operands as they lie in the cache's bytes, in registers; tcgen05 would take them from shared memory as 16-bit numbers, four times
@@ -179,7 +179,7 @@ struct Shape {
   static constexpr int R = 8 * NT;
   static constexpr bool kSplitQ = sizeof(T) == 4;                     // queries in two halves
   // Of a CTA, one to an SM: as many as have the registers that they need (8 heads of 128, 32 sequences of up to 32768
-  // places: 12 warps 68 us, 10 warps 75, 14 warps of 144 registers 87).
+  // places: 12 warps 68 us at that time, 10 warps 75, 14 warps of 144 registers 87).
   static constexpr int kWarps = D == 256 ? 7 : NT == 2 || kSplitQ ? 8 : 12;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kStep = 2 * Granule<D>::kBytes;

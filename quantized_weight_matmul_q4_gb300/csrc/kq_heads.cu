@@ -8,8 +8,8 @@
 //   block:     m = fp16(min v), s = fp16((max v - min v) * (1 / 15)), c = clamp(rint((v - m) / s), 0, 15)
 //
 // What bounds it (one GB300, in a graph, inputs larger than L2): of many rows half memory, half the issue of
-// instructions. 4099 rows of 32 + 8 bf16 heads of 128, normed and turned: 21.6 us (0.60 of the copy bandwidth); 8191 tokens of 8 heads
-// written to the cache: 22 us, two thirds of them the codes; read back: 13 us (0.52). One row: 2 us, the launch and three loads
+// instructions. 4099 rows of 32 + 8 bf16 heads of 128, normed and turned: 21.7 us (0.59 of the copy bandwidth); 8191 tokens of 8 heads
+// written to the cache: 20 us, most of it the codes; read back: 13 us (0.5). One row: 2 us, the launch and three loads
 // one after the other.
 #include <cuda_bf16.h>
 
