@@ -245,41 +245,50 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
     }
     c0 = static_cast<int64_t>(blockIdx.x) * kWarps * line.per;
   };
-  if (n_seqs <= 32) {
-    // Every warp for itself, a sequence to a lane: 37 places 9.9 us, one sequence of 1000 14.3, where the passes below with their
-    // eight barriers take 10.7 and 15.2.
-    Sequence s = {};
-    if (lane < n_seqs) s.load(p, lane, R);
-    int64_t segments = static_cast<int64_t>(p.c.heads) * s.tiles, steps = segments * s.steps;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      segments += __shfl_xor_sync(0xffffffffu, segments, o);
-      steps += __shfl_xor_sync(0xffffffffu, steps, o);
-    }
+  // Up to 32 sequences whose units 32 bits hold: every warp for itself, a sequence to a lane (37 places 9.3 us, one sequence of 1000
+  // 13.9, where the passes below with their eight barriers take 10.7 and 15.2).
+  Sequence q = {};
+  bool small = n_seqs <= 32;
+  if (small) {
+    if (lane < n_seqs) q.load(p, lane, R);
+    small = __all_sync(0xffffffffu, static_cast<int64_t>(p.c.heads) * q.tiles * (q.steps + kSegmentUnits) < (1 << 25));
+  }
+  if (small) {
+    const int mine = p.c.heads * q.tiles;
+    const int segments = __reduce_add_sync(0xffffffffu, mine), steps = __reduce_add_sync(0xffffffffu, mine * q.steps);
     lay(segments, steps);
     if (c0 >= total) return;
-    const int size = line.size(s);
-    int64_t x = line.units(s, p.c.heads), first = -x;
+    const int size = line.size(q), units = mine * size, per = static_cast<int>(line.per);
+    int x = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    first += x;
-    total = __shfl_sync(0xffffffffu, x, 31);
+    const int first = x - units, all = __shfl_sync(0xffffffffu, x, 31);
+    total = all;
     if (c0 >= total) return;
     // The cuts of this warp's run, by lanes 0 and 1: in the last sequence that begins at or before them.
-    const int64_t cut0 = c0 + warp * line.per, cut = cut0 + (lane & 1) * line.per;
+    const int64_t cut0 = c0 + warp * per, cut1 = cut0 + per;
     const int at0 = 31 - __clz(__ballot_sync(0xffffffffu, lane < n_seqs && first <= cut0));
-    const int at1 = 31 - __clz(__ballot_sync(0xffffffffu, lane < n_seqs && first <= cut0 + line.per));
-    const int at = lane & 1 ? at1 : at0;
-    const int64_t from = __shfl_sync(0xffffffffu, first, at);
-    const int of = __shfl_sync(0xffffffffu, size, at);
-    const int64_t seg = from + quotient(cut - from, of) * of, cut_u = cut >= total ? total : seg + line.cut_at(cut - seg, of);
+    const int at1 = 31 - __clz(__ballot_sync(0xffffffffu, lane < n_seqs && first <= cut1));
+    const int64_t cut = lane & 1 ? cut1 : cut0;
+    const int from = __shfl_sync(0xffffffffu, first, lane & 1 ? at1 : at0), of = __shfl_sync(0xffffffffu, size, lane & 1 ? at1 : at0);
+    int cut_u = all;
+    if (cut < all) {
+      const int off = static_cast<int>(cut) - from, in = off % of;
+      cut_u = from + off - in + static_cast<int>(line.cut_at(in, of));
+    }
     u = __shfl_sync(0xffffffffu, cut_u, 0);
     u1 = __shfl_sync(0xffffffffu, cut_u, 1);
     b = at0;
     seq_at = __shfl_sync(0xffffffffu, first, at0);
+    q.n0 = __shfl_sync(0xffffffffu, q.n0, at0);
+    q.len = __shfl_sync(0xffffffffu, q.len, at0);
+    q.rows = __shfl_sync(0xffffffffu, q.rows, at0);
+    q.tiles = __shfl_sync(0xffffffffu, q.tiles, at0);
+    q.first = __shfl_sync(0xffffffffu, q.first, at0);
+    q.steps = __shfl_sync(0xffffffffu, q.steps, at0);
     __syncthreads();         // (what thread 0 has cleared)
   } else {
     int64_t before = 0;
@@ -356,12 +365,11 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
     __syncthreads();
     u = cut_u[warp], b = cut_b[warp], seq_at = cut_seq[warp];
     u1 = cut_u[warp + 1];
+    if (u < u1) q.load(p, b, R);
   }
 
   uint32_t phases = 0;       // of each stage's next copy
   int stages = S;            // that copies go to; a held piece takes the last kHeld
-  Sequence q;
-  if (u < u1) q.load(p, b, R);
 
   while (u < u1) {
     {                        // a run may begin where a sequence ends, and goes on through others
