@@ -140,7 +140,8 @@ __device__ __forceinline__ void store_cluster(uint32_t addr, uint64_t v) {
 // What the CTAs that work on a row share: the row's cluster, or (ctas = 1) one CTA.
 struct Team {
   int ctas, rank;
-  uint64_t* slots;           // [2]: what this CTA tells the others, in turn; [2], [3]: and with its histogram
+  uint64_t* slots;           // [2]: what this CTA tells the others, in turn; [2], [3]: and with its histogram; [4], [5]: what
+                             // the others may still be reading when it tells the next
   uint64_t* part;            // [2 * kWarps]
   uint64_t* hist;            // [kBins], this CTA's
   uint64_t* all;             // [kBins], the team's
@@ -194,8 +195,9 @@ struct Team {
     return reduce(v, [](uint64_t a, uint64_t b) { return max(a, b); }, 0);
   }
 
-  // This CTA's sums, told to the others with its next histogram or sync, and the team's once that is done.
-  __device__ __forceinline__ void tell(uint64_t v, uint64_t w) const {
+  // This CTA's sums, told to the others with its next histogram or sync, and the team's once that is done. A word is written
+  // again only after a sync that follows its last reading: `to` is where they go.
+  __device__ __forceinline__ void tell(uint64_t v, uint64_t w, int to = 2) const {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -210,10 +212,10 @@ struct Team {
       v = part[lane];
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if ((lane & 15) == 0) slots[2 + (lane >> 4)] = v;
+      if ((lane & 15) == 0) slots[to + (lane >> 4)] = v;
     }
   }
-  __device__ __forceinline__ uint64_t told(int word, uint64_t* before = nullptr) const {
+  __device__ __forceinline__ uint64_t told(int word, uint64_t* before = nullptr) const {      // of slots[2 + word]
     const int lane = threadIdx.x & 31;
     uint64_t v = lane < ctas ? load_cluster(mapa_shared(slots + 2 + word, lane)) : 0, b = lane < rank ? v : 0;
 #pragma unroll
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint32_t table[256];
   __shared__ float per_T[2];
-  __shared__ uint64_t least, slots[4], part[2 * kWarps], found_above;
+  __shared__ uint64_t least, slots[6], part[2 * kWarps], found_above;
   __shared__ float partf[kWarps];
   __shared__ int bin_of, found;
   __shared__ float up_to, available;
@@ -640,7 +642,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
           const float beyond = value_of(hi);
           uint64_t mine = 0;
           all_from(beyond, [&](float l, int) { mine += l > beyond ? row.w(l) : 0; });
-          team.tell(0, mine);
+          // In words of its own: if the search ends with its first histogram, no sync follows before the choice tells.
+          team.tell(mine, 0, 4);
           beyond_told = true;
         }
       }
@@ -658,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         });
         if (threadIdx.x == 0) found = -1;
         const uint64_t* h = team.gather([](uint64_t v, uint64_t w) { return v + w; });
-        if (beyond_told) above = team.told(1), beyond_told = false;
+        if (beyond_told) above = team.told(2), beyond_told = false;
         uint64_t bin[kPerThread], mine = 0;
 #pragma unroll
         for (int i = 0; i < kPerThread; ++i) mine += bin[i] = h[kPerThread * threadIdx.x + i];
