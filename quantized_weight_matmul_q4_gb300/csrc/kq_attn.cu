@@ -50,7 +50,7 @@
 namespace kq {
 namespace {
 
-constexpr float kLow = -1e30f;          // the maximum before any score
+constexpr float kLow = -3.402823466e38f;           // the maximum before any score: no finite score is below it
 constexpr float kAhead = 4.f;           // how far a score may pass the maximum (log2) before it is moved
 constexpr float kTop = 10.f;            // weights are 2^(score - maximum + kTop): 2^14 at most
 constexpr int kSegmentUnits = 3;        // what beginning and ending a segment costs, in steps of 32 places
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
         qs[nt][k][0] = pack_half2(sums[4 * k], sums[4 * k + 1]);
         qs[nt][k][1] = G > 2 ? pack_half2(sums[(4 * k + 2) % G], sums[(4 * k + 3) % G]) : 0u;
       }
-      const float f = most < 0x1p118f ? p.a.scale * 1.44269504f * pow2(10 + min(e, 117)) : NAN;
+      const float f = seen_of(i) <= 0 ? 0.f : most < 0x1p118f ? p.a.scale * 1.44269504f * pow2(10 + min(e, 117)) : NAN;
 #pragma unroll
       for (int c = 0; c < 2; ++c) factor[nt][c] = __shfl_sync(0xffffffffu, f, 4 * (2 * tig + c));
     }
@@ -527,7 +527,9 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
       top[nt][0] = top[nt][1] = kLow;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        om[nt][j] = 0.f;
+        // A row whose scores all lie below fp32's range has no weights, as one that sees nothing, but is not a row of zeros: with
+        // this total, which no weight leaves anything of, it becomes 0 / 0. (A score is its factor times less than 2^20.)
+        om[nt][j] = j >= 2 && fabsf(factor[nt][j & 1]) > 0x1p100f ? 0x1p-140f : 0.f;
 #pragma unroll
         for (int g = 0; g < G; ++g) o[nt][g][0][j] = o[nt][g][1][j] = 0.f;
       }
