@@ -19,8 +19,8 @@
 // Scores are exact products summed in fp32. Weights are rounded to fp16 as operands (a relative 2^-12 each time,
 // twice for those of the codes, which 16-bit outputs do not show). For fp32 rows, and where Q8_1 rows are asked for (a code
 // that a rounding moves is a whole step), weights are split into two halves, the codes are operands less 8, and sums of a granule
-// are added in fp32; fp32 queries are split as well. Weights are relative to a power of two not below the largest s so far, so that none
-// leaves fp16's range.
+// are added in fp32; fp32 queries are split as well. A weight's products with s are relative to a power of two not below the largest
+// s so far, so that none leaves fp16's range; the total and the sum of the m + 8 s take weights that are not.
 //
 // Work is shared out evenly whatever the sequences' lengths: all (sequence, key head, tile of rows) segments stand
 // in one line, of which each warp takes an equal run. Where segments are few and short, the line is of pieces of so many steps of
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
     }
 
     float o[NT][G][2][4], om[NT][4], top[NT][2];
-    int sigma = kSplit ? -24 : 0;                                     // weights are relative to 2^sigma
+    int sigma = kSplit ? -24 : 0;                                     // products with s are relative to 2^sigma
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       top[nt][0] = top[nt][1] = kLow;
@@ -676,12 +676,14 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
       if constexpr (!kSplit && D >= 128) sizes = gid < G ? sizes : 0;
 
       // Scores less their columns' offset; the maximum is moved where one passes it by kAhead, sigma where an s passes 2^sigma.
-      // Rows of 16 bits have sigma 0 until an s is 2 or more (its exponent's highest bit is set).
+      // Rows of 16 bits have sigma 0 until an s is 2 or more (its exponent's highest bit is set). Split weights are taken times
+      // 2^-sigma (exactly, in fp32) from the first.
       float x[2][NT][4];
+      const auto sigma_x = [&] { return kSplit ? static_cast<float>(sigma) : 0.f; };
       const auto shift = [&] {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float off[2] = {top[nt][0] + (static_cast<float>(sigma) - kTop), top[nt][1] + (static_cast<float>(sigma) - kTop)};
+          const float off[2] = {top[nt][0] + (sigma_x() - kTop), top[nt][1] + (sigma_x() - kTop)};
 #pragma unroll
           for (int w = 0; w < 2; ++w)
 #pragma unroll
@@ -707,7 +709,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
         largest = fminf(fmaxf(fmaxf(__low2float(big), __high2float(big)), 0.f), 65504.f);
       };
       if constexpr (kSplit) find_largest();
-      if (__any_sync(0xffffffffu, ahead > kTop + kAhead - static_cast<float>(sigma) ||
+      if (__any_sync(0xffffffffu, ahead > kTop + kAhead - sigma_x() ||
                                       (kSplit ? largest > pow2(sigma) : (sizes & 0x40004000u) != 0))) {
         if constexpr (!kSplit) {
           find_largest();
@@ -728,8 +730,8 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
             m = fmaxf(m, top[nt][c]);
             const float f = exp2_fast(top[nt][c] - m), fs = f * by;
             top[nt][c] = m;
-            om[nt][c] *= kSplit ? f : fs;
-            om[nt][c + 2] *= kSplit ? f : fs;
+            om[nt][c] *= f;
+            om[nt][c + 2] *= f;
 #pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -745,11 +747,13 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
       const float scale_m = sigma > 0 ? 0.0625f : 0.5f;
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        // Weights, transposed as operands. Rows of 16 bits: the weights times 2^(kTop - sigma) rounded to fp16, and for each
-        // block's codes their products with s (at most 2^15: s is below 2 with sigma 0, else s / 2^sigma at most 1). fp32
-        // rows: these products taken in fp32, and the weights times 2^kTop, all in two halves.
+        // Weights, transposed as operands. Rows of 16 bits: the weights times 2^kTop rounded to fp16, and for each block's codes these
+        // times 2^-sigma and s (at most 2^15: s is below 2 with sigma 0, else s / 2^sigma at most 1; what 2^-sigma takes from a weight
+        // is below 2^(sigma - 35) of the largest, and does not show in the total). fp32 rows: products with s taken in fp32, and the
+        // weights times 2^kTop, all in two halves.
         uint32_t pw[NT][2];
         [[maybe_unused]] uint32_t pl[kSplit ? NT : 1][2];
+        [[maybe_unused]] __half2 ps[kSplit ? 1 : NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -762,6 +766,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
               pl[nt][k] = transpose8(pack_half2(low_part(y), low_part(z)));
             } else {
               pw[nt][k] = transpose8(pack_half2(x[w][nt][2 * k], x[w][nt][2 * k + 1]));
+              ps[nt][k] = __hmul2(bits_half2(pw[nt][k]), __float2half2_rn(pow2(-sigma)));
             }
           }
         }
@@ -842,8 +847,8 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
                 for (int j = 0; j < 4; ++j) o[nt][g][k][j] += of[k][j];
               }
             } else {
-              uint32_t b0 = half2_bits(__hmul2(bits_half2(pw[nt][0]), bits_half2(va[w][g])));
-              uint32_t b1 = half2_bits(__hmul2(bits_half2(pw[nt][1]), bits_half2(vb[w][g])));
+              uint32_t b0 = half2_bits(__hmul2(ps[nt][0], bits_half2(va[w][g])));
+              uint32_t b1 = half2_bits(__hmul2(ps[nt][1], bits_half2(vb[w][g])));
               if (kEdge) {
                 b0 &= __hne2_mask(bits_half2(pw[nt][0]), __half2half2(__ushort_as_half(0)));
                 b1 &= __hne2_mask(bits_half2(pw[nt][1]), __half2half2(__ushort_as_half(0)));
@@ -903,7 +908,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
     float* sums = reinterpret_cast<float*>(ring + (first_piece ? (S - Sh::kHeld) * Sh::kStep : 0));
     float(&most_of)[R] = stat[warp][first_piece ? 0 : 1][0];
     float(&total_of)[R] = stat[warp][first_piece ? 0 : 1][1];
-    const float up = kSplit ? pow2(sigma) : 0x1p24f, up_odd = kSplit ? up : 0x1p20f;
+    const float up = pow2(sigma + (kSplit ? 0 : 24)), up_odd = pow2(sigma + (kSplit ? 0 : 20));
     __syncwarp();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -911,7 +916,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
       for (int c = 0; c < 2; ++c) {
         const int r = 8 * nt + 2 * tig + c;
         if (gid == 0) {
-          most_of[r] = top[nt][c] + (kSplit ? 0.f : static_cast<float>(sigma));
+          most_of[r] = top[nt][c];
           total_of[r] = om[nt][c + 2];
         }
 #pragma unroll

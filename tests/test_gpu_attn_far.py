@@ -2,9 +2,10 @@
 import numpy as np
 import pytest
 
-from _attnutil import f64
+import quantized_weight_matmul_q4_gb300 as kq
+from _attnutil import HALF, f64, random_cache, torch_dtype
 from oracle import attn_oracle as ao
-from test_gpu_attn import _case, _run
+from test_gpu_attn import _bound, _case, _check, _dev, _run
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +67,50 @@ def test_scores_beyond_fp32():
     for size, nan in ((-3e35, True), (-1e15, False)):
         O, _ = _run(case[0], case[1], torch.full_like(case[2], size), *case[3:], scale=1e20)
         assert bool(torch.isnan(O).all()) == nan and (nan or bool(torch.isfinite(O).all()))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("Xq", [False, True])
+def test_many_light_places_beside_a_large_block(dtype, Xq):
+    """A few heavy places and some 10^5 with 2^-19 of their weight, in runs of thousands of places, and a block of a very large s that
+    no row gives weight to. Values are constant in a block: o is the share of the light places in the total."""
+    import torch
+    D, P, L, B = 64, 65536, 131072, 512
+    rng = np.random.default_rng(3)
+    cache = random_cache(rng, 2, 1, P, D)
+    place = np.arange(L).reshape(2, 1, P // 16, 16)
+    k = np.where(place % 32768 == 77, 0.0, np.log(0.9) - 19 * np.log(2))
+    k[place % 4096 == 5] = -100.0
+    v = np.where(place % 32768 == 77, -1.0, 1.0)
+    v[place % 4096 == 5] = 0.0
+    constant_blocks(cache, False, k)
+    constant_blocks(cache, True, v)
+    s = cache[..., 18 * D:].view(np.float16).reshape(2, 1, P // 16, 16, 2, 2)
+    s[place % 4096 == 5, 0] = 60000.0
+    Q = torch.ones(B, 1, D, device="cuda", dtype=torch_dtype(dtype))
+    table = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda").expand(B, 2).contiguous()
+    lens = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    O, _ = kq.kq_attn_q4(Q, _dev(cache), table, lens, scale=1 / D, Xq=Xq)
+    o, E, S = ao.attention(f64(Q[:1]), cache, np.array([[0, 1]]), P, [L], scale=1 / D)
+    assert abs(o[0, 0, 0]) < 0.95
+    _check(f64(O), o, E, S, dtype, "O", L, Xq)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("Xq", [False, True])
+@pytest.mark.parametrize("least,most,floor", [(2.0 ** -24, 2.0 ** -14, 2.0 ** -23), (2.0 ** -16, 2.0 ** -6, 2.0 ** -23), (1.0, 30.0, 2.0 ** -20)])
+def test_values_of_every_size(dtype, Xq, least, most, floor):
+    """Values next to fp16's least numbers, and ones whose s is 2 and more: m + 8 s to within an absolute error of `floor`, and the products
+    of weights with s to (1 + s) S 2^-35 of the largest weight, |c - 8| times that, for each of the places."""
+    D, P, lens = 128, 16, [200, 37, 1]
+    cache, t, Q, n, start = _case(int(1 / least) % 1000, D, 2, 4, P, lens, dtype=dtype)
+    rng = np.random.default_rng(5)
+    s = (least * (most / least) ** rng.random((*cache.shape[:3], 16, D // 32))).astype(np.float16)
+    m = (-15 * s.astype(np.float64) * rng.random(s.shape)).astype(np.float16)
+    cache[..., 18 * D:] = np.ascontiguousarray(np.concatenate([s, m], -1).reshape(*cache.shape[:3], -1)).view(np.uint8)
+    O, _ = _run(cache, t, Q, n, start, Xq=Xq)
+    o, E, S = ao.attention(f64(Q), cache, t, P, lens)
+    top = max(1.0, 2.0 ** np.ceil(np.log2(most)))
+    tol = _bound(o, E, S, dtype, max(lens), Xq) + floor + max(lens) * 8 * (1 + top) * top * 2.0 ** -35
+    tol = tol + HALF[dtype] * (np.abs(o) + tol) + (2.0 ** -25 if dtype == "fp16" else 0)
+    assert np.all(np.abs(f64(O) - o) <= tol), (np.abs(f64(O) - o) / tol).max()
