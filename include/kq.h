@@ -485,7 +485,8 @@ KQ_API kq_status kq_kv_gather_q4(const void* cache, int64_t n_pages, int32_t pag
  * Q: dtype; O: dtype [N][n_q_heads * head_dim], or NULL; Xq: N * (n_q_heads * head_dim / 32) * 36
  * bytes, the Q8_1 blocks of the unrounded o, or NULL; one of the two is given. Rows of Q that belong
  * to no sequence are not read, and theirs of O and Xq left as they were. O, Xq and ws overlap neither the inputs nor one another.
- * A place whose page is out of range counts as one that no row sees, and KQ_DEVERR_PAGE is recorded.
+ * A place whose page is out of range counts as one that no row sees, and KQ_DEVERR_PAGE is recorded; table entries of places that no
+ * row sees are not looked at (those before a window may be anything).
  * A query head with an infinity, a NaN or a value of 2^118 or more gives NaN, and so does one with a score (times log2 e) above
  * fp32's range, or with none that is not below it. N * n_q_heads <= 2^30.
  * ws: at least kq_attn_q4_workspace_bytes(...) bytes, whatever they hold; calls that may

@@ -406,14 +406,14 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
     const int mine = max(0, t1 - t0);
     const int whole0 = ((low_most - 1) >> 5) + 1, wholes = max(0, (seen_least >> 5) - whole0);
 
-    // Granules of this warp's steps: lane k % 32 has the two of step t0 + k (-1: none, or its page is out of range), and makes
-    // their copies, as one where they lie side by side.
+    // Granules of this warp's steps: lane k % 32 has the two of step t0 + k (-1: one that no row sees, whose page may be gone, or its
+    // page is out of range), and makes their copies, as one where they lie side by side.
     const int per_page = p.c.page_shift - 4;
     const int32_t* table = p.c.table + b * p.c.ldt;
-    const int last_granule = (seen_most - 1) >> 4;
+    const int first_granule = low_least >> 4, last_granule = (seen_most - 1) >> 4;
     auto granule_at = [&](int g) -> int {
       const int64_t i = static_cast<int64_t>(g) >> per_page;
-      const int page = g <= last_granule && i < p.c.ldt ? table[i] : -1;
+      const int page = g >= first_granule && g <= last_granule && i < p.c.ldt ? table[i] : -1;
       if (page < 0 || page >= p.c.n_pages) return -1;
       return static_cast<int>(((static_cast<int64_t>(page) * p.c.heads + h) << per_page) + (g & ((1 << per_page) - 1)));
     };
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
         const int g = 2 * (t0 + k + lane);
         ga = granule_at(g);
         gb = per_page > 0 && g < last_granule && ga >= 0 ? ga + 1 : granule_at(g + 1);
-        if (ga < 0 || (gb < 0 && g < last_granule)) report_error(p.err, ERR_PAGE);
+        if ((ga < 0 && g >= first_granule) || (gb < 0 && g < last_granule)) report_error(p.err, ERR_PAGE);
       }
     };
     auto issue = [&](int to) {

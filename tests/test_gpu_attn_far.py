@@ -1,4 +1,4 @@
-"""kq_attn_q4 where scores, weights or parameters are far from the usual ones."""
+"""kq_attn_q4 where scores, weights or parameters are far from the usual ones, and in tables whose older pages are gone."""
 import numpy as np
 import pytest
 
@@ -114,3 +114,23 @@ def test_values_of_every_size(dtype, Xq, least, most, floor):
     tol = _bound(o, E, S, dtype, max(lens), Xq) + floor + max(lens) * 8 * (1 + top) * top * 2.0 ** -35
     tol = tol + HALF[dtype] * (np.abs(o) + tol) + (2.0 ** -25 if dtype == "fp16" else 0)
     assert np.all(np.abs(f64(O) - o) <= tol), (np.abs(f64(O) - o) / tol).max()
+
+
+@pytest.mark.parametrize("P", [16, 32])
+@pytest.mark.parametrize("dtype,new", [("bf16", None), ("fp32", [1, 3, 2])])
+def test_pages_older_than_the_window_may_be_gone(P, dtype, new):
+    """A window that begins in the second half of 32 places, whose first half's page is no longer in the table."""
+    lens, window = [63, 130, 97], 14
+    case = _case(P, 128, 2, 4, P, lens, new, dtype=dtype)
+    want, _ = _run(*case, window=window)
+    t = case[1].copy()
+    for b, n in enumerate(lens):
+        first = n - (new[b] if new else 1) + 1 - window
+        t[b, :first // P] = -1
+    got, _ = _run(case[0], t, *case[2:], window=window)
+    assert np.array_equal(f64(got), f64(want))
+    assert kq.kq_get_device_error() == 0
+    # One that is seen is recorded.
+    t[1, (lens[1] - 1) // P] = -1
+    _run(case[0], t, *case[2:], window=window)
+    assert kq.kq_get_device_error() == kq.KQ_DEVERR_PAGE
