@@ -491,12 +491,14 @@ KQ_API kq_status kq_kv_gather_q4(const void* cache, int64_t n_pages, int32_t pag
  * fp32's range, or with none that is not below it. N * n_q_heads <= 2^30.
  * ws: at least kq_attn_q4_workspace_bytes(...) bytes, whatever they hold; calls that may
  * overlap need one each.
- * Scores, softmax statistics and sums are fp32; a score is a sum of exact products of q and the codes (fp32 q: of its first 22 bits).
- * The softmax's weights, their products with s, and m + 8 s are rounded for the tensor cores: to fp16 (relative 2^-12 each; the rows o
- * are then rounded to 16 bits themselves), or, for fp32 rows and wherever Xq is asked for, to two fp16 halves (2^-23). Below fp16's
- * range errors are absolute: 2^-35 of the largest weight; (1 + s) S 2^-35 of it for products with s, S the power of two not below
- * the largest s gone over (at least 1); 2^-23 for m + 8 s, 2^-20 where an s of 2 or more has been gone over. Made for the rows of decode steps: any number
- * of new rows is taken, in tiles that each read the cache again.
+ * Scores, softmax statistics and sums are fp32; a score is a sum of exact products of q and the codes (fp32 q: of its first 22 bits) by
+ * the tensor cores, whose additions cut off: it is within 2^-18 of scale * Sum (s c + |m|) |q| over the head. The softmax's
+ * weights, their products with s, and m + 8 s are rounded for the tensor cores: to fp16 (relative 2^-11 each; the rows o are then
+ * rounded to 16 bits themselves; what the sums cut off is below 2^-16 of Sum_t p_t (s c + |m|)), or, for fp32 rows and wherever Xq is
+ * asked for, to two fp16 halves (2^-22). Below fp16's range errors are absolute: 2^-35 of the largest weight; (1 + s) S 2^-35
+ * of it for products with s, S the power of two not below the largest s gone over (at least 1); 2^-23 for m + 8 s, 2^-20 where
+ * an s of 2 or more has been gone over.
+ * Made for the rows of decode steps: any number of new rows is taken, in tiles that each read the cache again.
  */
 KQ_API size_t kq_attn_q4_workspace_bytes(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int64_t N,
                                          int64_t n_seqs);

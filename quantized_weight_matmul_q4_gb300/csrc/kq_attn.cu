@@ -16,8 +16,8 @@
 // sum is a product of the m + 8 s, which also gives Sum_t p_t by a row of ones; it is taken for each step by itself and
 // added in fp32.
 //
-// Scores are exact products summed in fp32. Weights are rounded to fp16 as operands (a relative 2^-12 each time,
-// twice for those of the codes, which 16-bit outputs do not show). For fp32 rows, and where Q8_1 rows are asked for (a code
+// Scores are exact products summed in fp32. Weights are rounded to fp16 as operands (a relative 2^-11 at most each time,
+// twice for those of the codes, which 16-bit outputs show in their last bit). For fp32 rows, and where Q8_1 rows are asked for (a code
 // that a rounding moves is a whole step), weights are split into two halves, the codes are operands less 8, and sums of a granule
 // are added in fp32; fp32 queries are split as well. A weight's products with s are relative to a power of two not below the largest
 // s so far, so that none leaves fp16's range; the total and the sum of the m + 8 s take weights that are not.
