@@ -115,7 +115,8 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return (a | b) >> 32 == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
 }
 
-// a / b for 0 <= a, exactly: (a + 1/2) / b is at least 1 / (2 b) from a whole number, far above its rounding for a < 2^20.
+// a / b for 0 <= a, exactly: (a + 1/2) / b is at least 1 / (2 b) from a whole number, and the quotient, of 2 ulp at most, within
+// 2^-22 of itself: 1 / (4 b) for a < 2^20, half of that distance.
 __device__ __forceinline__ int divide(int a, int b) {
   return a < (1 << 20) ? static_cast<int>(__fdividef(static_cast<float>(a) + 0.5f, static_cast<float>(b))) : a / b;
 }
