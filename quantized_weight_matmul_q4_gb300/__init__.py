@@ -471,6 +471,7 @@ def kq_kv_gather_q4(cache, block_table, positions, seq_ids=None, dtype=None, K=N
     sequences seq_ids (as in kq_kv_append_q4). Rows of places that there are not are left as they were."""
     torch = _torch()
     c, pages, page, H, D, bt, ldt, seqs = _kv_cache(cache, block_table)
+    at = _dev(positions, "positions", torch.int32)
     N = positions.numel()
     shape = (N, H, D)
     if dtype is None:
@@ -481,7 +482,7 @@ def kq_kv_gather_q4(cache, block_table, positions, seq_ids=None, dtype=None, K=N
         V = _out(shape, dtype, cache.device, stream)
     k, ldk = _head_rows(K, "K", shape, dtype)
     v, ldv = _head_rows(V, "V", shape, dtype)
-    check(lib().kq_kv_gather_q4(c, pages, page, H, D, bt, ldt, seqs, _sized(positions, "positions", N, torch.int32),
+    check(lib().kq_kv_gather_q4(c, pages, page, H, D, bt, ldt, seqs, at,
                                 _sized(seq_ids, "seq_ids", N, torch.int32), _dtype(K, "K"), k, ldk, v, ldv, N,
                                 _stream(stream)), "kq_kv_gather_q4")
     return K, V
