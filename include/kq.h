@@ -521,7 +521,7 @@ KQ_API kq_status kq_attn_q4(int dtype, const void* Q, int64_t ldq, int32_t n_q_h
  * any other gives token 0 with probability 0.
  * logits: dtype [N][V], rows ld apart, V <= 524288. temperature, top_p, min_p: fp32 [N], or NULL
  * (1, 1, 0); top_k: int32 [N] or NULL; u: fp32 [N]; ids: int32 [N], probs: fp32 [N] or NULL, written.
- * Weights are within 2^-30 of theirs, relative (with 2^-43 of the largest); the sums that are
+ * Weights are within 2^-30 of theirs, relative (with 2^-43 of the largest), for T from 2^-126 to 2^110; the sums that are
  * compared are exact sums of them, so the choice is that of the definition unless two sums
  * that it compares are that close. Logits further apart than fp32's largest number count as infinitely far.
  * N * V <= 2^40.

@@ -30,11 +30,11 @@
 // order of the line: results do not depend on scheduling.
 //
 // What bounds it (one GB300, calls in a graph over caches larger than L2, both kernels): at many places the issue of instructions. A
-// granule of 16 places of a head of 128 costs a warp 363 for up to 8 rows,
-// nearly twice that where weights are split: 32 sequences of up to 32768 places, 64 query heads on 8 of 128, 73 us (0.67 of
+// granule of 16 places of a head of 128 costs a warp 355 for up to 8 rows,
+// nearly twice that where weights are split: 32 sequences of up to 32768 places, 64 query heads on 8 of 128, 72 us (0.67 of
 // the copy bandwidth), one of 131072 with 32 heads on 8, 43 us (0.58). Below some 4000 places a sequence the ends bound it:
 // finding the runs, pages and queries 3 to 4 us before the first step, 3 us for outputs and the second kernel. One sequence of
-// 1000 places 14 us, 256 of up to 900 37 us (0.28). Tensor cores are a third busy, with mma.sync: the codes are
+// 1000 places 14 us, 256 of up to 900 38 us (0.28). Tensor cores are a third busy, with mma.sync: the codes are
 // operands as they lie in the cache's bytes, in registers; tcgen05 would take them from shared memory as 16-bit numbers, four times
 // what was loaded to write and to read again, for tiles of which 8 of 128 rows are used.
 #include <cuda_bf16.h>
@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(Shape<T, D, NT, FINE>::kThreads) attn_q4_kerne
     }
     c0 = static_cast<int64_t>(blockIdx.x) * kWarps * line.per;
   };
-  // Up to 32 sequences whose units 32 bits hold: every warp for itself, a sequence to a lane (37 places 9.3 us, one sequence of 1000
-  // 13.9, where the passes below with their eight barriers take 10.7 and 15.2).
+  // Up to 32 sequences whose units 32 bits hold: every warp for itself, a sequence to a lane (37 places 9.3 us at that time, one sequence
+  // of 1000 13.9, where the passes below with their eight barriers took 10.7 and 15.2).
   Sequence q = {};
   bool small = n_seqs <= 32;
   if (small) {

@@ -124,7 +124,7 @@ struct Gamma {
 // v = (v * r) * gamma (gamma null: v), r = 1 / sqrt(Sum v^2 / D + eps). Where squares leave fp32's range, or are so small that
 // their sum loses bits, the head is taken times the power of two that brings the larger of max |v| and sqrt(eps) to between 1 and
 // 2 (in two factors: it can be beyond 2^127), and r is that of those values. (In 64 bits instead, and so for every
-// head since the compiler ran them beside the usual path: 120 us for 4099 x 40 heads of 128, against 17.)
+// head since the compiler ran them beside the usual path: 120 us for 4099 x 40 heads of 128, against 25 for fp32 alone at that time.)
 template <int LANES, typename Gammas>
 __device__ __forceinline__ void norm_head(float (&v)[8], const Gammas& gamma, bool mine, float inv_D, float eps) {
   float ss = 0.f;
