@@ -489,6 +489,8 @@ KQ_API kq_status kq_kv_gather_q4(const void* cache, int64_t n_pages, int32_t pag
  * row sees are not looked at (those before a window may be anything).
  * A query head with an infinity, a NaN or a value of 2^118 or more gives NaN, and so does one with a score (times log2 e) above
  * fp32's range, or with none that is not below it. N * n_q_heads <= 2^30.
+ * A NaN among a place's keys makes the rows that see it NaN, one among its values their elements of that block (one whose place has less
+ * than 2^-34 of a row's largest weight may not).
  * ws: at least kq_attn_q4_workspace_bytes(...) bytes, whatever they hold; calls that may
  * overlap need one each.
  * Scores, softmax statistics and sums are fp32; a score is a sum of exact products of q and the codes (fp32 q: of its first 22 bits) by
